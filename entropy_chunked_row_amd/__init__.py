@@ -11,6 +11,8 @@ kernels; if liblp.so is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
+import ctypes
 from typing import Optional, Tuple
 
 from . import _lib
@@ -21,7 +23,8 @@ __all__ = [
     "lp_lm_head_workspace_bytes", "lp_kl_full_vocab", "lp_prob_diff", "lp_version", "lp_timing_enable",
     "lp_timing_read", "lp_timing_clock", "lp_logprobs_entropy_k", "lp_lm_head_logprobs_entropy_k",
     "lp_lm_head_logprobs_entropy_backward_k", "lp_prob_diff_stats", "lp_lm_head_kl_workspace_bytes",
-    "lp_lm_head_kl", "lp_lm_head_kl_backward", "LPError", "load",
+    "lp_lm_head_kl", "lp_lm_head_kl_backward", "LogitRules", "lp_process_logits", "lp_processed_logprobs_entropy",
+    "lp_processed_logprobs_entropy_backward", "lp_processed_workspace_bytes", "LPError", "load",
 ]
 
 
@@ -446,3 +449,200 @@ def lp_lm_head_kl_backward(student_hidden, student_weight, teacher_hidden, teach
                                     _stream(stream))
     check("lp_lm_head_kl_backward", st)
     return dH, dW
+
+
+# ---------------------------------------------------------------------------
+# logit rules
+# ---------------------------------------------------------------------------
+
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(device, stream):
+    """Context in which a call on `device` allocates and launches: outputs and
+    workspaces come from the memory of the stream that the kernels run on, and
+    `device` is current while they are launched."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, expected {device}")
+        return torch.cuda.stream(stream)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return _NO_SCOPE
+
+
+class LogitRules:
+    """Penalties for repeated tokens, biases and a grammar mask on T rows of
+    logits (struct lp_logit_rules; a rule left None is off).
+
+    tokens [B, L] int32 with contiguous rows, hist_len [T] int32: row t's
+    history is the first hist_len[t] tokens of buffer row_seq[t] (int32 [T];
+    None: buffer t), its first prompt_len[t] the prompt (int32 [T]; None: no
+    prompt).  repetition, frequency, presence: fp32 [T].  bias_offsets int64
+    [T + 1] into bias_tokens (int32) and bias_values (fp32).  allowed [T, W]
+    int32 or uint32 with contiguous rows, W >= ceil(V / 32).
+
+    Types and layouts are checked here, the lengths that depend on T and V and
+    the device by each call that takes the rules.  The tensors are kept, not
+    copied: what they hold when a call runs on the stream is what it reads."""
+
+    __slots__ = ("c", "_kept", "_per_row", "_buffers", "_offsets", "_words")
+
+    def __init__(self, tokens=None, hist_len=None, prompt_len=None, row_seq=None, repetition=None, frequency=None,
+                 presence=None, bias_offsets=None, bias_tokens=None, bias_values=None, allowed=None):
+        torch = _torch()
+        i32, f32 = torch.int32, torch.float32
+        c = _lib.LogitRulesC()
+        per_row = []
+        for name, t, dt in (("hist_len", hist_len, i32), ("prompt_len", prompt_len, i32), ("row_buffer", row_seq, i32),
+                            ("repetition", repetition, f32), ("frequency", frequency, f32), ("presence", presence, f32)):
+            if t is not None:
+                _vec(t, "row_seq" if name == "row_buffer" else name, dt)
+                per_row.append(("row_seq" if name == "row_buffer" else name, t))
+                setattr(c, name, t.data_ptr())
+        self._buffers = None
+        if tokens is not None:
+            if tokens.dtype != i32:
+                raise TypeError(f"tokens must be torch.int32, got {tokens.dtype}")
+            ld = _rows(tokens, "tokens")
+            if hist_len is None:
+                raise ValueError("tokens need hist_len")
+            # no buffers, or buffers of no tokens: nobody has a history
+            if tokens.numel():
+                c.tokens, c.buffers, c.ld_tokens, c.max_len = tokens.data_ptr(), tokens.size(0), ld, tokens.size(1)
+                self._buffers = None if row_seq is not None else tokens.size(0)
+            else:
+                c.repetition = c.frequency = c.presence = None
+        elif any(t is not None for t in (hist_len, prompt_len, row_seq, repetition, frequency, presence)):
+            raise ValueError("penalties need tokens and hist_len")
+        self._offsets = bias_offsets
+        if bias_offsets is not None:
+            _vec(bias_offsets, "bias_offsets", torch.int64)
+            if bias_tokens is None or bias_values is None:
+                raise ValueError("biases need bias_tokens and bias_values")
+            _vec(bias_tokens, "bias_tokens", i32)
+            _vec(bias_values, "bias_values", f32, bias_tokens.numel())
+            c.bias_count = bias_tokens.numel()
+            c.bias_offsets = bias_offsets.data_ptr()
+            c.bias_tokens, c.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
+        elif bias_tokens is not None or bias_values is not None:
+            raise ValueError("biases need bias_offsets")
+        self._words = allowed
+        if allowed is not None:
+            if allowed.dtype != i32 and allowed.dtype != torch.uint32:
+                raise TypeError(f"allowed must be int32 or uint32, got {allowed.dtype}")
+            c.ld_allowed = _rows(allowed, "allowed")
+            c.allowed = allowed.data_ptr()
+        self.c = c
+        self._per_row = per_row
+        self._kept = [(n, t) for n, t in (("tokens", tokens), ("bias_offsets", bias_offsets),
+                                          ("bias_tokens", bias_tokens), ("bias_values", bias_values),
+                                          ("allowed", allowed)) if t is not None]
+
+    def _check(self, T, V, device):
+        """The ctypes argument for a call on T rows of V columns on `device`."""
+        for name, t in self._per_row:
+            if t.numel() != T:
+                raise ValueError(f"{name} must have {T} elements, got {t.numel()}")
+        if self._buffers is not None and self._buffers < T:
+            raise ValueError(f"tokens must have a buffer for each of {T} rows, got {self._buffers}")
+        if self._offsets is not None and self._offsets.numel() != T + 1:
+            raise ValueError(f"bias_offsets must have {T + 1} elements, got {self._offsets.numel()}")
+        w = self._words
+        if w is not None and (w.size(0) != T or w.size(1) < (V + 31) // 32):
+            raise ValueError(f"allowed must be [{T}, >= {(V + 31) // 32}], got {list(w.shape)}")
+        for name, t in self._per_row:
+            if t.device != device:
+                _on(device, **{name: t})
+        for name, t in self._kept:
+            if t.device != device:
+                _on(device, **{name: t})
+        return ctypes.byref(self.c)
+
+
+def _processed_operands(logits, rules):
+    """(T, V, ld, rules argument) of logits [T, V] under `rules` (None: no rules)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [T, V]")
+    T, V = logits.shape
+    return T, V, _rows(logits, "logits"), None if rules is None else rules._check(T, V, logits.device)
+
+
+def lp_process_logits(logits, rules, mask=None, *, out=None, stream=None):
+    """logits [T, V] under `rules` (LogitRules or None), rounded once to their dtype.  Rows with mask 0 are not
+    written; out may be the logits themselves (in place)."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    T, V, ld, c_rules = _processed_operands(logits, rules)
+    mask = _vec(mask, "mask", torch.uint8, T)
+    if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype):
+        raise ValueError("out must have the logits' shape and dtype")
+    ld_out = V if out is None else _rows(out, "out")
+    dev = logits.device
+    _on(dev, logits=logits, mask=mask, out=out)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((T, V), dtype=logits.dtype, device=dev)
+        st = lib.lp_process_logits(_ptr(logits), dtype, T, V, ld, c_rules, _ptr(mask), _ptr(out), ld_out,
+                                   _stream(stream))
+    check("lp_process_logits", st)
+    return out
+
+
+def lp_processed_workspace_bytes(T: int, V: int) -> int:
+    return int(load().lp_processed_workspace_bytes(T, V))
+
+
+def lp_processed_logprobs_entropy(logits, rules, targets, mask=None, temperature: float = 1.0, *,
+                                  want_entropy: bool = True, want_lse: bool = True, workspace=None, stream=None):
+    """(logprob, entropy, lse) of softmax(rules(logits) / temperature); logits [T, V], rules LogitRules or None."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    T, V, ld, c_rules = _processed_operands(logits, rules)
+    targets = _vec(targets, "targets", torch.int64, T)
+    mask = _vec(mask, "mask", torch.uint8, T)
+    dev = logits.device
+    _on(dev, logits=logits, targets=targets, mask=mask)
+    f32 = dict(dtype=torch.float32, device=dev)
+    with _scope(dev, stream):
+        lp = torch.empty(T, **f32)
+        H = torch.empty(T, **f32) if want_entropy else None
+        lse = torch.empty(T, **f32) if want_lse else None
+        ws, ws_bytes = _workspace(lp_processed_workspace_bytes(T, V), dev, workspace)
+        st = lib.lp_processed_logprobs_entropy(_ptr(logits), dtype, T, V, ld, c_rules, _ptr(targets), _ptr(mask),
+                                               float(temperature), _ptr(lp), _ptr(H), _ptr(lse), _ptr(ws), ws_bytes,
+                                               _stream(stream))
+    check("lp_processed_logprobs_entropy", st)
+    return lp, H, lse
+
+
+def lp_processed_logprobs_entropy_backward(logits, rules, targets, mask, temperature: float, lse, entropy,
+                                           grad_logprob, grad_entropy=None, *, grad_logits=None, stream=None):
+    """Gradient [T, V] of sum g_lp * logprob + g_H * entropy with respect to the raw logits, in their dtype."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    T, V, ld, c_rules = _processed_operands(logits, rules)
+    targets = _vec(targets, "targets", torch.int64, T)
+    mask = _vec(mask, "mask", torch.uint8, T)
+    lse = _vec(lse, "lse", torch.float32, T)
+    entropy = _vec(entropy, "entropy", torch.float32, T)
+    grad_logprob = _vec(grad_logprob, "grad_logprob", torch.float32, T)
+    grad_entropy = _vec(grad_entropy, "grad_entropy", torch.float32, T)
+    if grad_logits is not None and (grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype):
+        raise ValueError("grad_logits must have the logits' shape and dtype")
+    ld_grad = V if grad_logits is None else _rows(grad_logits, "grad_logits")
+    dev = logits.device
+    _on(dev, logits=logits, targets=targets, mask=mask, lse=lse, entropy=entropy, grad_logprob=grad_logprob,
+        grad_entropy=grad_entropy, grad_logits=grad_logits)
+    with _scope(dev, stream):
+        if grad_logits is None:
+            grad_logits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+        st = lib.lp_processed_logprobs_entropy_backward(
+            _ptr(logits), dtype, T, V, ld, c_rules, _ptr(targets), _ptr(mask), float(temperature), _ptr(lse),
+            _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(grad_logits), ld_grad, _stream(stream))
+    check("lp_processed_logprobs_entropy_backward", st)
+    return grad_logits

@@ -17,6 +17,17 @@ c_vp = ctypes.c_void_p
 c_f = ctypes.c_float
 c_int = ctypes.c_int
 
+
+class LogitRulesC(ctypes.Structure):
+    """struct lp_logit_rules of include/lp.h."""
+    _fields_ = [("tokens", c_vp), ("buffers", c_i64), ("ld_tokens", c_i64), ("max_len", c_i64), ("row_buffer", c_vp), ("prompt_len", c_vp),
+                ("hist_len", c_vp), ("repetition", c_vp), ("frequency", c_vp), ("presence", c_vp),
+                ("bias_offsets", c_vp), ("bias_tokens", c_vp), ("bias_values", c_vp), ("bias_count", c_i64),
+                ("allowed", c_vp), ("ld_allowed", c_i64)]
+
+
+c_rules = ctypes.POINTER(LogitRulesC)
+
 # name -> (restype, argtypes); mirrors include/lp.h
 SIGNATURES = {
     "lp_version": (c_int, []),
@@ -51,6 +62,12 @@ SIGNATURES = {
     "lp_lm_head_kl_backward": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64,
                                        c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.c_size_t,
                                        c_vp]),
+    "lp_process_logits": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_rules, c_vp, c_vp, c_i64, c_vp]),
+    "lp_processed_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64]),
+    "lp_processed_logprobs_entropy": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_rules, c_vp, c_vp, c_f, c_vp, c_vp,
+                                              c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "lp_processed_logprobs_entropy_backward": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_rules, c_vp, c_vp, c_f, c_vp,
+                                                       c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
     "lp_timing_enable": (None, [c_int]),
     "lp_timing_read": (c_int, [ctypes.c_char_p, ctypes.POINTER(c_i64), ctypes.POINTER(ctypes.c_double)]),
     "lp_timing_clock": (c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i64)]),

@@ -541,4 +541,187 @@ lp_status lp_prob_diff_stats(const float* lp_a, const float* lp_b, const uint8_t
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// logit rules
+// ---------------------------------------------------------------------------
+
+static bool i32_aligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p && !aligned(p, 4)) return false;
+  return true;
+}
+
+// Whether two row-major blocks of T rows share bytes, taken as address ranges.
+static bool ranges_overlap(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t T, int64_t V, size_t e) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t(T - 1) * ld_b + V) * e && y < x + (uintptr_t(T - 1) * ld_a + V) * e;
+}
+
+// Checks shared by the calls under rules; fills the fields every one of them
+// has.  T == 0 passes with nothing examined beyond the sizes.
+static lp_status check_rules(const char* fn, const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                             const lp_logit_rules* rules, const uint8_t* mask, lp::RulesArgs* a) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", fn, static_cast<int>(dtype));
+  if (T < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: T < 0", fn);
+  if (V <= 0 || V > kMaxV) return fail(LP_ERR_INVALID_ARGUMENT, "%s: V out of range (1..2^30)", fn);
+  if (ld < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld < V", fn);
+  if (T > (int64_t(1) << 40) || ld > (int64_t(1) << 40) / (T > 0 ? T : 1))
+    return fail(LP_ERR_UNSUPPORTED, "%s: T x ld past 2^40 elements", fn);
+  memset(a, 0, sizeof(*a));
+  a->x = logits;
+  a->ld = ld;
+  a->V = static_cast<int>(V);
+  a->T = T;
+  a->mask = mask;
+  if (T == 0) return LP_OK;
+  if (!logits) return fail(LP_ERR_INVALID_ARGUMENT, "%s: logits are required", fn);
+  if (!aligned(logits, dtype_bytes(dtype))) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned logits", fn);
+  if (!rules) return LP_OK;
+  const lp_logit_rules& r = *rules;
+  if (!i32_aligned({r.tokens, r.row_buffer, r.prompt_len, r.hist_len, r.repetition, r.frequency, r.presence,
+                    r.bias_tokens, r.bias_values, r.allowed}) ||
+      (r.bias_offsets && !aligned(r.bias_offsets, 8)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned rules array", fn);
+  if (r.tokens) {
+    if (!r.hist_len) return fail(LP_ERR_INVALID_ARGUMENT, "%s: tokens need hist_len", fn);
+    if (r.buffers < 1 || r.max_len < 1 || r.buffers > 0x7fffffff || r.max_len > 0x7fffffff ||
+        r.ld_tokens < r.max_len || r.ld_tokens > (int64_t(1) << 40) / r.buffers)
+      return fail(LP_ERR_INVALID_ARGUMENT,
+                  "%s: buffers and max_len must be in 1..2^31-1, ld_tokens >= max_len, the buffers below 2^40 tokens",
+                  fn);
+    if (!r.row_buffer && r.buffers < T)
+      return fail(LP_ERR_INVALID_ARGUMENT, "%s: without row_buffer every row needs a buffer of its own", fn);
+  } else if (r.repetition || r.frequency || r.presence) {
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: penalties need tokens and hist_len", fn);
+  }
+  if (r.bias_offsets) {
+    if (r.bias_count < 0 || r.bias_count > 0x7fffffff)
+      return fail(LP_ERR_INVALID_ARGUMENT, "%s: bias_count must be in 0..2^31-1", fn);
+    if (r.bias_count > 0 && (!r.bias_tokens || !r.bias_values))
+      return fail(LP_ERR_INVALID_ARGUMENT, "%s: biases need bias_tokens and bias_values", fn);
+  } else if (r.bias_tokens || r.bias_values) {
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: biases need bias_offsets", fn);
+  }
+  if (r.allowed && r.ld_allowed < (V + 31) / 32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_allowed must be >= ceil(V / 32)", fn);
+  // a history without any penalty changes nothing and is not read
+  if (r.tokens && (r.repetition || r.frequency || r.presence)) {
+    a->tokens = r.tokens;
+    a->buffers = r.buffers;
+    a->ld_tokens = r.ld_tokens;
+    a->max_len = r.max_len;
+    a->row_buffer = r.row_buffer;
+    a->prompt_len = r.prompt_len;
+    a->hist_len = r.hist_len;
+    a->repetition = r.repetition;
+    a->frequency = r.frequency;
+    a->presence = r.presence;
+  }
+  if (r.bias_offsets && r.bias_count > 0) {
+    a->bias_offsets = r.bias_offsets;
+    a->bias_tokens = r.bias_tokens;
+    a->bias_values = r.bias_values;
+    a->bias_count = r.bias_count;
+  }
+  a->allowed = r.allowed;
+  a->ld_allowed = r.ld_allowed;
+  return LP_OK;
+}
+
+lp_status lp_process_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                            const lp_logit_rules* rules, const uint8_t* mask, void* out, int64_t ld_out,
+                            void* stream) {
+  const char* fn = "lp_process_logits";
+  lp::RulesArgs a;
+  lp_status st = check_rules(fn, logits, dtype, T, V, ld, rules, mask, &a);
+  if (st != LP_OK) return st;
+  if (ld_out < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_out < V", fn);
+  if (T == 0) return ok();
+  if (ld_out > (int64_t(1) << 40) / T) return fail(LP_ERR_UNSUPPORTED, "%s: T x ld_out past 2^40 elements", fn);
+  if (!out || !aligned(out, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: out is required and must be aligned", fn);
+  if (!(out == logits && ld_out == ld) && ranges_overlap(logits, ld, out, ld_out, T, V, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: out overlaps the logits without being them", fn);
+  a.out = out;
+  a.ld_out = ld_out;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_process_logits(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+size_t lp_processed_workspace_bytes(int64_t T, int64_t V) {
+  if (T < 0 || T > (int64_t(1) << 40) || V <= 0 || V > kMaxV) return 0;
+  const size_t n = lp::processed_workspace_bytes(T, V);
+  return n > 256 ? n : 256;
+}
+
+lp_status lp_processed_logprobs_entropy(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                        const lp_logit_rules* rules, const int64_t* targets, const uint8_t* mask,
+                                        float temperature, float* logprob, float* entropy, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "lp_processed_logprobs_entropy";
+  lp::RulesArgs a;
+  lp_status st = check_rules(fn, logits, dtype, T, V, ld, rules, mask, &a);
+  if (st != LP_OK) return st;
+  if (!isfinite(temperature)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: temperature not finite", fn);
+  if (T == 0) return ok();
+  if (!targets || !logprob) return fail(LP_ERR_INVALID_ARGUMENT, "%s: targets and logprob are required", fn);
+  if (!aligned(targets, 8) || !f32_aligned({logprob, entropy, lse}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t need = lp_processed_workspace_bytes(T, V);
+  if (!workspace || workspace_bytes < need)
+    return fail(LP_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %zu bytes, got %zu", fn, need,
+                workspace ? workspace_bytes : size_t(0));
+  if (!aligned(workspace, 256)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
+  a.targets = targets;
+  a.c = exp2_scale(temperature);
+  a.logprob = logprob;
+  a.entropy_out = entropy;
+  a.lse_out = lse;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_processed_score(static_cast<int>(dtype), a, static_cast<char*>(workspace),
+                                            static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dtype, int64_t T, int64_t V,
+                                                 int64_t ld, const lp_logit_rules* rules, const int64_t* targets,
+                                                 const uint8_t* mask, float temperature, const float* lse,
+                                                 const float* entropy, const float* grad_logprob,
+                                                 const float* grad_entropy, void* grad_logits, int64_t ld_grad,
+                                                 void* stream) {
+  const char* fn = "lp_processed_logprobs_entropy_backward";
+  lp::RulesArgs a;
+  lp_status st = check_rules(fn, logits, dtype, T, V, ld, rules, mask, &a);
+  if (st != LP_OK) return st;
+  if (!isfinite(temperature)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: temperature not finite", fn);
+  if (ld_grad < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_grad < V", fn);
+  if (T == 0) return ok();
+  if (ld_grad > (int64_t(1) << 40) / T) return fail(LP_ERR_UNSUPPORTED, "%s: T x ld_grad past 2^40 elements", fn);
+  if (!targets || !lse || !grad_logprob || !grad_logits || (grad_entropy && !entropy))
+    return fail(LP_ERR_INVALID_ARGUMENT,
+                "%s: targets, lse, grad_logprob and grad_logits are required, and entropy with grad_entropy", fn);
+  if (!aligned(targets, 8) || !f32_aligned({lse, entropy, grad_logprob, grad_entropy}) ||
+      !aligned(grad_logits, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  if (ranges_overlap(logits, ld, grad_logits, ld_grad, T, V, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: grad_logits overlaps the logits", fn);
+  a.targets = targets;
+  a.c = exp2_scale(temperature);
+  a.inv_tau = temperature_applies(temperature) ? 1.0f / temperature : 1.0f;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.grad_logprob = grad_logprob;
+  a.grad_entropy = grad_entropy;
+  a.out = grad_logits;
+  a.ld_out = ld_grad;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_processed_grad(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
 }  // extern "C"

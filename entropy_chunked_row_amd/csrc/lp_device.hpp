@@ -22,6 +22,7 @@ namespace lp {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kLog2e = 1.44269504088896340736f;
 // Reference exponent of a state that has seen nothing.  Finite on purpose: a
 // -inf element then gives t = -inf (probability 0) instead of NaN.
 constexpr float kNegBig = -3.402823466e38f;
@@ -125,6 +126,18 @@ __device__ __forceinline__ Stat stat_block_allreduce(Stat st, Stat* sm) {
 // element types: 16-byte vectors and exact widening to fp32
 // ---------------------------------------------------------------------------
 
+// Two fp32 values rounded to nearest even and packed (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (f16x2_t{static_cast<_Float16>(lo), static_cast<_Float16>(hi)}));
+}
+
 struct Bf16 {
   static constexpr int kBytes = 2;
   static constexpr int kPerVec = 8;
@@ -141,6 +154,12 @@ struct Bf16 {
   __device__ static __forceinline__ float load1(const char* p, int64_t i) {
     const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
     return __uint_as_float(static_cast<uint32_t>(b) << 16);
+  }
+  __device__ static __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  }
+  __device__ static __forceinline__ void store1(char* p, int64_t i, float x) {
+    reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
   }
 };
 
@@ -164,6 +183,12 @@ struct Fp16 {
   __device__ static __forceinline__ float load1(const char* p, int64_t i) {
     return half_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
   }
+  __device__ static __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]), pack_f16x2(x[6], x[7])};
+  }
+  __device__ static __forceinline__ void store1(char* p, int64_t i, float x) {
+    reinterpret_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+  }
 };
 
 struct Fp32 {
@@ -178,6 +203,10 @@ struct Fp32 {
   __device__ static __forceinline__ float load1(const char* p, int64_t i) {
     return reinterpret_cast<const float*>(p)[i];
   }
+  __device__ static __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+  }
+  __device__ static __forceinline__ void store1(char* p, int64_t i, float x) { reinterpret_cast<float*>(p)[i] = x; }
 };
 
 // Dual (student u, teacher v) state for KL(teacher || student).

@@ -78,6 +78,59 @@ hipError_t launch_prob_diff_stats(const float* a, const float* b, const uint8_t*
                                   void* ws, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// logit rules
+// ---------------------------------------------------------------------------
+
+// The lp_logit_rules of a call plus its operands; fields of other calls stay
+// null.
+struct RulesArgs {
+  const void* x;
+  int64_t ld;
+  int V;
+  int64_t T;
+  const uint8_t* mask;
+  // rules (any of tokens, bias_offsets, allowed may be null: that rule is off)
+  const int32_t* tokens;
+  int64_t buffers, ld_tokens, max_len;
+  const int32_t* row_buffer;
+  const int32_t* prompt_len;
+  const int32_t* hist_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int64_t* bias_offsets;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  int64_t bias_count;
+  const uint32_t* allowed;
+  int64_t ld_allowed;
+  // processed logits, or the gradient of the raw ones
+  void* out;
+  int64_t ld_out;
+  // scoring and its gradient
+  const int64_t* targets;
+  float c;        // log2(e) / tau_effective
+  float inv_tau;  // 1 / tau_effective
+  float* logprob;
+  float* entropy_out;
+  float* lse_out;
+  const float* lse;
+  const float* entropy;
+  const float* grad_logprob;
+  const float* grad_entropy;
+  // set by the launchers
+  int64_t row0;
+  int slice, nslices;
+  float* part;  // [T x nslices x 3] states (mc, s, a)
+  float* zy;    // [T] processed logit of the target
+};
+
+size_t processed_workspace_bytes(int64_t T, int64_t V);
+hipError_t launch_process_logits(int dtype, const RulesArgs& a, hipStream_t s);
+hipError_t launch_processed_score(int dtype, const RulesArgs& a, char* ws, hipStream_t s);
+hipError_t launch_processed_grad(int dtype, const RulesArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // fused LM head
 // ---------------------------------------------------------------------------
 

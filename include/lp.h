@@ -332,6 +332,109 @@ lp_status lp_prob_diff_stats(const float* lp_a, const float* lp_b, const uint8_t
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Logit rules: what a sampler does to a row of logits before it draws from
+ * them, per row t and vocabulary entry j, each step one fp32 operation:
+ *   1. penalties for repeated tokens.  The row's history is the first
+ *      hist_len[t] tokens of its token buffer; the first prompt_len[t] of
+ *      them are the prompt, the rest its output.  With n = times j stands in
+ *      the output:  j in prompt or output:  z > 0 ? z / repetition[t]
+ *                                                 : z * repetition[t];
+ *                   n > 0:                  z - frequency[t] * n - presence[t].
+ *   2. bias: z + the value listed for j (of an id listed more than once the
+ *      last entry counts).
+ *   3. grammar: bit j % 32 of allowed[t][j / 32] = 0 makes z = -inf, whatever
+ *      it was (NaN and +inf too).
+ * The temperature, where a call takes one, applies after the rules.
+ *
+ * The struct is read on the host during the call; its arrays are device
+ * pointers.  A rule is off where its array is NULL; a NULL struct turns every
+ * rule off.
+ * tokens        int32 [buffers x ld_tokens], a token buffer per row, of which
+ *               max_len <= ld_tokens tokens are used.  An id outside [0, V)
+ *               stands for nothing (padding).
+ * row_buffer    int32 [T]: which buffer row t reads (rows of one sequence
+ *               share a buffer and see prefixes of it); an index outside
+ *               [0, buffers) gives an empty history.  NULL: row t reads
+ *               buffer t (buffers >= T).
+ * hist_len      int32 [T], required with tokens; clamped to [0, max_len].
+ * prompt_len    int32 [T]; NULL: everything is output.
+ * repetition, frequency, presence   fp32 [T]; NULL: 1, 0 and 0.  repetition
+ *               must be > 0 (not checked: device data).
+ * bias_offsets  int64 [T + 1]: row t lists entries bias_offsets[t] up to
+ *               bias_offsets[t + 1] of bias_tokens (int32) and bias_values
+ *               (fp32), each of bias_count entries (at most 2^31 - 1; offsets
+ *               are clamped to it).  Ids outside [0, V) are ignored.
+ * allowed       uint32 [T x ld_allowed], ld_allowed >= ceil(V / 32); bits past V
+ *               are ignored.
+ */
+typedef struct lp_logit_rules {
+  const int32_t* tokens;
+  int64_t buffers;
+  int64_t ld_tokens;
+  int64_t max_len;
+  const int32_t* row_buffer;
+  const int32_t* prompt_len;
+  const int32_t* hist_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int64_t* bias_offsets;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  int64_t bias_count;
+  const uint32_t* allowed;
+  int64_t ld_allowed;
+} lp_logit_rules;
+
+/*
+ * out = the logits under the rules, rounded once to `dtype`.  No temperature.
+ * logits [T x ld], out [T x ld_out] of `dtype`; out may be the logits
+ * themselves (same pointer and ld; the one call that writes an input) but may
+ * not overlap them otherwise.  Rows with mask[t] == 0 are left as they were in out, and
+ * so are columns past V.  A row whose grammar allows nothing becomes all -inf.
+ * Needs no workspace.
+ */
+lp_status lp_process_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                            const lp_logit_rules* rules, const uint8_t* mask, void* out, int64_t ld_out,
+                            void* stream);
+
+/*
+ * Log-prob of the target and entropy of softmax(rules(logits) / temperature),
+ * the distribution a sampler under these rules draws from, without writing
+ * the processed logits (which stay fp32: they are not rounded to `dtype`).
+ * logprob fp32 [T] (required); entropy, lse fp32 [T] or NULL; lse is the
+ * log-sum-exp of the tempered processed logits, saved for the backward.
+ * A target that the grammar does not allow has log-prob -inf.  A row that allows
+ * nothing has lse -inf, and NaN in logprob and entropy.
+ * workspace >= lp_processed_workspace_bytes(T, V) bytes, 256-byte aligned; scratch only.
+ */
+size_t lp_processed_workspace_bytes(int64_t T, int64_t V);
+lp_status lp_processed_logprobs_entropy(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                        const lp_logit_rules* rules, const int64_t* targets, const uint8_t* mask,
+                                        float temperature, float* logprob, float* entropy, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of sum over scored rows of grad_logprob[t] * logprob[t] +
+ * grad_entropy[t] * entropy[t] with respect to the RAW logits:
+ *   slope_j / temperature * (g (1[j = target] - p_j) - gH p_j (log p_j + H)),
+ * slope_j = the derivative of the repetition penalty (1 / repetition where
+ * z > 0, repetition elsewhere) for j in the history, 1 otherwise, and 0 where the
+ * grammar does not allow j.  The rules themselves get no gradient.
+ * lse, entropy  fp32 [T] of the forward (entropy may be NULL without grad_entropy).
+ * grad_logits   [T x ld_grad] of `dtype`, rounded once, OVERWRITTEN (unscored
+ *               rows get 0; columns past V are left); may not overlap the logits.
+ * A target outside [0, V) adds nothing but the row's softmax term.
+ * Needs no workspace.
+ */
+lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dtype, int64_t T, int64_t V,
+                                                 int64_t ld, const lp_logit_rules* rules, const int64_t* targets,
+                                                 const uint8_t* mask, float temperature, const float* lse,
+                                                 const float* entropy, const float* grad_logprob,
+                                                 const float* grad_entropy, void* grad_logits, int64_t ld_grad,
+                                                 void* stream);
+
+/*
  * Per-kernel timing (observability; not part of the method).  While enabled,
  * each library launch is bracketed by two HIP events recorded on its own
  * stream.  lp_timing_enable(1) clears earlier records and starts recording,

@@ -527,3 +527,67 @@ def lm_head_kl_backward(hidden_s, weight_s, hidden_t, weight_t, mask, grad_kl):
     dH[rows] = dZ @ Ws
     dW = dZ.T @ hs[rows]
     return dH, dW
+
+
+# ---------------------------------------------------------------------------
+# logit rules: penalties for repeated tokens, biases, a grammar mask
+# ---------------------------------------------------------------------------
+
+def apply_rules(logits, prompts=None, outputs=None, repetition=None, frequency=None, presence=None, biases=None,
+                allowed=None):
+    """(processed logits, d processed / d raw) in fp64, one row at a time.
+
+    prompts / outputs: a list of token ids per row (ids outside [0, V) are
+    skipped); biases: a list of (id, value) per row, the last entry of an id
+    counting; allowed: bool [T, V] or None.  The order is: repetition penalty
+    on every token of the prompt or the output, frequency and presence
+    penalties on tokens of the output, the bias, the grammar.
+    """
+    z = np.array(logits, dtype=np.float64)
+    T, V = z.shape
+    slope = np.ones_like(z)
+    for t in range(T):
+        times = {}
+        for j in (outputs[t] if outputs is not None else ()):
+            if 0 <= j < V:
+                times[int(j)] = times.get(int(j), 0) + 1
+        seen = set(times) | {int(j) for j in (prompts[t] if prompts is not None else ()) if 0 <= j < V}
+        rho = 1.0 if repetition is None else float(repetition[t])
+        for j in seen:
+            slope[t, j] = 1.0 / rho if z[t, j] > 0 else rho
+            z[t, j] = z[t, j] / rho if z[t, j] > 0 else z[t, j] * rho
+        for j, n in times.items():
+            if frequency is not None:
+                z[t, j] -= float(frequency[t]) * n
+            if presence is not None:
+                z[t, j] -= float(presence[t])
+        if biases is not None:
+            for j, b in {int(j): float(b) for j, b in biases[t] if 0 <= j < V}.items():
+                z[t, j] += b
+        if allowed is not None:
+            z[t, ~allowed[t]] = -np.inf
+            slope[t, ~allowed[t]] = 0.0
+    return z, slope
+
+
+def processed_backward(processed, slope, targets, mask, temperature, grad_logprob, grad_entropy):
+    """d / d raw logits of sum over scored rows of g * logprob + gH * entropy,
+    from apply_rules' results.  Columns of slope 0 (not allowed) get 0."""
+    zt = tempered(processed, temperature)
+    tau = float(temperature) if temperature_applies(temperature) else 1.0
+    T, V = zt.shape
+    out = np.zeros((T, V))
+    for t in np.nonzero(_scored(mask, T))[0]:
+        live = slope[t] != 0
+        if not live.any():
+            continue
+        logp = log_softmax(zt[t:t + 1])[0]
+        p = np.exp(logp)
+        safe = np.where(np.isneginf(logp), 0.0, logp)
+        d = -float(grad_logprob[t]) * p
+        if 0 <= targets[t] < V:
+            d[targets[t]] += float(grad_logprob[t])
+        if grad_entropy is not None:
+            d -= float(grad_entropy[t]) * p * (safe - (p * safe).sum())
+        out[t, live] = d[live] * slope[t, live] / tau
+    return out
