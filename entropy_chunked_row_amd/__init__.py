@@ -24,7 +24,8 @@ __all__ = [
     "lp_timing_read", "lp_timing_clock", "lp_logprobs_entropy_k", "lp_lm_head_logprobs_entropy_k",
     "lp_lm_head_logprobs_entropy_backward_k", "lp_prob_diff_stats", "lp_lm_head_kl_workspace_bytes",
     "lp_lm_head_kl", "lp_lm_head_kl_backward", "LogitRules", "lp_process_logits", "lp_processed_logprobs_entropy",
-    "lp_processed_logprobs_entropy_backward", "lp_processed_workspace_bytes", "LPError", "load",
+    "lp_processed_logprobs_entropy_backward", "lp_processed_workspace_bytes", "lp_embedding", "lp_embedding_backward",
+    "lp_embedding_workspace_bytes", "LPError", "load",
 ]
 
 
@@ -646,3 +647,69 @@ def lp_processed_logprobs_entropy_backward(logits, rules, targets, mask, tempera
             _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(grad_logits), ld_grad, _stream(stream))
     check("lp_processed_logprobs_entropy_backward", st)
     return grad_logits
+
+
+# ---------------------------------------------------------------------------
+# embedding
+# ---------------------------------------------------------------------------
+
+def lp_embedding(weight, tokens, scale: float = 1.0, *, out=None, stream=None):
+    """scale * weight[tokens] (weight [V, h] bf16/fp16/fp32; tokens int64 of any shape) in the weight's dtype,
+    [*tokens.shape, h]; ids outside [0, V) give zeros.  out: [N, h] with contiguous rows."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(weight)
+    ld_w = _rows(weight, "weight")
+    V, h = weight.shape
+    tokens = _vec(tokens, "tokens", torch.int64)
+    N = tokens.numel()
+    if out is not None and (out.dtype != weight.dtype or out.dim() != 2 or out.shape != (N, h)):
+        raise ValueError(f"out must be [{N}, {h}] of the weight's dtype")
+    ld_out = h if out is None else _rows(out, "out")
+    dev = weight.device
+    _on(dev, weight=weight, tokens=tokens, out=out)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((*tokens.shape, h), dtype=weight.dtype, device=dev)
+        st = lib.lp_embedding(_ptr(weight), dtype, V, h, ld_w, _ptr(tokens), N, float(scale), _ptr(out), ld_out,
+                              _stream(stream))
+    check("lp_embedding", st)
+    return out
+
+
+def lp_embedding_workspace_bytes(N: int, h: int, V: int) -> int:
+    return int(load().lp_embedding_workspace_bytes(N, h, V))
+
+
+def lp_embedding_backward(grad_out, tokens, V: int, scale: float = 1.0, *, grad_weight=None, accumulate: bool = False,
+                          workspace=None, stream=None):
+    """fp32 [V, h] gradient of lp_embedding's weight.  grad_out [N, h] with contiguous rows (or contiguous of any
+    shape [..., h]), tokens int64 with N elements.  With accumulate the sums are added to grad_weight (a tied head's)
+    and rows that no token names stay as they are."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(grad_out)
+    if grad_out.dim() != 2:
+        if grad_out.dim() < 1 or not grad_out.is_contiguous():
+            raise ValueError("grad_out must be 2-D with contiguous rows, or contiguous")
+        grad_out = grad_out.view(-1, grad_out.size(-1)) if grad_out.size(-1) else grad_out
+    ld_g = _rows(grad_out, "grad_out")
+    N, h = grad_out.shape
+    tokens = _vec(tokens, "tokens", torch.int64, N)
+    if grad_weight is None:
+        if accumulate:
+            raise ValueError("accumulate needs grad_weight")
+    else:
+        _vec(grad_weight, "grad_weight", torch.float32, V * h)
+        if grad_weight.shape != (V, h):
+            raise ValueError(f"grad_weight must be [{V}, {h}]")
+    dev = grad_out.device
+    _on(dev, grad_out=grad_out, tokens=tokens, grad_weight=grad_weight)
+    with _scope(dev, stream):
+        if grad_weight is None:
+            grad_weight = torch.empty((V, h), dtype=torch.float32, device=dev)
+        ws, ws_bytes = _workspace(lp_embedding_workspace_bytes(N, h, V), dev, workspace)
+        st = lib.lp_embedding_backward(_ptr(grad_out), dtype, N, h, ld_g, _ptr(tokens), V, float(scale),
+                                       1 if accumulate else 0, _ptr(grad_weight), _ptr(ws), ws_bytes, _stream(stream))
+    check("lp_embedding_backward", st)
+    return grad_weight

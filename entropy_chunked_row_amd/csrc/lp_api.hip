@@ -724,4 +724,95 @@ lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dt
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// embedding
+// ---------------------------------------------------------------------------
+
+static lp_status check_embedding(const char* fn, lp_dtype dtype, int64_t V, int64_t h, int64_t N, int64_t ld_a,
+                                 int64_t ld_b, float scale) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", fn, static_cast<int>(dtype));
+  if (N < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: N < 0", fn);
+  if (V <= 0 || V > kMaxV || h <= 0 || h > kMaxV)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: h and V must be in 1..2^30", fn);
+  if (ld_a < h || ld_b < h) return fail(LP_ERR_INVALID_ARGUMENT, "%s: leading dimensions must be >= h", fn);
+  if (!isfinite(scale)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: scale not finite", fn);
+  constexpr int64_t kMost = int64_t(1) << 60;
+  if (ld_a > kMost / (N > V ? N : V) || ld_b > kMost / (N > V ? N : V))
+    return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 elements", fn);
+  return LP_OK;
+}
+
+lp_status lp_embedding(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w, const int64_t* tokens,
+                       int64_t N, float scale, void* out, int64_t ld_out, void* stream) {
+  const char* fn = "lp_embedding";
+  lp_status st = check_embedding(fn, dtype, V, h, N, ld_w, ld_out, scale);
+  if (st != LP_OK) return st;
+  if (N == 0) return ok();
+  if (!weight || !tokens || !out) return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight, tokens and out are required", fn);
+  if (!aligned(weight, dtype_bytes(dtype)) || !aligned(out, dtype_bytes(dtype)) || !aligned(tokens, 8))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  lp::EmbedArgs a;
+  a.weight = weight;
+  a.ld_w = ld_w;
+  a.V = static_cast<int>(V);
+  a.h = static_cast<int>(h);
+  a.tokens = tokens;
+  a.N = N;
+  a.scale = scale;
+  a.out = out;
+  a.ld_out = ld_out;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_embedding(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+size_t lp_embedding_workspace_bytes(int64_t N, int64_t h, int64_t V) {
+  lp::EmbedWorkspace w;
+  return lp::embedding_workspace_layout(N, h, V, &w) ? w.total : 0;
+}
+
+lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N, int64_t h, int64_t ld_g,
+                                const int64_t* tokens, int64_t V, float scale, int accumulate, float* grad_weight,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "lp_embedding_backward";
+  lp_status st = check_embedding(fn, dtype, V, h, N, ld_g, ld_g, scale);
+  if (st != LP_OK) return st;
+  lp::EmbedWorkspace w;
+  if (!lp::embedding_workspace_layout(N, h, V, &w)) return fail(LP_ERR_UNSUPPORTED, "%s: more than 2^31-1 positions", fn);
+  if (!grad_weight || (N > 0 && (!grad_out || !tokens)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: grad_out, tokens and grad_weight are required", fn);
+  if (!aligned(grad_out, dtype_bytes(dtype)) || !aligned(grad_weight, 4) || !aligned(tokens, 8))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (N == 0) {
+    // no positions: the gradient is still defined
+    if (accumulate) return ok();
+    clear_pending_hip_error();
+    hipError_t e = lp::launch_zero_f32(grad_weight, V * h, s);
+    if (e != hipSuccess) return hip_fail(e, fn);
+    return ok();
+  }
+  if (!workspace || workspace_bytes < w.total)
+    return fail(LP_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %zu bytes, got %zu", fn, w.total,
+                workspace ? workspace_bytes : size_t(0));
+  if (!aligned(workspace, 256)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
+  lp::EmbedGradArgs a;
+  memset(&a, 0, sizeof(a));
+  a.grad = grad_out;
+  a.ld_g = ld_g;
+  a.N = N;
+  a.h = static_cast<int>(h);
+  a.V = static_cast<int>(V);
+  a.tokens = tokens;
+  a.scale = scale;
+  a.accumulate = accumulate != 0;
+  a.grad_weight = grad_weight;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_embedding_backward(static_cast<int>(dtype), a, static_cast<char*>(workspace), w, s);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
 }  // extern "C"

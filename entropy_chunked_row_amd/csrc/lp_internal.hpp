@@ -131,6 +131,52 @@ hipError_t launch_processed_score(int dtype, const RulesArgs& a, char* ws, hipSt
 hipError_t launch_processed_grad(int dtype, const RulesArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// embedding
+// ---------------------------------------------------------------------------
+
+struct EmbedArgs {
+  const void* weight;
+  int64_t ld_w;
+  int V, h;
+  const int64_t* tokens;  // [N]
+  int64_t N;
+  float scale;
+  void* out;
+  int64_t ld_out;
+};
+
+struct EmbedGradArgs {
+  const void* grad;
+  int64_t ld_g;
+  int64_t N;
+  int h, V;
+  const int64_t* tokens;
+  float scale;
+  bool accumulate;
+  float* grad_weight;  // [V x h]
+  // set by the launcher
+  uint32_t* keys[2];
+  uint32_t* pos[2];
+  uint32_t* counts;  // [256 x tiles]
+  uint32_t* first;   // [V]
+  float* partial;    // [N / 64 x h]
+  const uint32_t* sorted_keys;
+  const uint32_t* sorted_pos;
+  int tiles, key_bits, col_blocks;
+  int64_t row0;
+};
+
+struct EmbedWorkspace {
+  size_t keys_off[2], pos_off[2], counts_off, first_off, partial_off, total;
+};
+
+// False for sizes the gradient does not take (N past 2^31 - 1 among them).
+bool embedding_workspace_layout(int64_t N, int64_t h, int64_t V, EmbedWorkspace* w);
+hipError_t launch_embedding(int dtype, const EmbedArgs& a, hipStream_t s);
+hipError_t launch_embedding_backward(int dtype, const EmbedGradArgs& a, char* ws, const EmbedWorkspace& w,
+                                     hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // fused LM head
 // ---------------------------------------------------------------------------
 

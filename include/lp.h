@@ -435,6 +435,33 @@ lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dt
                                                  void* stream);
 
 /*
+ * Embedding lookup, out[i] = scale * weight[tokens[i]], the product in fp32
+ * and rounded once to `dtype`.
+ * weight [V x ld_w], out [N x ld_out] of `dtype`, h columns used; tokens int64
+ * [N].  An id outside [0, V) (padding) gives a row of zeros.  scale must be
+ * finite.  Columns of out past h are left.  N == 0 returns LP_OK without launching.
+ */
+lp_status lp_embedding(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w, const int64_t* tokens,
+                       int64_t N, float scale, void* out, int64_t ld_out, void* stream);
+
+/*
+ * Weight gradient of the lookup: grad_weight[v] (fp32 [V x h], contiguous)
+ *   = scale * sum of grad_out[i] over the i with tokens[i] = v.
+ * accumulate == 0: every row is OVERWRITTEN (0 where no token names it).
+ * accumulate != 0: the sums are added to what grad_weight holds and rows that
+ *   no token names are neither read nor written.  With a tied head this adds the embedding's
+ *   share to the grad_weight of lp_lm_head_logprobs_entropy_backward.
+ * grad_out [N x ld_g] of `dtype`; rows of ids outside [0, V) are ignored.
+ * Sums are fp32 in a fixed order (no float atomics): the same bits on every call.
+ * workspace >= lp_embedding_workspace_bytes(N, h, V) bytes (0: sizes not
+ *   supported; N is at most 2^31 - 1), 256-byte aligned; scratch only.
+ */
+size_t lp_embedding_workspace_bytes(int64_t N, int64_t h, int64_t V);
+lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N, int64_t h, int64_t ld_g,
+                                const int64_t* tokens, int64_t V, float scale, int accumulate, float* grad_weight,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Per-kernel timing (observability; not part of the method).  While enabled,
  * each library launch is bracketed by two HIP events recorded on its own
  * stream.  lp_timing_enable(1) clears earlier records and starts recording,

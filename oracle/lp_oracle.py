@@ -591,3 +591,28 @@ def processed_backward(processed, slope, targets, mask, temperature, grad_logpro
             d -= float(grad_entropy[t]) * p * (safe - (p * safe).sum())
         out[t, live] = d[live] * slope[t, live] / tau
     return out
+
+
+# ---------------------------------------------------------------------------
+# embedding lookup and its weight gradient
+# ---------------------------------------------------------------------------
+
+def embedding(weight, tokens, scale):
+    """scale * weight[token] per position, zeros for ids outside [0, V)."""
+    W = np.asarray(weight, dtype=np.float64)
+    tok = np.asarray(tokens).reshape(-1)
+    out = np.zeros((tok.size, W.shape[1]))
+    for i, v in enumerate(tok):
+        if 0 <= v < W.shape[0]:
+            out[i] = float(scale) * W[v]
+    return out
+
+
+def embedding_backward(grad_out, tokens, V, scale, base=None):
+    """base + scale * sum of the gradients of each token's positions, [V, h]."""
+    g = np.asarray(grad_out, dtype=np.float64)
+    out = np.zeros((V, g.shape[1])) if base is None else np.array(base, dtype=np.float64)
+    for i, v in enumerate(np.asarray(tokens).reshape(-1)):
+        if 0 <= v < V:
+            out[v] += float(scale) * g[i]
+    return out
