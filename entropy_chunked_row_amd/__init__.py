@@ -25,7 +25,7 @@ __all__ = [
     "lp_lm_head_logprobs_entropy_backward_k", "lp_prob_diff_stats", "lp_lm_head_kl_workspace_bytes",
     "lp_lm_head_kl", "lp_lm_head_kl_backward", "LogitRules", "lp_process_logits", "lp_processed_logprobs_entropy",
     "lp_processed_logprobs_entropy_backward", "lp_processed_workspace_bytes", "lp_embedding", "lp_embedding_backward",
-    "lp_embedding_workspace_bytes", "LPError", "load",
+    "lp_embedding_workspace_bytes", "lp_lm_head_w4_quantize", "lp_lm_head_w4_logits", "LPError", "load",
 ]
 
 
@@ -713,3 +713,69 @@ def lp_embedding_backward(grad_out, tokens, V: int, scale: float = 1.0, *, grad_
                                        1 if accumulate else 0, _ptr(grad_weight), _ptr(ws), ws_bytes, _stream(stream))
     check("lp_embedding_backward", st)
     return grad_weight
+
+
+# ---------------------------------------------------------------------------
+# 4-bit head
+# ---------------------------------------------------------------------------
+
+def lp_lm_head_w4_quantize(weight, group: int = 128, *, packed=None, scales=None, stream=None) -> Tuple:
+    """(packed uint8 [V, h / 2], scales bf16 [V, ceil(h / group)]) of a dense head weight [V, h] (bf16/fp16/fp32)."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(weight)
+    ld_w = _rows(weight, "weight")
+    V, h = weight.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    groups = (h + group - 1) // group
+    for name, t, dt, n in (("packed", packed, torch.uint8, h // 2), ("scales", scales, torch.bfloat16, groups)):
+        if t is not None and (t.dtype != dt or t.dim() != 2 or t.shape != (V, n)):
+            raise ValueError(f"{name} must be [{V}, {n}] {dt}")
+    dev = weight.device
+    _on(dev, weight=weight, packed=packed, scales=scales)
+    with _scope(dev, stream):
+        if packed is None:
+            packed = torch.empty((V, h // 2), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((V, groups), dtype=torch.bfloat16, device=dev)
+        st = lib.lp_lm_head_w4_quantize(_ptr(weight), dtype, V, h, ld_w, group, _ptr(packed), _rows(packed, "packed"),
+                                        _ptr(scales), _rows(scales, "scales"), _stream(stream))
+    check("lp_lm_head_w4_quantize", st)
+    return packed, scales
+
+
+def lp_lm_head_w4_logits(hidden, packed, scales, group: int = 128, *, out_dtype=None, out=None, stream=None):
+    """Logits [T, V] of hidden [T, h] (bf16/fp16) through a head of lp_lm_head_w4_quantize; out_dtype defaults to
+    hidden's."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(hidden)
+    ld_h = _rows(hidden, "hidden")
+    T, h = hidden.shape
+    if packed.dtype != torch.uint8:
+        raise TypeError(f"packed must be uint8, got {packed.dtype}")
+    if scales.dtype != torch.bfloat16:
+        raise TypeError(f"scales must be bfloat16, got {scales.dtype}")
+    ld_p, ld_s = _rows(packed, "packed"), _rows(scales, "scales")
+    V = packed.size(0)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if packed.size(1) * 2 != h or scales.shape != (V, (h + group - 1) // group):
+        raise ValueError(f"hidden [{T}, {h}], packed {list(packed.shape)} and scales {list(scales.shape)} disagree "
+                         f"(group {group})")
+    if out is not None:
+        if out.dim() != 2 or out.shape != (T, V) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be [{T}, {V}] of out_dtype")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = hidden.dtype
+    dev = hidden.device
+    _on(dev, hidden=hidden, packed=packed, scales=scales, out=out)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((T, V), dtype=out_dtype, device=dev)
+        st = lib.lp_lm_head_w4_logits(_ptr(hidden), dtype, T, h, ld_h, _ptr(packed), ld_p, _ptr(scales), ld_s, V, group,
+                                      _ptr(out), _dtype_code(out), _rows(out, "out"), _stream(stream))
+    check("lp_lm_head_w4_logits", st)
+    return out

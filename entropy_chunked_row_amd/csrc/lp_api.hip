@@ -815,4 +815,95 @@ lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N,
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// 4-bit head
+// ---------------------------------------------------------------------------
+
+static lp_status check_w4(const char* fn, int64_t V, int64_t h, int64_t group, const void* packed, int64_t ld_packed,
+                          const void* scales, int64_t ld_scales) {
+  if (V <= 0 || V > kMaxV || h <= 0 || h > kMaxV)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: h and V must be in 1..2^30", fn);
+  if (h % 32) return fail(LP_ERR_UNSUPPORTED, "%s: h must be a multiple of 32", fn);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(LP_ERR_UNSUPPORTED, "%s: group must be 32, 64 or 128", fn);
+  if (ld_packed < h / 2 || ld_scales < (h + group - 1) / group)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_packed must be >= h / 2 and ld_scales >= ceil(h / group)", fn);
+  if (ld_packed > (int64_t(1) << 60) / V || ld_scales > (int64_t(1) << 60) / V)
+    return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
+  if (ld_packed % 16) return fail(LP_ERR_UNSUPPORTED, "%s: ld_packed must be a multiple of 16", fn);
+  if (!packed || !scales) return fail(LP_ERR_INVALID_ARGUMENT, "%s: packed and scales are required", fn);
+  if (!aligned(packed, 16)) return fail(LP_ERR_UNSUPPORTED, "%s: packed must be 16-byte aligned", fn);
+  if (!aligned(scales, 2)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned scales", fn);
+  return LP_OK;
+}
+
+lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w,
+                                 int64_t group, void* packed, int64_t ld_packed, void* scales, int64_t ld_scales,
+                                 void* stream) {
+  const char* fn = "lp_lm_head_w4_quantize";
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", fn, static_cast<int>(dtype));
+  lp_status st = check_w4(fn, V, h, group, packed, ld_packed, scales, ld_scales);
+  if (st != LP_OK) return st;
+  if (ld_w < h) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_w < h", fn);
+  if (ld_w > (int64_t(1) << 59) / V) return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
+  if (!weight || !aligned(weight, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight is required and must be aligned", fn);
+  lp::W4QuantArgs a;
+  a.weight = weight;
+  a.ld_w = ld_w;
+  a.V = static_cast<int>(V);
+  a.h = static_cast<int>(h);
+  a.group = static_cast<int>(group);
+  a.groups = static_cast<int>((h + group - 1) / group);
+  a.packed = packed;
+  a.ld_p = ld_packed;
+  a.scales = static_cast<uint16_t*>(scales);
+  a.ld_s = ld_scales;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_w4_quantize(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, int64_t h, int64_t ld_h,
+                               const void* packed, int64_t ld_packed, const void* scales, int64_t ld_scales, int64_t V,
+                               int64_t group, void* out, lp_dtype out_dtype, int64_t ld_out, void* stream) {
+  const char* fn = "lp_lm_head_w4_logits";
+  if (dtype == LP_FP32) return fail(LP_ERR_UNSUPPORTED, "%s: hidden must be bf16 or fp16", fn);
+  if ((dtype != LP_BF16 && dtype != LP_FP16) ||
+      (out_dtype != LP_BF16 && out_dtype != LP_FP16 && out_dtype != LP_FP32))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d or %d", fn, static_cast<int>(dtype),
+                static_cast<int>(out_dtype));
+  if (T < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: T < 0", fn);
+  lp_status st = check_w4(fn, V, h, group, packed, ld_packed, scales, ld_scales);
+  if (st != LP_OK) return st;
+  if (ld_h < h || ld_out < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_h must be >= h and ld_out >= V", fn);
+  if (ld_h % 8) return fail(LP_ERR_UNSUPPORTED, "%s: ld_h must be a multiple of 8", fn);
+  if (T == 0) return ok();
+  if (T > (int64_t(1) << 40) || ld_h > (int64_t(1) << 59) / T || ld_out > (int64_t(1) << 59) / T)
+    return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
+  if (!hidden || !out) return fail(LP_ERR_INVALID_ARGUMENT, "%s: hidden and out are required", fn);
+  if (!aligned(hidden, 16)) return fail(LP_ERR_UNSUPPORTED, "%s: hidden must be 16-byte aligned", fn);
+  if (!aligned(out, dtype_bytes(out_dtype))) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned out", fn);
+  lp::W4Args a;
+  a.hidden = static_cast<const uint16_t*>(hidden);
+  a.ld_h = ld_h;
+  a.T = T;
+  a.h = static_cast<int>(h);
+  a.V = static_cast<int>(V);
+  a.group = static_cast<int>(group);
+  a.packed = packed;
+  a.ld_p = ld_packed;
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.ld_s = ld_scales;
+  a.out = out;
+  a.out_dtype = static_cast<int>(out_dtype);
+  a.ld_out = ld_out;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_w4_logits(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
 }  // extern "C"

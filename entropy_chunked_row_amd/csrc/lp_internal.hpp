@@ -177,6 +177,37 @@ hipError_t launch_embedding_backward(int dtype, const EmbedGradArgs& a, char* ws
                                      hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// 4-bit head
+// ---------------------------------------------------------------------------
+
+struct W4Args {
+  const uint16_t* hidden;  // bf16 or fp16 bits [T x ld_h]
+  int64_t ld_h;
+  int64_t T;
+  int h, V, group;
+  const void* packed;  // [V x ld_p bytes]
+  int64_t ld_p;
+  const uint16_t* scales;  // bf16 bits [V x ld_s]
+  int64_t ld_s;
+  void* out;
+  int out_dtype;
+  int64_t ld_out;
+};
+
+struct W4QuantArgs {
+  const void* weight;
+  int64_t ld_w;
+  int V, h, group, groups;
+  void* packed;
+  int64_t ld_p;
+  uint16_t* scales;
+  int64_t ld_s;
+};
+
+hipError_t launch_w4_logits(int dtype, const W4Args& a, hipStream_t s);
+hipError_t launch_w4_quantize(int dtype, const W4QuantArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // fused LM head
 // ---------------------------------------------------------------------------
 

@@ -1,0 +1,304 @@
+// Logits of few rows through an output head held in 4 bits with group scales:
+//   out[t][v] = sum over groups g of s[v][g] * sum over k in g of x[t][k] (q[v][k] - 8)
+// with q in 0..15, two to a byte (even column in the low half), s bf16, x
+// bf16 or fp16 and every sum in fp32.
+//
+// The head's bytes are the floor: h / 2 + 2 h / group bytes a vocabulary row,
+// read once for up to 64 rows of x.  Matrix cores do the products also for a
+// single row of x, because the vector unit is what the unpacking needs:
+//  * A nibble n becomes the 16-bit float 16 + n by one shift and one
+//    and-or on two nibbles at a time (its bits go into the top of the mantissa of
+//    16.0), exact in bf16 and fp16.
+//  * sum x (q - 8) = sum x (16 + q) - 24 sum x.  The second sum does not depend on
+//    v: one MFMA with a constant operand gives it to every row tile as
+//    the start value of its accumulator.
+//  * Nibbles s and s + 4 of a 32-bit word share a register, so x's columns take
+//    the order 0 4 1 5 2 6 3 7 within each 8 (a permutation of the sum).
+// A lane's 16 / 8 / 4 bytes (groups of 128 / 64 / 32) are cut so that each
+// MFMA stays inside one group, whose sum is then scaled once in fp32.
+#include "lp_device.hpp"
+#include "lp_internal.hpp"
+
+namespace lp {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+struct XBf16 {
+  static constexpr uint32_t kBase = 0x41804180u, kMask = 0x00780078u, kNeg24 = 0xc1c0c1c0u;
+  static constexpr int kBit = 3;  // mantissa position of a nibble's bit 0
+  __device__ static __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+  }
+};
+
+struct XFp16 {
+  static constexpr uint32_t kBase = 0x4c004c00u, kMask = 0x03c003c0u, kNeg24 = 0xce00ce00u;
+  static constexpr int kBit = 6;
+  __device__ static __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+};
+
+// Eight nibbles as 16 + n, in the order 0 4 1 5 2 6 3 7.
+template <class X>
+__device__ __forceinline__ u32x4 widen_nibbles(uint32_t w) {
+  u32x4 r;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int sh = X::kBit - 4 * s;
+    const uint32_t v = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
+    r[s] = (v & X::kMask) | X::kBase;
+  }
+  return r;
+}
+
+// Eight 16-bit values in the same order.
+__device__ __forceinline__ u32x4 order_x(u32x4 d) {
+  return u32x4{__builtin_amdgcn_perm(d.z, d.x, 0x05040100u), __builtin_amdgcn_perm(d.z, d.x, 0x07060302u),
+               __builtin_amdgcn_perm(d.w, d.y, 0x05040100u), __builtin_amdgcn_perm(d.w, d.y, 0x07060302u)};
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
+  return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+}
+
+__device__ __forceinline__ void store_logit(void* out, int dtype, int64_t i, float x) {
+  switch (dtype) {
+    case 0: Bf16::store1(static_cast<char*>(out), i, x); break;
+    case 1: Fp16::store1(static_cast<char*>(out), i, x); break;
+    default: Fp32::store1(static_cast<char*>(out), i, x); break;
+  }
+}
+
+// One workgroup: 16 RT vocabulary rows x 16 NT rows of x.  Its four waves take
+// every fourth chunk of 128 columns and add their sums through LDS at the end.
+template <class X, int G, int NT, int RT>
+__global__ void __launch_bounds__(256) k_w4_logits(W4Args a) {
+  constexpr int kGroups = 128 / G, kSteps = G / 32;  // per chunk, per group
+  __shared__ float sm[4][RT * 4][64];
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r16 = lane & 15, q = lane >> 4;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64;
+  const int h = a.h, chunks = (h + 127) / 128;
+
+  // rows past the end repeat the last one: their results are not stored
+  const char* wrow[RT];
+  const uint16_t* srow[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    int64_t v = v0 + r * 16 + r16;
+    v = v < a.V ? v : a.V - 1;
+    wrow[r] = static_cast<const char*>(a.packed) + v * a.ld_p;
+    srow[r] = a.scales + v * a.ld_s;
+  }
+  const uint16_t* xrow[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    int64_t row = t0 + t * 16 + r16;
+    row = row < a.T ? row : a.T - 1;
+    xrow[t] = a.hidden + row * a.ld_h;
+  }
+
+  f32x4 tot[NT][RT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) tot[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const u32x4 neg24{X::kNeg24, X::kNeg24, X::kNeg24, X::kNeg24};
+
+  struct Words {
+    uint32_t w[RT][kGroups][kSteps];
+    float s[RT][kGroups];
+  };
+  auto load = [&](int c, Words& d) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      // a lane's G / 4 columns lie inside the head or past its end as a whole
+      int k = c * 128 + g * G + q * (G / 4);
+      k = k < h ? k : 0;
+      int sg = c * kGroups + g;
+      sg = sg * G < h ? sg : 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(wrow[r] + k / 2);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) d.w[r][g][i] = p[i];
+        d.s[r][g] = bf16_at(srow[r], sg);
+      }
+    }
+  };
+
+  Words cur;
+  if (w < chunks) load(w, cur);
+  for (int c = w; c < chunks; c += 4) {
+    Words nxt;
+    if (c + 4 < chunks) load(c + 4, nxt);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      u32x4 x[NT][kSteps];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int k = c * 128 + g * G + q * (G / 4) + i * 8;
+          u32x4 d{0, 0, 0, 0};
+          if (k < h) d = *reinterpret_cast<const u32x4*>(xrow[t] + k);
+          x[t][i] = order_x(d);
+        }
+      f32x4 shift[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        shift[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) shift[t] = X::mfma(x[t][i], neg24, shift[t]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        u32x4 b[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) b[i] = widen_nibbles<X>(cur.w[r][g][i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          f32x4 acc = shift[t];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) acc = X::mfma(x[t][i], b[i], acc);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tot[t][r][j] = fmaf(cur.s[r][g], acc[j], tot[t][r][j]);
+        }
+      }
+    }
+    cur = nxt;
+  }
+
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sm[w][r * 4 + j][lane] = tot[t][r][j];
+    __syncthreads();
+    for (int e = w; e < RT * 4; e += 4) {
+      const float sum = (sm[0][e][lane] + sm[1][e][lane]) + (sm[2][e][lane] + sm[3][e][lane]);
+      const int64_t row = t0 + t * 16 + q * 4 + (e & 3);
+      const int64_t v = v0 + (e >> 2) * 16 + r16;
+      if (row < a.T && v < a.V) store_logit(a.out, a.out_dtype, row * a.ld_out + v, sum);
+    }
+  }
+}
+
+template <class X, int G>
+hipError_t launch_logits(const W4Args& a, hipStream_t s) {
+  // grid.y is at most 65535 blocks of 64 rows
+  constexpr int64_t kRows = int64_t(65535) * 64;
+  for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
+    W4Args b = a;
+    b.T = a.T - r0 < kRows ? a.T - r0 : kRows;
+    b.hidden = a.hidden + r0 * a.ld_h;
+    b.out = static_cast<char*>(a.out) + r0 * a.ld_out * (a.out_dtype == 2 ? 4 : 2);
+    const int nt = b.T >= 64 ? 4 : static_cast<int>((b.T + 15) / 16);
+    const unsigned gy = static_cast<unsigned>((b.T + 63) / 64);
+    TimedLaunch tl("k_w4_logits", s);
+    auto grid = [&](int rt) { return dim3(static_cast<unsigned>((int64_t(a.V) + 16 * rt - 1) / (16 * rt)), gy); };
+    switch (nt) {
+      case 1: hipLaunchKernelGGL((k_w4_logits<X, G, 1, 2>), grid(2), dim3(256), 0, s, b); break;
+      case 2: hipLaunchKernelGGL((k_w4_logits<X, G, 2, 2>), grid(2), dim3(256), 0, s, b); break;
+      case 3: hipLaunchKernelGGL((k_w4_logits<X, G, 3, 4>), grid(4), dim3(256), 0, s, b); break;
+      default: hipLaunchKernelGGL((k_w4_logits<X, G, 4, 4>), grid(4), dim3(256), 0, s, b); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <class X>
+hipError_t launch_logits_g(const W4Args& a, hipStream_t s) {
+  switch (a.group) {
+    case 32: return launch_logits<X, 32>(a, s);
+    case 64: return launch_logits<X, 64>(a, s);
+    default: return launch_logits<X, 128>(a, s);
+  }
+}
+
+// Eight columns a lane; the group / 8 lanes of a group agree on its scale.
+template <class Tr>
+__global__ void __launch_bounds__(256) k_w4_quantize(W4QuantArgs a) {
+  const int group = a.group, words = a.groups * (group / 8);  // per row, whole groups
+  const int64_t n = static_cast<int64_t>(a.V) * words;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  // n and stride are multiples of a group's lanes, which so stay together
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += stride) {
+    const int64_t v = i / words;
+    const int wd = static_cast<int>(i - v * words);
+    const bool in = wd * 8 < a.h;
+    const char* row = static_cast<const char*>(a.weight) + v * a.ld_w * Tr::kBytes;
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+    if (in) {
+      const char* p = row + static_cast<int64_t>(wd) * 8 * Tr::kBytes;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; k += Tr::kPerVec) Tr::unpack(*reinterpret_cast<const u32x4*>(p + k * Tr::kBytes), x + k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = Tr::load1(p, k);
+      }
+    }
+    // largest magnitude as bits: a NaN is larger than anything and stays
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = __float_as_uint(x[k]) & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
+    for (int off = 1; off < group / 8; off <<= 1) {
+      const uint32_t o = __shfl_xor(m, off, 64);
+      m = o > m ? o : m;
+    }
+    // a group with an infinity gets a NaN for its scale too
+    const uint32_t sb = m >= 0x7f800000u ? 0x7fc0u : pack_bf16x2(__fdiv_rn(__uint_as_float(m), 7.f), 0.f) & 0xffffu;
+    const float s = __uint_as_float(sb << 16);
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float y = s == 0.f ? 0.f : rintf(__fdiv_rn(x[k], s));
+      y = fminf(fmaxf(y, -8.f), 7.f);
+      word |= static_cast<uint32_t>(static_cast<int>(y) + 8) << (4 * k);
+    }
+    if (in) {
+      reinterpret_cast<uint32_t*>(static_cast<char*>(a.packed) + v * a.ld_p)[wd] = word;
+      if (wd % (group / 8) == 0) a.scales[v * a.ld_s + wd / (group / 8)] = static_cast<uint16_t>(sb);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_w4_logits(int dtype, const W4Args& a, hipStream_t s) {
+  return dtype == 0 ? launch_logits_g<XBf16>(a, s) : launch_logits_g<XFp16>(a, s);
+}
+
+hipError_t launch_w4_quantize(int dtype, const W4QuantArgs& a, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(a.V) * a.groups * (a.group / 8);
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 16384) blocks = 16384;
+  const dim3 g(static_cast<unsigned>(blocks)), b(256);
+  TimedLaunch tl("k_w4_quantize", s);
+  switch (dtype) {
+    case 0: hipLaunchKernelGGL(k_w4_quantize<Bf16>, g, b, 0, s, a); break;
+    case 1: hipLaunchKernelGGL(k_w4_quantize<Fp16>, g, b, 0, s, a); break;
+    default: hipLaunchKernelGGL(k_w4_quantize<Fp32>, g, b, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace lp

@@ -435,6 +435,36 @@ lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dt
                                                  void* stream);
 
 /*
+ * An output head in 4 bits with group scales, for the logits of few rows (a
+ * decode step): weight[v][k] = scales[v][k / group] * (q[v][k] - 8), q in 0..15.
+ * packed  uint8 [V x ld_packed], ld_packed >= h / 2 bytes: byte j of a row
+ *         holds column 2 j in its low and 2 j + 1 in its high half.
+ * scales  bf16 [V x ld_scales], ld_scales >= ceil(h / group).
+ * group   32, 64 or 128.
+ * Restrictions (LP_ERR_UNSUPPORTED): h % 32 != 0, ld_packed % 16 != 0, packed not 16-byte
+ *   aligned, another group.
+ *
+ * lp_lm_head_w4_quantize lays a head out: per group, scale = amax / 7 rounded to
+ * bf16, q = clamp(round-half-even(w / scale), -8, 7) + 8 (8 where the scale
+ * is 0).  weight [V x ld_w] of `dtype`.  A group that holds a NaN or an
+ * infinity makes its row's logits NaN.
+ */
+lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w,
+                                 int64_t group, void* packed, int64_t ld_packed, void* scales, int64_t ld_scales,
+                                 void* stream);
+
+/*
+ * out[t][v] = hidden[t] . weight[v] of such a head; products and sums fp32,
+ * rounded once to out_dtype.  hidden bf16 or fp16 [T x ld_h] (further LP_ERR_UNSUPPORTED:
+ * fp32, ld_h % 8 != 0, not 16-byte aligned), out [T x ld_out] of out_dtype, columns past V left.
+ * Up to 64 rows read the head once; more rows read it again for every 64.
+ * Needs no workspace.  The result of a row does not depend on the other rows.
+ */
+lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, int64_t h, int64_t ld_h,
+                               const void* packed, int64_t ld_packed, const void* scales, int64_t ld_scales, int64_t V,
+                               int64_t group, void* out, lp_dtype out_dtype, int64_t ld_out, void* stream);
+
+/*
  * Embedding lookup, out[i] = scale * weight[tokens[i]], the product in fp32
  * and rounded once to `dtype`.
  * weight [V x ld_w], out [N x ld_out] of `dtype`, h columns used; tokens int64

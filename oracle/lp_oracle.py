@@ -616,3 +616,35 @@ def embedding_backward(grad_out, tokens, V, scale, base=None):
         if 0 <= v < V:
             out[v] += float(scale) * g[i]
     return out
+
+
+# ---------------------------------------------------------------------------
+# output head in 4 bits with group scales
+# ---------------------------------------------------------------------------
+
+def w4_quantize(weight32, group):
+    """(q in 0..15 [V, h], scales fp32 holding bf16 values [V, groups]) of an
+    fp32 weight: scale = amax / 7 in fp32 rounded to bf16, q = the nearest
+    whole number of w / scale (fp32, ties to even) clamped to -8..7, plus 8."""
+    w = np.asarray(weight32, dtype=np.float32)
+    V, h = w.shape
+    groups = -(-h // group)
+    q = np.full((V, h), 8, dtype=np.int64)
+    scales = np.zeros((V, groups), dtype=np.float32)
+    for g in range(groups):
+        part = w[:, g * group:(g + 1) * group]
+        s = (np.abs(part).max(1) / np.float32(7)).astype(np.float32)
+        b = s.view(np.uint32).astype(np.uint64)
+        b = (b + np.uint64(0x7fff) + ((b >> np.uint64(16)) & np.uint64(1))) >> np.uint64(16)
+        s = (b.astype(np.uint32) << np.uint32(16)).view(np.float32)
+        scales[:, g] = s
+        live = s > 0
+        r = np.rint(part[live] / s[live, None])
+        q[live, g * group:(g + 1) * group] = np.clip(r, -8, 7).astype(np.int64) + 8
+    return q, scales
+
+
+def w4_logits(hidden, q, scales, group):
+    """hidden @ (scales * (q - 8))^T in fp64."""
+    s = np.repeat(np.asarray(scales, dtype=np.float64), group, axis=1)[:, :np.asarray(q).shape[1]]
+    return np.asarray(hidden, dtype=np.float64) @ ((np.asarray(q) - 8) * s).T
