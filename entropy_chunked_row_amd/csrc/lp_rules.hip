@@ -10,14 +10,21 @@
 //   z4 = z3 + b_j            z5 = allowed_j ? z4 : -inf
 // each step one fp32 operation, rounded on its own (no contraction).
 //
-// The row is cut into slices of columns, one workgroup each.  A workgroup
-// counts the history tokens that fall into its slice in an LDS word per
-// column (bit 31: stands in the prompt; below: times in the output), then
-// streams the slice.  Counts are integers, so the order of the LDS atomics
-// does not change any result.  Nothing of size V is kept between calls and no
-// dense count matrix passes through memory: a dense one would cost 4 bytes a
-// column where the logits themselves cost 2.  Every slice rereads the row's
-// history (4 bytes a token, from L2).
+// Few columns of a row are touched by a history or a bias, and all others
+// pass unchanged, so the two are kept apart.  A workgroup owns a slice of a
+// row's columns (the whole row where there are rows enough) and
+//   1. sets a bit per touched column in an LDS bitmap, and counts the bits
+//      before each group of 128 columns: a touched column's rank in the slice
+//      is that count plus a popcount;
+//   2. counts by rank: a word per touched column (bit 31: stands in the prompt; below: times in
+//      the output), its column, and the last bias entry that names it;
+//   3. streams the slice, 16 bytes a lane, where the bitmap and the grammar's
+//      bits decide what a column gives, without branches;
+//   4. deals with the touched columns one by one, kRanks at a time.
+// Counts are integers and the bias entry is a maximum, so the order of the
+// LDS atomics does not change any result.  Nothing of size V is kept between
+// calls and no dense count matrix passes through memory (it would cost 4 bytes
+// a column where the logits cost 2); a history is read twice per slice.
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
@@ -26,15 +33,18 @@ namespace lp {
 namespace {
 
 constexpr uint32_t kPromptBit = 0x80000000u;
-constexpr int kLdsPad = 16;
+constexpr int kRanks = 2048;     // touched columns dealt with at a time
+constexpr int kMinSlice = 1024;
+constexpr int kMaxSlice = 163840;  // columns: 20 KB of bits and 5 KB of counts before them
+constexpr float kNoWeight = -1024.f;  // exponents below weigh exactly 0 in fp32
 
 enum RulesOp { kProcess = 0, kScore = 1, kGrad = 2 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Like stat_push with guards for -inf (weight 0, adds nothing to `a`); a NaN
-// stays a NaN in s and a.
-template <int N>
+// Like stat_push for values that may be -inf: those weigh 0 and add nothing to
+// `a`.  A NaN stays a NaN in s and a.
+template <int N, int CH>
 __device__ __forceinline__ void stat_push_masked(Stat& st, const float* x, float c) {
   float vm = x[0];
 #pragma unroll
@@ -42,16 +52,19 @@ __device__ __forceinline__ void stat_push_masked(Stat& st, const float* x, float
   const float vmc = vm * c;
   if (vmc > st.mc) stat_rebase(st, vmc);
   const float nmc = -st.mc;
-  float ps = 0.f, pa = 0.f;
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float t = fmaf(x[k], c, nmc);
-    const float e = fast_exp2(t);
-    ps += e;
-    pa = fmaf(e, t == neg_inf() ? 0.f : t, pa);
+  for (int g = 0; g < N; g += CH) {
+    float ps = 0.f, pa = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const float t = fmaf(x[g + k], c, nmc);
+      const float e = fast_exp2(t);
+      ps += e;
+      pa = fmaf(e, fmaxf(t, kNoWeight), pa);
+    }
+    st.s += ps;
+    st.a += pa;
   }
-  st.s += ps;
-  st.a += pa;
 }
 
 // Merge in which an empty side (s == 0) adds nothing and a NaN side wins.
@@ -86,103 +99,132 @@ __device__ __forceinline__ Stat stat_wave_merge_nan(Stat st) {
 // One row's scalars.
 struct RowRules {
   float rho, f, p;
-  const uint32_t* words;  // LDS words of the slice, or null: no history
-  const uint32_t* bias;   // LDS: 1 + list position of the column's bias, 0 = none; or null
-  const float* values;    // the row's bias values
-  const uint32_t* allowed;
-  // gradient
-  float g, gh, nlse2, H, c, inv_tau;
+  const float* values;      // the row's bias values
+  const uint32_t* allowed;  // the row's grammar, or null
+  const uint32_t* bits;     // LDS: touched columns of the slice, or null
+  float c;
+  // gradient: d = [j = y] gy - p_j (ga + gb t_j), t_j the log2 of p_j
+  float nlse2, ga, gb, gy;
   int64_t y;
 };
 
-// Rules on N columns from `col`, whose LDS words start at `at`.  slope: d
-// processed / d raw (kGrad only).  Returns a bit per column: 1 = not allowed.
-template <int N, bool SLOPE>
-__device__ __forceinline__ uint32_t apply_rules(const RowRules& r, float* z, float* slope, int at, int col) {
-  if (SLOPE) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) slope[k] = 1.f;
+// N bits from position `pos` of a bit array (bit k of the result = pos + k).
+template <int N>
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int pos) {
+  const int w = pos >> 5, sh = pos & 31;
+  uint32_t v = words[w] >> sh;
+  if (N > 1 && sh > 32 - N) v |= words[w + 1] << (32 - sh);
+  return v;
+}
+
+// x where the bit is set, -inf elsewhere, without a compare.
+__device__ __forceinline__ float keep_if(uint32_t bits, int k, float x) {
+  const uint32_t m = static_cast<uint32_t>(static_cast<int32_t>(bits << (31 - k)) >> 31);
+  return __uint_as_float((m & __float_as_uint(x)) | (~m & 0xff800000u));
+}
+
+__device__ __forceinline__ float grad_of(const RowRules& r, float z, float slope, int64_t col) {
+  const float t = fmaf(z, r.c, r.nlse2);
+  const float p = fast_exp2(t);
+  float d = -p * fmaf(r.gb, fmaxf(t, kNoWeight), r.ga);
+  if (col == r.y) d += r.gy;
+  return d * slope;
+}
+
+// What N streamed columns give (slice-relative `rel`, row column `col`):
+//   kProcess  -inf where not allowed; touched columns keep their raw value
+//   kScore    touched columns and those not allowed become -inf (weigh nothing)
+//   kGrad     their gradient, 0 where not allowed
+template <int OP, int N>
+__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, int rel, int col) {
+  uint32_t live = ~0u;
+  if (r.allowed) live = bits_at<N>(r.allowed, col);
+  if (r.bits) {
+    const uint32_t touched = bits_at<N>(r.bits, rel);
+    live = OP == kProcess ? live | touched : live & ~touched;
   }
-  if (r.words) {
-    uint32_t w[N];
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const u32x4 q = *reinterpret_cast<const u32x4*>(r.words + at + k);
-        w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k) w[k] = r.words[at + k];
-    }
-    uint32_t any = 0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) any |= w[k];
-    if (any) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (w[k]) {
-          const bool up = z[k] > 0.f;
-          if (SLOPE) slope[k] = up ? __frcp_rn(r.rho) : r.rho;
-          z[k] = up ? __fdiv_rn(z[k], r.rho) : __fmul_rn(z[k], r.rho);
-          const uint32_t n = w[k] & ~kPromptBit;
-          if (n) z[k] = __fsub_rn(__fsub_rn(z[k], __fmul_rn(r.f, static_cast<float>(n))), r.p);
-        }
-      }
-    }
-  }
-  if (r.bias) {
+  if (OP == kGrad) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const uint32_t w = r.bias[at + k];
-      if (w) z[k] = __fadd_rn(z[k], r.values[w - 1]);
+      const float d = grad_of(r, z[k], 1.f, col + k);
+      z[k] = (live >> k) & 1u ? d : 0.f;
     }
-  }
-  uint32_t shut = 0;
-  if (r.allowed) {
-    const int wi = col >> 5, sh = col & 31;
-    uint32_t bits = r.allowed[wi] >> sh;
-    if (N > 1 && sh > 32 - N) bits |= r.allowed[wi + 1] << (32 - sh);
-    shut = ~bits;
+  } else if (r.allowed || (OP == kScore && r.bits)) {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if ((shut >> k) & 1u) z[k] = neg_inf();
-  }
-  return shut;
-}
-
-// dL/draw of N columns from `col`; z holds the processed logits on entry.  A
-// column that is not allowed gets 0 whatever its value and the row's.
-template <int N>
-__device__ __forceinline__ void grad_cols(const RowRules& r, float* z, const float* slope, uint32_t shut, int col) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float t = fmaf(z[k], r.c, r.nlse2);
-    const float p = fast_exp2(t);
-    const float lt = t == neg_inf() ? 0.f : t * kLn2;
-    float d = -p * fmaf(r.gh, lt + r.H, r.g);
-    if (col + k == r.y) d += r.g;
-    d = d * r.inv_tau * slope[k];
-    z[k] = (shut >> k) & 1u ? 0.f : d;
+    for (int k = 0; k < N; ++k) z[k] = keep_if(live, k, z[k]);
   }
 }
 
-template <class Tr, int OP, int N>
-__device__ __forceinline__ void finish_cols(const RowRules& r, float* z, Stat& st, int at, int col) {
-  float slope[N];
-  const uint32_t shut = apply_rules<N, OP == kGrad>(r, z, slope, at, col);
-  if (OP == kScore) stat_push_masked<N>(st, z, r.c);
-  if (OP == kGrad) grad_cols<N>(r, z, slope, shut, col);
+// The rules on one touched column: w its count word, b its bias entry + 1.
+// False if the grammar does not allow it.
+__device__ __forceinline__ bool touched_col(const RowRules& r, uint32_t w, uint32_t b, int col, float& z,
+                                            float& slope) {
+  slope = 1.f;
+  if (w) {
+    const bool up = z > 0.f;
+    slope = up ? __frcp_rn(r.rho) : r.rho;
+    z = up ? __fdiv_rn(z, r.rho) : __fmul_rn(z, r.rho);
+    const uint32_t n = w & ~kPromptBit;
+    if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(r.f, static_cast<float>(n))), r.p);
+  }
+  if (b) z = __fadd_rn(z, r.values[b - 1]);
+  if (r.allowed && !(bits_at<1>(r.allowed, col) & 1u)) {
+    z = neg_inf();
+    return false;
+  }
+  return true;
+}
+
+// Exclusive sum over the workgroup; *total = the whole.
+template <int NT>
+__device__ __forceinline__ uint32_t block_exclusive_sum(uint32_t v, uint32_t* sm, uint32_t* total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  uint32_t x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63) sm[w] = x;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 64; ++k) {
+    if (k < w) before += sm[k];
+    all += sm[k];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// The outputs of a row from its whole state and its target's processed logit.
+__device__ __forceinline__ void store_score(const RulesArgs& a, int64_t row, Stat st, float zy) {
+  const float l2s = log2f(st.s);
+  const int64_t y = a.targets[row];
+  float lp = __builtin_nanf("");
+  if (y >= 0 && y < a.V) lp = (fmaf(zy, a.c, -st.mc) - l2s) * kLn2;
+  a.logprob[row] = lp;
+  if (a.entropy_out) a.entropy_out[row] = (l2s - st.a / st.s) * kLn2;
+  if (a.lse_out) a.lse_out[row] = (st.mc + l2s) * kLn2;
+}
+
+__device__ __forceinline__ void store_unscored(const RulesArgs& a, int64_t row) {
+  a.logprob[row] = 0.f;
+  if (a.entropy_out) a.entropy_out[row] = 0.f;
+  if (a.lse_out) a.lse_out[row] = 0.f;
 }
 
 template <class Tr, int OP, int NT, int U>
 __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+  __shared__ uint32_t sums[NT / 64];
+  __shared__ Stat sm[NT / 64];
+  __shared__ float zy;  // processed logit of the target, if it is a touched column
   constexpr int P = Tr::kPerVec;
   const int tid = threadIdx.x;
-  const unsigned rel = blockIdx.x / static_cast<unsigned>(a.nslices);
-  const int slice = static_cast<int>(blockIdx.x - rel * static_cast<unsigned>(a.nslices));
-  const int64_t row = a.row0 + rel;
+  const unsigned rel_row = blockIdx.x / static_cast<unsigned>(a.nslices);
+  const int slice = static_cast<int>(blockIdx.x - rel_row * static_cast<unsigned>(a.nslices));
+  const int64_t row = a.row0 + rel_row;
   const int c0 = slice * a.slice;
   const int n = a.V - c0 < a.slice ? a.V - c0 : a.slice;
   const char* xp = static_cast<const char*>(a.x) + (row * a.ld + c0) * Tr::kBytes;
@@ -195,39 +237,32 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
       for (int i = tid; i < sp.nvec; i += NT) vp[i] = u32x4{0, 0, 0, 0};
       if (tid < sp.tail) Tr::store1(op, sp.head + sp.nvec * P + tid, 0.f);
     }
+    if (OP == kScore && a.nslices == 1 && tid == 0) store_unscored(a, row);
     return;
   }
-  // Columns [0, head) and the tail go one by one, the rest as 16-byte vectors;
-  // where input and output rows differ in their 16-byte phase, all go singly.
-  RowSplit<Tr> sp(xp, n);
-  if (OP != kScore && ((reinterpret_cast<uintptr_t>(xp) ^ reinterpret_cast<uintptr_t>(op)) & 15u)) {
-    sp.head = 0;
-    sp.nvec = 0;
-    sp.tail = n;
-  }
-  const int base = 8 - sp.head;  // LDS position of column c0: vectors start at a multiple of 8
 
   RowRules r;
   r.rho = a.repetition ? a.repetition[row] : 1.f;
   r.f = a.frequency ? a.frequency[row] : 0.f;
   r.p = a.presence ? a.presence[row] : 0.f;
-  r.words = nullptr;
-  r.bias = nullptr;
   r.values = nullptr;
   r.allowed = a.allowed ? a.allowed + row * a.ld_allowed : nullptr;
+  r.bits = nullptr;
   r.c = a.c;
   if (OP == kGrad) {
-    r.g = a.grad_logprob[row];
-    r.gh = a.grad_entropy ? a.grad_entropy[row] : 0.f;
+    const float g = a.grad_logprob[row] * a.inv_tau;
+    const float gh = a.grad_entropy ? a.grad_entropy[row] * a.inv_tau : 0.f;
     r.nlse2 = -a.lse[row] * kLog2e;
-    r.H = a.grad_entropy ? a.entropy[row] : 0.f;
-    r.inv_tau = a.inv_tau;
-    r.y = a.targets[row];
+    r.ga = a.grad_entropy ? fmaf(gh, a.entropy[row], g) : g;
+    r.gb = gh * kLn2;
+    r.gy = g;
   }
+  if (OP != kProcess) r.y = a.targets[row];
 
-  int64_t len = 0, buf = row, b0 = 0, nb = 0;
+  int64_t len = 0, buf = row, b0 = 0, nb = 0, prompt = 0;
   if (a.tokens) {
     if (a.row_buffer) buf = a.row_buffer[row];
+    if (a.prompt_len) prompt = a.prompt_len[row];
     len = a.hist_len[row];
     len = len < a.max_len ? len : a.max_len;
     if (buf < 0 || buf >= a.buffers) len = 0;
@@ -239,49 +274,122 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     b1 = b1 < a.bias_count ? b1 : a.bias_count;
     nb = b1 > b0 ? b1 - b0 : 0;
   }
-  const int span = n + kLdsPad;
-  uint32_t* words = lds;
-  uint32_t* bias = lds + (a.tokens ? a.slice + kLdsPad : 0);
-  if (len > 0) {
-    r.words = words;
-    for (int i = tid; i < span; i += NT) words[i] = 0;
-  }
-  if (nb > 0) {
-    r.bias = bias;
-    r.values = a.bias_values + b0;
-    for (int i = tid; i < span; i += NT) bias[i] = 0;
-  }
-  if (len > 0 || nb > 0) {  // the same for the whole workgroup
+  const int32_t* tok = a.tokens + buf * a.ld_tokens;
+  const int32_t* btok = a.bias_tokens + b0;
+
+  const int ranks = a.slice < kRanks ? a.slice : kRanks;
+  uint32_t* bits = lds;                   // [slice / 32]
+  uint32_t* pre = bits + a.slice / 32;    // [slice / 128]
+  uint32_t* list = pre + a.slice / 128;   // [ranks]
+  uint32_t* cnt = list + ranks;           // [ranks]
+  uint32_t* bidx = cnt + ranks;           // [ranks], only with biases
+  uint32_t touched = 0;                   // columns of the slice
+
+  // Column of a token within the slice; one outside the vocabulary is
+  // negative or past every slice.
+  auto in_slice = [&](int32_t t, int& j) {
+    const int64_t d = static_cast<int64_t>(t) - c0;
+    j = static_cast<int>(d);
+    return d >= 0 && d < n;
+  };
+  auto rank_of = [&](int j) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(bits + (j >> 7) * 4);
+    const int k = (j >> 5) & 3;
+    const uint32_t word = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
+    uint32_t rk = pre[j >> 7] + __popc(word & ((1u << (j & 31)) - 1u));
+    if (k > 0) rk += __popc(q.x);
+    if (k > 1) rk += __popc(q.y);
+    if (k > 2) rk += __popc(q.z);
+    return rk;
+  };
+  // Step 2 for ranks [r0, r0 + ranks).
+  auto count = [&](uint32_t r0) {
+    for (int i = tid; i < ranks; i += NT) {
+      cnt[i] = 0;
+      if (nb > 0) bidx[i] = 0;
+    }
     __syncthreads();
-    if (len > 0) {
-      const int32_t* tok = a.tokens + buf * a.ld_tokens;
-      const int64_t prompt = a.prompt_len ? a.prompt_len[row] : 0;
 #pragma unroll 4
-      for (int64_t i = tid; i < len; i += NT) {
-        // a token outside the vocabulary is negative or past every slice
-        const int64_t j = static_cast<int64_t>(tok[i]) - c0;
-        if (j >= 0 && j < n) {
+    for (int64_t i = tid; i < len; i += NT) {
+      int j;
+      if (in_slice(tok[i], j)) {
+        const uint32_t k = rank_of(j) - r0;
+        if (k < static_cast<uint32_t>(ranks)) {
+          list[k] = j;
           if (i < prompt)
-            atomicOr(words + base + j, kPromptBit);
+            atomicOr(cnt + k, kPromptBit);
           else
-            atomicAdd(words + base + j, 1u);
+            atomicAdd(cnt + k, 1u);
         }
       }
     }
-    // the last entry listed for a column counts
     for (int64_t i = tid; i < nb; i += NT) {
-      const int64_t j = static_cast<int64_t>(a.bias_tokens[b0 + i]) - c0;
-      if (j >= 0 && j < n) atomicMax(bias + base + j, static_cast<uint32_t>(i) + 1u);
+      int j;
+      if (in_slice(btok[i], j)) {
+        const uint32_t k = rank_of(j) - r0;
+        if (k < static_cast<uint32_t>(ranks)) {
+          list[k] = j;
+          atomicMax(bidx + k, static_cast<uint32_t>(i) + 1u);  // the last entry listed counts
+        }
+      }
     }
     __syncthreads();
+  };
+
+  if (len > 0 || nb > 0) {  // the same for the whole workgroup
+    for (int i = tid; i < a.slice / 128; i += NT) reinterpret_cast<u32x4*>(bits)[i] = u32x4{0, 0, 0, 0};
+    __syncthreads();
+    int j;
+#pragma unroll 4
+    for (int64_t i = tid; i < len; i += NT)
+      if (in_slice(tok[i], j)) atomicOr(bits + (j >> 5), 1u << (j & 31));
+    for (int64_t i = tid; i < nb; i += NT)
+      if (in_slice(btok[i], j)) atomicOr(bits + (j >> 5), 1u << (j & 31));
+    __syncthreads();
+    const int per = (a.slice / 128 + NT - 1) / NT;
+    uint32_t mine = 0;
+    for (int k = 0; k < per; ++k) {
+      const int g = tid * per + k;
+      if (g < a.slice / 128) {
+        const u32x4 q = reinterpret_cast<const u32x4*>(bits)[g];
+        mine += __popc(q.x) + __popc(q.y) + __popc(q.z) + __popc(q.w);
+      }
+    }
+    uint32_t at = block_exclusive_sum<NT>(mine, sums, &touched);
+    for (int k = 0; k < per; ++k) {
+      const int g = tid * per + k;
+      if (g < a.slice / 128) {
+        const u32x4 q = reinterpret_cast<const u32x4*>(bits)[g];
+        pre[g] = at;
+        at += __popc(q.x) + __popc(q.y) + __popc(q.z) + __popc(q.w);
+      }
+    }
+    __syncthreads();
+    if (touched) {
+      r.bits = bits;
+      r.values = a.bias_values + b0;
+      count(0);
+    }
   }
 
-  Stat st = stat_empty();
-  if (tid < sp.head) {
-    float z = Tr::load1(xp, tid);
-    finish_cols<Tr, OP, 1>(r, &z, st, base + tid, c0 + tid);
-    if (OP != kScore) Tr::store1(op, tid, z);
+  // Columns [0, head) and the tail go one by one, the rest as 16-byte vectors;
+  // where input and output rows differ in their 16-byte phase, all go singly.
+  RowSplit<Tr> sp(xp, n);
+  if (OP != kScore && ((reinterpret_cast<uintptr_t>(xp) ^ reinterpret_cast<uintptr_t>(op)) & 15u)) {
+    sp.head = 0;
+    sp.nvec = 0;
+    sp.tail = n;
   }
+  Stat st = stat_empty();
+  auto single = [&](int j) {
+    float z = Tr::load1(xp, j);
+    stream_cols<OP, 1>(r, &z, j, c0 + j);
+    if (OP == kScore)
+      stat_push_masked<1, 1>(st, &z, r.c);
+    else
+      Tr::store1(op, j, z);
+  };
+  if (tid < sp.head) single(tid);
   const u32x4* vp = reinterpret_cast<const u32x4*>(xp + sp.head * Tr::kBytes);
   u32x4* wp = reinterpret_cast<u32x4*>(op + sp.head * Tr::kBytes);
   int i = tid;
@@ -289,46 +397,76 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     u32x4 w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(vp + i + u * NT);
+    float z[U * P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float z[P];
-      Tr::unpack(w[u], z);
-      const int at = (i + u * NT) * P;
-      finish_cols<Tr, OP, P>(r, z, st, 8 + at, c0 + sp.head + at);
-      if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z), wp + i + u * NT);
+      Tr::unpack(w[u], z + u * P);
+      const int rel = sp.head + (i + u * NT) * P;
+      stream_cols<OP, P>(r, z + u * P, rel, c0 + rel);
+      if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
     }
+    if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
   }
   for (; i < sp.nvec; i += NT) {
     float z[P];
     Tr::unpack(__builtin_nontemporal_load(vp + i), z);
-    finish_cols<Tr, OP, P>(r, z, st, 8 + i * P, c0 + sp.head + i * P);
-    if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z), wp + i);
+    stream_cols<OP, P>(r, z, sp.head + i * P, c0 + sp.head + i * P);
+    if (OP == kScore)
+      stat_push_masked<P, P>(st, z, r.c);
+    else
+      __builtin_nontemporal_store(Tr::pack(z), wp + i);
   }
-  for (int j = n - sp.tail + tid; j < n; j += NT) {
-    float z = Tr::load1(xp, j);
-    finish_cols<Tr, OP, 1>(r, &z, st, base + j, c0 + j);
-    if (OP != kScore) Tr::store1(op, j, z);
+  for (int j = n - sp.tail + tid; j < n; j += NT) single(j);
+
+  // Touched columns, after the stream has stored what lies around them.
+  for (uint32_t r0 = 0; r0 < touched; r0 += ranks) {
+    if (r0 > 0) {
+      __syncthreads();
+      count(r0);
+    } else if (OP != kScore) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stream's stores are done
+      __syncthreads();
+    }
+    const int m = touched - r0 < static_cast<uint32_t>(ranks) ? static_cast<int>(touched - r0) : ranks;
+    for (int k = tid; k < m; k += NT) {
+      const int j = static_cast<int>(list[k]);
+      float z = Tr::load1(xp, j), slope;
+      const bool ok = touched_col(r, cnt[k], nb > 0 ? bidx[k] : 0u, c0 + j, z, slope);
+      if (OP == kScore) {
+        stat_push_masked<1, 1>(st, &z, r.c);
+        if (c0 + j == r.y) zy = z;
+      } else {
+        Tr::store1(op, j, OP == kProcess ? z : ok ? grad_of(r, z, slope, c0 + j) : 0.f);
+      }
+    }
   }
 
   if (OP == kScore) {
-    __shared__ Stat sm[NT / 64];
     st = stat_wave_merge_nan(st);
     if ((tid & 63) == 0) sm[tid >> 6] = st;
     __syncthreads();
     if (tid == 0) {
 #pragma unroll
       for (int k = 1; k < NT / 64; ++k) st = stat_merge_nan(st, sm[k]);
-      float* pt = a.part + (row * a.nslices + slice) * 3;
-      pt[0] = st.mc;
-      pt[1] = st.s;
-      pt[2] = st.a;
-      const int64_t y = a.targets[row];
-      if (y >= c0 && y < c0 + n) {
-        const int j = static_cast<int>(y) - c0;
-        float z = Tr::load1(xp, j);
-        float unused;
-        apply_rules<1, false>(r, &z, &unused, base + j, static_cast<int>(y));
-        a.zy[row] = z;
+      const bool mine = r.y >= c0 && r.y < c0 + n;
+      float z = 0.f;
+      if (mine) {
+        const int j = static_cast<int>(r.y) - c0;
+        if (r.bits && (bits_at<1>(bits, j) & 1u)) {
+          z = zy;
+        } else {
+          z = Tr::load1(xp, j);
+          if (r.allowed && !(bits_at<1>(r.allowed, c0 + j) & 1u)) z = neg_inf();
+        }
+      }
+      if (a.nslices == 1) {
+        store_score(a, row, st, z);
+      } else {
+        float* pt = a.part + (row * a.nslices + slice) * 3;
+        pt[0] = st.mc;
+        pt[1] = st.s;
+        pt[2] = st.a;
+        if (mine) a.zy[row] = z;
       }
     }
   }
@@ -340,11 +478,7 @@ __global__ void __launch_bounds__(256) k_rules_join(RulesArgs a) {
   const int lane = threadIdx.x & 63;
   if (row >= a.T) return;
   if (a.mask && a.mask[row] == 0) {
-    if (lane == 0) {
-      a.logprob[row] = 0.f;
-      if (a.entropy_out) a.entropy_out[row] = 0.f;
-      if (a.lse_out) a.lse_out[row] = 0.f;
-    }
+    if (lane == 0) store_unscored(a, row);
     return;
   }
   Stat st = stat_empty();
@@ -353,33 +487,29 @@ __global__ void __launch_bounds__(256) k_rules_join(RulesArgs a) {
     st = stat_merge_nan(st, Stat{pt[0], pt[1], pt[2]});
   }
   st = stat_wave_merge_nan(st);
-  if (lane == 0) {
-    const float l2s = log2f(st.s);
-    const int64_t y = a.targets[row];
-    float lp = __builtin_nanf("");
-    if (y >= 0 && y < a.V) lp = (fmaf(a.zy[row], a.c, -st.mc) - l2s) * kLn2;
-    a.logprob[row] = lp;
-    if (a.entropy_out) a.entropy_out[row] = (l2s - st.a / st.s) * kLn2;
-    if (a.lse_out) a.lse_out[row] = (st.mc + l2s) * kLn2;
-  }
+  // a target outside the vocabulary has no processed logit: not read
+  const int64_t y = a.targets[row];
+  if (lane == 0) store_score(a, row, st, y >= 0 && y < a.V ? a.zy[row] : 0.f);
 }
 
-// Columns per workgroup: the widest slice that still gives every CU four
-// workgroups, so that long calls reread the history few times and a single
-// decode row still spreads over the chip.
-int slice_of(int64_t T, int64_t V) {
-  for (int s : {4096, 2048})
-    if (T * ((V + s - 1) / s) >= 1024) return s;
-  return 1024;
-}
-
-template <class Tr, int OP>
-hipError_t launch_rules_t(const RulesArgs& args, const char* name, hipStream_t s) {
-  constexpr int NT = 256;
-  RulesArgs a = args;
-  a.slice = slice_of(a.T, a.V);
+// Slices per row: one where there are rows enough for four workgroups a CU,
+// else as many as that takes, of at least kMinSlice columns.
+void set_slices(RulesArgs& a) {
+  const int64_t most = (int64_t(a.V) + kMinSlice - 1) / kMinSlice, least = (int64_t(a.V) + kMaxSlice - 1) / kMaxSlice;
+  int64_t n = (1024 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  n = n < most ? n : most;
+  n = n > least ? n : least;
+  a.slice = static_cast<int>(((a.V + n - 1) / n + 127) / 128 * 128);
   a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
-  const size_t lds = size_t(a.slice + kLdsPad) * 4 * ((a.tokens ? 1 : 0) + (a.bias_offsets ? 1 : 0));
+}
+
+template <class Tr, int OP, int NT>
+hipError_t launch_rules_nt(RulesArgs a, const char* name, hipStream_t s) {
+  size_t lds = 0;
+  if (a.tokens || a.bias_offsets) {
+    const int ranks = a.slice < kRanks ? a.slice : kRanks;
+    lds = size_t(a.slice) / 8 + a.slice / 32 + size_t(ranks) * 4 * (a.bias_offsets ? 3 : 2);
+  }
   // workgroups of a launch: far below 2^32 work-items whatever T
   const int64_t rows_per = (int64_t(1) << 22) / a.nslices > 0 ? (int64_t(1) << 22) / a.nslices : 1;
   for (int64_t r0 = 0; r0 < a.T; r0 += rows_per) {
@@ -391,6 +521,14 @@ hipError_t launch_rules_t(const RulesArgs& args, const char* name, hipStream_t s
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <class Tr, int OP>
+hipError_t launch_rules_t(const RulesArgs& a, const char* name, hipStream_t s) {
+  // a few vectors a lane at least, so that short slices do not idle waves
+  if (a.slice >= 16384) return launch_rules_nt<Tr, OP, 512>(a, name, s);
+  if (a.slice >= 4096) return launch_rules_nt<Tr, OP, 256>(a, name, s);
+  return launch_rules_nt<Tr, OP, 128>(a, name, s);
 }
 
 template <int OP>
@@ -405,25 +543,28 @@ hipError_t launch_rules(int dtype, const RulesArgs& a, const char* name, hipStre
 }  // namespace
 
 size_t processed_workspace_bytes(int64_t T, int64_t V) {
-  const int64_t slice = slice_of(T, V);
-  const int64_t ns = (V + slice - 1) / slice;
-  const size_t per_row = size_t(ns) * 12 + 4;
+  RulesArgs a;
+  a.T = T;
+  a.V = static_cast<int>(V);
+  set_slices(a);
+  const size_t per_row = size_t(a.nslices) * 12 + 4;
   if (size_t(T) > (size_t(1) << 60) / per_row) return 0;
   return (size_t(T) * per_row + 255) / 256 * 256;
 }
 
-hipError_t launch_process_logits(int dtype, const RulesArgs& a, hipStream_t s) {
+hipError_t launch_process_logits(int dtype, const RulesArgs& args, hipStream_t s) {
+  RulesArgs a = args;
+  set_slices(a);
   return launch_rules<kProcess>(dtype, a, "k_process_logits", s);
 }
 
 hipError_t launch_processed_score(int dtype, const RulesArgs& args, char* ws, hipStream_t s) {
   RulesArgs a = args;
-  a.slice = slice_of(a.T, a.V);
-  a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
+  set_slices(a);
   a.part = reinterpret_cast<float*>(ws);
   a.zy = a.part + a.T * a.nslices * 3;
   hipError_t e = launch_rules<kScore>(dtype, a, "k_processed_score", s);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.nslices == 1) return e;
   constexpr int64_t kRows = int64_t(1) << 22;
   for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
     RulesArgs b = a;
@@ -436,7 +577,9 @@ hipError_t launch_processed_score(int dtype, const RulesArgs& args, char* ws, hi
   return hipSuccess;
 }
 
-hipError_t launch_processed_grad(int dtype, const RulesArgs& a, hipStream_t s) {
+hipError_t launch_processed_grad(int dtype, const RulesArgs& args, hipStream_t s) {
+  RulesArgs a = args;
+  set_slices(a);
   return launch_rules<kGrad>(dtype, a, "k_processed_grad", s);
 }
 

@@ -15,7 +15,7 @@ import pytest
 
 from oracle import lp_oracle as O
 from tests.helpers import host, to_dev, to_dev_bits
-from tests.rules_cases import DTYPES, EPS, Rules
+from tests.rules_cases import DTYPES, EPS, Rules, to_bits
 
 pytestmark = pytest.mark.gpu
 TOL = 1e-5
@@ -319,3 +319,62 @@ def test_repeatable_bit_for_bit():
     for _ in range(3):
         b = lp.lp_processed_logprobs_entropy(x, rules, y, None, 0.7)
         assert all(torch.equal(p.view(torch.int32), q.view(torch.int32)) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_touched_columns_in_many_rows(dtype):
+    """Rows enough for one workgroup a row, whose histories and biases touch
+    most of the vocabulary: more columns than are dealt with at a time."""
+    torch = _torch()
+    lp = _lp()
+    rng = np.random.default_rng(12)
+    T, V, L = 1100, 9001, 12000
+    bits = to_bits(rng.normal(0, 3, (T, V)), dtype)
+    tok = rng.integers(0, V, (2, L)).astype(np.int32)
+    seq = (np.arange(T) % 2).astype(np.int32)
+    hist = rng.integers(0, L + 1, T).astype(np.int32)
+    hist[5:8] = [0, 1, L]
+    prompt = (hist // 3).astype(np.int32)
+    nb = rng.choice([0, 1, 40], T)
+    nb[6] = 5000
+    off = np.concatenate([[0], np.cumsum(nb)]).astype(np.int64)
+    ids = rng.integers(0, V, off[-1]).astype(np.int32)
+    val = rng.normal(0, 2, off[-1]).astype(np.float32)
+    rho, f = rng.uniform(0.7, 1.6, T).astype(np.float32), rng.uniform(0, 0.5, T).astype(np.float32)
+    words = rng.integers(-2**31, 2**31, (T, (V + 31) // 32)).astype(np.int32)
+    x = to_dev(bits) if dtype == "fp32" else to_dev_bits(bits, dtype)
+    y = rng.integers(0, V, T).astype(np.int64)
+    words[np.arange(T), y // 32] |= (np.uint32(1) << (y % 32).astype(np.uint32)).view(np.int32)
+    r = lp.LogitRules(tokens=to_dev(tok), hist_len=to_dev(hist), prompt_len=to_dev(prompt), row_seq=to_dev(seq),
+                      repetition=to_dev(rho), frequency=to_dev(f), presence=to_dev(f), bias_offsets=to_dev(off),
+                      bias_tokens=to_dev(ids), bias_values=to_dev(val), allowed=to_dev(words))
+    z = O.widen(bits, dtype)
+    slope = np.ones((T, V))
+    mag = np.abs(z)
+    for t in range(T):
+        h = tok[seq[t], :hist[t]]
+        times = np.bincount(h[prompt[t]:], minlength=V)
+        seen = np.bincount(h, minlength=V) > 0
+        slope[t, seen] = np.where(z[t, seen] > 0, 1 / float(rho[t]), float(rho[t]))
+        z[t] = z[t] * slope[t] - float(f[t]) * (times + (times > 0))
+        mag[t] = 2 * mag[t] + np.abs(float(f[t])) * (times + 1)
+        for j, b in {int(i): float(v) for i, v in zip(ids[off[t]:off[t + 1]], val[off[t]:off[t + 1]])}.items():
+            z[t, j] += b
+            mag[t, j] += abs(b)
+        ok = (words[t].view(np.uint32)[:, None] >> np.arange(32, dtype=np.uint32) & 1).reshape(-1)[:V] != 0
+        z[t, ~ok] = -np.inf
+        slope[t, ~ok] = 0
+    got = _wide(lp.lp_process_logits(x, r))
+    zf = np.where(np.isfinite(z), z, 0)
+    _same_or_near(got, z, EPS[dtype] / 2 * np.abs(zf) + 6 * 2.0 ** -24 * mag + 2.0 ** -25)
+    yd = to_dev(y)
+    a = lp.lp_processed_logprobs_entropy(x, r, yd, None, 0.9)
+    lp_o, H_o, lse_o = O.logprobs_entropy(z, y, None, 0.9)
+    for p, q in zip(a, (lp_o, H_o, lse_o)):
+        assert np.abs(host(p) - q).max() <= TOL
+    g = rng.normal(0, 1, T).astype(np.float32)
+    d = _wide(lp.lp_processed_logprobs_entropy_backward(x, r, yd, None, 0.9, a[2], a[1], to_dev(g), to_dev(f)))
+    want = O.processed_backward(z, slope, y, None, 0.9, g, f)
+    assert np.all(np.abs(d - want) <= EPS[dtype] / 2 * np.abs(want) + 2 * TOL * (np.abs(g) + f * 30)[:, None] * 1.6 + 2.0 ** -25)
+    lp.lp_process_logits(x, r, out=x)
+    assert np.array_equal(_wide(x), got)
