@@ -11,8 +11,11 @@
 // Frequent tokens: blocks of kChunk sorted positions that hold a single token
 // are summed first, by a workgroup each, into partial rows; the owner then
 // adds the partial rows of its run's whole blocks and, one by one, the
-// positions before and after them.  A run's length so costs its owner
-// length / kChunk + 2 kChunk additions.
+// positions before and after them.  The same launch writes the zeros of the
+// rows that no token names, which are most of dW's bytes.
+//
+// Up to kTinyN positions nothing is sorted: every owner finds its positions
+// among all of them with ballots, in one launch.
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
@@ -20,11 +23,18 @@ namespace lp {
 
 namespace {
 
-constexpr int kChunk = 64;       // sorted positions per partial row
-constexpr int kSortNT = 256;     // threads of a sorting workgroup
-constexpr int kSortTile = 2048;  // positions per sorting workgroup
-constexpr int kSmallN = 4096;    // sorted by one workgroup in LDS up to here
+constexpr int kChunk = 64;      // sorted positions per partial row
+constexpr int kSortNT = 256;    // threads of a sorting workgroup
+constexpr int kMaxTiles = 128;  // sorting workgroups
+constexpr int kMaxDigit = 10;   // bits per pass
+constexpr int kSmallN = 4096;   // sorted by one workgroup in LDS up to here
 constexpr int kSmallNT = 1024;
+constexpr int kTinyN = 256;     // not sorted up to here
+constexpr int kSumNT = 128;     // threads of a summing workgroup
+constexpr int kRunSpan = 16;    // sorted positions whose run starts a workgroup owns
+constexpr uint32_t kAbsent = 0xffffffffu;
+
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // ---------------------------------------------------------------------------
 // lookup
@@ -71,11 +81,10 @@ __device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t i) {
   return v >= 0 && v < a.V ? static_cast<uint32_t>(v) : static_cast<uint32_t>(a.V);
 }
 
-// Lanes of the wave with the same 8-bit digit (among live lanes).
-__device__ __forceinline__ uint64_t same_digit(uint32_t d, bool live) {
+// Lanes of the wave with the same digit of `bits` bits (among live lanes).
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, bool live, int bits) {
   uint64_t m = __ballot(live);
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
+  for (int b = 0; b < bits; ++b) {
     const uint64_t s = __ballot((d >> b) & 1u);
     m &= ((d >> b) & 1u) ? s : ~s;
   }
@@ -109,6 +118,10 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
     key[0][i] = key_of(a, i);
     pos[0][i] = i;
   }
+  if (a.first) {
+    for (int v = tid; v < a.V; v += kSmallNT) a.first[v] = kAbsent;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
   const int share = ((n + W - 1) / W + 63) / 64 * 64;
   const int i0 = w * share, i1 = i0 + share < n ? i0 + share : n;
   int cur = 0;
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
     for (int i = i0; i < i1; i += 64) {
       const bool live = i + lane < i1;
       const uint32_t d = live ? (key[cur][i + lane] >> shift) & 255u : 0;
-      const uint64_t m = same_digit(d, live);
+      const uint64_t m = same_digit(d, live, 8);
       if (live && lanes_below(m) == 0) cnt[w][d] += __popcll(m);
       wave_sync();
     }
@@ -155,7 +168,7 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
       const uint32_t kx = live ? key[cur][i + lane] : 0;
       const uint32_t px = live ? pos[cur][i + lane] : 0;
       const uint32_t d = (kx >> shift) & 255u;
-      const uint64_t m = same_digit(d, live);
+      const uint64_t m = same_digit(d, live, 8);
       const int below = lanes_below(m);
       uint32_t at = 0;
       if (live) at = base[d] + cnt[w][d] + below;
@@ -171,108 +184,111 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
     __syncthreads();
   }
   for (int i = tid; i < n; i += kSmallNT) {
-    a.keys[0][i] = key[cur][i];
+    const uint32_t k = key[cur][i];
+    a.keys[0][i] = k;
     a.pos[0][i] = pos[cur][i];
+    // the clearing stores above were waited for at the barriers since
+    if (a.first && k < static_cast<uint32_t>(a.V) && (i == 0 || key[cur][i - 1] != k)) a.first[k] = i;
   }
 }
 
-// One pass over 8 bits of the keys, three kernels: digit counts per tile,
-// their scan in (digit, tile) order, and the stable scatter.
+// One pass over `bits` bits of the keys, two kernels: digit counts per tile,
+// and the stable scatter, whose workgroups each add up the counts before them
+// (there are at most kMaxTiles tiles, so this costs less than a scan's launch).
 __device__ __forceinline__ uint32_t load_key(const EmbedGradArgs& a, int src, int64_t i) {
   return src < 0 ? key_of(a, i) : a.keys[src][i];
 }
 
-__global__ void __launch_bounds__(kSortNT) k_embed_count(EmbedGradArgs a, int shift, int src) {
-  __shared__ uint32_t cnt[256];
-  cnt[threadIdx.x] = 0;
+__global__ void __launch_bounds__(kSortNT) k_embed_count(EmbedGradArgs a, int shift, int bits, int src) {
+  __shared__ uint32_t cnt[1 << kMaxDigit];
+  const int bins = 1 << bits;
+  for (int d = threadIdx.x; d < bins; d += kSortNT) cnt[d] = 0;
   __syncthreads();
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSortTile;
-#pragma unroll
-  for (int k = 0; k < kSortTile / kSortNT; ++k) {
-    const int64_t i = t0 + k * kSortNT + threadIdx.x;
-    if (i < a.N) atomicAdd(&cnt[(load_key(a, src, i) >> shift) & 255u], 1u);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile, t1 = t0 + a.tile < a.N ? t0 + a.tile : a.N;
+  for (int64_t i = t0 + threadIdx.x; i < t1; i += kSortNT)
+    atomicAdd(&cnt[(load_key(a, src, i) >> shift) & (bins - 1)], 1u);
+  if (src < 0 && a.first) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kSortNT;
+    for (int64_t v = static_cast<int64_t>(blockIdx.x) * kSortNT + threadIdx.x; v < a.V; v += stride) a.first[v] = kAbsent;
   }
   __syncthreads();
-  a.counts[static_cast<int64_t>(threadIdx.x) * a.tiles + blockIdx.x] = cnt[threadIdx.x];
+  for (int d = threadIdx.x; d < bins; d += kSortNT) a.counts[static_cast<int64_t>(blockIdx.x) * bins + d] = cnt[d];
 }
 
-// Exclusive scan of 256 x tiles counts by one workgroup.
-__global__ void __launch_bounds__(1024) k_embed_scan(EmbedGradArgs a) {
-  __shared__ uint32_t wsum[16];
-  const int64_t n = static_cast<int64_t>(a.tiles) * 256;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint32_t carry = 0;
-  for (int64_t i0 = 0; i0 < n; i0 += 4096) {
-    const int64_t i = i0 + threadIdx.x * 4;  // n is a multiple of 256
-    u32x4 v{0, 0, 0, 0};
-    if (i < n) v = *reinterpret_cast<const u32x4*>(a.counts + i);
-    const uint32_t s = v.x + v.y + v.z + v.w;
-    uint32_t x = s;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const uint32_t y = __shfl_up(x, off, 64);
-      if (lane >= off) x += y;
-    }
-    if (lane == 63) wsum[w] = x;
-    __syncthreads();
-    uint32_t before = carry, total = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (k < w) before += wsum[k];
-      total += wsum[k];
-    }
-    carry += total;
-    uint32_t e = before + x - s;
-    if (i < n) *reinterpret_cast<u32x4*>(a.counts + i) = u32x4{e, e + v.x, e + v.x + v.y, e + v.x + v.y + v.z};
-    __syncthreads();
-  }
-}
-
-__global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int shift, int src, int dst) {
-  constexpr int W = kSortNT / 64, kShare = kSortTile / W;
-  __shared__ uint32_t cnt[W][256];
+__global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int shift, int bits, int src, int dst,
+                                                           bool last) {
+  constexpr int W = kSortNT / 64, kPer = (1 << kMaxDigit) / kSortNT;
+  __shared__ uint32_t cnt[W][1 << kMaxDigit];
+  __shared__ uint32_t wsum[W];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int bins = 1 << bits;
+  for (int d = threadIdx.x; d < bins; d += kSortNT)
 #pragma unroll
-  for (int k = 0; k < W; ++k) cnt[k][threadIdx.x] = 0;
+    for (int k = 0; k < W; ++k) cnt[k][d] = 0;
   __syncthreads();
-  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * kShare;
-  uint32_t kx[kShare / 64];
+  const int share = a.tile / W;  // a multiple of 64
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * a.tile + static_cast<int64_t>(w) * share;
+  const int64_t s1 = s0 + share < a.N ? s0 + share : a.N;
+  for (int64_t i = s0 + lane; i < s1; i += 64) atomicAdd(&cnt[w][(load_key(a, src, i) >> shift) & (bins - 1)], 1u);
+  // digits of this thread: kPer neighbours, so that the scan over digits is
+  // one over threads
+  uint32_t before[kPer], total[kPer], mine = 0;
 #pragma unroll
-  for (int k = 0; k < kShare / 64; ++k) {
-    const int64_t i = s0 + k * 64 + lane;
-    kx[k] = i < a.N ? load_key(a, src, i) : 0;
+  for (int k = 0; k < kPer; ++k) before[k] = total[k] = 0;
+  for (int t = 0; t < a.tiles; ++t) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int d = threadIdx.x * kPer + k;
+      const uint32_t c = d < bins ? a.counts[static_cast<int64_t>(t) * bins + d] : 0;
+      total[k] += c;
+      if (t < static_cast<int>(blockIdx.x)) before[k] += c;
+    }
   }
 #pragma unroll
-  for (int k = 0; k < kShare / 64; ++k) {
-    const bool live = s0 + k * 64 + lane < a.N;
-    const uint32_t d = (kx[k] >> shift) & 255u;
-    const uint64_t m = same_digit(d, live);
-    if (live && lanes_below(m) == 0) cnt[w][d] += __popcll(m);
-    wave_sync();
+  for (int k = 0; k < kPer; ++k) mine += total[k];
+  uint32_t x = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63) wsum[w] = x;
+  __syncthreads();
+  uint32_t base = x - mine;
+#pragma unroll
+  for (int k = 0; k < W; ++k)
+    if (k < w) base += wsum[k];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int d = threadIdx.x * kPer + k;
+    if (d < bins) {
+      uint32_t s = base + before[k];
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        const uint32_t c = cnt[u][d];
+        cnt[u][d] = s;
+        s += c;
+      }
+    }
+    base += total[k];
   }
   __syncthreads();
-  uint32_t s = a.counts[static_cast<int64_t>(threadIdx.x) * a.tiles + blockIdx.x];
-#pragma unroll
-  for (int k = 0; k < W; ++k) {
-    const uint32_t c = cnt[k][threadIdx.x];
-    cnt[k][threadIdx.x] = s;
-    s += c;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kShare / 64; ++k) {
-    const int64_t i = s0 + k * 64 + lane;
-    const bool live = i < a.N;
-    const uint32_t d = (kx[k] >> shift) & 255u;
-    const uint64_t m = same_digit(d, live);
+  for (int64_t i0 = s0; i0 < s1; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool live = i < s1;
+    const uint32_t kx = live ? load_key(a, src, i) : 0;
+    const uint32_t d = (kx >> shift) & (bins - 1);
+    const uint64_t m = same_digit(d, live, bits);
     const int below = lanes_below(m);
     const uint32_t at = cnt[w][d] + below;
     wave_sync();
     if (live && below == 0) cnt[w][d] += __popcll(m);
     wave_sync();
     if (live) {
-      a.keys[dst][at] = kx[k];
+      a.keys[dst][at] = kx;
       a.pos[dst][at] = src < 0 ? static_cast<uint32_t>(i) : a.pos[src][i];
+      // where a token's run begins: a minimum, whatever the order
+      if (last && a.first && kx < static_cast<uint32_t>(a.V)) atomicMin(a.first + kx, at);
     }
   }
 }
@@ -281,163 +297,238 @@ __global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int 
 // sums
 // ---------------------------------------------------------------------------
 
-// First sorted position of each token (0xffffffff: not there), for the form
-// that writes every row of dW.
-__global__ void __launch_bounds__(256) k_embed_clear(uint32_t* p, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) p[i] = 0xffffffffu;
+// x[0..P) = the P columns from `col` of the gradient at position i.
+template <class Tr, bool VEC>
+__device__ __forceinline__ void load_cols(const EmbedGradArgs& a, uint32_t i, int64_t col, float* x) {
+  const char* p = static_cast<const char*>(a.grad) + static_cast<int64_t>(i) * a.ld_g * Tr::kBytes;
+  if constexpr (VEC)
+    Tr::unpack(*reinterpret_cast<const u32x4*>(p + col * Tr::kBytes), x);
+  else
+    x[0] = Tr::load1(p, col);
 }
 
-__global__ void __launch_bounds__(256) k_embed_first(EmbedGradArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.N) return;
-  const uint32_t k = a.sorted_keys[i];
-  if (k < static_cast<uint32_t>(a.V) && (i == 0 || a.sorted_keys[i - 1] != k)) a.first[k] = static_cast<uint32_t>(i);
-}
-
-// acc[0..P) += the P columns from `col` of the gradients at sorted positions
-// [i0, i1), in that order.
+// acc[0..P) += the gradients at sorted positions [i0, i1), in that order, kAhead
+// rows in flight.
 template <class Tr, bool VEC>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int64_t i0, int64_t i1, int64_t col) {
-  constexpr int P = VEC ? Tr::kPerVec : 1;
+  constexpr int P = VEC ? Tr::kPerVec : 1, kAhead = 8;
   int64_t i = i0;
-  for (; i + 4 <= i1; i += 4) {
-    float x[4][P];
+  for (; i + kAhead <= i1; i += kAhead) {
+    float x[kAhead][P];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const char* p = static_cast<const char*>(a.grad) + static_cast<int64_t>(a.sorted_pos[i + u]) * a.ld_g * Tr::kBytes;
-      if constexpr (VEC)
-        Tr::unpack(*reinterpret_cast<const u32x4*>(p + col * Tr::kBytes), x[u]);
-      else
-        x[u][0] = Tr::load1(p, col);
-    }
+    for (int u = 0; u < kAhead; ++u) load_cols<Tr, VEC>(a, a.sorted_pos[i + u], col, x[u]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll
       for (int k = 0; k < P; ++k) acc[k] += x[u][k];
   }
   for (; i < i1; ++i) {
     float x[P];
-    const char* p = static_cast<const char*>(a.grad) + static_cast<int64_t>(a.sorted_pos[i]) * a.ld_g * Tr::kBytes;
-    if constexpr (VEC)
-      Tr::unpack(*reinterpret_cast<const u32x4*>(p + col * Tr::kBytes), x);
-    else
-      x[0] = Tr::load1(p, col);
+    load_cols<Tr, VEC>(a, a.sorted_pos[i], col, x);
 #pragma unroll
     for (int k = 0; k < P; ++k) acc[k] += x[k];
   }
 }
 
-// Partial rows of the whole blocks that hold one token.
-template <class Tr, bool VEC, int NT>
-__global__ void __launch_bounds__(NT) k_embed_partial(EmbedGradArgs a) {
-  constexpr int P = VEC ? Tr::kPerVec : 1;
-  const int64_t c = blockIdx.x / a.col_blocks + a.row0;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * NT + threadIdx.x) * P;
-  const uint32_t k = a.sorted_keys[c * kChunk];
-  if (k == static_cast<uint32_t>(a.V) || a.sorted_keys[c * kChunk + kChunk - 1] != k || col >= a.h) return;
-  float acc[P];
+// Stores the P columns of a finished row of dW.
+template <int P, bool ACC>
+__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t v, int64_t col, const float* acc) {
+  float* out = a.grad_weight + static_cast<int64_t>(v) * a.h + col;
+  if constexpr (P % 4 == 0) {
 #pragma unroll
-  for (int j = 0; j < P; ++j) acc[j] = 0.f;
-  add_rows<Tr, VEC>(a, acc, c * kChunk, (c + 1) * kChunk, col);
-  float* out = a.partial + c * a.h + col;
+    for (int j = 0; j < P; j += 4) {
+      f32x4_a4 x{acc[j] * a.scale, acc[j + 1] * a.scale, acc[j + 2] * a.scale, acc[j + 3] * a.scale};
+      f32x4_a4* q = reinterpret_cast<f32x4_a4*>(out + j);
+      *q = ACC ? *q + x : x;
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < P; ++j)
-    if (col + j < a.h) out[j] = acc[j];
+    for (int j = 0; j < P; ++j) out[j] = ACC ? out[j] + acc[j] * a.scale : acc[j] * a.scale;
+  }
 }
 
-// One workgroup per row of dW and column block.  ACC: the rows that some
-// position names, found as run starts; otherwise every row.
-template <class Tr, bool VEC, bool ACC, int NT>
-__global__ void __launch_bounds__(NT) k_embed_rows(EmbedGradArgs a) {
+// Workgroups [0, parts): partial rows of the whole blocks that hold one token.
+// The others: zeros in the rows that no token names, fill_rows rows each.
+template <class Tr, bool VEC>
+__global__ void __launch_bounds__(kSumNT) k_embed_partial(EmbedGradArgs a) {
   constexpr int P = VEC ? Tr::kPerVec : 1;
-  const int64_t b = blockIdx.x / a.col_blocks + a.row0;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * NT + threadIdx.x) * P;
-  int64_t i = b;
-  uint32_t v;
-  if (ACC) {
-    v = a.sorted_keys[i];
-    if (v == static_cast<uint32_t>(a.V) || (i > 0 && a.sorted_keys[i - 1] == v)) return;
-  } else {
-    v = static_cast<uint32_t>(b);
-    const uint32_t f = a.first[b];
-    i = f == 0xffffffffu ? a.N : f;
+  if (blockIdx.x < a.parts) {
+    const int64_t c = blockIdx.x / a.col_blocks + a.row0;
+    const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
+    const uint32_t k = a.sorted_keys[c * kChunk];
+    if (k == static_cast<uint32_t>(a.V) || a.sorted_keys[c * kChunk + kChunk - 1] != k || col >= a.h) return;
+    float acc[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) acc[j] = 0.f;
+    add_rows<Tr, VEC>(a, acc, c * kChunk, (c + 1) * kChunk, col);
+    float* out = a.partial + c * a.h + col;
+#pragma unroll
+    for (int j = 0; j < P; ++j) out[j] = acc[j];
+    return;
   }
-  // end of the run: the next 64 positions, then ever finer 64ths of the rest
-  // (keys are sorted, so the run's positions come first in every sample)
-  int64_t e = i, rest = a.N - i, step = 1;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x - a.parts) * a.fill_rows;
+  for (int r = 0; r < a.fill_rows; ++r) {
+    const int64_t v = v0 + r;
+    if (v >= a.V) return;
+    if (a.first[v] != kAbsent) continue;
+    float* out = a.grad_weight + v * a.h;
+    int j = threadIdx.x * 4;
+    for (; j + 4 <= a.h; j += kSumNT * 4)
+      __builtin_nontemporal_store((f32x4_a4{0.f, 0.f, 0.f, 0.f}), reinterpret_cast<f32x4_a4*>(out + j));
+    for (; j < a.h; ++j) out[j] = 0.f;  // the last, short group of one lane
+  }
+}
+
+// Rows of dW that some token names: a workgroup owns the runs that start in
+// its kRunSpan sorted positions, for one block of columns.
+template <class Tr, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
+  constexpr int P = VEC ? Tr::kPerVec : 1;
+  const int64_t p0 = (blockIdx.x / a.col_blocks + a.row0) * kRunSpan;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
   const int lane = threadIdx.x & 63;
-  while (rest > 0) {
-    const bool in = (lane + 1) * step <= rest && a.sorted_keys[e + (lane + 1) * step - 1] == v;
-    const uint64_t m = __ballot(in);
-    const int full = ~m ? __builtin_ctzll(~m) : 64;
-    e += full * step;
-    rest -= full * step;
-    if (step > 1) {
-      // the end lies within the next step
-      rest = rest < step - 1 ? rest : step - 1;
-      step = (rest + 63) / 64;
+  const int64_t p = p0 + lane;
+  const bool there = lane < kRunSpan && p < a.N;
+  const uint32_t key = there ? a.sorted_keys[p] : 0;
+  const bool start = there && key != static_cast<uint32_t>(a.V) && (p == 0 || a.sorted_keys[p - 1] != key);
+  const uint64_t ends = __ballot(there && (p == 0 || a.sorted_keys[p - 1] != key));  // also the unknown ids' start
+  for (uint64_t todo = __ballot(start); todo; todo &= todo - 1) {
+    const int at = __builtin_ctzll(todo);
+    const uint32_t v = __shfl(key, at, 64);
+    const int64_t i = p0 + at;
+    const uint64_t later = at < 63 ? ends >> (at + 1) : 0;
+    int64_t e;
+    if (later) {
+      e = i + 1 + __builtin_ctzll(later);
     } else {
-      if (full < 64) break;
-      step = (rest + 63) / 64;
+      // end of the run: the next 64 positions, then ever finer 64ths of the
+      // rest (keys are sorted, so the run's positions come first in a sample)
+      e = i;
+      int64_t rest = a.N - i, step = 1;
+      while (rest > 0) {
+        const bool in = (lane + 1) * step <= rest && a.sorted_keys[e + (lane + 1) * step - 1] == v;
+        const uint64_t m = __ballot(in);
+        const int full = ~m ? __builtin_ctzll(~m) : 64;
+        e += full * step;
+        rest -= full * step;
+        if (step > 1) {
+          rest = rest < step - 1 ? rest : step - 1;  // the end lies within the next step
+        } else if (full < 64) {
+          break;
+        }
+        step = (rest + 63) / 64;
+      }
     }
-  }
-  if (col >= a.h) return;
-  float acc[P];
+    if (col >= a.h) continue;
+    float acc[P];
 #pragma unroll
-  for (int j = 0; j < P; ++j) acc[j] = 0.f;
-  const int64_t c0 = (i + kChunk - 1) / kChunk, c1 = e / kChunk;
-  if (c0 < c1) {
-    add_rows<Tr, VEC>(a, acc, i, c0 * kChunk, col);
-    for (int64_t c = c0; c < c1; ++c) {
-      const float* p = a.partial + c * a.h + col;
+    for (int j = 0; j < P; ++j) acc[j] = 0.f;
+    const int64_t c0 = (i + kChunk - 1) / kChunk, c1 = e / kChunk;
+    if (c0 < c1) {
+      add_rows<Tr, VEC>(a, acc, i, c0 * kChunk, col);
+      for (int64_t c = c0; c < c1; ++c) {
+        const float* q = a.partial + c * a.h + col;
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-        if (col + j < a.h) acc[j] += p[j];
+        for (int j = 0; j < P; ++j) acc[j] += q[j];
+      }
+      add_rows<Tr, VEC>(a, acc, c1 * kChunk, e, col);
+    } else {
+      add_rows<Tr, VEC>(a, acc, i, e, col);
     }
-    add_rows<Tr, VEC>(a, acc, c1 * kChunk, e, col);
-  } else {
-    add_rows<Tr, VEC>(a, acc, i, e, col);
+    store_row<P, ACC>(a, v, col, acc);
   }
-  float* out = a.grad_weight + static_cast<int64_t>(v) * a.h + col;
+}
+
+// Up to kTinyN positions, unsorted.  ACC: a workgroup per position, which
+// owns the row of its token if no earlier position has it.  Otherwise a
+// workgroup per `rows` rows of dW.  A wave holds all tokens in its lanes.
+template <class Tr, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows) {
+  constexpr int P = VEC ? Tr::kPerVec : 1, K = kTinyN / 64;
+  const int lane = threadIdx.x & 63;
+  uint32_t key[K];
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    if (col + j < a.h) {
-      const float x = acc[j] * a.scale;
-      out[j] = ACC ? out[j] + x : x;
+  for (int k = 0; k < K; ++k) key[k] = k * 64 + lane < a.N ? key_of(a, k * 64 + lane) : static_cast<uint32_t>(a.V);
+  for (int r = 0; r < rows; ++r) {
+    int64_t v = static_cast<int64_t>(blockIdx.x) * rows + r;
+    if (ACC) {
+      const int i = static_cast<int>(blockIdx.x);
+      v = key_of(a, i);
+      if (v == a.V) return;
+      bool earlier = false;
+#pragma unroll
+      for (int k = 0; k < K; ++k) earlier |= k * 64 + lane < i && key[k] == static_cast<uint32_t>(v);
+      if (__any(earlier)) return;
+    } else if (v >= a.V) {
+      return;
+    }
+    uint64_t hit[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) hit[k] = __ballot(key[k] == static_cast<uint32_t>(v));
+    for (int64_t col = static_cast<int64_t>(threadIdx.x) * P; col < a.h; col += kSumNT * P) {
+      float acc[P];
+#pragma unroll
+      for (int j = 0; j < P; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        for (uint64_t m = hit[k]; m; m &= m - 1) {
+          float x[P];
+          load_cols<Tr, VEC>(a, k * 64 + __builtin_ctzll(m), col, x);
+#pragma unroll
+          for (int j = 0; j < P; ++j) acc[j] += x[j];
+        }
+      }
+      store_row<P, ACC>(a, static_cast<uint32_t>(v), col, acc);
     }
   }
 }
 
 template <class Tr, bool VEC>
+hipError_t launch_tiny(const EmbedGradArgs& a, hipStream_t s) {
+  TimedLaunch tl("k_embedding_grad", s);
+  if (a.accumulate) {
+    hipLaunchKernelGGL((k_embed_tiny<Tr, VEC, true>), dim3(static_cast<unsigned>(a.N)), dim3(kSumNT), 0, s, a, 1);
+  } else {
+    // several rows a workgroup once there are workgroups enough to fill the chip
+    int rows = a.V / 4096;
+    rows = rows < 1 ? 1 : rows > 64 ? 64 : rows;
+    hipLaunchKernelGGL((k_embed_tiny<Tr, VEC, false>), dim3((a.V + rows - 1) / rows), dim3(kSumNT), 0, s, a, rows);
+  }
+  return hipGetLastError();
+}
+
+template <class Tr, bool VEC>
 hipError_t launch_sums(EmbedGradArgs a, hipStream_t s) {
-  constexpr int NT = 128;
   constexpr int P = VEC ? Tr::kPerVec : 1;
-  a.col_blocks = static_cast<int>((a.h + int64_t(NT) * P - 1) / (int64_t(NT) * P));
+  a.col_blocks = static_cast<int>((a.h + int64_t(kSumNT) * P - 1) / (int64_t(kSumNT) * P));
   TimedLaunch tl("k_embedding_grad", s);
   // workgroups per launch: far below 2^32 work-items
   const int64_t per = (int64_t(1) << 23) / a.col_blocks;
-  const int64_t chunks = a.N / kChunk;
-  for (int64_t r0 = 0; r0 < chunks; r0 += per) {
-    a.row0 = r0;
+  a.fill_rows = 16 > a.V >> 22 ? 16 : a.V >> 22;
+  const int64_t chunks = a.N / kChunk, fills = a.accumulate ? 0 : (int64_t(a.V) + a.fill_rows - 1) / a.fill_rows;
+  for (int64_t r0 = 0; r0 == 0 || r0 < chunks; r0 += per) {
     const int64_t n = chunks - r0 < per ? chunks - r0 : per;
-    hipLaunchKernelGGL((k_embed_partial<Tr, VEC, NT>), dim3(static_cast<unsigned>(n * a.col_blocks)), dim3(NT), 0, s, a);
+    const int64_t more = r0 + n == chunks ? fills : 0;
+    a.row0 = r0;
+    a.parts = static_cast<unsigned>(n * a.col_blocks);
+    if (a.parts + more > 0)
+      hipLaunchKernelGGL((k_embed_partial<Tr, VEC>), dim3(static_cast<unsigned>(a.parts + more)), dim3(kSumNT), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t rows = a.accumulate ? a.N : a.V;
-  for (int64_t r0 = 0; r0 < rows; r0 += per) {
+  const int64_t spans = (a.N + kRunSpan - 1) / kRunSpan;
+  for (int64_t r0 = 0; r0 < spans; r0 += per) {
     a.row0 = r0;
-    const int64_t n = rows - r0 < per ? rows - r0 : per;
+    const int64_t n = spans - r0 < per ? spans - r0 : per;
     const dim3 g(static_cast<unsigned>(n * a.col_blocks));
     if (a.accumulate)
-      hipLaunchKernelGGL((k_embed_rows<Tr, VEC, true, NT>), g, dim3(NT), 0, s, a);
+      hipLaunchKernelGGL((k_embed_runs<Tr, VEC, true>), g, dim3(kSumNT), 0, s, a);
     else
-      hipLaunchKernelGGL((k_embed_rows<Tr, VEC, false, NT>), g, dim3(NT), 0, s, a);
+      hipLaunchKernelGGL((k_embed_runs<Tr, VEC, false>), g, dim3(kSumNT), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 template <class Tr>
@@ -445,7 +536,16 @@ hipError_t launch_sums_t(const EmbedGradArgs& a, hipStream_t s) {
   // 16-byte loads need every gradient row on the 16-byte grid and whole vectors
   const bool vec = reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 && (a.ld_g * Tr::kBytes) % 16 == 0 &&
                    a.h % Tr::kPerVec == 0;
+  if (a.N <= kTinyN) return vec ? launch_tiny<Tr, true>(a, s) : launch_tiny<Tr, false>(a, s);
   return vec ? launch_sums<Tr, true>(a, s) : launch_sums<Tr, false>(a, s);
+}
+
+// Sorting tiles: 512 positions at least, kMaxTiles tiles at most.
+void set_tiles(EmbedGradArgs& a) {
+  int64_t n = (a.N + 511) / 512;
+  n = n < 1 ? 1 : n < kMaxTiles ? n : kMaxTiles;
+  a.tile = ((a.N + n - 1) / n + 255) / 256 * 256;
+  a.tiles = static_cast<int>((a.N + a.tile - 1) / a.tile);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -455,7 +555,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 bool embedding_workspace_layout(int64_t N, int64_t h, int64_t V, EmbedWorkspace* w) {
   // positions are 32-bit; 2^31 keeps tile and block counts far below 2^32
   if (N < 0 || N > 0x7fffffff || h <= 0 || h > (int64_t(1) << 30) || V <= 0 || V > (int64_t(1) << 30)) return false;
-  const size_t n = static_cast<size_t>(N), tiles = (n + kSortTile - 1) / kSortTile;
+  const size_t n = static_cast<size_t>(N);
   size_t off = 0;
   for (int k = 0; k < 2; ++k) {
     w->keys_off[k] = off;
@@ -464,7 +564,7 @@ bool embedding_workspace_layout(int64_t N, int64_t h, int64_t V, EmbedWorkspace*
     off += round256(n * 4);
   }
   w->counts_off = off;
-  off += round256(tiles * 256 * 4);
+  off += round256(size_t(kMaxTiles) * (1 << kMaxDigit) * 4);
   w->first_off = off;
   off += round256(static_cast<size_t>(V) * 4);
   w->partial_off = off;
@@ -494,38 +594,30 @@ hipError_t launch_embedding_backward(int dtype, const EmbedGradArgs& args, char*
     a.pos[k] = reinterpret_cast<uint32_t*>(ws + w.pos_off[k]);
   }
   a.counts = reinterpret_cast<uint32_t*>(ws + w.counts_off);
-  a.first = reinterpret_cast<uint32_t*>(ws + w.first_off);
+  a.first = a.accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + w.first_off);
   a.partial = reinterpret_cast<float*>(ws + w.partial_off);
-  a.tiles = static_cast<int>((a.N + kSortTile - 1) / kSortTile);
+  set_tiles(a);
   a.key_bits = 0;
   while ((static_cast<int64_t>(a.V) >> a.key_bits) != 0) ++a.key_bits;  // V itself is the key of unknown ids
   hipError_t e;
   int last = 0;
-  if (a.N <= kSmallN) {
+  if (a.N > kSmallN) {
+    TimedLaunch tl("k_embedding_sort", s);
+    const int passes = (a.key_bits + kMaxDigit - 1) / kMaxDigit, bits = (a.key_bits + passes - 1) / passes;
+    for (int k = 0, src = -1; k < passes; ++k, src = last) {
+      last = src == 0 ? 1 : 0;
+      hipLaunchKernelGGL(k_embed_count, dim3(a.tiles), dim3(kSortNT), 0, s, a, k * bits, bits, src);
+      hipLaunchKernelGGL(k_embed_scatter, dim3(a.tiles), dim3(kSortNT), 0, s, a, k * bits, bits, src, last,
+                         k + 1 == passes);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  } else if (a.N > kTinyN) {
     TimedLaunch tl("k_embedding_sort", s);
     hipLaunchKernelGGL(k_embed_sort_small, dim3(1), dim3(kSmallNT), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-  } else {
-    TimedLaunch tl("k_embedding_sort", s);
-    int src = -1;
-    for (int shift = 0; shift < a.key_bits; shift += 8) {
-      last = src == 0 ? 1 : 0;
-      hipLaunchKernelGGL(k_embed_count, dim3(a.tiles), dim3(kSortNT), 0, s, a, shift, src);
-      hipLaunchKernelGGL(k_embed_scan, dim3(1), dim3(1024), 0, s, a);
-      hipLaunchKernelGGL(k_embed_scatter, dim3(a.tiles), dim3(kSortNT), 0, s, a, shift, src, last);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      src = last;
-    }
   }
   a.sorted_keys = a.keys[last];
   a.sorted_pos = a.pos[last];
-  if (!a.accumulate) {
-    hipLaunchKernelGGL(k_embed_clear, dim3(static_cast<unsigned>((a.V + 255) / 256)), dim3(256), 0, s, a.first,
-                       static_cast<int64_t>(a.V));
-    if (a.N > 0)
-      hipLaunchKernelGGL(k_embed_first, dim3(static_cast<unsigned>((a.N + 255) / 256)), dim3(256), 0, s, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   switch (dtype) {
     case 0: return launch_sums_t<Bf16>(a, s);
     case 1: return launch_sums_t<Fp16>(a, s);

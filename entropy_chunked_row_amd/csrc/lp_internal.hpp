@@ -157,12 +157,15 @@ struct EmbedGradArgs {
   // set by the launcher
   uint32_t* keys[2];
   uint32_t* pos[2];
-  uint32_t* counts;  // [256 x tiles]
-  uint32_t* first;   // [V]
+  uint32_t* counts;  // [tiles x digits]
+  uint32_t* first;   // [V] first sorted position of a token, or null (accumulate)
   float* partial;    // [N / 64 x h]
   const uint32_t* sorted_keys;
   const uint32_t* sorted_pos;
+  int64_t tile;  // positions per sorting workgroup
   int tiles, key_bits, col_blocks;
+  unsigned parts;  // workgroups that sum partial rows
+  int fill_rows;   // rows of dW per workgroup that writes zeros
   int64_t row0;
 };
 

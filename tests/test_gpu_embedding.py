@@ -82,7 +82,8 @@ def _check_grad(got, G, tok, V, scale, base=None):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,h,V,skew,extra", [
     (1, 1, 1, False, 0), (1, 40, 300, False, 0), (64, 256, 1024, False, 0), (63, 7, 5, True, 0), (65, 8, 2, True, 0),
-    (1000, 1031, 300, True, 0), (257, 64, 70000, False, 0), (4096, 24, 500, True, 0), (4097, 24, 500, True, 0),
+    (1000, 1031, 300, True, 0), (256, 40, 60, True, 0), (255, 12, 70000, False, 1), (300, 2, 9000, False, 0),
+    (257, 64, 70000, False, 0), (4096, 24, 500, True, 0), (4097, 24, 500, True, 0),
     (6000, 33, 66000, False, 3), (9001, 16, 3, True, 8), (20000, 8, 257, True, 0), (5000, 4, 17000000, False, 0)])
 def test_gradient(dtype, N, h, V, skew, extra):
     torch = _torch()
