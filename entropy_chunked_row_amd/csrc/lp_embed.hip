@@ -120,7 +120,6 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
   }
   if (a.first) {
     for (int v = tid; v < a.V; v += kSmallNT) a.first[v] = kAbsent;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
   const int share = ((n + W - 1) / W + 63) / 64 * 64;
   const int i0 = w * share, i1 = i0 + share < n ? i0 + share : n;
@@ -187,8 +186,6 @@ __global__ void __launch_bounds__(kSmallNT) k_embed_sort_small(EmbedGradArgs a) 
     const uint32_t k = key[cur][i];
     a.keys[0][i] = k;
     a.pos[0][i] = pos[cur][i];
-    // the clearing stores above were waited for at the barriers since
-    if (a.first && k < static_cast<uint32_t>(a.V) && (i == 0 || key[cur][i - 1] != k)) a.first[k] = i;
   }
 }
 
@@ -215,8 +212,7 @@ __global__ void __launch_bounds__(kSortNT) k_embed_count(EmbedGradArgs a, int sh
   for (int d = threadIdx.x; d < bins; d += kSortNT) a.counts[static_cast<int64_t>(blockIdx.x) * bins + d] = cnt[d];
 }
 
-__global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int shift, int bits, int src, int dst,
-                                                           bool last) {
+__global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int shift, int bits, int src, int dst) {
   constexpr int W = kSortNT / 64, kPer = (1 << kMaxDigit) / kSortNT;
   __shared__ uint32_t cnt[W][1 << kMaxDigit];
   __shared__ uint32_t wsum[W];
@@ -235,13 +231,18 @@ __global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int 
   uint32_t before[kPer], total[kPer], mine = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) before[k] = total[k] = 0;
-  for (int t = 0; t < a.tiles; ++t) {
+  static_assert(kPer == 4, "a thread's digits are one 16-byte load");
+  if (static_cast<int>(threadIdx.x) * kPer < bins) {  // bins is a multiple of 4
+    const uint32_t* p = a.counts + threadIdx.x * kPer;
+#pragma unroll 16
+    for (int t = 0; t < a.tiles; ++t) {
+      const u32x4 c = *reinterpret_cast<const u32x4*>(p + static_cast<int64_t>(t) * bins);
+      const uint32_t on = t < static_cast<int>(blockIdx.x) ? ~0u : 0u;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int d = threadIdx.x * kPer + k;
-      const uint32_t c = d < bins ? a.counts[static_cast<int64_t>(t) * bins + d] : 0;
-      total[k] += c;
-      if (t < static_cast<int>(blockIdx.x)) before[k] += c;
+      for (int k = 0; k < kPer; ++k) {
+        total[k] += c[k];
+        before[k] += c[k] & on;
+      }
     }
   }
 #pragma unroll
@@ -287,8 +288,6 @@ __global__ void __launch_bounds__(kSortNT) k_embed_scatter(EmbedGradArgs a, int 
     if (live) {
       a.keys[dst][at] = kx;
       a.pos[dst][at] = src < 0 ? static_cast<uint32_t>(i) : a.pos[src][i];
-      // where a token's run begins: a minimum, whatever the order
-      if (last && a.first && kx < static_cast<uint32_t>(a.V)) atomicMin(a.first + kx, at);
     }
   }
 }
@@ -309,9 +308,9 @@ __device__ __forceinline__ void load_cols(const EmbedGradArgs& a, uint32_t i, in
 
 // acc[0..P) += the gradients at sorted positions [i0, i1), in that order, kAhead
 // rows in flight.
-template <class Tr, bool VEC>
+template <class Tr, bool VEC, int kAhead>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int64_t i0, int64_t i1, int64_t col) {
-  constexpr int P = VEC ? Tr::kPerVec : 1, kAhead = 8;
+  constexpr int P = VEC ? Tr::kPerVec : 1;
   int64_t i = i0;
   for (; i + kAhead <= i1; i += kAhead) {
     float x[kAhead][P];
@@ -347,43 +346,57 @@ __device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t v, in
   }
 }
 
-// Workgroups [0, parts): partial rows of the whole blocks that hold one token.
-// The others: zeros in the rows that no token names, fill_rows rows each.
+// Workgroups below `parts`: partial rows of the whole blocks that hold one
+// token.  The others note where each token's run begins.
 template <class Tr, bool VEC>
 __global__ void __launch_bounds__(kSumNT) k_embed_partial(EmbedGradArgs a) {
   constexpr int P = VEC ? Tr::kPerVec : 1;
-  if (blockIdx.x < a.parts) {
-    const int64_t c = blockIdx.x / a.col_blocks + a.row0;
-    const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
-    const uint32_t k = a.sorted_keys[c * kChunk];
-    if (k == static_cast<uint32_t>(a.V) || a.sorted_keys[c * kChunk + kChunk - 1] != k || col >= a.h) return;
-    float acc[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) acc[j] = 0.f;
-    add_rows<Tr, VEC>(a, acc, c * kChunk, (c + 1) * kChunk, col);
-    float* out = a.partial + c * a.h + col;
-#pragma unroll
-    for (int j = 0; j < P; ++j) out[j] = acc[j];
+  if (blockIdx.x >= a.parts) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x - a.parts) * kSumNT + threadIdx.x;
+    if (i < a.N) {
+      const uint32_t k = a.sorted_keys[i];
+      if (k != static_cast<uint32_t>(a.V) && (i == 0 || a.sorted_keys[i - 1] != k)) a.first[k] = static_cast<uint32_t>(i);
+    }
     return;
   }
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x - a.parts) * a.fill_rows;
-  for (int r = 0; r < a.fill_rows; ++r) {
-    const int64_t v = v0 + r;
-    if (v >= a.V) return;
-    if (a.first[v] != kAbsent) continue;
-    float* out = a.grad_weight + v * a.h;
-    int j = threadIdx.x * 4;
-    for (; j + 4 <= a.h; j += kSumNT * 4)
-      __builtin_nontemporal_store((f32x4_a4{0.f, 0.f, 0.f, 0.f}), reinterpret_cast<f32x4_a4*>(out + j));
-    for (; j < a.h; ++j) out[j] = 0.f;  // the last, short group of one lane
+  const int64_t c = blockIdx.x / a.col_blocks + a.row0;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
+  const uint32_t k = a.sorted_keys[c * kChunk];
+  if (k == static_cast<uint32_t>(a.V) || a.sorted_keys[c * kChunk + kChunk - 1] != k || col >= a.h) return;
+  float acc[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) acc[j] = 0.f;
+  add_rows<Tr, VEC, 16>(a, acc, c * kChunk, (c + 1) * kChunk, col);
+  float* out = a.partial + c * a.h + col;
+#pragma unroll
+  for (int j = 0; j < P; ++j) out[j] = acc[j];
+}
+
+// Zeros in the rows of dW that no token names.
+__device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t block) {
+  const int64_t v0 = block * a.fill_rows;
+  const int lane = threadIdx.x & 63;
+  for (int r0 = 0; r0 < a.fill_rows; r0 += 64) {
+    const int64_t v = v0 + r0 + lane;
+    uint64_t todo = __ballot(r0 + lane < a.fill_rows && v < a.V && a.first[v] == kAbsent);
+    for (; todo; todo &= todo - 1) {
+      float* out = a.grad_weight + (v0 + r0 + __builtin_ctzll(todo)) * a.h;
+      int j = threadIdx.x * 4;
+      for (; j + 4 <= a.h; j += kSumNT * 4)
+        *reinterpret_cast<f32x4_a4*>(out + j) = f32x4_a4{0.f, 0.f, 0.f, 0.f};
+      for (; j < a.h; ++j) out[j] = 0.f;  // the last, short group of one lane
+    }
   }
 }
 
 // Rows of dW that some token names: a workgroup owns the runs that start in
-// its kRunSpan sorted positions, for one block of columns.
+// its kRunSpan sorted positions, for one block of columns.  Workgroups from
+// `parts` on write zeros instead: their stores keep the memory busy while the
+// others wait for theirs.
 template <class Tr, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
   constexpr int P = VEC ? Tr::kPerVec : 1;
+  if (!ACC && blockIdx.x >= a.parts) return fill_rows(a, blockIdx.x - a.parts);
   const int64_t p0 = (blockIdx.x / a.col_blocks + a.row0) * kRunSpan;
   const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
   const int lane = threadIdx.x & 63;
@@ -425,15 +438,15 @@ __global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
     for (int j = 0; j < P; ++j) acc[j] = 0.f;
     const int64_t c0 = (i + kChunk - 1) / kChunk, c1 = e / kChunk;
     if (c0 < c1) {
-      add_rows<Tr, VEC>(a, acc, i, c0 * kChunk, col);
+      add_rows<Tr, VEC, 8>(a, acc, i, c0 * kChunk, col);
       for (int64_t c = c0; c < c1; ++c) {
         const float* q = a.partial + c * a.h + col;
 #pragma unroll
         for (int j = 0; j < P; ++j) acc[j] += q[j];
       }
-      add_rows<Tr, VEC>(a, acc, c1 * kChunk, e, col);
+      add_rows<Tr, VEC, 8>(a, acc, c1 * kChunk, e, col);
     } else {
-      add_rows<Tr, VEC>(a, acc, i, e, col);
+      add_rows<Tr, VEC, 8>(a, acc, i, e, col);
     }
     store_row<P, ACC>(a, v, col, acc);
   }
@@ -506,13 +519,12 @@ hipError_t launch_sums(EmbedGradArgs a, hipStream_t s) {
   const int64_t per = (int64_t(1) << 23) / a.col_blocks;
   a.fill_rows = 16 > a.V >> 22 ? 16 : a.V >> 22;
   const int64_t chunks = a.N / kChunk, fills = a.accumulate ? 0 : (int64_t(a.V) + a.fill_rows - 1) / a.fill_rows;
-  for (int64_t r0 = 0; r0 == 0 || r0 < chunks; r0 += per) {
-    const int64_t n = chunks - r0 < per ? chunks - r0 : per;
-    const int64_t more = r0 + n == chunks ? fills : 0;
+  for (int64_t r0 = 0; r0 < chunks; r0 += per) {
     a.row0 = r0;
+    const int64_t n = chunks - r0 < per ? chunks - r0 : per;
     a.parts = static_cast<unsigned>(n * a.col_blocks);
-    if (a.parts + more > 0)
-      hipLaunchKernelGGL((k_embed_partial<Tr, VEC>), dim3(static_cast<unsigned>(a.parts + more)), dim3(kSumNT), 0, s, a);
+    const int64_t more = a.first && r0 + n == chunks ? (a.N + kSumNT - 1) / kSumNT : 0;
+    hipLaunchKernelGGL((k_embed_partial<Tr, VEC>), dim3(static_cast<unsigned>(a.parts + more)), dim3(kSumNT), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -520,7 +532,8 @@ hipError_t launch_sums(EmbedGradArgs a, hipStream_t s) {
   for (int64_t r0 = 0; r0 < spans; r0 += per) {
     a.row0 = r0;
     const int64_t n = spans - r0 < per ? spans - r0 : per;
-    const dim3 g(static_cast<unsigned>(n * a.col_blocks));
+    a.parts = static_cast<unsigned>(n * a.col_blocks);
+    const dim3 g(static_cast<unsigned>(a.parts + (r0 + n == spans ? fills : 0)));
     if (a.accumulate)
       hipLaunchKernelGGL((k_embed_runs<Tr, VEC, true>), g, dim3(kSumNT), 0, s, a);
     else
@@ -603,12 +616,12 @@ hipError_t launch_embedding_backward(int dtype, const EmbedGradArgs& args, char*
   int last = 0;
   if (a.N > kSmallN) {
     TimedLaunch tl("k_embedding_sort", s);
-    const int passes = (a.key_bits + kMaxDigit - 1) / kMaxDigit, bits = (a.key_bits + passes - 1) / passes;
+    const int passes = (a.key_bits + kMaxDigit - 1) / kMaxDigit, least = (a.key_bits + passes - 1) / passes;
+    const int bits = least < 2 ? 2 : least;
     for (int k = 0, src = -1; k < passes; ++k, src = last) {
       last = src == 0 ? 1 : 0;
       hipLaunchKernelGGL(k_embed_count, dim3(a.tiles), dim3(kSortNT), 0, s, a, k * bits, bits, src);
-      hipLaunchKernelGGL(k_embed_scatter, dim3(a.tiles), dim3(kSortNT), 0, s, a, k * bits, bits, src, last,
-                         k + 1 == passes);
+      hipLaunchKernelGGL(k_embed_scatter, dim3(a.tiles), dim3(kSortNT), 0, s, a, k * bits, bits, src, last);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   } else if (a.N > kTinyN) {

@@ -164,7 +164,7 @@ struct EmbedGradArgs {
   const uint32_t* sorted_pos;
   int64_t tile;  // positions per sorting workgroup
   int tiles, key_bits, col_blocks;
-  unsigned parts;  // workgroups that sum partial rows
+  unsigned parts;  // workgroups of a launch that sum; the others write zeros
   int fill_rows;   // rows of dW per workgroup that writes zeros
   int64_t row0;
 };
