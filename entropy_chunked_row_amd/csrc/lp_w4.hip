@@ -14,8 +14,12 @@
 //    the start value of its accumulator.
 //  * Nibbles s and s + 4 of a 32-bit word share a register, so x's columns take
 //    the order 0 4 1 5 2 6 3 7 within each 8 (a permutation of the sum).
-// A lane's 16 / 8 / 4 bytes (groups of 128 / 64 / 32) are cut so that each
-// MFMA stays inside one group, whose sum is then scaled once in fp32.
+// A lane loads 16 bytes, 32 columns of a row; the 4 x 4 words of a row's four
+// lanes are transposed in registers (v_permlane32_swap, v_permlane16_swap), so that one
+// MFMA takes 32 neighbouring columns and stays inside one group, whose sum is
+// then scaled in fp32.
+#include <type_traits>
+
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
@@ -63,10 +67,6 @@ __device__ __forceinline__ u32x4 order_x(u32x4 d) {
                __builtin_amdgcn_perm(d.w, d.y, 0x05040100u), __builtin_amdgcn_perm(d.w, d.y, 0x07060302u)};
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
-  return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
-}
-
 __device__ __forceinline__ void store_logit(void* out, int dtype, int64_t i, float x) {
   switch (dtype) {
     case 0: Bf16::store1(static_cast<char*>(out), i, x); break;
@@ -75,17 +75,43 @@ __device__ __forceinline__ void store_logit(void* out, int dtype, int64_t i, flo
   }
 }
 
+// w[a] of lane row q becomes w[q] of lane row a (lane rows: 16 lanes each).
+__device__ __forceinline__ u32x4 transpose_rows(u32x4 w) {
+  auto p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+  auto r = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+  auto lo = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
+  auto hi = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+template <int N>
+struct ScaleVec;  // N bf16 values at any 2-byte boundary
+template <>
+struct ScaleVec<2> {
+  typedef uint32_t type __attribute__((ext_vector_type(1), aligned(2)));
+};
+template <>
+struct ScaleVec<4> {
+  typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <>
+struct ScaleVec<8> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+};
+
+constexpr int kSpan = 256;  // columns a wave takes at a time: a row's 128-byte line
+
 // One workgroup: 16 RT vocabulary rows x 16 NT rows of x.  Its four waves take
-// every fourth chunk of 128 columns and add their sums through LDS at the end.
+// every fourth span of columns and add their sums through LDS at the end.
 template <class X, int G, int NT, int RT>
 __global__ void __launch_bounds__(256) k_w4_logits(W4Args a) {
-  constexpr int kGroups = 128 / G, kSteps = G / 32;  // per chunk, per group
+  constexpr int kGroups = kSpan / G, kSteps = G / 32;  // per span, per group
   __shared__ float sm[4][RT * 4][64];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, q = lane >> 4;
   const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64;
-  const int h = a.h, chunks = (h + 127) / 128;
+  const int h = a.h, spans = h / kSpan;  // whole ones; a last, short one follows
 
   // rows past the end repeat the last one: their results are not stored
   const char* wrow[RT];
@@ -113,68 +139,94 @@ __global__ void __launch_bounds__(256) k_w4_logits(W4Args a) {
 
   const u32x4 neg24{X::kNeg24, X::kNeg24, X::kNeg24, X::kNeg24};
 
-  struct Words {
-    uint32_t w[RT][kGroups][kSteps];
-    float s[RT][kGroups];
+  struct Span {
+    u32x4 w[RT][2];
+    uint32_t s[RT][kGroups / 2];
   };
-  auto load = [&](int c, Words& d) {
+  auto load = [&](int c, Span& d, auto whole) {
+    constexpr bool full = decltype(whole)::value;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      // a lane's G / 4 columns lie inside the head or past its end as a whole
-      int k = c * 128 + g * G + q * (G / 4);
-      k = k < h ? k : 0;
-      int sg = c * kGroups + g;
-      sg = sg * G < h ? sg : 0;
+    for (int r = 0; r < RT; ++r) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(wrow[r] + k / 2);
+      for (int f = 0; f < 2; ++f) {
+        // a lane's 32 columns lie inside the head or past its end as a whole
+        int k = c * kSpan + f * 128 + q * 32;
+        k = full || k < h ? k : 0;
+        d.w[r][f] = *reinterpret_cast<const u32x4*>(wrow[r] + k / 2);
+      }
+      if (full) {
+        const auto v = *reinterpret_cast<const typename ScaleVec<kGroups>::type*>(srow[r] + c * kGroups);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) d.w[r][g][i] = p[i];
-        d.s[r][g] = bf16_at(srow[r], sg);
+        for (int i = 0; i < kGroups / 2; ++i) d.s[r][i] = v[i];
+      } else {
+        const int last = (h - 1) / G;
+#pragma unroll
+        for (int i = 0; i < kGroups / 2; ++i) {
+          const int g0 = c * kGroups + 2 * i, g1 = g0 + 1;
+          d.s[r][i] = srow[r][g0 < last ? g0 : last] | static_cast<uint32_t>(srow[r][g1 < last ? g1 : last]) << 16;
+        }
       }
     }
   };
 
-  Words cur;
-  if (w < chunks) load(w, cur);
-  for (int c = w; c < chunks; c += 4) {
-    Words nxt;
-    if (c + 4 < chunks) load(c + 4, nxt);
+  auto add = [&](int c, const Span& cur, auto whole) {
+    constexpr bool full = decltype(whole)::value;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      u32x4 x[NT][kSteps];
+    for (int f = 0; f < 2; ++f) {
+      u32x4 x[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const int k = c * 128 + g * G + q * (G / 4) + i * 8;
-          u32x4 d{0, 0, 0, 0};
-          if (k < h) d = *reinterpret_cast<const u32x4*>(xrow[t] + k);
+        for (int i = 0; i < 4; ++i) {
+          const int k = c * kSpan + f * 128 + i * 32 + q * 8;
+          u32x4 d = *reinterpret_cast<const u32x4*>(xrow[t] + (full || k < h ? k : 0));
+          if (!full && k >= h) d = u32x4{0, 0, 0, 0};
           x[t][i] = order_x(d);
         }
-      f32x4 shift[NT];
+      u32x4 words[RT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        shift[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < RT; ++r) words[r] = transpose_rows(cur.w[r][f]);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) shift[t] = X::mfma(x[t][i], neg24, shift[t]);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        u32x4 b[kSteps];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) b[i] = widen_nibbles<X>(cur.w[r][g][i]);
+      for (int g = 0; g < 128 / G; ++g) {
+        f32x4 shift[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          f32x4 acc = shift[t];
+          shift[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) acc = X::mfma(x[t][i], b[i], acc);
+          for (int i = 0; i < kSteps; ++i) shift[t] = X::mfma(x[t][g * kSteps + i], neg24, shift[t]);
+        }
+        const int gs = f * (128 / G) + g;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tot[t][r][j] = fmaf(cur.s[r][g], acc[j], tot[t][r][j]);
+        for (int r = 0; r < RT; ++r) {
+          const uint32_t pair = cur.s[r][gs / 2];
+          const float sc = __uint_as_float(gs & 1 ? pair & 0xffff0000u : pair << 16);
+          u32x4 b[kSteps];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) b[i] = widen_nibbles<X>(words[r][g * kSteps + i]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            f32x4 acc = shift[t];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) acc = X::mfma(x[t][g * kSteps + i], b[i], acc);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tot[t][r][j] = fmaf(sc, acc[j], tot[t][r][j]);
+          }
         }
       }
     }
+  };
+
+  Span cur;
+  if (w < spans) load(w, cur, std::true_type());
+  for (int c = w; c < spans; c += 4) {
+    Span nxt;
+    if (c + 4 < spans) load(c + 4, nxt, std::true_type());
+    add(c, cur, std::true_type());
     cur = nxt;
+  }
+  if (spans * kSpan < h && (spans & 3) == w) {
+    load(spans, cur, std::false_type());
+    add(spans, cur, std::false_type());
   }
 
 #pragma unroll
