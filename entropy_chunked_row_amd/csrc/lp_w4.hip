@@ -14,12 +14,9 @@
 //    the start value of its accumulator.
 //  * Nibbles s and s + 4 of a 32-bit word share a register, so x's columns take
 //    the order 0 4 1 5 2 6 3 7 within each 8 (a permutation of the sum).
-// A lane loads 16 bytes, 32 columns of a row; the 4 x 4 words of a row's four
-// lanes are transposed in registers (v_permlane32_swap, v_permlane16_swap), so that one
-// MFMA takes 32 neighbouring columns and stays inside one group, whose sum is
-// then scaled in fp32.
-#include <type_traits>
-
+// A lane loads 16 bytes, 32 columns of a row, and lanes exchange words in
+// registers until each MFMA stays inside one group, whose sum is then scaled
+// in fp32.
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
@@ -48,15 +45,18 @@ struct XFp16 {
   }
 };
 
-// Eight nibbles as 16 + n, in the order 0 4 1 5 2 6 3 7.
+// Eight nibbles as 16 + n, in the order 0 4 1 5 2 6 3 7.  The and-or is
+// spelled out: with both constants as literals it would be two instructions.
 template <class X>
-__device__ __forceinline__ u32x4 widen_nibbles(uint32_t w) {
+__device__ __forceinline__ u32x4 widen_nibbles(uint32_t w, uint32_t base) {
   u32x4 r;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int sh = X::kBit - 4 * s;
     const uint32_t v = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
-    r[s] = (v & X::kMask) | X::kBase;
+    uint32_t o;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(o) : "v"(v), "s"(X::kMask), "v"(base));
+    r[s] = o;
   }
   return r;
 }
@@ -75,13 +75,27 @@ __device__ __forceinline__ void store_logit(void* out, int dtype, int64_t i, flo
   }
 }
 
-// w[a] of lane row q becomes w[q] of lane row a (lane rows: 16 lanes each).
-__device__ __forceinline__ u32x4 transpose_rows(u32x4 w) {
-  auto p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
-  auto r = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-  auto lo = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
-  auto hi = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
+// A lane row is 16 lanes; lane row q loads columns 32 q .. 32 q + 31 of a
+// chunk of 128 as four words.  words_of exchanges words between lane rows until each
+// word index i holds columns of one group only (none for groups of 128, one
+// exchange for 64, a full 4 x 4 transpose for 32); column_of is the first of
+// the eight columns that lane row q then holds in word i.
+template <int G>
+__device__ __forceinline__ u32x4 words_of(u32x4 w) {
+  if constexpr (G == 128) return w;
+  const auto p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+  const auto r = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+  if constexpr (G == 64) return u32x4{p[0], r[0], p[1], r[1]};
+  const auto lo = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
   return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+template <int G>
+__device__ __forceinline__ int column_of(int i, int q) {
+  if (G == 128) return 32 * q + 8 * i;
+  if (G == 64) return 64 * (i >> 1) + 32 * (q & 1) + 16 * (q >> 1) + 8 * (i & 1);
+  return 32 * i + 8 * q;
 }
 
 template <int N>
@@ -94,35 +108,183 @@ template <>
 struct ScaleVec<4> {
   typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
 };
-template <>
-struct ScaleVec<8> {
-  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+
+// Columns are taken in chunks of 128, and the chunks of a row fall into
+// kRanges ranges of equal length.  Every kernel adds a range's groups in order
+// and then the ranges in order, so a row's logits have the same bits
+// whichever kernel computes them.
+constexpr int kChunk = 128;
+constexpr int kRanges = 8;
+
+// Words and scales of a 16-row tile for one chunk.
+template <int G>
+struct Chunk {
+  static constexpr int kGroups = kChunk / G;
+  u32x4 w;
+  uint32_t s[(kGroups + 1) / 2];
+
+  // wrow: the lane's row from its own 16 bytes of chunk 0 on; srow: its
+  // scales.  tail: the row's last chunk is shorter than kChunk and this is it.
+  __device__ __forceinline__ void load(const char* wrow, const uint16_t* srow, int c, int q, int h, bool tail) {
+    // a lane's 32 columns lie inside the head or past its end as a whole
+    int at = c * (kChunk / 2);
+    if (tail && c * kChunk + q * 32 >= h) at = -q * 16;
+    w = *reinterpret_cast<const u32x4*>(wrow + at);
+    const int g0 = c * kGroups;
+    if constexpr (kGroups == 1) {
+      s[0] = srow[g0];
+    } else if (!tail) {
+      const auto v = *reinterpret_cast<const typename ScaleVec<kGroups>::type*>(srow + g0);
+#pragma unroll
+      for (int i = 0; i < kGroups / 2; ++i) s[i] = v[i];
+    } else {
+      const int last = (h - 1) / G;
+#pragma unroll
+      for (int i = 0; i < kGroups / 2; ++i) {
+        const int a = g0 + 2 * i, b = a + 1;
+        s[i] = srow[a < last ? a : last] | static_cast<uint32_t>(srow[b < last ? b : last]) << 16;
+      }
+    }
+  }
+
+  __device__ __forceinline__ float scale(int g) const {
+    return __uint_as_float(g & 1 ? s[g / 2] & 0xffff0000u : s[g / 2] << 16);
+  }
 };
 
-constexpr int kSpan = 256;  // columns a wave takes at a time: a row's 128-byte line
+// The chunk's 8 columns k .. k + 7 of a row of x, ordered; zero past the end.
+__device__ __forceinline__ u32x4 load_x(const uint16_t* xrow, int k, int h) {
+  u32x4 d = *reinterpret_cast<const u32x4*>(xrow + (k < h ? k : 0));
+  if (k >= h) d = u32x4{0, 0, 0, 0};
+  return order_x(d);
+}
 
-// One workgroup: 16 RT vocabulary rows x 16 NT rows of x.  Its four waves take
-// every fourth span of columns and add their sums through LDS at the end.
-template <class X, int G, int NT, int RT>
-__global__ void __launch_bounds__(256) k_w4_logits(W4Args a) {
-  constexpr int kGroups = kSpan / G, kSteps = G / 32;  // per span, per group
-  __shared__ float sm[4][RT * 4][64];
+// Start value of a group's sums: -24 sum x.
+template <class X, int S>
+__device__ __forceinline__ f32x4 shift_of(const u32x4* x) {
+  const u32x4 neg24{X::kNeg24, X::kNeg24, X::kNeg24, X::kNeg24};
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < S; ++i) acc = X::mfma(x[i], neg24, acc);
+  return acc;
+}
+
+// Up to 16 rows of x and 8 KC chunks: x stays in registers.  A workgroup is
+// resident and walks over pairs of 16-row tiles of the head; its wave w holds x's
+// chunks of range w and reads that part of every tile, one tile ahead.  Per
+// word of the head that leaves the unpacking, the products and a share of a
+// multiply-add per group: no traffic for x, which at 16 rows would be four
+// times that of the head.  The waves' sums meet in LDS once per pair.
+template <class X, int G, int KC>
+__global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
+  constexpr int kGroups = kChunk / G, S = G / 32;
+  // the groups' start values, kept where they take no more registers than this
+  constexpr bool kKeepShift = KC * kGroups * 4 <= 40;
+  __shared__ f32x4 red[2][2][kRanges][64];  // [turn][tile of the pair][wave][lane]
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, q = lane >> 4;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64;
-  const int h = a.h, spans = h / kSpan;  // whole ones; a last, short one follows
+  const int h = a.h, chunks = (h + kChunk - 1) / kChunk;
+  // the window of KC chunks read, all of which exist: it ends with the row
+  // where the wave's own range does, and x is 0 in chunks before the range
+  const int own = w * KC, c0 = own < chunks - KC ? own : chunks - KC;
+  const bool tail = h % kChunk != 0 && c0 + KC == chunks;
+  const int64_t tiles = (static_cast<int64_t>(a.V) + 15) / 16;
+  uint32_t base = X::kBase;
+  asm volatile("" : "+v"(base));  // in a register
 
-  // rows past the end repeat the last one: their results are not stored
+  u32x4 x[KC][4];
+  f32x4 shift[KC][kGroups];
+  {
+    const uint16_t* xrow = a.hidden + (r16 < a.T ? r16 : a.T - 1) * a.ld_h;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[c][i] = load_x(xrow, c0 + c >= own ? (c0 + c) * kChunk + column_of<G>(i, q) : h, h);
+      if (kKeepShift) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) shift[c][g] = shift_of<X, S>(x[c] + g * S);
+      }
+    }
+  }
+
+  // Two buffers in turn, so that a load's registers are next touched when its
+  // tile's turn comes (moving them would wait for the load).
+  Chunk<G> buf[2][KC];
+  auto load = [&](int64_t tile, Chunk<G>(&d)[KC]) {
+    if (tile >= tiles) return;
+    int64_t v = tile * 16 + r16;
+    v = v < a.V ? v : a.V - 1;  // rows past the end repeat the last one
+    const char* wrow = static_cast<const char*>(a.packed) + v * a.ld_p + c0 * (kChunk / 2) + q * 16;
+    const uint16_t* srow = a.scales + v * a.ld_s + c0 * kGroups;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) d[c].load(wrow, srow, c, q, h - c0 * kChunk, c + 1 == KC && tail);
+  };
+  auto add = [&](const Chunk<G>(&d)[KC]) {
+    f32x4 tot{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const u32x4 words = words_of<G>(d[c].w);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        f32x4 acc = kKeepShift ? shift[c][g] : shift_of<X, S>(x[c] + g * S);
+#pragma unroll
+        for (int i = 0; i < S; ++i) acc = X::mfma(x[c][g * S + i], widen_nibbles<X>(words[g * S + i], base), acc);
+        const float sc = d[c].scale(g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tot[j] = fmaf(sc, acc[j], tot[j]);
+      }
+    }
+    return tot;
+  };
+
+  const int64_t step = 2 * static_cast<int64_t>(gridDim.x);
+  int64_t tile = 2 * static_cast<int64_t>(blockIdx.x);
+  load(tile, buf[0]);
+  for (int b = 0; tile < tiles; tile += step, b ^= 1) {
+    load(tile + 1, buf[1]);
+    red[b][0][w][lane] = add(buf[0]);
+    load(tile + step, buf[0]);
+    red[b][1][w][lane] = add(buf[1]);  // of a tile past the end: not stored
+    __syncthreads();
+    // 512 sums; the buffer is written again two turns on, behind the next barrier
+    const int l = (threadIdx.x & 255) >> 2, j = threadIdx.x & 3, second = threadIdx.x >> 8;
+    const int64_t row = (l >> 4) * 4 + j, v = (tile + second) * 16 + (l & 15);
+    if (row < a.T && v < a.V) {
+      float sum = red[b][second][0][l][j];
+#pragma unroll
+      for (int k = 1; k < kRanges; ++k) sum += red[b][second][k][l][j];
+      store_logit(a.out, a.out_dtype, row * a.ld_out + v, sum);
+    }
+  }
+}
+
+// Any number of rows of x and columns.  A workgroup takes 16 RT rows of the head
+// per wave and 16 NT rows of x, which its waves share: x's chunk pairs pass
+// through LDS, two buffers in turn, already in the products' order.
+template <class X, int G, int NT, int RT>
+__global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
+  constexpr int kGroups = kChunk / G, S = G / 32;
+  __shared__ u32x4 xs[2][2 * 4 * NT][64];  // [buffer][chunk, step, x tile][lane]
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r16 = lane & 15, q = lane >> 4;
+  const int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + w) * (16 * RT);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64;
+  const int h = a.h, chunks = (h + kChunk - 1) / kChunk;
+  const int per = (chunks + kRanges - 1) / kRanges;
+
   const char* wrow[RT];
   const uint16_t* srow[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     int64_t v = v0 + r * 16 + r16;
-    v = v < a.V ? v : a.V - 1;
-    wrow[r] = static_cast<const char*>(a.packed) + v * a.ld_p;
+    v = v < a.V ? v : a.V - 1;  // rows past the end repeat the last one: not stored
+    wrow[r] = static_cast<const char*>(a.packed) + v * a.ld_p + q * 16;
     srow[r] = a.scales + v * a.ld_s;
   }
+  uint32_t base = X::kBase;
+  asm volatile("" : "+v"(base));  // in a register
+  // wave w brings step w of the eight steps of a chunk pair, for every x tile
   const uint16_t* xrow[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -131,139 +293,154 @@ __global__ void __launch_bounds__(256) k_w4_logits(W4Args a) {
     xrow[t] = a.hidden + row * a.ld_h;
   }
 
-  f32x4 tot[NT][RT];
+  f32x4 tot[NT][RT], part[NT][RT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) tot[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RT; ++r) tot[t][r] = part[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const u32x4 neg24{X::kNeg24, X::kNeg24, X::kNeg24, X::kNeg24};
-
-  struct Span {
-    u32x4 w[RT][2];
-    uint32_t s[RT][kGroups / 2];
+  u32x4 xn[NT];
+  auto fetch_x = [&](int c) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xn[t] = load_x(xrow[t], (c + (w >> 2)) * kChunk + column_of<G>(w & 3, q), h);
   };
-  auto load = [&](int c, Span& d, auto whole) {
-    constexpr bool full = decltype(whole)::value;
+  auto put_x = [&](int buf) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        // a lane's 32 columns lie inside the head or past its end as a whole
-        int k = c * kSpan + f * 128 + q * 32;
-        k = full || k < h ? k : 0;
-        d.w[r][f] = *reinterpret_cast<const u32x4*>(wrow[r] + k / 2);
-      }
-      if (full) {
-        const auto v = *reinterpret_cast<const typename ScaleVec<kGroups>::type*>(srow[r] + c * kGroups);
-#pragma unroll
-        for (int i = 0; i < kGroups / 2; ++i) d.s[r][i] = v[i];
-      } else {
-        const int last = (h - 1) / G;
-#pragma unroll
-        for (int i = 0; i < kGroups / 2; ++i) {
-          const int g0 = c * kGroups + 2 * i, g1 = g0 + 1;
-          d.s[r][i] = srow[r][g0 < last ? g0 : last] | static_cast<uint32_t>(srow[r][g1 < last ? g1 : last]) << 16;
-        }
-      }
-    }
+    for (int t = 0; t < NT; ++t) xs[buf][w * NT + t][lane] = xn[t];
   };
 
-  auto add = [&](int c, const Span& cur, auto whole) {
-    constexpr bool full = decltype(whole)::value;
+  // two buffers in turn: moving a load's registers would wait for it
+  Chunk<G> buf[2][RT][2];
+  auto load = [&](int c, Chunk<G>(&d)[RT][2]) {
+    // a chunk past the end repeats the last one; x is 0 there
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int cc = c + f < chunks ? c + f : chunks - 1;
+        d[r][f].load(wrow[r], srow[r], cc, q, h, (cc + 1) * kChunk > h);
+      }
+  };
+  int left = per;  // chunks to the end of the range
+  auto add = [&](int c, const Chunk<G>(&d)[RT][2], int b) {
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      u32x4 x[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = c * kSpan + f * 128 + i * 32 + q * 8;
-          u32x4 d = *reinterpret_cast<const u32x4*>(xrow[t] + (full || k < h ? k : 0));
-          if (!full && k >= h) d = u32x4{0, 0, 0, 0};
-          x[t][i] = order_x(d);
-        }
       u32x4 words[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) words[r] = transpose_rows(cur.w[r][f]);
+      for (int r = 0; r < RT; ++r) words[r] = words_of<G>(d[r][f].w);
 #pragma unroll
-      for (int g = 0; g < 128 / G; ++g) {
-        f32x4 shift[NT];
+      for (int g = 0; g < kGroups; ++g) {
+        u32x4 bw[RT][S];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int i = 0; i < S; ++i) bw[r][i] = widen_nibbles<X>(words[r][g * S + i], base);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          shift[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          u32x4 x[S];
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) shift[t] = X::mfma(x[t][g * kSteps + i], neg24, shift[t]);
-        }
-        const int gs = f * (128 / G) + g;
+          for (int i = 0; i < S; ++i) x[i] = xs[b][(f * 4 + g * S + i) * NT + t][lane];
+          const f32x4 start = shift_of<X, S>(x);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const uint32_t pair = cur.s[r][gs / 2];
-          const float sc = __uint_as_float(gs & 1 ? pair & 0xffff0000u : pair << 16);
-          u32x4 b[kSteps];
+          for (int r = 0; r < RT; ++r) {
+            f32x4 acc = start;
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i) b[i] = widen_nibbles<X>(words[r][g * kSteps + i]);
+            for (int i = 0; i < S; ++i) acc = X::mfma(x[i], bw[r][i], acc);
+            const float sc = d[r][f].scale(g);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            f32x4 acc = shift[t];
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) acc = X::mfma(x[t][g * kSteps + i], b[i], acc);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tot[t][r][j] = fmaf(sc, acc[j], tot[t][r][j]);
+            for (int j = 0; j < 4; ++j) part[t][r][j] = fmaf(sc, acc[j], part[t][r][j]);
           }
         }
       }
+      if (--left == 0 || c + f + 1 >= chunks) {  // the end of a range
+        left = per;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              tot[t][r][j] += part[t][r][j];
+              part[t][r][j] = 0.f;
+            }
+      }
     }
   };
 
-  Span cur;
-  if (w < spans) load(w, cur, std::true_type());
-  for (int c = w; c < spans; c += 4) {
-    Span nxt;
-    if (c + 4 < spans) load(c + 4, nxt, std::true_type());
-    add(c, cur, std::true_type());
-    cur = nxt;
-  }
-  if (spans * kSpan < h && (spans & 3) == w) {
-    load(spans, cur, std::false_type());
-    add(spans, cur, std::false_type());
-  }
-
+  fetch_x(0);
+  load(0, buf[0]);
+  put_x(0);
+  __syncthreads();
+  int c = 0;
+  while (c < chunks) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (t) __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+      if (c < chunks) {
+        const bool more = c + 2 < chunks;
+        if (more) {
+          fetch_x(c + 2);
+          load(c + 2, buf[k ^ 1]);
+        }
+        add(c, buf[k], k);
+        if (more) {
+          // this buffer of x was last read before the barrier that ended the
+          // previous turn
+          put_x(k ^ 1);
+          __syncthreads();
+        }
+        c += 2;
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sm[w][r * 4 + j][lane] = tot[t][r][j];
-    __syncthreads();
-    for (int e = w; e < RT * 4; e += 4) {
-      const float sum = (sm[0][e][lane] + sm[1][e][lane]) + (sm[2][e][lane] + sm[3][e][lane]);
-      const int64_t row = t0 + t * 16 + q * 4 + (e & 3);
-      const int64_t v = v0 + (e >> 2) * 16 + r16;
-      if (row < a.T && v < a.V) store_logit(a.out, a.out_dtype, row * a.ld_out + v, sum);
-    }
+      for (int j = 0; j < 4; ++j) {
+        const int64_t row = t0 + t * 16 + q * 4 + j, v = v0 + r * 16 + r16;
+        if (row < a.T && v < a.V) store_logit(a.out, a.out_dtype, row * a.ld_out + v, tot[t][r][j]);
+      }
+}
+
+template <class X, int G>
+hipError_t launch_few(const W4Args& a, int per, hipStream_t s) {
+  // one resident workgroup a CU, two where the registers of x leave room
+  const int64_t pairs = (int64_t(a.V) + 31) / 32, most = per <= 3 ? 512 : 256;
+  const dim3 g(static_cast<unsigned>(pairs < most ? pairs : most)), b(512);
+  TimedLaunch tl("k_w4_logits", s);
+  switch (per) {
+    case 1: hipLaunchKernelGGL((k_w4_few<X, G, 1>), g, b, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_w4_few<X, G, 2>), g, b, 0, s, a); break;
+    case 3: hipLaunchKernelGGL((k_w4_few<X, G, 3>), g, b, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((k_w4_few<X, G, 4>), g, b, 0, s, a); break;
+    case 5: hipLaunchKernelGGL((k_w4_few<X, G, 5>), g, b, 0, s, a); break;
+    case 6: hipLaunchKernelGGL((k_w4_few<X, G, 6>), g, b, 0, s, a); break;
+    default: hipLaunchKernelGGL((k_w4_few<X, G, 7>), g, b, 0, s, a); break;
   }
+  return hipGetLastError();
 }
 
 template <class X, int G>
 hipError_t launch_logits(const W4Args& a, hipStream_t s) {
+  const int per = ((a.h + kChunk - 1) / kChunk + kRanges - 1) / kRanges;
+  if (a.T <= 16 && per <= 7) return launch_few<X, G>(a, per, s);
   // grid.y is at most 65535 blocks of 64 rows
   constexpr int64_t kRows = int64_t(65535) * 64;
+  constexpr int RT = 2;
   for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
     W4Args b = a;
     b.T = a.T - r0 < kRows ? a.T - r0 : kRows;
     b.hidden = a.hidden + r0 * a.ld_h;
     b.out = static_cast<char*>(a.out) + r0 * a.ld_out * (a.out_dtype == 2 ? 4 : 2);
     const int nt = b.T >= 64 ? 4 : static_cast<int>((b.T + 15) / 16);
-    const unsigned gy = static_cast<unsigned>((b.T + 63) / 64);
+    const dim3 g(static_cast<unsigned>((int64_t(a.V) + 128 * RT - 1) / (128 * RT)), static_cast<unsigned>((b.T + 63) / 64));
     TimedLaunch tl("k_w4_logits", s);
-    auto grid = [&](int rt) { return dim3(static_cast<unsigned>((int64_t(a.V) + 16 * rt - 1) / (16 * rt)), gy); };
     switch (nt) {
-      case 1: hipLaunchKernelGGL((k_w4_logits<X, G, 1, 2>), grid(2), dim3(256), 0, s, b); break;
-      case 2: hipLaunchKernelGGL((k_w4_logits<X, G, 2, 2>), grid(2), dim3(256), 0, s, b); break;
-      case 3: hipLaunchKernelGGL((k_w4_logits<X, G, 3, 4>), grid(4), dim3(256), 0, s, b); break;
-      default: hipLaunchKernelGGL((k_w4_logits<X, G, 4, 4>), grid(4), dim3(256), 0, s, b); break;
+      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, RT>), g, dim3(512), 0, s, b); break;
+      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, RT>), g, dim3(512), 0, s, b); break;
+      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, RT>), g, dim3(512), 0, s, b); break;
+      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, RT>), g, dim3(512), 0, s, b); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
