@@ -98,17 +98,6 @@ __device__ __forceinline__ int column_of(int i, int q) {
   return 32 * i + 8 * q;
 }
 
-template <int N>
-struct ScaleVec;  // N bf16 values at any 2-byte boundary
-template <>
-struct ScaleVec<2> {
-  typedef uint32_t type __attribute__((ext_vector_type(1), aligned(2)));
-};
-template <>
-struct ScaleVec<4> {
-  typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
-};
-
 // Columns are taken in chunks of 128, and the chunks of a row fall into
 // kRanges ranges of equal length.  Every kernel adds a range's groups in order
 // and then the ranges in order, so a row's logits have the same bits
@@ -116,39 +105,60 @@ struct ScaleVec<4> {
 constexpr int kChunk = 128;
 constexpr int kRanges = 8;
 
-// Words and scales of a 16-row tile for one chunk.
-template <int G>
-struct Chunk {
-  static constexpr int kGroups = kChunk / G;
-  u32x4 w;
-  uint32_t s[(kGroups + 1) / 2];
+// Words and scales of a 16-row tile for KC neighbouring chunks, as loaded:
+// scales are unpacked where they are used, for any work on a loaded value
+// next to its load would wait for the load.  TAIL: columns may end inside the
+// chunks (otherwise loads need no branch, which would part them from the
+// products they run ahead of).
+template <int G, int KC, bool TAIL>
+struct Tile {
+  static constexpr int kGroups = kChunk / G, kScales = KC * kGroups;
+  u32x4 w[KC];
+  uint32_t s[(kScales + 1) / 2];
 
-  // wrow: the lane's row from its own 16 bytes of chunk 0 on; srow: its
-  // scales.  tail: the row's last chunk is shorter than kChunk and this is it.
-  __device__ __forceinline__ void load(const char* wrow, const uint16_t* srow, int c, int q, int h, bool tail) {
-    // a lane's 32 columns lie inside the head or past its end as a whole
-    int at = c * (kChunk / 2);
-    if (tail && c * kChunk + q * 32 >= h) at = -q * 16;
-    w = *reinterpret_cast<const u32x4*>(wrow + at);
-    const int g0 = c * kGroups;
-    if constexpr (kGroups == 1) {
-      s[0] = srow[g0];
-    } else if (!tail) {
-      const auto v = *reinterpret_cast<const typename ScaleVec<kGroups>::type*>(srow + g0);
+  // wrow: the lane's row from its own 16 bytes of chunk 0 on; srow: the row's
+  // scales.  Chunks c .. c + KC - 1; what lies past column h is read from
+  // elsewhere in the row (x is 0 there).
+  __device__ __forceinline__ void load(const char* wrow, const uint16_t* srow, int c, int q, int h) {
+    if (!TAIL || (c + KC) * kChunk <= h) {
 #pragma unroll
-      for (int i = 0; i < kGroups / 2; ++i) s[i] = v[i];
+      for (int k = 0; k < KC; ++k) w[k] = *reinterpret_cast<const u32x4*>(wrow + (c + k) * (kChunk / 2));
+      const uint16_t* p = srow + c * kGroups;
+      typedef u32x4 x4 __attribute__((aligned(2)));
+      typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(2)));
+      typedef uint32_t x1 __attribute__((aligned(2)));
+#pragma unroll
+      for (int i = 0; i + 8 <= kScales; i += 8) {
+        const u32x4 v = *reinterpret_cast<const x4*>(p + i);
+        s[i / 2] = v.x, s[i / 2 + 1] = v.y, s[i / 2 + 2] = v.z, s[i / 2 + 3] = v.w;
+      }
+      constexpr int r4 = kScales / 8 * 8, r2 = kScales / 4 * 4, r1 = kScales / 2 * 2;
+      if constexpr (r2 > r4) {
+        const auto v = *reinterpret_cast<const x2*>(p + r4);
+        s[r4 / 2] = v.x, s[r4 / 2 + 1] = v.y;
+      }
+      if constexpr (r1 > r2) s[r2 / 2] = *reinterpret_cast<const x1*>(p + r2);
+      if constexpr (kScales > r1) s[r1 / 2] = p[r1];
     } else {
       const int last = (h - 1) / G;
 #pragma unroll
-      for (int i = 0; i < kGroups / 2; ++i) {
-        const int a = g0 + 2 * i, b = a + 1;
+      for (int k = 0; k < KC; ++k) {
+        // a lane's 32 columns lie inside the head or past its end as a whole
+        const int at = (c + k) * kChunk + q * 32 < h ? (c + k) * (kChunk / 2) : -q * 16;
+        w[k] = *reinterpret_cast<const u32x4*>(wrow + at);
+      }
+#pragma unroll
+      for (int i = 0; i < (kScales + 1) / 2; ++i) {
+        const int a = c * kGroups + 2 * i, b = a + 1;
         s[i] = srow[a < last ? a : last] | static_cast<uint32_t>(srow[b < last ? b : last]) << 16;
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // issued here, not where registers would be saved
   }
 
-  __device__ __forceinline__ float scale(int g) const {
-    return __uint_as_float(g & 1 ? s[g / 2] & 0xffff0000u : s[g / 2] << 16);
+  __device__ __forceinline__ float scale(int k, int g) const {
+    const int i = k * kGroups + g;
+    return __uint_as_float(i & 1 ? s[i / 2] & 0xffff0000u : s[i / 2] << 16);
   }
 };
 
@@ -161,8 +171,8 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t* xrow, int k, int h) {
 
 // Start value of a group's sums: -24 sum x.
 template <class X, int S>
-__device__ __forceinline__ f32x4 shift_of(const u32x4* x) {
-  const u32x4 neg24{X::kNeg24, X::kNeg24, X::kNeg24, X::kNeg24};
+__device__ __forceinline__ f32x4 shift_of(const u32x4* x, uint32_t n = X::kNeg24) {
+  const u32x4 neg24{n, n, n, n};
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < S; ++i) acc = X::mfma(x[i], neg24, acc);
@@ -175,7 +185,7 @@ __device__ __forceinline__ f32x4 shift_of(const u32x4* x) {
 // word of the head that leaves the unpacking, the products and a share of a
 // multiply-add per group: no traffic for x, which at 16 rows would be four
 // times that of the head.  The waves' sums meet in LDS once per pair.
-template <class X, int G, int KC>
+template <class X, int G, int KC, bool TAIL>
 __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
   constexpr int kGroups = kChunk / G, S = G / 32;
   // the groups' start values, kept where they take no more registers than this
@@ -187,7 +197,6 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
   // the window of KC chunks read, all of which exist: it ends with the row
   // where the wave's own range does, and x is 0 in chunks before the range
   const int own = w * KC, c0 = own < chunks - KC ? own : chunks - KC;
-  const bool tail = h % kChunk != 0 && c0 + KC == chunks;
   const int64_t tiles = (static_cast<int64_t>(a.V) + 15) / 16;
   uint32_t base = X::kBase;
   asm volatile("" : "+v"(base));  // in a register
@@ -209,31 +218,32 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
   }
 
   // Two buffers in turn, so that a load's registers are next touched when its
-  // tile's turn comes (moving them would wait for the load).
-  Chunk<G> buf[2][KC];
-  auto load = [&](int64_t tile, Chunk<G>(&d)[KC]) {
-    if (tile >= tiles) return;
+  // tile's turn comes (moving them would wait for the load).  A third buffer
+  // measured no faster.
+  Tile<G, KC, TAIL> buf[2];
+  auto load = [&](int64_t tile, Tile<G, KC, TAIL>& d) {
     int64_t v = tile * 16 + r16;
     v = v < a.V ? v : a.V - 1;  // rows past the end repeat the last one
-    const char* wrow = static_cast<const char*>(a.packed) + v * a.ld_p + c0 * (kChunk / 2) + q * 16;
-    const uint16_t* srow = a.scales + v * a.ld_s + c0 * kGroups;
-#pragma unroll
-    for (int c = 0; c < KC; ++c) d[c].load(wrow, srow, c, q, h - c0 * kChunk, c + 1 == KC && tail);
+    d.load(static_cast<const char*>(a.packed) + v * a.ld_p + q * 16, a.scales + v * a.ld_s, c0, q, h);
   };
-  auto add = [&](const Chunk<G>(&d)[KC]) {
+  auto add = [&](const Tile<G, KC, TAIL>& d) {
     f32x4 tot{0.f, 0.f, 0.f, 0.f};
+    uint32_t neg24 = X::kNeg24;
+    if (!kKeepShift) asm volatile("" : "+v"(neg24));  // or the compiler would keep the start values all the same
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
-      const u32x4 words = words_of<G>(d[c].w);
+      const u32x4 words = words_of<G>(d.w[c]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        f32x4 acc = kKeepShift ? shift[c][g] : shift_of<X, S>(x[c] + g * S);
+        f32x4 acc = kKeepShift ? shift[c][g] : shift_of<X, S>(x[c] + g * S, neg24);
 #pragma unroll
         for (int i = 0; i < S; ++i) acc = X::mfma(x[c][g * S + i], widen_nibbles<X>(words[g * S + i], base), acc);
-        const float sc = d[c].scale(g);
+        const float sc = d.scale(c, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tot[j] = fmaf(sc, acc[j], tot[j]);
       }
+      // x and the buffers fill the registers: no chunk may run ahead
+      if (!kKeepShift) __builtin_amdgcn_sched_barrier(0);
     }
     return tot;
   };
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
 // Any number of rows of x and columns.  A workgroup takes 16 RT rows of the head
 // per wave and 16 NT rows of x, which its waves share: x's chunk pairs pass
 // through LDS, two buffers in turn, already in the products' order.
-template <class X, int G, int NT, int RT>
+template <class X, int G, int NT, int RT, bool TAIL>
 __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
   constexpr int kGroups = kChunk / G, S = G / 32;
   __shared__ u32x4 xs[2][2 * 4 * NT][64];  // [buffer][chunk, step, x tile][lane]
@@ -310,24 +320,18 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
   };
 
   // two buffers in turn: moving a load's registers would wait for it
-  Chunk<G> buf[2][RT][2];
-  auto load = [&](int c, Chunk<G>(&d)[RT][2]) {
-    // a chunk past the end repeats the last one; x is 0 there
+  Tile<G, 2, TAIL> buf[2][RT];
+  auto load = [&](int c, Tile<G, 2, TAIL>(&d)[RT]) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int cc = c + f < chunks ? c + f : chunks - 1;
-        d[r][f].load(wrow[r], srow[r], cc, q, h, (cc + 1) * kChunk > h);
-      }
+    for (int r = 0; r < RT; ++r) d[r].load(wrow[r], srow[r], c, q, h);
   };
   int left = per;  // chunks to the end of the range
-  auto add = [&](int c, const Chunk<G>(&d)[RT][2], int b) {
+  auto add = [&](int c, const Tile<G, 2, TAIL>(&d)[RT], int b) {
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       u32x4 words[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) words[r] = words_of<G>(d[r][f].w);
+      for (int r = 0; r < RT; ++r) words[r] = words_of<G>(d[r].w[f]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         u32x4 bw[RT][S];
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
             f32x4 acc = start;
 #pragma unroll
             for (int i = 0; i < S; ++i) acc = X::mfma(x[i], bw[r][i], acc);
-            const float sc = d[r][f].scale(g);
+            const float sc = d[r].scale(f, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) part[t][r][j] = fmaf(sc, acc[j], part[t][r][j]);
           }
@@ -403,28 +407,26 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
       }
 }
 
-template <class X, int G>
+template <class X, int G, bool TAIL>
 hipError_t launch_few(const W4Args& a, int per, hipStream_t s) {
   // one resident workgroup a CU, two where the registers of x leave room
   const int64_t pairs = (int64_t(a.V) + 31) / 32, most = per <= 3 ? 512 : 256;
   const dim3 g(static_cast<unsigned>(pairs < most ? pairs : most)), b(512);
   TimedLaunch tl("k_w4_logits", s);
   switch (per) {
-    case 1: hipLaunchKernelGGL((k_w4_few<X, G, 1>), g, b, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((k_w4_few<X, G, 2>), g, b, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((k_w4_few<X, G, 3>), g, b, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((k_w4_few<X, G, 4>), g, b, 0, s, a); break;
-    case 5: hipLaunchKernelGGL((k_w4_few<X, G, 5>), g, b, 0, s, a); break;
-    case 6: hipLaunchKernelGGL((k_w4_few<X, G, 6>), g, b, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_w4_few<X, G, 7>), g, b, 0, s, a); break;
+    case 1: hipLaunchKernelGGL((k_w4_few<X, G, 1, TAIL>), g, b, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_w4_few<X, G, 2, TAIL>), g, b, 0, s, a); break;
+    case 3: hipLaunchKernelGGL((k_w4_few<X, G, 3, TAIL>), g, b, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((k_w4_few<X, G, 4, TAIL>), g, b, 0, s, a); break;
+    case 5: hipLaunchKernelGGL((k_w4_few<X, G, 5, TAIL>), g, b, 0, s, a); break;
+    case 6: hipLaunchKernelGGL((k_w4_few<X, G, 6, TAIL>), g, b, 0, s, a); break;
+    default: hipLaunchKernelGGL((k_w4_few<X, G, 7, TAIL>), g, b, 0, s, a); break;
   }
   return hipGetLastError();
 }
 
-template <class X, int G>
-hipError_t launch_logits(const W4Args& a, hipStream_t s) {
-  const int per = ((a.h + kChunk - 1) / kChunk + kRanges - 1) / kRanges;
-  if (a.T <= 16 && per <= 7) return launch_few<X, G>(a, per, s);
+template <class X, int G, bool TAIL>
+hipError_t launch_wide(const W4Args& a, hipStream_t s) {
   // grid.y is at most 65535 blocks of 64 rows
   constexpr int64_t kRows = int64_t(65535) * 64;
   constexpr int RT = 2;
@@ -437,15 +439,23 @@ hipError_t launch_logits(const W4Args& a, hipStream_t s) {
     const dim3 g(static_cast<unsigned>((int64_t(a.V) + 128 * RT - 1) / (128 * RT)), static_cast<unsigned>((b.T + 63) / 64));
     TimedLaunch tl("k_w4_logits", s);
     switch (nt) {
-      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, RT>), g, dim3(512), 0, s, b); break;
-      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, RT>), g, dim3(512), 0, s, b); break;
-      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, RT>), g, dim3(512), 0, s, b); break;
-      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, RT>), g, dim3(512), 0, s, b); break;
+      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, RT, TAIL>), g, dim3(512), 0, s, b); break;
+      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, RT, TAIL>), g, dim3(512), 0, s, b); break;
+      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, RT, TAIL>), g, dim3(512), 0, s, b); break;
+      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, RT, TAIL>), g, dim3(512), 0, s, b); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <class X, int G>
+hipError_t launch_logits(const W4Args& a, hipStream_t s) {
+  const int per = ((a.h + kChunk - 1) / kChunk + kRanges - 1) / kRanges;
+  if (a.T <= 16 && per <= 7)
+    return a.h % kChunk ? launch_few<X, G, true>(a, per, s) : launch_few<X, G, false>(a, per, s);
+  return a.h % (2 * kChunk) ? launch_wide<X, G, true>(a, s) : launch_wide<X, G, false>(a, s);
 }
 
 template <class X>
