@@ -162,11 +162,12 @@ struct Tile {
   }
 };
 
-// The chunk's 8 columns k .. k + 7 of a row of x, ordered; zero past the end.
+// Columns k .. k + 7 of a row of x; zero past the end.
+template <bool TAIL>
 __device__ __forceinline__ u32x4 load_x(const uint16_t* xrow, int k, int h) {
-  u32x4 d = *reinterpret_cast<const u32x4*>(xrow + (k < h ? k : 0));
-  if (k >= h) d = u32x4{0, 0, 0, 0};
-  return order_x(d);
+  u32x4 d = *reinterpret_cast<const u32x4*>(xrow + (!TAIL || k < h ? k : 0));
+  if (TAIL && k >= h) d = u32x4{0, 0, 0, 0};
+  return d;
 }
 
 // Start value of a group's sums: -24 sum x.
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
     for (int c = 0; c < KC; ++c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[c][i] = load_x(xrow, c0 + c >= own ? (c0 + c) * kChunk + column_of<G>(i, q) : h, h);
+        x[c][i] = order_x(load_x<true>(xrow, c0 + c >= own ? (c0 + c) * kChunk + column_of<G>(i, q) : h, h));
       if (kKeepShift) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) shift[c][g] = shift_of<X, S>(x[c] + g * S);
@@ -272,13 +273,13 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
 // Any number of rows of x and columns.  A workgroup takes 16 RT rows of the head
 // per wave and 16 NT rows of x, which its waves share: x's chunk pairs pass
 // through LDS, two buffers in turn, already in the products' order.
-template <class X, int G, int NT, int RT, bool TAIL>
-__global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
+template <class X, int G, int NT, int RT, int NW, bool TAIL>
+__global__ void __launch_bounds__(64 * NW, 2) k_w4_wide(W4Args a) {
   constexpr int kGroups = kChunk / G, S = G / 32;
   __shared__ u32x4 xs[2][2 * 4 * NT][64];  // [buffer][chunk, step, x tile][lane]
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, q = lane >> 4;
-  const int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + w) * (16 * RT);
+  const int64_t v0 = (static_cast<int64_t>(blockIdx.x) * NW + w) * (16 * RT);
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64;
   const int h = a.h, chunks = (h + kChunk - 1) / kChunk;
   const int per = (chunks + kRanges - 1) / kRanges;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
   }
   uint32_t base = X::kBase;
   asm volatile("" : "+v"(base));  // in a register
-  // wave w brings step w of the eight steps of a chunk pair, for every x tile
+  // each wave brings an equal share of the eight steps of a chunk pair
   const uint16_t* xrow[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -309,14 +310,22 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) tot[t][r] = part[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  u32x4 xn[NT];
+  constexpr int XS = 8 / NW;
+  u32x4 xn[XS][NT];
   auto fetch_x = [&](int c) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xn[t] = load_x(xrow[t], (c + (w >> 2)) * kChunk + column_of<G>(w & 3, q), h);
+    for (int i = 0; i < XS; ++i) {
+      const int step = w * XS + i;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        xn[i][t] = load_x<TAIL>(xrow[t], (c + (step >> 2)) * kChunk + column_of<G>(step & 3, q), h);
+    }
   };
   auto put_x = [&](int buf) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xs[buf][w * NT + t][lane] = xn[t];
+    for (int i = 0; i < XS; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) xs[buf][(w * XS + i) * NT + t][lane] = order_x(xn[i][t]);
   };
 
   // two buffers in turn: moving a load's registers would wait for it
@@ -327,36 +336,21 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
   };
   int left = per;  // chunks to the end of the range
   auto add = [&](int c, const Tile<G, 2, TAIL>(&d)[RT], int b) {
+    constexpr int kAll = 2 * kGroups;
+    u32x4 x[NT][S];  // of a group; the next one's replaces it step by step
+    f32x4 acc[2][NT][RT];
+    // The products of a group run while the sums of the one before it are
+    // scaled, which would otherwise wait for the last product.
+    auto scale_in = [&](int group) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      u32x4 words[RT];
+      for (int r = 0; r < RT; ++r) {
+        const float sc = d[r].scale(group / kGroups, group % kGroups);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) words[r] = words_of<G>(d[r].w[f]);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        u32x4 bw[RT][S];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int i = 0; i < S; ++i) bw[r][i] = widen_nibbles<X>(words[r][g * S + i], base);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          u32x4 x[S];
-#pragma unroll
-          for (int i = 0; i < S; ++i) x[i] = xs[b][(f * 4 + g * S + i) * NT + t][lane];
-          const f32x4 start = shift_of<X, S>(x);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            f32x4 acc = start;
-#pragma unroll
-            for (int i = 0; i < S; ++i) acc = X::mfma(x[i], bw[r][i], acc);
-            const float sc = d[r].scale(f, g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[t][r][j] = fmaf(sc, acc[j], part[t][r][j]);
-          }
-        }
+          for (int j = 0; j < 4; ++j) part[t][r][j] = fmaf(sc, acc[group & 1][t][r][j], part[t][r][j]);
       }
-      if (--left == 0 || c + f + 1 >= chunks) {  // the end of a range
+      if (group % kGroups == kGroups - 1 && (--left == 0 || c + group / kGroups + 1 >= chunks)) {  // end of a range
         left = per;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -368,34 +362,67 @@ __global__ void __launch_bounds__(512) k_w4_wide(W4Args a) {
               part[t][r][j] = 0.f;
             }
       }
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t][i] = xs[b][i * NT + t][lane];
+    u32x4 words[RT];
+#pragma unroll
+    for (int group = 0; group < kAll; ++group) {
+      const int f = group / kGroups, g = group % kGroups;
+      if (g == 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) words[r] = words_of<G>(d[r].w[f]);
+      }
+      f32x4 start[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) start[t] = shift_of<X, S>(x[t]);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const u32x4 bw = widen_nibbles<X>(words[r][g * S + i], base);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const f32x4 from = i == 0 ? start[t] : acc[group & 1][t][r];
+            acc[group & 1][t][r] = X::mfma(x[t][i], bw, from);
+          }
+        }
+        if (group + 1 < kAll) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[t][i] = xs[b][((group + 1) * S + i) * NT + t][lane];
+        }
+      }
+      if (group > 0) scale_in(group - 1);
     }
+    scale_in(kAll - 1);
   };
 
   fetch_x(0);
   load(0, buf[0]);
   put_x(0);
   __syncthreads();
+  // The loads ahead carry no condition (past the end they repeat the last
+  // pair): behind a branch the wait for the older loads would wait for them too.
+  const int last = (chunks - 1) / 2 * 2;
   int c = 0;
-  while (c < chunks) {
+  while (true) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (c < chunks) {
-        const bool more = c + 2 < chunks;
-        if (more) {
-          fetch_x(c + 2);
-          load(c + 2, buf[k ^ 1]);
-        }
-        add(c, buf[k], k);
-        if (more) {
-          // this buffer of x was last read before the barrier that ended the
-          // previous turn
-          put_x(k ^ 1);
-          __syncthreads();
-        }
-        c += 2;
-      }
+      const int next = c < last ? c + 2 : last;
+      fetch_x(next);
+      load(next, buf[k ^ 1]);
+      add(c, buf[k], k);
+      if (c == last) goto done;
+      // this buffer of x was last read before the barrier that ended the
+      // previous turn
+      put_x(k ^ 1);
+      __syncthreads();
+      c += 2;
     }
   }
+done:
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -429,20 +456,24 @@ template <class X, int G, bool TAIL>
 hipError_t launch_wide(const W4Args& a, hipStream_t s) {
   // grid.y is at most 65535 blocks of 64 rows
   constexpr int64_t kRows = int64_t(65535) * 64;
-  constexpr int RT = 2;
+  constexpr int NW = 8;
   for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
     W4Args b = a;
     b.T = a.T - r0 < kRows ? a.T - r0 : kRows;
     b.hidden = a.hidden + r0 * a.ld_h;
     b.out = static_cast<char*>(a.out) + r0 * a.ld_out * (a.out_dtype == 2 ? 4 : 2);
     const int nt = b.T >= 64 ? 4 : static_cast<int>((b.T + 15) / 16);
-    const dim3 g(static_cast<unsigned>((int64_t(a.V) + 128 * RT - 1) / (128 * RT)), static_cast<unsigned>((b.T + 63) / 64));
+    // two tiles of the head a wave share its x operands; with four tiles of x
+    // the registers hold one
+    const int rt = nt == 4 ? 1 : 2;
+    const dim3 g(static_cast<unsigned>((int64_t(a.V) + 16 * NW * rt - 1) / (16 * NW * rt)),
+                 static_cast<unsigned>((b.T + 63) / 64));
     TimedLaunch tl("k_w4_logits", s);
     switch (nt) {
-      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, RT, TAIL>), g, dim3(512), 0, s, b); break;
-      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, RT, TAIL>), g, dim3(512), 0, s, b); break;
-      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, RT, TAIL>), g, dim3(512), 0, s, b); break;
-      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, RT, TAIL>), g, dim3(512), 0, s, b); break;
+      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, 1, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
