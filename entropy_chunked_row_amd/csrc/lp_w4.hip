@@ -45,21 +45,31 @@ struct XFp16 {
   }
 };
 
-// Eight nibbles as 16 + n, in the order 0 4 1 5 2 6 3 7.  The and-or is
-// spelled out: with both constants as literals it would be two instructions.
+// The two constants of the unpacking, in registers: as literals they would
+// make the and-or two instructions.  The instruction itself is left to the
+// compiler, which knows how many cycles lie between it and a matrix
+// instruction that reads its result.
 template <class X>
-__device__ __forceinline__ u32x4 widen_nibbles(uint32_t w, uint32_t base) {
-  u32x4 r;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int sh = X::kBit - 4 * s;
-    const uint32_t v = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
-    uint32_t o;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(o) : "v"(v), "s"(X::kMask), "v"(base));
-    r[s] = o;
+struct Nibbles {
+  uint32_t mask, base;
+
+  __device__ __forceinline__ Nibbles() : mask(X::kMask), base(X::kBase) {
+    asm volatile("" : "+s"(mask));
+    asm volatile("" : "+v"(base));
   }
-  return r;
-}
+
+  // Eight nibbles as 16 + n, in the order 0 4 1 5 2 6 3 7.
+  __device__ __forceinline__ u32x4 widen(uint32_t w) const {
+    u32x4 r;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int sh = X::kBit - 4 * s;
+      const uint32_t v = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
+      r[s] = (v & mask) | base;
+    }
+    return r;
+  }
+};
 
 // Eight 16-bit values in the same order.
 __device__ __forceinline__ u32x4 order_x(u32x4 d) {
@@ -199,8 +209,7 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
   // where the wave's own range does, and x is 0 in chunks before the range
   const int own = w * KC, c0 = own < chunks - KC ? own : chunks - KC;
   const int64_t tiles = (static_cast<int64_t>(a.V) + 15) / 16;
-  uint32_t base = X::kBase;
-  asm volatile("" : "+v"(base));  // in a register
+  const Nibbles<X> nibbles;
 
   u32x4 x[KC][4];
   f32x4 shift[KC][kGroups];
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
       for (int g = 0; g < kGroups; ++g) {
         f32x4 acc = kKeepShift ? shift[c][g] : shift_of<X, S>(x[c] + g * S, neg24);
 #pragma unroll
-        for (int i = 0; i < S; ++i) acc = X::mfma(x[c][g * S + i], widen_nibbles<X>(words[g * S + i], base), acc);
+        for (int i = 0; i < S; ++i) acc = X::mfma(x[c][g * S + i], nibbles.widen(words[g * S + i]), acc);
         const float sc = d.scale(c, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tot[j] = fmaf(sc, acc[j], tot[j]);
@@ -293,8 +302,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_w4_wide(W4Args a) {
     wrow[r] = static_cast<const char*>(a.packed) + v * a.ld_p + q * 16;
     srow[r] = a.scales + v * a.ld_s;
   }
-  uint32_t base = X::kBase;
-  asm volatile("" : "+v"(base));  // in a register
+  const Nibbles<X> nibbles;
   // each wave brings an equal share of the eight steps of a chunk pair
   const uint16_t* xrow[NT];
 #pragma unroll
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_w4_wide(W4Args a) {
       for (int i = 0; i < S; ++i) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const u32x4 bw = widen_nibbles<X>(words[r][g * S + i], base);
+          const u32x4 bw = nibbles.widen(words[r][g * S + i]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const f32x4 from = i == 0 ? start[t] : acc[group & 1][t][r];
@@ -434,6 +442,11 @@ done:
       }
 }
 
+// Chunks per range up to which x's registers leave room for two buffers; with
+// groups of 32 the buffers' scales take more (measured at 7168 columns: 328 us
+// spilling, 126 us through k_w4_wide; at 7168 with groups of 128 83 us here, 99 there).
+constexpr int most_chunks(int group) { return group == 32 ? 5 : 7; }
+
 template <class X, int G, bool TAIL>
 hipError_t launch_few(const W4Args& a, int per, hipStream_t s) {
   // one resident workgroup a CU, two where the registers of x leave room
@@ -446,8 +459,13 @@ hipError_t launch_few(const W4Args& a, int per, hipStream_t s) {
     case 3: hipLaunchKernelGGL((k_w4_few<X, G, 3, TAIL>), g, b, 0, s, a); break;
     case 4: hipLaunchKernelGGL((k_w4_few<X, G, 4, TAIL>), g, b, 0, s, a); break;
     case 5: hipLaunchKernelGGL((k_w4_few<X, G, 5, TAIL>), g, b, 0, s, a); break;
-    case 6: hipLaunchKernelGGL((k_w4_few<X, G, 6, TAIL>), g, b, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_w4_few<X, G, 7, TAIL>), g, b, 0, s, a); break;
+    default:
+      if constexpr (most_chunks(G) == 7) {
+        if (per == 6)
+          hipLaunchKernelGGL((k_w4_few<X, G, 6, TAIL>), g, b, 0, s, a);
+        else
+          hipLaunchKernelGGL((k_w4_few<X, G, 7, TAIL>), g, b, 0, s, a);
+      }
   }
   return hipGetLastError();
 }
@@ -484,7 +502,7 @@ hipError_t launch_wide(const W4Args& a, hipStream_t s) {
 template <class X, int G>
 hipError_t launch_logits(const W4Args& a, hipStream_t s) {
   const int per = ((a.h + kChunk - 1) / kChunk + kRanges - 1) / kRanges;
-  if (a.T <= 16 && per <= 7)
+  if (a.T <= 16 && per <= most_chunks(G))
     return a.h % kChunk ? launch_few<X, G, true>(a, per, s) : launch_few<X, G, false>(a, per, s);
   return a.h % (2 * kChunk) ? launch_wide<X, G, true>(a, s) : launch_wide<X, G, false>(a, s);
 }

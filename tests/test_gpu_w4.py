@@ -222,3 +222,18 @@ def test_decode_step_captured_and_on_another_stream():
         e = float(_tol(x64, s_o.astype(np.float64), 64, np.zeros_like(z), "fp32").max()) / 0.8
         for a, b, t in ((got[2], lp_o, 2 * e + 1e-5), (got[3], H_o, 40 * e + 1e-5), (got[5], lp_o, 2 * e + 1e-5)):
             assert np.abs(host(a) - b).max() <= t
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 16, 17, 33, 49, 64])
+def test_the_same_bits_on_every_call(T, group):
+    """And no NaN, which a register read before it is written would bring now
+    and then."""
+    torch = _torch()
+    for h, V in ((1120, 700), (2048, 700), (5120, 90)):
+        q, s = _head(V, h, group, h)
+        x, p, sc = torch.randn(T, h, device="cuda").bfloat16(), to_dev(_pack(q)), to_dev_bits(s, "bf16")
+        first = _lp().lp_lm_head_w4_logits(x, p, sc, group, out_dtype=torch.float32)
+        assert torch.isfinite(first).all()
+        for _ in range(8):
+            assert torch.equal(_lp().lp_lm_head_w4_logits(x, p, sc, group, out_dtype=torch.float32), first)
