@@ -109,12 +109,18 @@ struct RowRules {
 };
 
 // N bits from position `pos` of a bit array (bit k of the result = pos + k).
-template <int N>
+// BYTES: the position is known to be a multiple of N, N is 8 or 4, and one
+// byte has them all.  Otherwise the word behind is read only if they reach it.
+template <int N, bool BYTES = false>
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int pos) {
+  if (BYTES) {
+    const uint32_t v = reinterpret_cast<const uint8_t*>(words)[pos >> 3];
+    return N == 8 ? v : v >> (pos & 4);
+  }
   const int w = pos >> 5, sh = pos & 31;
-  uint32_t v = words[w] >> sh;
-  if (N > 1 && sh > 32 - N) v |= words[w + 1] << (32 - sh);
-  return v;
+  if (N == 1) return words[w] >> sh;
+  const int more = sh > 32 - N ? 1 : 0;
+  return __builtin_amdgcn_alignbit(words[w + more], words[w], sh);
 }
 
 // x where the bit is set, -inf elsewhere, without a compare.
@@ -131,18 +137,16 @@ __device__ __forceinline__ float grad_of(const RowRules& r, float z, float slope
   return d * slope;
 }
 
-// What N streamed columns give (slice-relative `rel`, row column `col`):
+// What N streamed columns from `col` give; `allowed` and `touched` hold a bit
+// per column, bit 0 first (only looked at where the row has such bits):
 //   kProcess  -inf where not allowed; touched columns keep their raw value
 //   kScore    touched columns and those not allowed become -inf (weigh nothing)
 //   kGrad     their gradient, 0 where not allowed
 template <int OP, int N>
-__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, int rel, int col) {
+__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched, int col) {
   uint32_t live = ~0u;
-  if (r.allowed) live = bits_at<N>(r.allowed, col);
-  if (r.bits) {
-    const uint32_t touched = bits_at<N>(r.bits, rel);
-    live = OP == kProcess ? live | touched : live & ~touched;
-  }
+  if (r.allowed) live = allowed;
+  if (r.bits) live = OP == kProcess ? live | touched : live & ~touched;
   if (OP == kGrad) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -212,6 +216,53 @@ __device__ __forceinline__ void store_unscored(const RulesArgs& a, int64_t row) 
   a.logprob[row] = 0.f;
   if (a.entropy_out) a.entropy_out[row] = 0.f;
   if (a.lse_out) a.lse_out[row] = 0.f;
+}
+
+// The slice's 16-byte vectors, U of them in flight a lane.  The bits are
+// loaded ahead of the vectors, so that the first vector's work waits for
+// nothing issued behind it.  ALIGNED: head == 0, and a vector's bits are one byte.
+template <class Tr, int OP, int NT, int U, bool ALIGNED>
+__device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, const char* xp, char* op, int nvec, int head,
+                                               int c0) {
+  constexpr int P = Tr::kPerVec;
+  const u32x4* vp = reinterpret_cast<const u32x4*>(xp + head * Tr::kBytes);
+  u32x4* wp = reinterpret_cast<u32x4*>(op + head * Tr::kBytes);
+  int i = threadIdx.x;
+  for (; i + (U - 1) * NT < nvec; i += U * NT) {
+    uint32_t ok[U], hit[U];
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) ok[u] = hit[u] = 0;
+    if (r.allowed) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) ok[u] = bits_at<P, ALIGNED>(r.allowed, c0 + head + (i + u * NT) * P);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(vp + i + u * NT);
+    if (r.bits) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) hit[u] = bits_at<P, ALIGNED>(r.bits, head + (i + u * NT) * P);
+    }
+    float z[U * P];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Tr::unpack(w[u], z + u * P);
+      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u], c0 + head + (i + u * NT) * P);
+      if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
+    }
+    if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
+  }
+  for (; i < nvec; i += NT) {
+    const int rel = head + i * P;
+    const uint32_t ok = r.allowed ? bits_at<P, ALIGNED>(r.allowed, c0 + rel) : 0u;
+    float z[P];
+    Tr::unpack(__builtin_nontemporal_load(vp + i), z);
+    stream_cols<OP, P>(r, z, ok, r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, c0 + rel);
+    if (OP == kScore)
+      stat_push_masked<P, P>(st, z, r.c);
+    else
+      __builtin_nontemporal_store(Tr::pack(z), wp + i);
+  }
 }
 
 template <class Tr, int OP, int NT, int U>
@@ -383,39 +434,17 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   Stat st = stat_empty();
   auto single = [&](int j) {
     float z = Tr::load1(xp, j);
-    stream_cols<OP, 1>(r, &z, j, c0 + j);
+    stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u, c0 + j);
     if (OP == kScore)
       stat_push_masked<1, 1>(st, &z, r.c);
     else
       Tr::store1(op, j, z);
   };
   if (tid < sp.head) single(tid);
-  const u32x4* vp = reinterpret_cast<const u32x4*>(xp + sp.head * Tr::kBytes);
-  u32x4* wp = reinterpret_cast<u32x4*>(op + sp.head * Tr::kBytes);
-  int i = tid;
-  for (; i + (U - 1) * NT < sp.nvec; i += U * NT) {
-    u32x4 w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(vp + i + u * NT);
-    float z[U * P];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      Tr::unpack(w[u], z + u * P);
-      const int rel = sp.head + (i + u * NT) * P;
-      stream_cols<OP, P>(r, z + u * P, rel, c0 + rel);
-      if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
-    }
-    if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
-  }
-  for (; i < sp.nvec; i += NT) {
-    float z[P];
-    Tr::unpack(__builtin_nontemporal_load(vp + i), z);
-    stream_cols<OP, P>(r, z, sp.head + i * P, c0 + sp.head + i * P);
-    if (OP == kScore)
-      stat_push_masked<P, P>(st, z, r.c);
-    else
-      __builtin_nontemporal_store(Tr::pack(z), wp + i);
-  }
+  if (sp.head == 0)
+    stream_vectors<Tr, OP, NT, U, true>(r, st, xp, op, sp.nvec, 0, c0);
+  else
+    stream_vectors<Tr, OP, NT, U, false>(r, st, xp, op, sp.nvec, sp.head, c0);
   for (int j = n - sp.tail + tid; j < n; j += NT) single(j);
 
   // Touched columns, after the stream has stored what lies around them.
@@ -516,7 +545,7 @@ hipError_t launch_rules_nt(RulesArgs a, const char* name, hipStream_t s) {
     const int64_t rows = a.T - r0 < rows_per ? a.T - r0 : rows_per;
     a.row0 = r0;
     TimedLaunch tl(name, s);
-    hipLaunchKernelGGL((k_rules<Tr, OP, NT, 2>), dim3(static_cast<unsigned>(rows * a.nslices)), dim3(NT), lds, s, a);
+    hipLaunchKernelGGL((k_rules<Tr, OP, NT, OP == kScore ? 4 : 2>), dim3(static_cast<unsigned>(rows * a.nslices)), dim3(NT), lds, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
