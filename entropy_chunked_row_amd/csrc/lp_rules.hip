@@ -139,14 +139,16 @@ __device__ __forceinline__ float grad_of(const RowRules& r, float z, float slope
 
 // What N streamed columns from `col` give; `allowed` and `touched` hold a bit
 // per column, bit 0 first (only looked at where the row has such bits):
-//   kProcess  -inf where not allowed; touched columns keep their raw value
+//   kProcess  -inf where not allowed, else the raw value
 //   kScore    touched columns and those not allowed become -inf (weigh nothing)
 //   kGrad     their gradient, 0 where not allowed
+// What kProcess and kGrad give for a touched column is written over later; in
+// place it may only be the raw value or, where not allowed, the final -inf.
 template <int OP, int N>
 __device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched, int col) {
   uint32_t live = ~0u;
   if (r.allowed) live = allowed;
-  if (r.bits) live = OP == kProcess ? live | touched : live & ~touched;
+  if (OP == kScore && r.bits) live &= ~touched;
   if (OP == kGrad) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -238,8 +240,8 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
       for (int u = 0; u < U; ++u) ok[u] = bits_at<P, ALIGNED>(r.allowed, c0 + head + (i + u * NT) * P);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(vp + i + u * NT);
-    if (r.bits) {
+    for (int u = 0; u < U; ++u) w[u] = vp[i + u * NT];
+    if (OP == kScore && r.bits) {
 #pragma unroll
       for (int u = 0; u < U; ++u) hit[u] = bits_at<P, ALIGNED>(r.bits, head + (i + u * NT) * P);
     }
@@ -256,8 +258,8 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
     const int rel = head + i * P;
     const uint32_t ok = r.allowed ? bits_at<P, ALIGNED>(r.allowed, c0 + rel) : 0u;
     float z[P];
-    Tr::unpack(__builtin_nontemporal_load(vp + i), z);
-    stream_cols<OP, P>(r, z, ok, r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, c0 + rel);
+    Tr::unpack(vp[i], z);
+    stream_cols<OP, P>(r, z, ok, OP == kScore && r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, c0 + rel);
     if (OP == kScore)
       stat_push_masked<P, P>(st, z, r.c);
     else
@@ -353,6 +355,19 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     if (k > 2) rk += __popc(q.z);
     return rk;
   };
+  // The first kHeld x NT tokens stay in registers between the two steps.
+  constexpr int kHeld = 8;
+  int held[kHeld];  // column within the slice, -1: none
+  auto note = [&](int j, int64_t i, uint32_t r0) {
+    const uint32_t k = rank_of(j) - r0;
+    if (k < static_cast<uint32_t>(ranks)) {
+      list[k] = j;
+      if (i < prompt)
+        atomicOr(cnt + k, kPromptBit);
+      else
+        atomicAdd(cnt + k, 1u);
+    }
+  };
   // Step 2 for ranks [r0, r0 + ranks).
   auto count = [&](uint32_t r0) {
     for (int i = tid; i < ranks; i += NT) {
@@ -360,19 +375,12 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
       if (nb > 0) bidx[i] = 0;
     }
     __syncthreads();
-#pragma unroll 4
-    for (int64_t i = tid; i < len; i += NT) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (held[k] >= 0) note(held[k], tid + k * NT, r0);
+    for (int64_t i = tid + kHeld * NT; i < len; i += NT) {
       int j;
-      if (in_slice(tok[i], j)) {
-        const uint32_t k = rank_of(j) - r0;
-        if (k < static_cast<uint32_t>(ranks)) {
-          list[k] = j;
-          if (i < prompt)
-            atomicOr(cnt + k, kPromptBit);
-          else
-            atomicAdd(cnt + k, 1u);
-        }
-      }
+      if (in_slice(tok[i], j)) note(j, i, r0);
     }
     for (int64_t i = tid; i < nb; i += NT) {
       int j;
@@ -388,11 +396,22 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   };
 
   if (len > 0 || nb > 0) {  // the same for the whole workgroup
+    // loaded while the bits are cleared; a position past the end reads the
+    // first token and drops it
+    int32_t t[kHeld];
+    if (len > 0) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) t[k] = tok[tid + k * NT < len ? tid + k * NT : 0];
+    }
     for (int i = tid; i < a.slice / 128; i += NT) reinterpret_cast<u32x4*>(bits)[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
     int j;
-#pragma unroll 4
-    for (int64_t i = tid; i < len; i += NT)
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      held[k] = tid + k * NT < len && in_slice(t[k], j) ? j : -1;
+      if (held[k] >= 0) atomicOr(bits + (held[k] >> 5), 1u << (held[k] & 31));
+    }
+    for (int64_t i = tid + kHeld * NT; i < len; i += NT)
       if (in_slice(tok[i], j)) atomicOr(bits + (j >> 5), 1u << (j & 31));
     for (int64_t i = tid; i < nb; i += NT)
       if (in_slice(btok[i], j)) atomicOr(bits + (j >> 5), 1u << (j & 31));
