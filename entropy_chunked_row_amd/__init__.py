@@ -11,7 +11,6 @@ kernels; if liblp.so is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -29,9 +28,15 @@ __all__ = [
 ]
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -456,7 +461,17 @@ def lp_lm_head_kl_backward(student_hidden, student_weight, teacher_hidden, teach
 # logit rules
 # ---------------------------------------------------------------------------
 
-_NO_SCOPE = contextlib.nullcontext()
+class _NoScope:
+    """No context: `device` is current already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SCOPE = _NoScope()
 
 
 def _scope(device, stream):
@@ -468,9 +483,23 @@ def _scope(device, stream):
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, expected {device}")
         return torch.cuda.stream(stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
     return _NO_SCOPE
+
+
+def _raw_stream(device, stream):
+    """hipStream_t of `stream`, or of `device`'s current stream (looked up without making a Stream object, which
+    costs a small call more than its launch)."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _same_device(device, named):
+    """Every (name, tensor) lives on `device`."""
+    index = device.index
+    for name, t in named:
+        if t is not None and (not t.is_cuda or t.get_device() != index):
+            _on(device, **{name: t})
 
 
 class LogitRules:
@@ -488,20 +517,15 @@ class LogitRules:
     the device by each call that takes the rules.  The tensors are kept, not
     copied: what they hold when a call runs on the stream is what it reads."""
 
-    __slots__ = ("c", "_kept", "_per_row", "_buffers", "_offsets", "_words")
+    __slots__ = ("c", "_per_row", "_whole", "_buffers", "_offsets", "_words")
 
     def __init__(self, tokens=None, hist_len=None, prompt_len=None, row_seq=None, repetition=None, frequency=None,
                  presence=None, bias_offsets=None, bias_tokens=None, bias_values=None, allowed=None):
         torch = _torch()
         i32, f32 = torch.int32, torch.float32
-        c = _lib.LogitRulesC()
-        per_row = []
-        for name, t, dt in (("hist_len", hist_len, i32), ("prompt_len", prompt_len, i32), ("row_buffer", row_seq, i32),
-                            ("repetition", repetition, f32), ("frequency", frequency, f32), ("presence", presence, f32)):
-            if t is not None:
-                _vec(t, "row_seq" if name == "row_buffer" else name, dt)
-                per_row.append(("row_seq" if name == "row_buffer" else name, t))
-                setattr(c, name, t.data_ptr())
+        self.c = c = _lib.LogitRulesC()
+        self._per_row = per_row = []
+        self._whole = whole = []
         self._buffers = None
         if tokens is not None:
             if tokens.dtype != i32:
@@ -509,24 +533,44 @@ class LogitRules:
             ld = _rows(tokens, "tokens")
             if hist_len is None:
                 raise ValueError("tokens need hist_len")
+            whole.append(("tokens", tokens))
             # no buffers, or buffers of no tokens: nobody has a history
             if tokens.numel():
                 c.tokens, c.buffers, c.ld_tokens, c.max_len = tokens.data_ptr(), tokens.size(0), ld, tokens.size(1)
-                self._buffers = None if row_seq is not None else tokens.size(0)
-            else:
-                c.repetition = c.frequency = c.presence = None
+                if row_seq is None:
+                    self._buffers = tokens.size(0)
+            for name, t, dt in (("hist_len", hist_len, i32), ("prompt_len", prompt_len, i32), ("row_seq", row_seq, i32),
+                                ("repetition", repetition, f32), ("frequency", frequency, f32),
+                                ("presence", presence, f32)):
+                if t is not None:
+                    if t.dtype != dt or not t.is_contiguous():
+                        _vec(t, name, dt)
+                    per_row.append((name, t))
+            if c.tokens:
+                c.hist_len = hist_len.data_ptr()
+                if prompt_len is not None:
+                    c.prompt_len = prompt_len.data_ptr()
+                if row_seq is not None:
+                    c.row_buffer = row_seq.data_ptr()
+                if repetition is not None:
+                    c.repetition = repetition.data_ptr()
+                if frequency is not None:
+                    c.frequency = frequency.data_ptr()
+                if presence is not None:
+                    c.presence = presence.data_ptr()
         elif any(t is not None for t in (hist_len, prompt_len, row_seq, repetition, frequency, presence)):
             raise ValueError("penalties need tokens and hist_len")
         self._offsets = bias_offsets
         if bias_offsets is not None:
-            _vec(bias_offsets, "bias_offsets", torch.int64)
             if bias_tokens is None or bias_values is None:
                 raise ValueError("biases need bias_tokens and bias_values")
+            _vec(bias_offsets, "bias_offsets", torch.int64)
             _vec(bias_tokens, "bias_tokens", i32)
-            _vec(bias_values, "bias_values", f32, bias_tokens.numel())
-            c.bias_count = bias_tokens.numel()
-            c.bias_offsets = bias_offsets.data_ptr()
+            n = bias_tokens.numel()
+            _vec(bias_values, "bias_values", f32, n)
+            c.bias_offsets, c.bias_count = bias_offsets.data_ptr(), n
             c.bias_tokens, c.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
+            whole += (("bias_offsets", bias_offsets), ("bias_tokens", bias_tokens), ("bias_values", bias_values))
         elif bias_tokens is not None or bias_values is not None:
             raise ValueError("biases need bias_offsets")
         self._words = allowed
@@ -535,11 +579,7 @@ class LogitRules:
                 raise TypeError(f"allowed must be int32 or uint32, got {allowed.dtype}")
             c.ld_allowed = _rows(allowed, "allowed")
             c.allowed = allowed.data_ptr()
-        self.c = c
-        self._per_row = per_row
-        self._kept = [(n, t) for n, t in (("tokens", tokens), ("bias_offsets", bias_offsets),
-                                          ("bias_tokens", bias_tokens), ("bias_values", bias_values),
-                                          ("allowed", allowed)) if t is not None]
+            whole.append(("allowed", allowed))
 
     def _check(self, T, V, device):
         """The ctypes argument for a call on T rows of V columns on `device`."""
@@ -553,12 +593,8 @@ class LogitRules:
         w = self._words
         if w is not None and (w.size(0) != T or w.size(1) < (V + 31) // 32):
             raise ValueError(f"allowed must be [{T}, >= {(V + 31) // 32}], got {list(w.shape)}")
-        for name, t in self._per_row:
-            if t.device != device:
-                _on(device, **{name: t})
-        for name, t in self._kept:
-            if t.device != device:
-                _on(device, **{name: t})
+        _same_device(device, self._per_row)
+        _same_device(device, self._whole)
         return ctypes.byref(self.c)
 
 
@@ -582,12 +618,12 @@ def lp_process_logits(logits, rules, mask=None, *, out=None, stream=None):
         raise ValueError("out must have the logits' shape and dtype")
     ld_out = V if out is None else _rows(out, "out")
     dev = logits.device
-    _on(dev, logits=logits, mask=mask, out=out)
+    _same_device(dev, (("logits", logits), ("mask", mask), ("out", out)))
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((T, V), dtype=logits.dtype, device=dev)
         st = lib.lp_process_logits(_ptr(logits), dtype, T, V, ld, c_rules, _ptr(mask), _ptr(out), ld_out,
-                                   _stream(stream))
+                                   _raw_stream(dev, stream))
     check("lp_process_logits", st)
     return out
 
@@ -606,7 +642,7 @@ def lp_processed_logprobs_entropy(logits, rules, targets, mask=None, temperature
     targets = _vec(targets, "targets", torch.int64, T)
     mask = _vec(mask, "mask", torch.uint8, T)
     dev = logits.device
-    _on(dev, logits=logits, targets=targets, mask=mask)
+    _same_device(dev, (("logits", logits), ("targets", targets), ("mask", mask)))
     f32 = dict(dtype=torch.float32, device=dev)
     with _scope(dev, stream):
         lp = torch.empty(T, **f32)
@@ -615,7 +651,7 @@ def lp_processed_logprobs_entropy(logits, rules, targets, mask=None, temperature
         ws, ws_bytes = _workspace(lp_processed_workspace_bytes(T, V), dev, workspace)
         st = lib.lp_processed_logprobs_entropy(_ptr(logits), dtype, T, V, ld, c_rules, _ptr(targets), _ptr(mask),
                                                float(temperature), _ptr(lp), _ptr(H), _ptr(lse), _ptr(ws), ws_bytes,
-                                               _stream(stream))
+                                               _raw_stream(dev, stream))
     check("lp_processed_logprobs_entropy", st)
     return lp, H, lse
 
@@ -637,14 +673,14 @@ def lp_processed_logprobs_entropy_backward(logits, rules, targets, mask, tempera
         raise ValueError("grad_logits must have the logits' shape and dtype")
     ld_grad = V if grad_logits is None else _rows(grad_logits, "grad_logits")
     dev = logits.device
-    _on(dev, logits=logits, targets=targets, mask=mask, lse=lse, entropy=entropy, grad_logprob=grad_logprob,
-        grad_entropy=grad_entropy, grad_logits=grad_logits)
+    _same_device(dev, (("logits", logits), ("targets", targets), ("mask", mask), ("lse", lse), ("entropy", entropy),
+                       ("grad_logprob", grad_logprob), ("grad_entropy", grad_entropy), ("grad_logits", grad_logits)))
     with _scope(dev, stream):
         if grad_logits is None:
             grad_logits = torch.empty((T, V), dtype=logits.dtype, device=dev)
         st = lib.lp_processed_logprobs_entropy_backward(
             _ptr(logits), dtype, T, V, ld, c_rules, _ptr(targets), _ptr(mask), float(temperature), _ptr(lse),
-            _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(grad_logits), ld_grad, _stream(stream))
+            _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(grad_logits), ld_grad, _raw_stream(dev, stream))
     check("lp_processed_logprobs_entropy_backward", st)
     return grad_logits
 
@@ -667,12 +703,12 @@ def lp_embedding(weight, tokens, scale: float = 1.0, *, out=None, stream=None):
         raise ValueError(f"out must be [{N}, {h}] of the weight's dtype")
     ld_out = h if out is None else _rows(out, "out")
     dev = weight.device
-    _on(dev, weight=weight, tokens=tokens, out=out)
+    _same_device(dev, (("weight", weight), ("tokens", tokens), ("out", out)))
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((*tokens.shape, h), dtype=weight.dtype, device=dev)
         st = lib.lp_embedding(_ptr(weight), dtype, V, h, ld_w, _ptr(tokens), N, float(scale), _ptr(out), ld_out,
-                              _stream(stream))
+                              _raw_stream(dev, stream))
     check("lp_embedding", st)
     return out
 
@@ -704,13 +740,14 @@ def lp_embedding_backward(grad_out, tokens, V: int, scale: float = 1.0, *, grad_
         if grad_weight.shape != (V, h):
             raise ValueError(f"grad_weight must be [{V}, {h}]")
     dev = grad_out.device
-    _on(dev, grad_out=grad_out, tokens=tokens, grad_weight=grad_weight)
+    _same_device(dev, (("grad_out", grad_out), ("tokens", tokens), ("grad_weight", grad_weight)))
     with _scope(dev, stream):
         if grad_weight is None:
             grad_weight = torch.empty((V, h), dtype=torch.float32, device=dev)
         ws, ws_bytes = _workspace(lp_embedding_workspace_bytes(N, h, V), dev, workspace)
         st = lib.lp_embedding_backward(_ptr(grad_out), dtype, N, h, ld_g, _ptr(tokens), V, float(scale),
-                                       1 if accumulate else 0, _ptr(grad_weight), _ptr(ws), ws_bytes, _stream(stream))
+                                       1 if accumulate else 0, _ptr(grad_weight), _ptr(ws), ws_bytes,
+                                       _raw_stream(dev, stream))
     check("lp_embedding_backward", st)
     return grad_weight
 
@@ -733,14 +770,14 @@ def lp_lm_head_w4_quantize(weight, group: int = 128, *, packed=None, scales=None
         if t is not None and (t.dtype != dt or t.dim() != 2 or t.shape != (V, n)):
             raise ValueError(f"{name} must be [{V}, {n}] {dt}")
     dev = weight.device
-    _on(dev, weight=weight, packed=packed, scales=scales)
+    _same_device(dev, (("weight", weight), ("packed", packed), ("scales", scales)))
     with _scope(dev, stream):
         if packed is None:
             packed = torch.empty((V, h // 2), dtype=torch.uint8, device=dev)
         if scales is None:
             scales = torch.empty((V, groups), dtype=torch.bfloat16, device=dev)
         st = lib.lp_lm_head_w4_quantize(_ptr(weight), dtype, V, h, ld_w, group, _ptr(packed), _rows(packed, "packed"),
-                                        _ptr(scales), _rows(scales, "scales"), _stream(stream))
+                                        _ptr(scales), _rows(scales, "scales"), _raw_stream(dev, stream))
     check("lp_lm_head_w4_quantize", st)
     return packed, scales
 
@@ -771,11 +808,11 @@ def lp_lm_head_w4_logits(hidden, packed, scales, group: int = 128, *, out_dtype=
     elif out_dtype is None:
         out_dtype = hidden.dtype
     dev = hidden.device
-    _on(dev, hidden=hidden, packed=packed, scales=scales, out=out)
+    _same_device(dev, (("hidden", hidden), ("packed", packed), ("scales", scales), ("out", out)))
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((T, V), dtype=out_dtype, device=dev)
         st = lib.lp_lm_head_w4_logits(_ptr(hidden), dtype, T, h, ld_h, _ptr(packed), ld_p, _ptr(scales), ld_s, V, group,
-                                      _ptr(out), _dtype_code(out), _rows(out, "out"), _stream(stream))
+                                      _ptr(out), _dtype_code(out), _rows(out, "out"), _raw_stream(dev, stream))
     check("lp_lm_head_w4_logits", st)
     return out

@@ -129,31 +129,32 @@ __device__ __forceinline__ float keep_if(uint32_t bits, int k, float x) {
   return __uint_as_float((m & __float_as_uint(x)) | (~m & 0xff800000u));
 }
 
-__device__ __forceinline__ float grad_of(const RowRules& r, float z, float slope, int64_t col) {
+// The target's own term, gy, is added by its caller.
+__device__ __forceinline__ float grad_of(const RowRules& r, float z) {
   const float t = fmaf(z, r.c, r.nlse2);
   const float p = fast_exp2(t);
-  float d = -p * fmaf(r.gb, fmaxf(t, kNoWeight), r.ga);
-  if (col == r.y) d += r.gy;
-  return d * slope;
+  return -p * fmaf(r.gb, fmaxf(t, kNoWeight), r.ga);
 }
 
 // What N streamed columns from `col` give; `allowed` and `touched` hold a bit
 // per column, bit 0 first (only looked at where the row has such bits):
 //   kProcess  -inf where not allowed, else the raw value
 //   kScore    touched columns and those not allowed become -inf (weigh nothing)
-//   kGrad     their gradient, 0 where not allowed
+//   kGrad     their gradient without the target's own term, 0 where not allowed
 // What kProcess and kGrad give for a touched column is written over later; in
 // place it may only be the raw value or, where not allowed, the final -inf.
 template <int OP, int N>
-__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched, int col) {
+__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched) {
   uint32_t live = ~0u;
   if (r.allowed) live = allowed;
   if (OP == kScore && r.bits) live &= ~touched;
   if (OP == kGrad) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float d = grad_of(r, z[k], 1.f, col + k);
-      z[k] = (live >> k) & 1u ? d : 0.f;
+      const float d = grad_of(r, z[k]);
+      // bits, not a product: a NaN beside the grammar gives 0 too
+      const uint32_t m = static_cast<uint32_t>(static_cast<int32_t>(live << (31 - k)) >> 31);
+      z[k] = r.allowed ? __uint_as_float(__float_as_uint(d) & m) : d;
     }
   } else if (r.allowed || (OP == kScore && r.bits)) {
 #pragma unroll
@@ -249,7 +250,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Tr::unpack(w[u], z + u * P);
-      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u], c0 + head + (i + u * NT) * P);
+      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u]);
       if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
     }
     if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
@@ -259,7 +260,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
     const uint32_t ok = r.allowed ? bits_at<P, ALIGNED>(r.allowed, c0 + rel) : 0u;
     float z[P];
     Tr::unpack(vp[i], z);
-    stream_cols<OP, P>(r, z, ok, OP == kScore && r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, c0 + rel);
+    stream_cols<OP, P>(r, z, ok, OP == kScore && r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u);
     if (OP == kScore)
       stat_push_masked<P, P>(st, z, r.c);
     else
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   Stat st = stat_empty();
   auto single = [&](int j) {
     float z = Tr::load1(xp, j);
-    stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u, c0 + j);
+    stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u);
     if (OP == kScore)
       stat_push_masked<1, 1>(st, &z, r.c);
     else
@@ -466,14 +467,22 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     stream_vectors<Tr, OP, NT, U, false>(r, st, xp, op, sp.nvec, sp.head, c0);
   for (int j = n - sp.tail + tid; j < n; j += NT) single(j);
 
-  // Touched columns, after the stream has stored what lies around them.
+  // Touched columns and the target's, after the stream has stored what lies
+  // around them.
+  const bool mine = OP != kProcess && r.y >= c0 && r.y < c0 + n;  // the target is in this slice
+  if (OP != kScore && (touched || mine)) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stream's stores are done
+    __syncthreads();
+  }
+  if (OP == kGrad && mine && tid == 0) {
+    const int j = static_cast<int>(r.y) - c0;
+    if (!(r.bits && (bits_at<1>(bits, j) & 1u)) && !(r.allowed && !(bits_at<1>(r.allowed, c0 + j) & 1u)))
+      Tr::store1(op, j, grad_of(r, Tr::load1(xp, j)) + r.gy);
+  }
   for (uint32_t r0 = 0; r0 < touched; r0 += ranks) {
     if (r0 > 0) {
       __syncthreads();
       count(r0);
-    } else if (OP != kScore) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stream's stores are done
-      __syncthreads();
     }
     const int m = touched - r0 < static_cast<uint32_t>(ranks) ? static_cast<int>(touched - r0) : ranks;
     for (int k = tid; k < m; k += NT) {
@@ -484,7 +493,8 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
         stat_push_masked<1, 1>(st, &z, r.c);
         if (c0 + j == r.y) zy = z;
       } else {
-        Tr::store1(op, j, OP == kProcess ? z : ok ? grad_of(r, z, slope, c0 + j) : 0.f);
+        if (OP == kGrad) z = ok ? (grad_of(r, z) + (c0 + j == r.y ? r.gy : 0.f)) * slope : 0.f;
+        Tr::store1(op, j, z);
       }
     }
   }
@@ -496,7 +506,6 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     if (tid == 0) {
 #pragma unroll
       for (int k = 1; k < NT / 64; ++k) st = stat_merge_nan(st, sm[k]);
-      const bool mine = r.y >= c0 && r.y < c0 + n;
       float z = 0.f;
       if (mine) {
         const int j = static_cast<int>(r.y) - c0;

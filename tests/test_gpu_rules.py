@@ -277,7 +277,7 @@ def test_captured_and_on_another_stream():
     cs = [Rules(5, 9001, "fp16", seed=s, empty_row=False) for s in (1, 2, 3)]
     first, rules = cs[0].device()
     x = first.clone()
-    kept = {n: t for n, t in rules._kept + rules._per_row}
+    kept = {n: t for n, t in rules._whole + rules._per_row}
     y = to_dev(cs[0].targets)
     g = torch.linspace(-1, 1, 5, device="cuda")
 
