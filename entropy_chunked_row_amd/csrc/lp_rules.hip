@@ -18,9 +18,14 @@
 //      is that count plus a popcount;
 //   2. counts by rank: a word per touched column (bit 31: stands in the prompt; below: times in
 //      the output), its column, and the last bias entry that names it;
-//   3. streams the slice, 16 bytes a lane, where the bitmap and the grammar's
-//      bits decide what a column gives, without branches;
-//   4. deals with the touched columns one by one, kRanks at a time.
+//   3. computes what touched columns give: a thread each, from a gathered
+//      logit, the first kRanks of them before the stream, into LDS;
+//   4. streams the slice, 16 bytes a lane; the grammar's bits decide what an
+//      untouched column gives, and touched ones are filled in from step 3.
+//      Scoring only leaves them out of the stream and adds them by themselves;
+//      the others store whole vectors this way (storing touched columns singly
+//      behind the stream cost 100 of 600 us at 4096 x 151936: each is a
+//      partial write of memory that the stream's store has left the cache for).
 // Counts are integers and the bias entry is a maximum, so the order of the
 // LDS atomics does not change any result.  Nothing of size V is kept between
 // calls and no dense count matrix passes through memory (it would cost 4 bytes
@@ -102,6 +107,9 @@ struct RowRules {
   const float* values;      // the row's bias values
   const uint32_t* allowed;  // the row's grammar, or null
   const uint32_t* bits;     // LDS: touched columns of the slice, or null
+  const uint32_t* pre;      // LDS: bits before each 128 columns
+  const uint32_t* given;    // LDS: what the touched columns of ranks < ranks give (fp32 bits)
+  int ranks;
   float c;
   // gradient: d = [j = y] gy - p_j (ga + gb t_j), t_j the log2 of p_j
   float nlse2, ga, gb, gy;
@@ -136,15 +144,29 @@ __device__ __forceinline__ float grad_of(const RowRules& r, float z) {
   return -p * fmaf(r.gb, fmaxf(t, kNoWeight), r.ga);
 }
 
-// What N streamed columns from `col` give; `allowed` and `touched` hold a bit
-// per column, bit 0 first (only looked at where the row has such bits):
+// Touched columns before slice column j.
+__device__ __forceinline__ uint32_t rank_of(const uint32_t* bits, const uint32_t* pre, int j) {
+  const u32x4 q = *reinterpret_cast<const u32x4*>(bits + (j >> 7) * 4);
+  const int k = (j >> 5) & 3;
+  const uint32_t word = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
+  uint32_t rk = pre[j >> 7] + __popc(word & ((1u << (j & 31)) - 1u));
+  if (k > 0) rk += __popc(q.x);
+  if (k > 1) rk += __popc(q.y);
+  if (k > 2) rk += __popc(q.z);
+  return rk;
+}
+
+// What N streamed columns give, from slice column `rel` on; `allowed` and
+// `touched` hold a bit per column, bit 0 first (only looked at where the row
+// has such bits):
 //   kProcess  -inf where not allowed, else the raw value
 //   kScore    touched columns and those not allowed become -inf (weigh nothing)
 //   kGrad     their gradient without the target's own term, 0 where not allowed
-// What kProcess and kGrad give for a touched column is written over later; in
-// place it may only be the raw value or, where not allowed, the final -inf.
+// and for kProcess and kGrad touched columns what step 3 gave them.  Those of
+// later ranks are written over later; in place they may only be the raw value
+// or, where not allowed, the final -inf.
 template <int OP, int N>
-__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched) {
+__device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched, int rel) {
   uint32_t live = ~0u;
   if (r.allowed) live = allowed;
   if (OP == kScore && r.bits) live &= ~touched;
@@ -159,6 +181,18 @@ __device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_
   } else if (r.allowed || (OP == kScore && r.bits)) {
 #pragma unroll
     for (int k = 0; k < N; ++k) z[k] = keep_if(live, k, z[k]);
+  }
+  if (OP != kScore && (touched & ((1u << N) - 1u))) {
+    const int first = static_cast<int>(rank_of(r.bits, r.pre, rel));
+    float got[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int at = first + __popc(touched & ((1u << k) - 1u));
+      got[k] = __uint_as_float(r.given[at < r.ranks ? at : 0]);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (((touched >> k) & 1u) && first + __popc(touched & ((1u << k) - 1u)) < r.ranks) z[k] = got[k];
   }
 }
 
@@ -242,7 +276,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = vp[i + u * NT];
-    if (OP == kScore && r.bits) {
+    if (r.bits) {
 #pragma unroll
       for (int u = 0; u < U; ++u) hit[u] = bits_at<P, ALIGNED>(r.bits, head + (i + u * NT) * P);
     }
@@ -250,7 +284,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Tr::unpack(w[u], z + u * P);
-      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u]);
+      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u], head + (i + u * NT) * P);
       if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
     }
     if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
@@ -260,7 +294,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
     const uint32_t ok = r.allowed ? bits_at<P, ALIGNED>(r.allowed, c0 + rel) : 0u;
     float z[P];
     Tr::unpack(vp[i], z);
-    stream_cols<OP, P>(r, z, ok, OP == kScore && r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u);
+    stream_cols<OP, P>(r, z, ok, r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, rel);
     if (OP == kScore)
       stat_push_masked<P, P>(st, z, r.c);
     else
@@ -302,6 +336,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   r.values = nullptr;
   r.allowed = a.allowed ? a.allowed + row * a.ld_allowed : nullptr;
   r.bits = nullptr;
+  r.pre = r.given = nullptr;
   r.c = a.c;
   if (OP == kGrad) {
     const float g = a.grad_logprob[row] * a.inv_tau;
@@ -346,21 +381,11 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     j = static_cast<int>(d);
     return d >= 0 && d < n;
   };
-  auto rank_of = [&](int j) {
-    const u32x4 q = *reinterpret_cast<const u32x4*>(bits + (j >> 7) * 4);
-    const int k = (j >> 5) & 3;
-    const uint32_t word = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
-    uint32_t rk = pre[j >> 7] + __popc(word & ((1u << (j & 31)) - 1u));
-    if (k > 0) rk += __popc(q.x);
-    if (k > 1) rk += __popc(q.y);
-    if (k > 2) rk += __popc(q.z);
-    return rk;
-  };
   // The first kHeld x NT tokens stay in registers between the two steps.
   constexpr int kHeld = 8;
   int held[kHeld];  // column within the slice, -1: none
   auto note = [&](int j, int64_t i, uint32_t r0) {
-    const uint32_t k = rank_of(j) - r0;
+    const uint32_t k = rank_of(bits, pre, j) - r0;
     if (k < static_cast<uint32_t>(ranks)) {
       list[k] = j;
       if (i < prompt)
@@ -386,7 +411,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     for (int64_t i = tid; i < nb; i += NT) {
       int j;
       if (in_slice(btok[i], j)) {
-        const uint32_t k = rank_of(j) - r0;
+        const uint32_t k = rank_of(bits, pre, j) - r0;
         if (k < static_cast<uint32_t>(ranks)) {
           list[k] = j;
           atomicMax(bidx + k, static_cast<uint32_t>(i) + 1u);  // the last entry listed counts
@@ -443,6 +468,26 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     }
   }
 
+  // What the touched column of rank r0 + k gives.
+  auto touched_gives = [&](int k) {
+    const int j = static_cast<int>(list[k]);
+    float z = Tr::load1(xp, j), slope;
+    const bool ok = touched_col(r, cnt[k], nb > 0 ? bidx[k] : 0u, c0 + j, z, slope);
+    if (OP == kGrad) z = ok ? (grad_of(r, z) + (c0 + j == r.y ? r.gy : 0.f)) * slope : 0.f;
+    return z;
+  };
+  if (OP != kScore && touched) {
+    const int m = touched < static_cast<uint32_t>(ranks) ? static_cast<int>(touched) : ranks;
+    for (int k = tid; k < m; k += NT) {
+      const float z = touched_gives(k);
+      cnt[k] = __float_as_uint(z);
+    }
+    r.pre = pre;
+    r.given = cnt;
+    r.ranks = ranks;
+    __syncthreads();
+  }
+
   // Columns [0, head) and the tail go one by one, the rest as 16-byte vectors;
   // where input and output rows differ in their 16-byte phase, all go singly.
   RowSplit<Tr> sp(xp, n);
@@ -454,7 +499,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   Stat st = stat_empty();
   auto single = [&](int j) {
     float z = Tr::load1(xp, j);
-    stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u);
+    stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u, j);
     if (OP == kScore)
       stat_push_masked<1, 1>(st, &z, r.c);
     else
@@ -467,11 +512,10 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     stream_vectors<Tr, OP, NT, U, false>(r, st, xp, op, sp.nvec, sp.head, c0);
   for (int j = n - sp.tail + tid; j < n; j += NT) single(j);
 
-  // Touched columns and the target's, after the stream has stored what lies
-  // around them.
   const bool mine = OP != kProcess && r.y >= c0 && r.y < c0 + n;  // the target is in this slice
-  if (OP != kScore && (touched || mine)) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stream's stores are done
+  // What is stored singly from here on lies between the stream's stores.
+  if (OP != kScore && (mine || touched > static_cast<uint32_t>(ranks))) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // those are done
     __syncthreads();
   }
   if (OP == kGrad && mine && tid == 0) {
@@ -479,21 +523,19 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     if (!(r.bits && (bits_at<1>(bits, j) & 1u)) && !(r.allowed && !(bits_at<1>(r.allowed, c0 + j) & 1u)))
       Tr::store1(op, j, grad_of(r, Tr::load1(xp, j)) + r.gy);
   }
-  for (uint32_t r0 = 0; r0 < touched; r0 += ranks) {
+  for (uint32_t r0 = OP == kScore ? 0 : ranks; r0 < touched; r0 += ranks) {
     if (r0 > 0) {
       __syncthreads();
       count(r0);
     }
     const int m = touched - r0 < static_cast<uint32_t>(ranks) ? static_cast<int>(touched - r0) : ranks;
     for (int k = tid; k < m; k += NT) {
+      const float z = touched_gives(k);
       const int j = static_cast<int>(list[k]);
-      float z = Tr::load1(xp, j), slope;
-      const bool ok = touched_col(r, cnt[k], nb > 0 ? bidx[k] : 0u, c0 + j, z, slope);
       if (OP == kScore) {
         stat_push_masked<1, 1>(st, &z, r.c);
         if (c0 + j == r.y) zy = z;
       } else {
-        if (OP == kGrad) z = ok ? (grad_of(r, z) + (c0 + j == r.y ? r.gy : 0.f)) * slope : 0.f;
         Tr::store1(op, j, z);
       }
     }
