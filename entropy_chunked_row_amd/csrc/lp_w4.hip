@@ -20,6 +20,12 @@
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
+// Measured: one row of 5120 x 151936, groups of 128: 75 us (5.4 TB/s); 8 rows,
+// groups of 64: 90 us; 40 rows of 7168 x 129280, groups of 32: 205 us.  Few rows
+// are bound by HBM (and short of it by the waves' meeting once per 32 rows),
+// many by the vector unit: unpacking and scaling are half of its time there, and the
+// products 0.3 of the matrix unit's.
+
 namespace lp {
 
 namespace {
@@ -443,8 +449,8 @@ done:
 }
 
 // Chunks per range up to which x's registers leave room for two buffers; with
-// groups of 32 the buffers' scales take more (measured at 7168 columns: 328 us
-// spilling, 126 us through k_w4_wide; at 7168 with groups of 128 83 us here, 99 there).
+// groups of 32 the buffers' scales take more (one row of 7168 x 129280: 328 us
+// spilling, 126 us through k_w4_wide; with groups of 128 83 us here, 99 there).
 constexpr int most_chunks(int group) { return group == 32 ? 5 : 7; }
 
 template <class X, int G, bool TAIL>
@@ -474,7 +480,7 @@ template <class X, int G, bool TAIL>
 hipError_t launch_wide(const W4Args& a, hipStream_t s) {
   // grid.y is at most 65535 blocks of 64 rows
   constexpr int64_t kRows = int64_t(65535) * 64;
-  constexpr int NW = 8;
+  constexpr int NW = 8;  // four waves measured the same
   for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
     W4Args b = a;
     b.T = a.T - r0 < kRows ? a.T - r0 : kRows;

@@ -458,7 +458,9 @@ lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, 
  * rounded once to out_dtype.  hidden bf16 or fp16 [T x ld_h] (further LP_ERR_UNSUPPORTED:
  * fp32, ld_h % 8 != 0, not 16-byte aligned), out [T x ld_out] of out_dtype, columns past V left.
  * Up to 64 rows read the head once; more rows read it again for every 64.
- * Needs no workspace.  The result of a row does not depend on the other rows.
+ * Needs no workspace.  The result of a row does not depend on the other rows,
+ * bit for bit.  Sums run on 24 times the values of hidden: rows that hold an
+ * infinity or magnitudes past 2^120 give NaN.
  */
 lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, int64_t h, int64_t ld_h,
                                const void* packed, int64_t ld_packed, const void* scales, int64_t ld_scales, int64_t V,
