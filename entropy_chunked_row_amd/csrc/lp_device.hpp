@@ -141,6 +141,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 struct Bf16 {
   static constexpr int kBytes = 2;
   static constexpr int kPerVec = 8;
+  __device__ static __forceinline__ constexpr uint32_t neg_inf_bits() { return 0xff80u; }
   __device__ static __forceinline__ void unpack(u32x4 w, float* x) {
     x[0] = __uint_as_float(w.x << 16);
     x[1] = __uint_as_float(w.x & 0xffff0000u);
@@ -170,6 +171,7 @@ __device__ __forceinline__ float half_bits_to_float(uint32_t b) {
 struct Fp16 {
   static constexpr int kBytes = 2;
   static constexpr int kPerVec = 8;
+  __device__ static __forceinline__ constexpr uint32_t neg_inf_bits() { return 0xfc00u; }
   __device__ static __forceinline__ void unpack(u32x4 w, float* x) {
     x[0] = half_bits_to_float(w.x & 0xffffu);
     x[1] = half_bits_to_float(w.x >> 16);
@@ -194,6 +196,7 @@ struct Fp16 {
 struct Fp32 {
   static constexpr int kBytes = 4;
   static constexpr int kPerVec = 4;
+  __device__ static __forceinline__ constexpr uint32_t neg_inf_bits() { return 0xff800000u; }
   __device__ static __forceinline__ void unpack(u32x4 w, float* x) {
     x[0] = __uint_as_float(w.x);
     x[1] = __uint_as_float(w.y);

@@ -124,14 +124,9 @@ struct RowRules {
 };
 
 // N bits from position `pos` of a bit array (bit k of the result = pos + k).
-// BYTES: the position is known to be a multiple of N, N is 8 or 4, and one
-// byte has them all.  Otherwise the word behind is read only if they reach it.
-template <int N, bool BYTES = false>
+// The word behind is read only if they reach it.
+template <int N>
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int pos) {
-  if (BYTES) {
-    const uint32_t v = reinterpret_cast<const uint8_t*>(words)[pos >> 3];
-    return N == 8 ? v : v >> (pos & 4);
-  }
   const int w = pos >> 5, sh = pos & 31;
   if (N == 1) return words[w] >> sh;
   const int more = sh > 32 - N ? 1 : 0;
@@ -163,6 +158,32 @@ __device__ __forceinline__ uint32_t rank_of(const uint32_t* bits, const uint32_t
   return rk;
 }
 
+// A bit per column that takes part in the stream.
+template <int OP>
+__device__ __forceinline__ uint32_t live_bits(const RowRules& r, uint32_t allowed, uint32_t touched) {
+  uint32_t live = ~0u;
+  if (r.allowed) live = allowed;
+  if (OP == kScore && r.bits) live &= ~touched;
+  return live;
+}
+
+// -inf over the columns of a vector of 16-bit logits whose bit is not set, two
+// at a time before they are widened: three instructions a pair, where
+// keep_if would take four.
+__device__ __forceinline__ u32x4 mask_vector(u32x4 w, uint32_t live, uint32_t neg_inf_pair) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  live &= 0xffu;
+  const s16x2 both = __builtin_bit_cast(s16x2, live | live << 16);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const s16x2 up = both << s16x2{static_cast<short>(15 - 2 * k), static_cast<short>(14 - 2 * k)};
+    uint32_t m = __builtin_bit_cast(uint32_t, up >> s16x2{15, 15});
+    asm("" : "+v"(m));  // stays a mask: as compares and selects it would be six instructions
+    w[k] = (m & w[k]) | (~m & neg_inf_pair);
+  }
+  return w;
+}
+
 // What N streamed columns give, from slice column `rel` on; `allowed` and
 // `touched` hold a bit per column, bit 0 first (only looked at where the row
 // has such bits):
@@ -172,11 +193,10 @@ __device__ __forceinline__ uint32_t rank_of(const uint32_t* bits, const uint32_t
 // and for kProcess and kGrad touched columns what step 3 gave them.  Those of
 // later ranks are written over later; in place they may only be the raw value
 // or, where not allowed, the final -inf.
-template <int OP, int N>
+// MASKED: the -inf are in place already (mask_vector).
+template <int OP, int N, bool MASKED = false>
 __device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_t allowed, uint32_t touched, int rel) {
-  uint32_t live = ~0u;
-  if (r.allowed) live = allowed;
-  if (OP == kScore && r.bits) live &= ~touched;
+  const uint32_t live = live_bits<OP>(r, allowed, touched);
   if (OP == kGrad) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -185,7 +205,7 @@ __device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_
       const uint32_t m = static_cast<uint32_t>(static_cast<int32_t>(live << (31 - k)) >> 31);
       z[k] = r.allowed ? __uint_as_float(__float_as_uint(d) & m) : d;
     }
-  } else if (r.allowed || (OP == kScore && r.bits)) {
+  } else if (!MASKED && (r.allowed || (OP == kScore && r.bits))) {
 #pragma unroll
     for (int k = 0; k < N; ++k) z[k] = keep_if(live, k, z[k]);
   }
@@ -264,48 +284,62 @@ __device__ __forceinline__ void store_unscored(const RulesArgs& a, int64_t row) 
 
 // The slice's 16-byte vectors, U of them in flight a lane.  The bits are
 // loaded ahead of the vectors, so that the first vector's work waits for
-// nothing issued behind it.  ALIGNED: head == 0, and a vector's bits are one byte.
+// nothing issued behind it.  ALIGNED: head == 0, and a vector's bits are one
+// byte (half of one with fp32).  Addresses are a base that the workgroup shares plus a
+// 32-bit offset: one instruction a load.
 template <class Tr, int OP, int NT, int U, bool ALIGNED>
 __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, const char* xp, char* op, int nvec, int head,
                                                int c0) {
   constexpr int P = Tr::kPerVec;
-  const u32x4* vp = reinterpret_cast<const u32x4*>(xp + head * Tr::kBytes);
-  u32x4* wp = reinterpret_cast<u32x4*>(op + head * Tr::kBytes);
-  int i = threadIdx.x;
-  for (; i + (U - 1) * NT < nvec; i += U * NT) {
+  constexpr bool kPairs = Tr::kBytes == 2 && OP != kGrad;
+  const uint32_t neg_inf_pair = Tr::neg_inf_bits() * 0x10001u;
+  const char* xv = xp + head * Tr::kBytes;
+  char* ov = op + head * Tr::kBytes;
+  const uint8_t* allowed_bytes = reinterpret_cast<const uint8_t*>(r.allowed) + (c0 >> 3);
+  const uint8_t* touched_bytes = reinterpret_cast<const uint8_t*>(r.bits);
+  auto byte_bits = [&](const uint8_t* p, uint32_t i) {
+    return P == 8 ? static_cast<uint32_t>(p[i]) : static_cast<uint32_t>(p[i >> 1]) >> ((i & 1) * 4);
+  };
+  auto allowed_of = [&](uint32_t i) {
+    return ALIGNED ? byte_bits(allowed_bytes, i) : bits_at<P>(r.allowed, c0 + head + static_cast<int>(i) * P);
+  };
+  auto touched_of = [&](uint32_t i) {
+    return ALIGNED ? byte_bits(touched_bytes, i) : bits_at<P>(r.bits, head + static_cast<int>(i) * P);
+  };
+  const bool masked = r.allowed || (OP == kScore && r.bits);
+  auto finish = [&](u32x4 w, float* z, uint32_t ok, uint32_t hit, uint32_t i) {
+    if (kPairs && masked) w = mask_vector(w, live_bits<OP>(r, ok, hit), neg_inf_pair);
+    Tr::unpack(w, z);
+    stream_cols<OP, P, kPairs>(r, z, ok, hit, head + static_cast<int>(i) * P);
+    if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z), reinterpret_cast<u32x4*>(ov + i * 16u));
+  };
+  uint32_t i = threadIdx.x;
+  const uint32_t n = nvec;
+  for (; i + (U - 1) * NT < n; i += U * NT) {
     uint32_t ok[U], hit[U];
     u32x4 w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) ok[u] = hit[u] = 0;
     if (r.allowed) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) ok[u] = bits_at<P, ALIGNED>(r.allowed, c0 + head + (i + u * NT) * P);
+      for (int u = 0; u < U; ++u) ok[u] = allowed_of(i + u * NT);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = vp[i + u * NT];
+    for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const u32x4*>(xv + (i + u * NT) * 16u);
     if (r.bits) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) hit[u] = bits_at<P, ALIGNED>(r.bits, head + (i + u * NT) * P);
+      for (int u = 0; u < U; ++u) hit[u] = touched_of(i + u * NT);
     }
     float z[U * P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      Tr::unpack(w[u], z + u * P);
-      stream_cols<OP, P>(r, z + u * P, ok[u], hit[u], head + (i + u * NT) * P);
-      if (OP != kScore) __builtin_nontemporal_store(Tr::pack(z + u * P), wp + i + u * NT);
-    }
+    for (int u = 0; u < U; ++u) finish(w[u], z + u * P, ok[u], hit[u], i + u * NT);
     if (OP == kScore) stat_push_masked<U * P, P>(st, z, r.c);
   }
-  for (; i < nvec; i += NT) {
-    const int rel = head + i * P;
-    const uint32_t ok = r.allowed ? bits_at<P, ALIGNED>(r.allowed, c0 + rel) : 0u;
+  for (; i < n; i += NT) {
+    const uint32_t ok = r.allowed ? allowed_of(i) : 0u, hit = r.bits ? touched_of(i) : 0u;
     float z[P];
-    Tr::unpack(vp[i], z);
-    stream_cols<OP, P>(r, z, ok, r.bits ? bits_at<P, ALIGNED>(r.bits, rel) : 0u, rel);
-    if (OP == kScore)
-      stat_push_masked<P, P>(st, z, r.c);
-    else
-      __builtin_nontemporal_store(Tr::pack(z), wp + i);
+    finish(*reinterpret_cast<const u32x4*>(xv + i * 16u), z, ok, hit, i);
+    if (OP == kScore) stat_push_masked<P, P>(st, z, r.c);
   }
 }
 
