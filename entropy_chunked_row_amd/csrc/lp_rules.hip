@@ -266,11 +266,12 @@ __device__ __forceinline__ uint32_t block_exclusive_sum(uint32_t v, uint32_t* sm
 }
 
 // The outputs of a row from its whole state and its target's processed logit.
+// s == 0: nothing has weight (shut out, -inf, or so low that z c leaves fp32).
 __device__ __forceinline__ void store_score(const RulesArgs& a, int64_t row, Stat st, float zy) {
   const float l2s = log2f(st.s);
   const int64_t y = a.targets[row];
   float lp = __builtin_nanf("");
-  if (y >= 0 && y < a.V) lp = (fmaf(zy, a.c, -st.mc) - l2s) * kLn2;
+  if (y >= 0 && y < a.V && st.s != 0.f) lp = (fmaf(zy, a.c, -st.mc) - l2s) * kLn2;
   a.logprob[row] = lp;
   if (a.entropy_out) a.entropy_out[row] = (l2s - st.a / st.s) * kLn2;
   if (a.lse_out) a.lse_out[row] = (st.mc + l2s) * kLn2;
@@ -386,6 +387,10 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     r.ga = a.grad_entropy ? fmaf(gh, a.entropy[row], g) : g;
     r.gb = gh * kLn2;
     r.gy = g;
+    if (a.lse[row] == neg_inf()) {  // nothing has weight: no gradient
+      r.nlse2 = neg_inf();
+      r.ga = r.gb = r.gy = 0.f;
+    }
   }
   if (OP != kProcess) r.y = a.targets[row];
 

@@ -404,8 +404,10 @@ lp_status lp_process_logits(const void* logits, lp_dtype dtype, int64_t T, int64
  * the processed logits (which stay fp32: they are not rounded to `dtype`).
  * logprob fp32 [T] (required); entropy, lse fp32 [T] or NULL; lse is the
  * log-sum-exp of the tempered processed logits, saved for the backward.
- * A target that the grammar does not allow has log-prob -inf.  A row that allows
- * nothing has lse -inf, and NaN in logprob and entropy.
+ * A target that the grammar does not allow has log-prob -inf.  A processed logit
+ * below -2.35e38 temperature weighs nothing, as -inf does (the exponent
+ * z log2(e) / temperature is fp32): so does the lowest value of bf16 and fp32.
+ * A row in which nothing has weight has lse -inf, NaN in logprob and entropy, and gradient 0.
  * workspace >= lp_processed_workspace_bytes(T, V) bytes, 256-byte aligned; scratch only.
  */
 size_t lp_processed_workspace_bytes(int64_t T, int64_t V);

@@ -239,3 +239,41 @@ def test_captured_and_on_another_stream():
         other = step(side)
         side.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(other, eager)), k
+
+
+@pytest.mark.parametrize("N,h,V", [(5, 6, 9), (300, 516, 70), (5000, 30, 400)])
+def test_a_weight_gradient_off_the_16_byte_grid(N, h, V):
+    """dW may start at any fp32: its neighbours stay."""
+    torch = _torch()
+    lp = _lp()
+    g = torch.randn(N, h, device="cuda")
+    t = torch.randint(0, V, (N,), device="cuda")
+    want = lp.lp_embedding_backward(g, t, V, 2.0)
+    buf = torch.full((V * h + 8,), 3.0, device="cuda")
+    for off in (1, 2, 3):
+        dw = buf[off:off + V * h].view(V, h)
+        lp.lp_embedding_backward(g, t, V, 2.0, grad_weight=dw)
+        assert torch.equal(dw, want) and bool((buf[:off] == 3).all()) and bool((buf[off + V * h:] == 3).all())
+        lp.lp_embedding_backward(g, t, V, 2.0, grad_weight=dw, accumulate=True)
+        assert torch.equal(dw, want + want)
+        buf.fill_(3.0)
+
+
+def test_inputs_unchanged_and_two_streams_at_once():
+    """No call writes its inputs, and calls that overlap on two streams, each
+    with its own outputs and workspace, agree with the calls made alone."""
+    torch = _torch()
+    lp = _lp()
+    w = torch.randn(3000, 264, device="cuda").bfloat16()
+    gs = [torch.randn(6000, 264, device="cuda").bfloat16() for _ in range(2)]
+    ts = [torch.randint(-2, 3002, (6000,), device="cuda") for _ in range(2)]
+    kept = [x.clone() for x in (w, *gs, *ts)]
+    alone = [(lp.lp_embedding(w, t, 0.5), lp.lp_embedding_backward(g, t, 3000, 0.5)) for g, t in zip(gs, ts)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [(lp.lp_embedding(w, t, 0.5, stream=s), lp.lp_embedding_backward(g, t, 3000, 0.5, stream=s))
+               for g, t, s in zip(gs, ts, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for p, q in zip(got, alone) for a, b in zip(p, q))
+    assert all(torch.equal(a, b) for a, b in zip(kept, (w, *gs, *ts)))

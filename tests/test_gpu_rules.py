@@ -378,3 +378,81 @@ def test_many_touched_columns_in_many_rows(dtype):
     assert np.all(np.abs(d - want) <= EPS[dtype] / 2 * np.abs(want) + 2 * TOL * (np.abs(g) + f * 30)[:, None] * 1.6 + 2.0 ** -25)
     lp.lp_process_logits(x, r, out=x)
     assert np.array_equal(_wide(x), got)
+
+
+def test_inputs_unchanged_and_two_streams_at_once():
+    """No call writes its inputs (the logits processed in place apart), and
+    calls that overlap on two streams agree with the calls made alone."""
+    torch = _torch()
+    lp = _lp()
+    cs = [Rules(300, 5003, "bf16", seed=s, L=500, empty_row=False) for s in (31, 32)]
+    dv = [c.device() for c in cs]
+    ys = [to_dev(c.targets) for c in cs]
+    g = torch.linspace(-1, 1, 300, device="cuda")
+    inputs = [t for x, r in dv for t in (x, *(v for _, v in r._whole + r._per_row))] + ys + [g]
+    kept = [t.clone() for t in inputs]
+
+    def step(k, stream=None):
+        (x, r), y = dv[k], ys[k]
+        a = lp.lp_processed_logprobs_entropy(x, r, y, None, 0.7, stream=stream)
+        d = lp.lp_processed_logprobs_entropy_backward(x, r, y, None, 0.7, a[2], a[1], g, g, stream=stream)
+        return [lp.lp_process_logits(x, r, stream=stream), *a, d]
+
+    alone = [step(k) for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [step(k, streams[k]) for k in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for p, q in zip(got, alone) for a, b in zip(p, q))
+    assert all(torch.equal(a, b) for a, b in zip(kept, inputs))
+
+
+def test_temperatures_that_do_not_apply():
+    """tau <= 0 and tau == 1 leave the logits as they are, in both directions."""
+    torch = _torch()
+    lp = _lp()
+    c = Rules(6, 300, "fp32", seed=9, empty_row=False)
+    x, r = c.device()
+    y, g = to_dev(c.targets), torch.ones(6, device="cuda")
+    base = lp.lp_processed_logprobs_entropy(x, r, y, None, 1.0)
+    d = lp.lp_processed_logprobs_entropy_backward(x, r, y, None, 1.0, base[2], base[1], g, g)
+    for tau in (0.0, -2.0):
+        a = lp.lp_processed_logprobs_entropy(x, r, y, None, tau)
+        assert all(torch.equal(p, q) for p, q in zip(a, base))
+        assert torch.equal(lp.lp_processed_logprobs_entropy_backward(x, r, y, None, tau, a[2], a[1], g, g), d)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_of_the_types_lowest_value(dtype):
+    """Allowed logits that all hold the lowest fp16 share the weight evenly:
+    what the grammar shuts out stays out.  The lowest bf16 and fp32 weigh nothing:
+    rows of them are NaN with lse -inf, and have no gradient."""
+    torch = _torch()
+    lp = _lp()
+    t = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[dtype]
+    V = 2000
+    x = torch.full((2, V), torch.finfo(t).min, dtype=t, device="cuda")
+    x[1, :1000] = 0  # not allowed, and far above the others
+    words = torch.full((2, (V + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    words[1, :1000 // 32] = 0
+    words[1, 1000 // 32] = -1 << (1000 % 32)
+    y = torch.tensor([5, 1500], device="cuda")
+    rules = lp.LogitRules(allowed=words)
+    lp_g, H_g, lse_g = lp.lp_processed_logprobs_entropy(x, rules, y)
+    g = torch.ones(2, device="cuda")
+    d = _wide(lp.lp_processed_logprobs_entropy_backward(x, rules, y, None, 1.0, lse_g, H_g, g, g))
+    if dtype == "fp16":
+        n = np.array([V, 1000])
+        assert np.abs(host(lp_g) + np.log(n)).max() <= TOL and np.abs(host(H_g) - np.log(n)).max() <= TOL
+        # log2 p carries roundings at 94502 = 65504 log2(e): of mc + log2 s and of lse log2(e), 2^-8 each, of lse
+        # itself, 2^-9 log2(e), and of the product of the rounded ln 2 and log2(e), 94502 2^-24: 0.0163 together,
+        # so p by 1.14 %, and the entropy's p (log p + H) by 1.14 % of p; 2^-5 covers both.
+        want = np.zeros((2, V))
+        want[0], want[1, 1000:] = -1 / n[0], -1 / n[1]
+        want[0, 5] += 1
+        want[1, 1500] += 1
+        assert np.all(np.abs(d - want) <= np.abs(want) * 2.0 ** -11 + 1e-3 * 2 ** -5)
+    else:
+        assert np.all(np.isnan(host(lp_g))) and np.all(np.isnan(host(H_g))) and np.all(host(lse_g) == -np.inf)
+        assert np.all(d == 0)
