@@ -318,11 +318,18 @@ __global__ void __launch_bounds__(64 * NW, 2) k_w4_wide(W4Args a) {
     xrow[t] = a.hidden + row * a.ld_h;
   }
 
-  f32x4 tot[NT][RT], part[NT][RT];
+  // A lane's sums: of the range in hand in registers, of the ranges before it in
+  // LDS where the registers would not hold two tiles of the head beside four
+  // of x (64 rows of 5120 x 129280, groups of 128: 205 us with one tile, 160
+  // so; with three tiles of x both fit, and LDS is 2 % slower).
+  constexpr bool kTotInLds = NT == 4;
+  __shared__ f32x4 lds_tot[kTotInLds ? NW : 1][kTotInLds ? NT : 1][RT][64];
+  f32x4 reg_tot[NT][RT], part[NT][RT];
+  auto tot = [&](int t, int r) -> f32x4& { return kTotInLds ? lds_tot[w][t][r][lane] : reg_tot[t][r]; };
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) tot[t][r] = part[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RT; ++r) tot(t, r) = part[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   constexpr int XS = 8 / NW;
   u32x4 xn[XS][NT];
@@ -369,12 +376,10 @@ __global__ void __launch_bounds__(64 * NW, 2) k_w4_wide(W4Args a) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              tot[t][r][j] += part[t][r][j];
-              part[t][r][j] = 0.f;
-            }
+          for (int r = 0; r < RT; ++r) {
+            tot(t, r) += part[t][r];
+            part[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
       }
     };
 #pragma unroll
@@ -440,12 +445,14 @@ done:
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r) {
+      const f32x4 sum = tot(t, r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t row = t0 + t * 16 + q * 4 + j, v = v0 + r * 16 + r16;
-        if (row < a.T && v < a.V) store_logit(a.out, a.out_dtype, row * a.ld_out + v, tot[t][r][j]);
+        if (row < a.T && v < a.V) store_logit(a.out, a.out_dtype, row * a.ld_out + v, sum[j]);
       }
+    }
 }
 
 // Chunks per range up to which x's registers leave room for two buffers; with
@@ -487,17 +494,15 @@ hipError_t launch_wide(const W4Args& a, hipStream_t s) {
     b.hidden = a.hidden + r0 * a.ld_h;
     b.out = static_cast<char*>(a.out) + r0 * a.ld_out * (a.out_dtype == 2 ? 4 : 2);
     const int nt = b.T >= 64 ? 4 : static_cast<int>((b.T + 15) / 16);
-    // two tiles of the head a wave share its x operands; with four tiles of x
-    // the registers hold one
-    const int rt = nt == 4 ? 1 : 2;
-    const dim3 g(static_cast<unsigned>((int64_t(a.V) + 16 * NW * rt - 1) / (16 * NW * rt)),
+    constexpr int RT = 2;  // two tiles of the head a wave share its x operands
+    const dim3 g(static_cast<unsigned>((int64_t(a.V) + 16 * NW * RT - 1) / (16 * NW * RT)),
                  static_cast<unsigned>((b.T + 63) / 64));
     TimedLaunch tl("k_w4_logits", s);
     switch (nt) {
-      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
-      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
-      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, 2, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
-      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, 1, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      case 1: hipLaunchKernelGGL((k_w4_wide<X, G, 1, RT, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      case 2: hipLaunchKernelGGL((k_w4_wide<X, G, 2, RT, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      case 3: hipLaunchKernelGGL((k_w4_wide<X, G, 3, RT, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
+      default: hipLaunchKernelGGL((k_w4_wide<X, G, 4, RT, NW, TAIL>), g, dim3(64 * NW), 0, s, b); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
