@@ -645,13 +645,14 @@ __global__ void __launch_bounds__(256) k_rules_join(RulesArgs a) {
   if (lane == 0) store_score(a, row, st, y >= 0 && y < a.V ? a.zy[row] : 0.f);
 }
 
-// Slices per row: one where there are rows enough for four workgroups a CU,
-// else as many as that takes, of at least kMinSlice columns.  (256 x 129280 fp16:
-// 1024 workgroups 40 us, 2048 46, 8192 73; 4096 rows of 151936: one slice 0.61 ms,
-// two 0.59, but scoring 0.52 ms with one, 0.525 with two.)
+// Slices per row: one where there are rows enough for three workgroups a CU,
+// which is what their registers let be resident, else as many as that takes, of
+// at least kMinSlice columns.  (256 x 129280 fp16: 768 workgroups 36 us, 1024 40,
+// 2048 46, 8192 73; 4096 rows of 151936: one slice 0.61 ms, two 0.59, but scoring
+// 0.52 ms with one, 0.525 with two.)
 void set_slices(RulesArgs& a) {
   const int64_t most = (int64_t(a.V) + kMinSlice - 1) / kMinSlice, least = (int64_t(a.V) + kMaxSlice - 1) / kMaxSlice;
-  int64_t n = (1024 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  int64_t n = (768 + a.T - 1) / (a.T > 0 ? a.T : 1);
   n = n < most ? n : most;
   n = n > least ? n : least;
   a.slice = static_cast<int>(((a.V + n - 1) / n + 127) / 128 * 128);
