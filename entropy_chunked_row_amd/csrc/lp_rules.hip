@@ -26,12 +26,12 @@
 //      the others store whole vectors this way (storing touched columns singly
 //      behind the stream cost 100 of 600 us at 4096 x 151936: each is a
 //      partial write of memory that the stream's store has left the cache for).
-// Bound: HBM, from a few hundred rows on.  Measured: scoring 8192 x 151936 bf16
-// 0.52 ms (5.1 TB/s of what it must read; without any rule 0.41 ms), gradient of
-// 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing 256 x 129280 fp16 with
-// histories of up to 4096 tokens 38 us (of which 14 us are the histories' latency:
-// every workgroup of so short a call starts with its history), one row of
-// 151936 7 us.  An LDS word per column in place of bitmap and ranks took 2.5 ms
+// Bound: HBM and, when scoring, the vector unit.  Measured: scoring 8192 x 151936
+// bf16 0.51 ms (5.2 TB/s of what it must read, vector unit 85 % busy; without any
+// rule 0.38 ms), gradient of 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing
+// 256 x 129280 fp16 with histories of up to 4096 tokens 32 us (of which 9 us are
+// the histories' latency: every workgroup of so short a call starts with its
+// history), one row of 151936 7 us.  An LDS word per column in place of bitmap and ranks took 2.5 ms
 // on the first (slices of 4096 columns, each with its own history pass).
 // Counts are integers and the bias entry is a maximum, so the order of the
 // LDS atomics does not change any result.  Nothing of size V is kept between

@@ -20,11 +20,12 @@
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
-// Measured: one row of 5120 x 151936, groups of 128: 75 us (5.4 TB/s); 8 rows,
-// groups of 64: 90 us; 40 rows of 7168 x 129280, groups of 32: 205 us.  Few rows
+// Measured: one row of 5120 x 151936, groups of 128: 73 us (5.5 TB/s); 8 rows,
+// groups of 64: 89 us; 40 rows of 7168 x 129280, groups of 32: 195 us.  Few rows
 // are bound by HBM (and short of it by the waves' meeting once per 32 rows),
-// many by the vector unit: unpacking and scaling are half of its time there, and the
-// products 0.3 of the matrix unit's.
+// many by no unit alone: unpacking and scaling take half of the vector unit's time
+// and the products 0.3 of the matrix unit's, 145 us together without the
+// loads, with one workgroup a CU to hide what is left.
 
 namespace lp {
 
