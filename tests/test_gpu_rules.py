@@ -456,3 +456,16 @@ def test_rows_of_the_types_lowest_value(dtype):
     else:
         assert np.all(np.isnan(host(lp_g))) and np.all(np.isnan(host(H_g))) and np.all(host(lse_g) == -np.inf)
         assert np.all(d == 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [70001, 70016])
+def test_process_slices_of_long_rows(dtype, V):
+    """Rows in four slices each, of many vectors a lane, in place too."""
+    c = Rules(200, V, dtype, seed=V, L=700)
+    x, rules = c.device()
+    z, _ = c.processed()
+    got = _wide(_lp().lp_process_logits(x, rules))
+    _same_or_near(got, z, _process_tol(c, z))
+    _lp().lp_process_logits(x, rules, out=x)
+    assert np.array_equal(_wide(x), got, equal_nan=True)

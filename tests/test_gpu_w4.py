@@ -237,3 +237,19 @@ def test_the_same_bits_on_every_call(T, group):
         assert torch.isfinite(first).all()
         for _ in range(8):
             assert torch.equal(_lp().lp_lm_head_w4_logits(x, p, sc, group, out_dtype=torch.float32), first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,h,V,group", [(64, 512, 300, 32), (70, 768, 515, 64), (129, 2304, 257, 128)])
+def test_blocks_of_64_rows_of_whole_chunk_pairs(dtype, T, h, V, group):
+    """Several ranges of chunks and no column past the last pair."""
+    q, s = _head(V, h, group, T + h)
+    xb = to_bits(np.random.default_rng(T).normal(0, 1, (T, h)), dtype)
+    x, s64 = O.widen(xb, dtype), O.widen(s, "bf16")
+    want = O.w4_logits(x, q, s64, group)
+    f = lambda a: host(_lp().lp_lm_head_w4_logits(a, to_dev(_pack(q)), to_dev_bits(s, "bf16"), group,  # noqa: E731
+                                                  out_dtype=_torch().float32))
+    hid = to_dev_bits(xb, dtype)
+    got = f(hid)
+    assert np.all(np.abs(got - want) <= _tol(x, s64, group, want, "fp32"))
+    assert np.array_equal(f(hid[:40]), got[:40]) and np.array_equal(f(hid[3:8]), got[3:8])
