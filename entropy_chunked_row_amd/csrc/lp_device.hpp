@@ -286,6 +286,11 @@ __device__ __forceinline__ KLState kl_merge(KLState x, KLState y) {
   return r;
 }
 
+// 16 bytes of a row from any element on: one load, also off the 16-byte grid.
+typedef unsigned int u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+__device__ __forceinline__ u32x4 load_vec(const char* p) { return *reinterpret_cast<const u32x4_a2*>(p); }
+
 // Split of a row of `n` elements at `p` into a scalar head (up to the first
 // 16-byte boundary), whole 16-byte vectors, and a scalar tail.
 template <class Tr>

@@ -56,18 +56,13 @@ __global__ void __launch_bounds__(256) k_embedding(EmbedArgs a) {
     const bool known = v >= 0 && v < a.V;
     const char* src = static_cast<const char*>(a.weight) + (known ? v : 0) * a.ld_w * Tr::kBytes;
     char* dst = static_cast<char*>(a.out) + i * a.ld_out * Tr::kBytes;
-    RowSplit<Tr> sp(src, a.h);
-    if ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15u) {
-      sp.head = 0;
-      sp.nvec = 0;
-      sp.tail = a.h;
-    }
+    const RowSplit<Tr> sp(dst, a.h);  // stores on the 16-byte grid, loads where they fall
     if (lane < sp.head) Tr::store1(dst, lane, known ? Tr::load1(src, lane) * a.scale : 0.f);
-    const u32x4* vp = reinterpret_cast<const u32x4*>(src + sp.head * Tr::kBytes);
+    const char* vp = src + sp.head * Tr::kBytes;
     u32x4* wp = reinterpret_cast<u32x4*>(dst + sp.head * Tr::kBytes);
     for (int j = lane; j < sp.nvec; j += 64) {
       float x[P];
-      Tr::unpack(vp[j], x);
+      Tr::unpack(load_vec(vp + static_cast<int64_t>(j) * 16), x);
 #pragma unroll
       for (int k = 0; k < P; ++k) x[k] = known ? x[k] * a.scale : 0.f;
       __builtin_nontemporal_store(Tr::pack(x), wp + j);
@@ -307,7 +302,7 @@ template <class Tr, bool VEC>
 __device__ __forceinline__ void load_cols(const EmbedGradArgs& a, uint32_t i, int64_t col, float* x) {
   const char* p = static_cast<const char*>(a.grad) + static_cast<int64_t>(i) * a.ld_g * Tr::kBytes;
   if constexpr (VEC)
-    Tr::unpack(*reinterpret_cast<const u32x4*>(p + col * Tr::kBytes), x);
+    Tr::unpack(load_vec(p + col * Tr::kBytes), x);
   else
     x[0] = Tr::load1(p, col);
 }
@@ -335,11 +330,22 @@ __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int
   }
 }
 
-// Stores the P columns of a finished row of dW.
+// A lane's P columns end with the row: the last lane's begin before `col`, and
+// it stores those from the skip(col)-th on, the ones before are its neighbour's.
+template <int P>
+__device__ __forceinline__ int skip(const EmbedGradArgs& a, int64_t col) {
+  return P > 1 && col + P > a.h ? static_cast<int>(col + P - a.h) : 0;
+}
+
+// Stores the P columns of a finished row of dW, but the first `from`.
 template <int P, bool ACC>
-__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t v, int64_t col, const float* acc) {
+__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t v, int64_t col, int from, const float* acc) {
   float* out = a.grad_weight + static_cast<int64_t>(v) * a.h + col;
-  if constexpr (P % 4 == 0) {
+  if (from > 0) {
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+      if (j >= from) out[j] = ACC ? out[j] + acc[j] * a.scale : acc[j] * a.scale;
+  } else if constexpr (P % 4 == 0) {
 #pragma unroll
     for (int j = 0; j < P; j += 4) {
       f32x4_a4 x{acc[j] * a.scale, acc[j + 1] * a.scale, acc[j + 2] * a.scale, acc[j + 3] * a.scale};
@@ -366,9 +372,10 @@ __global__ void __launch_bounds__(kSumNT) k_embed_partial(EmbedGradArgs a) {
     return;
   }
   const int64_t c = blockIdx.x / a.col_blocks + a.row0;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
+  int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
   const uint32_t k = a.sorted_keys[c * kChunk];
   if (k == static_cast<uint32_t>(a.V) || a.sorted_keys[c * kChunk + kChunk - 1] != k || col >= a.h) return;
+  col -= skip<P>(a, col);  // what two lanes then store is the same
   float acc[P];
 #pragma unroll
   for (int j = 0; j < P; ++j) acc[j] = 0.f;
@@ -378,19 +385,28 @@ __global__ void __launch_bounds__(kSumNT) k_embed_partial(EmbedGradArgs a) {
   for (int j = 0; j < P; ++j) out[j] = acc[j];
 }
 
-// Zeros in the rows of dW that no token names.
+// Zeros in the rows of dW that no token names: neighbours among them are one
+// stretch of memory, whose stores start on the 128-byte grid.
 __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t block) {
   const int64_t v0 = block * a.fill_rows;
   const int lane = threadIdx.x & 63;
   for (int r0 = 0; r0 < a.fill_rows; r0 += 64) {
     const int64_t v = v0 + r0 + lane;
     uint64_t todo = __ballot(r0 + lane < a.fill_rows && v < a.V && a.first[v] == kAbsent);
-    for (; todo; todo &= todo - 1) {
-      float* out = a.grad_weight + (v0 + r0 + __builtin_ctzll(todo)) * a.h;
-      int j = threadIdx.x * 4;
-      for (; j + 4 <= a.h; j += kSumNT * 4)
-        *reinterpret_cast<f32x4_a4*>(out + j) = f32x4_a4{0.f, 0.f, 0.f, 0.f};
-      for (; j < a.h; ++j) out[j] = 0.f;  // the last, short group of one lane
+    while (todo) {
+      const int at = __builtin_ctzll(todo);
+      const uint64_t rest = ~(todo >> at);
+      const int rows = rest ? __builtin_ctzll(rest) : 64;
+      todo = at + rows < 64 ? todo >> (at + rows) << (at + rows) : 0;
+      float* out = a.grad_weight + (v0 + r0 + at) * a.h;
+      const int64_t n = static_cast<int64_t>(rows) * a.h;
+      const int64_t lead = (32 - (reinterpret_cast<uintptr_t>(out) >> 2 & 31u)) & 31u, head = lead < n ? lead : n;
+      if (static_cast<int64_t>(threadIdx.x) < head) out[threadIdx.x] = 0.f;
+      const int64_t vecs = (n - head) / 4;
+      u32x4* grid = reinterpret_cast<u32x4*>(out + head);
+      for (int64_t j = threadIdx.x; j < vecs; j += kSumNT) grid[j] = u32x4{0, 0, 0, 0};
+      const int64_t left = head + vecs * 4 + threadIdx.x;
+      if (left < n) out[left] = 0.f;
     }
   }
 }
@@ -404,7 +420,9 @@ __global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
   constexpr int P = VEC ? Tr::kPerVec : 1;
   if (!ACC && blockIdx.x >= a.parts) return fill_rows(a, blockIdx.x - a.parts);
   const int64_t p0 = (blockIdx.x / a.col_blocks + a.row0) * kRunSpan;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
+  const int64_t first_col = (static_cast<int64_t>(blockIdx.x % a.col_blocks) * kSumNT + threadIdx.x) * P;
+  const int from = skip<P>(a, first_col);
+  const int64_t col = first_col - from;
   const int lane = threadIdx.x & 63;
   const int64_t p = p0 + lane;
   const bool there = lane < kRunSpan && p < a.N;
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
         step = (rest + 63) / 64;
       }
     }
-    if (col >= a.h) continue;
+    if (first_col >= a.h) continue;
     float acc[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) acc[j] = 0.f;
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kSumNT) k_embed_runs(EmbedGradArgs a) {
     } else {
       add_rows<Tr, VEC, 8>(a, acc, i, e, col);
     }
-    store_row<P, ACC>(a, v, col, acc);
+    store_row<P, ACC>(a, v, col, from, acc);
   }
 }
 
@@ -484,7 +502,9 @@ __global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows
     uint64_t hit[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) hit[k] = __ballot(key[k] == static_cast<uint32_t>(v));
-    for (int64_t col = static_cast<int64_t>(threadIdx.x) * P; col < a.h; col += kSumNT * P) {
+    for (int64_t own = static_cast<int64_t>(threadIdx.x) * P; own < a.h; own += kSumNT * P) {
+      const int from = skip<P>(a, own);
+      const int64_t col = own - from;
       float acc[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) acc[j] = 0.f;
@@ -497,7 +517,7 @@ __global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows
           for (int j = 0; j < P; ++j) acc[j] += x[j];
         }
       }
-      store_row<P, ACC>(a, static_cast<uint32_t>(v), col, acc);
+      store_row<P, ACC>(a, static_cast<uint32_t>(v), col, from, acc);
     }
   }
 }
@@ -552,9 +572,13 @@ hipError_t launch_sums(EmbedGradArgs a, hipStream_t s) {
 
 template <class Tr>
 hipError_t launch_sums_t(const EmbedGradArgs& a, hipStream_t s) {
-  // 16-byte loads need every gradient row on the 16-byte grid and whole vectors
-  const bool vec = reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 && (a.ld_g * Tr::kBytes) % 16 == 0 &&
-                   a.h % Tr::kPerVec == 0;
+  // 16 bytes a lane where rows are whole vectors on the 16-byte grid, and for
+  // long rows on any boundary; short ones leave too few lanes at work (30000
+  // positions, V = 30000 and 1000: h = 257 64 and 50 us by vectors, 61 and 47
+  // singly; h = 801 73 and 55, 78 and 51; 32768 x 5119, V = 40000: 299, 492).
+  const bool whole = reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 && (a.ld_g * Tr::kBytes) % 16 == 0 &&
+                     a.h % Tr::kPerVec == 0;
+  const bool vec = whole || a.h >= 768;
   if (a.N <= kTinyN) return vec ? launch_tiny<Tr, true>(a, s) : launch_tiny<Tr, false>(a, s);
   return vec ? launch_sums<Tr, true>(a, s) : launch_sums<Tr, false>(a, s);
 }

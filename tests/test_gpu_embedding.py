@@ -277,3 +277,40 @@ def test_inputs_unchanged_and_two_streams_at_once():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for p, q in zip(got, alone) for a, b in zip(p, q))
     assert all(torch.equal(a, b) for a, b in zip(kept, (w, *gs, *ts)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,h,V,off", [(100, 768, 500, 1), (200, 1025, 900, 2), (300, 1026, 4000, 3), (3000, 771, 900, 1),
+                                       (5000, 1036, 700, 5), (4500, 1541, 3000, 6), (700, 2047, 130, 31)])
+def test_long_rows_on_any_boundary(dtype, N, h, V, off):
+    """Rows off the 16-byte grid and of a broken last vector; stretches of absent rows from any boundary on."""
+    torch = _torch()
+    lp = _lp()
+    _, G, tok = _case(N, h, V, dtype, N + h, True, 3)
+    tok[tok > V // 2] = V // 2  # the upper half of the vocabulary is one stretch
+    g, G64, t = _dev(G, dtype)[:, 3:], O.widen(G, dtype)[:, 3:], to_dev(tok)
+    whole = torch.full((off + V * h + 40,), 7.0, device="cuda")
+    out = whole[off:off + V * h].view(V, h)
+    lp.lp_embedding_backward(g, t, V, 1.5, grad_weight=out)
+    _check_grad(host(out), G64, tok, V, 1.5)
+    assert (whole[:off] == 7).all() and (whole[off + V * h:] == 7).all()
+    base = np.random.default_rng(4).normal(0, 1, (V, h)).astype(np.float32)
+    out.copy_(to_dev(base))
+    lp.lp_embedding_backward(g, t, V, -0.25, grad_weight=out, accumulate=True)
+    there = _check_grad(host(out), G64, tok, V, -0.25, base)
+    assert np.array_equal(host(out)[~there], base[~there])
+    assert (whole[:off] == 7).all() and (whole[off + V * h:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("h", [1, 9, 1031, 2050])
+def test_lookup_of_rows_at_every_boundary(dtype, h):
+    torch = _torch()
+    W, _, tok = _case(70, h, 90, dtype, h, extra=8)
+    for a, b in ((0, 1), (1, 0), (3, 6), (7, 2)):
+        w = _dev(W, dtype)[:, a:a + h]
+        want = O.embedding(O.widen(W, dtype)[:, a:a + h], tok, 1.0)  # a scale of 1 rounds nothing
+        buf = torch.full((70, h + 9), 5.0, dtype=w.dtype, device="cuda")
+        _lp().lp_embedding(w, to_dev(tok), 1.0, out=buf[:, b:b + h])
+        got = host(buf.float())
+        assert np.array_equal(got[:, b:b + h], want) and np.all(got[:, :b] == 5) and np.all(got[:, b + h:] == 5)
