@@ -320,8 +320,8 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, cons
   // decode step were written just before, and what is left of them in the
   // caches counts (256 x 129280: 43 us non-temporal, 39 plain).
   auto load = [&](uint32_t i) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(xv + i * 16u);
-    return OP == kProcess ? *p : __builtin_nontemporal_load(p);
+    if (OP == kProcess) return load_vec(xv + i * 16u);
+    return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xv + i * 16u)));
   };
   uint32_t i = threadIdx.x;
   const uint32_t n = nvec;
@@ -426,14 +426,9 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   const int32_t* tok = a.tokens + buf * a.ld_tokens;
   const int32_t* btok = a.bias_tokens + b0;
 
-  // Columns [0, head) and the tail go one by one, the rest as 16-byte vectors;
-  // where input and output rows differ in their 16-byte phase, all go singly.
-  RowSplit<Tr> sp(xp, n);
-  if (OP != kScore && ((reinterpret_cast<uintptr_t>(xp) ^ reinterpret_cast<uintptr_t>(op)) & 15u)) {
-    sp.head = 0;
-    sp.nvec = 0;
-    sp.tail = n;
-  }
+  // Columns [0, head) and the tail go one by one, the rest as 16-byte vectors
+  // on the grid of what is stored; loads go off it where the input's rows do.
+  const RowSplit<Tr> sp(OP == kScore ? xp : op, n);
   // All workgroups of a decode step read their histories at once: the first
   // logits come in meanwhile (256 x 129280 fp16: 36.3 -> 34.9 us; four vectors a
   // lane instead of two take registers that cost a workgroup a CU, 39).
@@ -441,7 +436,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   if (OP == kProcess && sp.nvec >= U * NT) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      ahead[u] = *reinterpret_cast<const u32x4*>(xp + sp.head * Tr::kBytes + (tid + u * NT) * 16u);
+      ahead[u] = load_vec(xp + sp.head * Tr::kBytes + (tid + u * NT) * 16u);
   }
 
   const int ranks = a.slice < kRanks ? a.slice : kRanks;

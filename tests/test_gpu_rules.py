@@ -469,3 +469,23 @@ def test_process_slices_of_long_rows(dtype, V):
     _same_or_near(got, z, _process_tol(c, z))
     _lp().lp_process_logits(x, rules, out=x)
     assert np.array_equal(_wide(x), got, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_logits_of_a_padded_vocabulary(dtype):
+    """Rows of the logits and of what is written start on different boundaries."""
+    c = Rules(21, 9001, dtype, seed=77, extra_cols=15, empty_row=False)
+    x, rules = c.device()
+    z, slope = c.processed()
+    got = _wide(_lp().lp_process_logits(x, rules))
+    _same_or_near(got, z, _process_tol(c, z))
+    y = to_dev(c.targets)
+    args = (rules, y, None, 0.7)
+    lp_g, H_g, lse_g = _lp().lp_processed_logprobs_entropy(x, *args)
+    g = to_dev(np.linspace(-1, 1, 21).astype(np.float32))
+    d = _lp().lp_processed_logprobs_entropy_backward(x, *args, lse_g, H_g, g, g)
+    same = x.contiguous()
+    assert np.array_equal(_wide(_lp().lp_process_logits(same, rules)), got, equal_nan=True)
+    assert np.abs(host(lp_g) - O.logprobs_entropy(z, c.targets, None, 0.7)[0]).max() <= TOL
+    # the same lse, so the same gradient to the bit, whatever the rows' boundaries
+    assert _torch().equal(_lp().lp_processed_logprobs_entropy_backward(same, *args, lse_g, H_g, g, g), d)
