@@ -385,29 +385,33 @@ __global__ void __launch_bounds__(kSumNT) k_embed_partial(EmbedGradArgs a) {
   for (int j = 0; j < P; ++j) out[j] = acc[j];
 }
 
-// Zeros in the rows of dW that no token names: neighbours among them are one
+// Zeros in the rows v0 + k of dW, k the set bits: neighbours among them are one
 // stretch of memory, whose stores start on the 128-byte grid.
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t v0, uint64_t todo) {
+  while (todo) {
+    const int at = __builtin_ctzll(todo);
+    const uint64_t rest = ~(todo >> at);
+    const int rows = rest ? __builtin_ctzll(rest) : 64;
+    todo = at + rows < 64 ? todo >> (at + rows) << (at + rows) : 0;
+    float* out = a.grad_weight + (v0 + at) * a.h;
+    const int64_t n = static_cast<int64_t>(rows) * a.h;
+    const int64_t lead = (32 - (reinterpret_cast<uintptr_t>(out) >> 2 & 31u)) & 31u, head = lead < n ? lead : n;
+    if (static_cast<int64_t>(threadIdx.x) < head) out[threadIdx.x] = 0.f;
+    const int64_t vecs = (n - head) / 4;
+    u32x4* grid = reinterpret_cast<u32x4*>(out + head);
+    for (int64_t j = threadIdx.x; j < vecs; j += kSumNT) grid[j] = u32x4{0, 0, 0, 0};
+    const int64_t left = head + vecs * 4 + threadIdx.x;
+    if (left < n) out[left] = 0.f;
+  }
+}
+
+// Zeros in the rows of dW that no token names.
 __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t block) {
   const int64_t v0 = block * a.fill_rows;
   const int lane = threadIdx.x & 63;
   for (int r0 = 0; r0 < a.fill_rows; r0 += 64) {
     const int64_t v = v0 + r0 + lane;
-    uint64_t todo = __ballot(r0 + lane < a.fill_rows && v < a.V && a.first[v] == kAbsent);
-    while (todo) {
-      const int at = __builtin_ctzll(todo);
-      const uint64_t rest = ~(todo >> at);
-      const int rows = rest ? __builtin_ctzll(rest) : 64;
-      todo = at + rows < 64 ? todo >> (at + rows) << (at + rows) : 0;
-      float* out = a.grad_weight + (v0 + r0 + at) * a.h;
-      const int64_t n = static_cast<int64_t>(rows) * a.h;
-      const int64_t lead = (32 - (reinterpret_cast<uintptr_t>(out) >> 2 & 31u)) & 31u, head = lead < n ? lead : n;
-      if (static_cast<int64_t>(threadIdx.x) < head) out[threadIdx.x] = 0.f;
-      const int64_t vecs = (n - head) / 4;
-      u32x4* grid = reinterpret_cast<u32x4*>(out + head);
-      for (int64_t j = threadIdx.x; j < vecs; j += kSumNT) grid[j] = u32x4{0, 0, 0, 0};
-      const int64_t left = head + vecs * 4 + threadIdx.x;
-      if (left < n) out[left] = 0.f;
-    }
+    zero_rows(a, v0 + r0, __ballot(r0 + lane < a.fill_rows && v < a.V && a.first[v] == kAbsent));
   }
 }
 
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows
   uint32_t key[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) key[k] = k * 64 + lane < a.N ? key_of(a, k * 64 + lane) : static_cast<uint32_t>(a.V);
+  uint64_t absent = 0;  // of the workgroup's rows, at most 64
   for (int r = 0; r < rows; ++r) {
     int64_t v = static_cast<int64_t>(blockIdx.x) * rows + r;
     if (ACC) {
@@ -497,11 +502,15 @@ __global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows
       for (int k = 0; k < K; ++k) earlier |= k * 64 + lane < i && key[k] == static_cast<uint32_t>(v);
       if (__any(earlier)) return;
     } else if (v >= a.V) {
-      return;
+      break;
     }
-    uint64_t hit[K];
+    uint64_t hit[K], any = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) hit[k] = __ballot(key[k] == static_cast<uint32_t>(v));
+    for (int k = 0; k < K; ++k) any |= hit[k] = __ballot(key[k] == static_cast<uint32_t>(v));
+    if (!ACC && !any) {
+      absent |= uint64_t(1) << r;
+      continue;
+    }
     for (int64_t own = static_cast<int64_t>(threadIdx.x) * P; own < a.h; own += kSumNT * P) {
       const int from = skip<P>(a, own);
       const int64_t col = own - from;
@@ -520,6 +529,7 @@ __global__ void __launch_bounds__(kSumNT) k_embed_tiny(EmbedGradArgs a, int rows
       store_row<P, ACC>(a, static_cast<uint32_t>(v), col, from, acc);
     }
   }
+  if (!ACC) zero_rows(a, static_cast<int64_t>(blockIdx.x) * rows, absent);
 }
 
 template <class Tr, bool VEC>
