@@ -126,36 +126,57 @@ constexpr int kRanges = 8;
 // scales are unpacked where they are used, for any work on a loaded value
 // next to its load would wait for the load.  TAIL: columns may end inside the
 // chunks (otherwise loads need no branch, which would part them from the
-// products they run ahead of).
-template <int G, int KC, bool TAIL>
+// products they run ahead of).  EXIST: all KC chunks exist, so that with TAIL
+// only the last one's columns may end, and its scales are loaded one by one.
+template <int G, int KC, bool TAIL, bool EXIST = false>
 struct Tile {
   static constexpr int kGroups = kChunk / G, kScales = KC * kGroups;
+  static constexpr bool kSingly = TAIL && EXIST;
   u32x4 w[KC];
   uint32_t s[(kScales + 1) / 2];
+  uint32_t last_s[kSingly ? kGroups : 1];
+
+  // `Loaded` of the scales from p on
+  template <int Loaded>
+  __device__ __forceinline__ void load_scales(const uint16_t* p) {
+    typedef u32x4 x4 __attribute__((aligned(2)));
+    typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(2)));
+    typedef uint32_t x1 __attribute__((aligned(2)));
+#pragma unroll
+    for (int i = 0; i + 8 <= Loaded; i += 8) {
+      const u32x4 v = *reinterpret_cast<const x4*>(p + i);
+      s[i / 2] = v.x, s[i / 2 + 1] = v.y, s[i / 2 + 2] = v.z, s[i / 2 + 3] = v.w;
+    }
+    constexpr int r4 = Loaded / 8 * 8, r2 = Loaded / 4 * 4, r1 = Loaded / 2 * 2;
+    if constexpr (r2 > r4) {
+      const auto v = *reinterpret_cast<const x2*>(p + r4);
+      s[r4 / 2] = v.x, s[r4 / 2 + 1] = v.y;
+    }
+    if constexpr (r1 > r2) s[r2 / 2] = *reinterpret_cast<const x1*>(p + r2);
+    if constexpr (Loaded > r1) s[r1 / 2] = p[r1];
+  }
 
   // wrow: the lane's row from its own 16 bytes of chunk 0 on; srow: the row's
   // scales.  Chunks c .. c + KC - 1; what lies past column h is read from
   // elsewhere in the row (x is 0 there).
   __device__ __forceinline__ void load(const char* wrow, const uint16_t* srow, int c, int q, int h) {
-    if (!TAIL || (c + KC) * kChunk <= h) {
+    if constexpr (kSingly) {
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const bool in = k + 1 < KC || (c + k) * kChunk + q * 32 < h;
+        w[k] = *reinterpret_cast<const u32x4*>(wrow + (in ? (c + k) * (kChunk / 2) : -q * 16));
+      }
+      load_scales<kScales - kGroups>(srow + c * kGroups);
+      const int last = (h - 1) / G;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int at = (c + KC - 1) * kGroups + g;
+        last_s[g] = srow[at < last ? at : last];
+      }
+    } else if (!TAIL || (c + KC) * kChunk <= h) {
 #pragma unroll
       for (int k = 0; k < KC; ++k) w[k] = *reinterpret_cast<const u32x4*>(wrow + (c + k) * (kChunk / 2));
-      const uint16_t* p = srow + c * kGroups;
-      typedef u32x4 x4 __attribute__((aligned(2)));
-      typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(2)));
-      typedef uint32_t x1 __attribute__((aligned(2)));
-#pragma unroll
-      for (int i = 0; i + 8 <= kScales; i += 8) {
-        const u32x4 v = *reinterpret_cast<const x4*>(p + i);
-        s[i / 2] = v.x, s[i / 2 + 1] = v.y, s[i / 2 + 2] = v.z, s[i / 2 + 3] = v.w;
-      }
-      constexpr int r4 = kScales / 8 * 8, r2 = kScales / 4 * 4, r1 = kScales / 2 * 2;
-      if constexpr (r2 > r4) {
-        const auto v = *reinterpret_cast<const x2*>(p + r4);
-        s[r4 / 2] = v.x, s[r4 / 2 + 1] = v.y;
-      }
-      if constexpr (r1 > r2) s[r2 / 2] = *reinterpret_cast<const x1*>(p + r2);
-      if constexpr (kScales > r1) s[r1 / 2] = p[r1];
+      load_scales<kScales>(srow + c * kGroups);
     } else {
       const int last = (h - 1) / G;
 #pragma unroll
@@ -174,6 +195,7 @@ struct Tile {
   }
 
   __device__ __forceinline__ float scale(int k, int g) const {
+    if (kSingly && k == KC - 1) return __uint_as_float(last_s[g] << 16);
     const int i = k * kGroups + g;
     return __uint_as_float(i & 1 ? s[i / 2] & 0xffff0000u : s[i / 2] << 16);
   }
@@ -237,13 +259,13 @@ __global__ void __launch_bounds__(512) k_w4_few(W4Args a) {
   // Two buffers in turn, so that a load's registers are next touched when its
   // tile's turn comes (moving them would wait for the load).  A third buffer
   // measured no faster.
-  Tile<G, KC, TAIL> buf[2];
-  auto load = [&](int64_t tile, Tile<G, KC, TAIL>& d) {
+  Tile<G, KC, TAIL, true> buf[2];
+  auto load = [&](int64_t tile, Tile<G, KC, TAIL, true>& d) {
     int64_t v = tile * 16 + r16;
     v = v < a.V ? v : a.V - 1;  // rows past the end repeat the last one
     d.load(static_cast<const char*>(a.packed) + v * a.ld_p + q * 16, a.scales + v * a.ld_s, c0, q, h);
   };
-  auto add = [&](const Tile<G, KC, TAIL>& d) {
+  auto add = [&](const Tile<G, KC, TAIL, true>& d) {
     f32x4 tot{0.f, 0.f, 0.f, 0.f};
     uint32_t neg24 = X::kNeg24;
     if (!kKeepShift) asm volatile("" : "+v"(neg24));  // or the compiler would keep the start values all the same
