@@ -8,7 +8,7 @@
 //   z1 = seen ? (z > 0 ? z / rho : z * rho) : z
 //   z2 = z1 - f * n          z3 = z2 - p * (n > 0)
 //   z4 = z3 + b_j            z5 = allowed_j ? z4 : -inf
-// each step one fp32 operation, rounded on its own (no contraction).
+// each step one fp32 operation, rounded on its own (touched_col).
 //
 // Few columns of a row are touched by a history or a bias, and all others
 // pass unchanged, so the two are kept apart.  A workgroup owns a slice of a
@@ -224,18 +224,25 @@ __device__ __forceinline__ void stream_cols(const RowRules& r, float* z, uint32_
 }
 
 // The rules on one touched column: w its count word, b its bias entry + 1.
-// False if the grammar does not allow it.
+// False if the grammar does not allow it.  The pragma keeps every product and
+// sum an operation of its own: it has to cover the operators themselves, the
+// rounding functions of the HIP headers (__fmul_rn and the like) are plain
+// operators there, and the product f n went unrounded into a multiply-add.
 __device__ __forceinline__ bool touched_col(const RowRules& r, uint32_t w, uint32_t b, int col, float& z,
                                             float& slope) {
+#pragma clang fp contract(off)
   slope = 1.f;
   if (w) {
     const bool up = z > 0.f;
-    slope = up ? __frcp_rn(r.rho) : r.rho;
-    z = up ? __fdiv_rn(z, r.rho) : __fmul_rn(z, r.rho);
+    slope = up ? 1.f / r.rho : r.rho;
+    z = up ? z / r.rho : z * r.rho;
     const uint32_t n = w & ~kPromptBit;
-    if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(r.f, static_cast<float>(n))), r.p);
+    if (n) {
+      z = z - r.f * static_cast<float>(n);
+      z = z - r.p;
+    }
   }
-  if (b) z = __fadd_rn(z, r.values[b - 1]);
+  if (b) z = z + r.values[b - 1];
   if (r.allowed && !(bits_at<1>(r.allowed, col) & 1u)) {
     z = neg_inf();
     return false;
