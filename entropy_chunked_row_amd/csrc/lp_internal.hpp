@@ -121,7 +121,7 @@ struct RulesArgs {
   // set by the launchers
   int64_t row0;
   int slice, nslices;
-  float* part;  // [T x nslices x 3] states (mc, s, a)
+  float* part;  // [T x nslices x 3] states (m, s, a)
   float* zy;    // [T] processed logit of the target
 };
 

@@ -37,6 +37,8 @@
 // LDS atomics does not change any result.  Nothing of size V is kept between
 // calls and no dense count matrix passes through memory (it would cost 4 bytes
 // a column where the logits cost 2); a history is read twice per slice.
+#include <type_traits>
+
 #include "lp_device.hpp"
 #include "lp_internal.hpp"
 
@@ -54,58 +56,124 @@ enum RulesOp { kProcess = 0, kScore = 1, kGrad = 2 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Like stat_push for values that may be -inf: those weigh 0 and add nothing to
-// `a`.  A NaN stays a NaN in s and a.
+// Softmax state of some of a row's columns under an exponent scale c: m their
+// largest value that has weight (-inf: none yet), s = sum 2^t and a = sum 2^t t
+// over exponents t relative to m c.  Where |m c| is below kFar ("near") they
+// are t = fma(x, c, -RN(m c)), which rounds once.  The rounding of m c itself,
+// which then stands in every t alike, is an exponent of its own: 1/2 at 2^24, 512
+// at 1e10, 1e22 at 1e30.  Past kFar, where finite masks lie, t = (x - m) c
+// instead, two operations but 0 at m whatever its size (in every column they
+// would cost one instruction more of 13).
+struct RowStat {
+  float m, s, a;
+};
+
+constexpr float kFar = 16777216.f;
+constexpr float kLargest = 3.402823466e38f;
+
+__device__ __forceinline__ bool is_near(float mc) { return fabsf(mc) < kFar; }
+
+// What exponents relative to m0 gain when they are taken relative to m1 >= m0.
+// Below kNoWeight nothing is left of a weight; the bound keeps s times the
+// shift finite, and takes an empty side (m0 = -inf) to nothing whatever m1.  The products are rounded here as they are in the exponents:
+// no contraction.
+__device__ __forceinline__ float stat_shift(float m0, float m1, float c) {
+#pragma clang fp contract(off)
+  const float r0 = m0 * c, r1 = m1 * c;
+  float d = r0 - r1;
+  if (!is_near(r0) || !is_near(r1)) {
+    d = (m0 - m1) * c;
+    // of near ones the rounding of their product is part
+    if (is_near(r0)) d -= fmaf(m0, c, -r0);
+    if (is_near(r1)) d += fmaf(m1, c, -r1);
+  }
+  return fmaxf(d, kNoWeight);
+}
+
+// A lane's state while it takes columns: with its reference exponent, which
+// moves only when a larger value comes.
+struct LaneStat : RowStat {
+  float nmc = 0.f;  // -RN(m c); 0 while m is -inf, whose exponents are then -inf or NaN
+};
+
+__device__ __forceinline__ LaneStat stat_none() { return LaneStat{{neg_inf(), 0.f, 0.f}}; }
+
+// Folds N values into the state.  They may be -inf, or so low that their
+// product with c leaves fp32: those weigh 0 and add nothing to `a`.  A NaN
+// stays a NaN in s and a.
 template <int N, int CH>
-__device__ __forceinline__ void stat_push_masked(Stat& st, const float* x, float c) {
+__device__ __forceinline__ void stat_push_masked(LaneStat& st, const float* x, float c) {
   float vm = x[0];
 #pragma unroll
   for (int k = 1; k < N; ++k) vm = fmaxf(vm, x[k]);
-  const float vmc = vm * c;
-  if (vmc > st.mc) stat_rebase(st, vmc);
-  const float nmc = -st.mc;
+  if (vm > st.m && vm * c >= -kLargest) {
+    const float d = stat_shift(st.m, vm, c), r = fast_exp2(d);
+    st.a = (st.a + st.s * d) * r;
+    st.s *= r;
+    st.m = vm;
+    st.nmc = -(vm * c);
+  }
+  auto fold = [&](auto exponent) {
 #pragma unroll
-  for (int g = 0; g < N; g += CH) {
-    float ps = 0.f, pa = 0.f;
+    for (int g = 0; g < N; g += CH) {
+      float ps = 0.f, pa = 0.f;
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const float t = fmaf(x[g + k], c, nmc);
-      const float e = fast_exp2(t);
-      ps += e;
-      pa = fmaf(e, fmaxf(t, kNoWeight), pa);
+      for (int k = 0; k < CH; ++k) {
+        const float t = exponent(x[g + k]);
+        const float e = fast_exp2(t);
+        ps += e;
+        pa = fmaf(e, fmaxf(t, kNoWeight), pa);
+      }
+      st.s += ps;
+      st.a += pa;
     }
-    st.s += ps;
-    st.a += pa;
-  }
+  };
+  if (is_near(st.nmc))
+    fold([&](float v) { return fmaf(v, c, st.nmc); });
+  else
+    fold([&](float v) { return (v - st.m) * c; });
 }
 
-// Merge in which an empty side (s == 0) adds nothing and a NaN side wins.
-__device__ __forceinline__ Stat stat_merge_nan(Stat x, Stat y) {
-  const float mc = fmaxf(x.mc, y.mc);
-  float s = 0.f, a = 0.f;
-  if (x.s != 0.f) {
-    const float d = x.mc - mc, r = fast_exp2(d);
-    s += x.s * r;
-    a += (x.a + x.s * d) * r;
+// op over N neighbouring lanes (a power of two), in each of them: moves inside
+// the registers (through LDS the twelve steps of a merge cost rows of 2344 to
+// 16609 columns 3 % of their time).  Halves of 8 and 16 lanes may be mirrored,
+// their lanes hold one value by then.
+template <int N, class Op>
+__device__ __forceinline__ float lanes_reduce(float x, Op op) {
+  auto moved = [](float v, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  if constexpr (N >= 2) x = op(x, moved(x, std::integral_constant<int, 0xb1>{}));    // quad: 1 0 3 2
+  if constexpr (N >= 4) x = op(x, moved(x, std::integral_constant<int, 0x4e>{}));    // quad: 2 3 0 1
+  if constexpr (N >= 8) x = op(x, moved(x, std::integral_constant<int, 0x141>{}));   // mirrored in 8
+  if constexpr (N >= 16) x = op(x, moved(x, std::integral_constant<int, 0x140>{}));  // mirrored in 16
+  if constexpr (N >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
   }
-  if (y.s != 0.f) {
-    const float d = y.mc - mc, r = fast_exp2(d);
-    s += y.s * r;
-    a += (y.a + y.s * d) * r;
+  if constexpr (N >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
   }
-  return Stat{mc, s, a};
+  return x;
 }
 
-__device__ __forceinline__ Stat stat_wave_merge_nan(Stat st) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    Stat o;
-    o.mc = __shfl_xor(st.mc, off, 64);
-    o.s = __shfl_xor(st.s, off, 64);
-    o.a = __shfl_xor(st.a, off, 64);
-    st = stat_merge_nan(st, o);
-  }
-  return st;
+// The whole of N states of N neighbouring lanes, in each: all move to the
+// largest value first, then sums and nothing else.  An empty state adds nothing
+// and a NaN one wins.
+template <int N>
+__device__ __forceinline__ RowStat stat_merge(RowStat st, float c) {
+  const float m = lanes_reduce<N>(st.m, [](float x, float y) { return fmaxf(x, y); });
+  const float d = stat_shift(st.m, m, c), r = fast_exp2(d);
+  auto sum = [](float x, float y) { return x + y; };
+  return RowStat{m, lanes_reduce<N>(st.s * r, sum), lanes_reduce<N>((st.a + st.s * d) * r, sum)};
+}
+
+// As stat_merge, of two states in one lane.
+__device__ __forceinline__ RowStat stat_add(RowStat x, RowStat y, float c) {
+  const float m = fmaxf(x.m, y.m);
+  const float dx = stat_shift(x.m, m, c), rx = fast_exp2(dx), dy = stat_shift(y.m, m, c), ry = fast_exp2(dy);
+  return RowStat{m, x.s * rx + y.s * ry, (x.a + x.s * dx) * rx + (y.a + y.s * dy) * ry};
 }
 
 // One row's scalars.
@@ -274,14 +342,17 @@ __device__ __forceinline__ uint32_t block_exclusive_sum(uint32_t v, uint32_t* sm
 
 // The outputs of a row from its whole state and its target's processed logit.
 // s == 0: nothing has weight (shut out, -inf, or so low that z c leaves fp32).
-__device__ __forceinline__ void store_score(const RulesArgs& a, int64_t row, Stat st, float zy) {
-  const float l2s = log2f(st.s);
+__device__ __forceinline__ void store_score(const RulesArgs& a, int64_t row, RowStat st, float zy) {
+#pragma clang fp contract(off)  // s is relative to the rounded product
+  const float mc = st.m * a.c, l2s = log2f(st.s);
+  const bool near = is_near(mc);
   const int64_t y = a.targets[row];
   float lp = __builtin_nanf("");
-  if (y >= 0 && y < a.V && st.s != 0.f) lp = (fmaf(zy, a.c, -st.mc) - l2s) * kLn2;
+  if (y >= 0 && y < a.V && st.s != 0.f) lp = ((near ? fmaf(zy, a.c, -mc) : (zy - st.m) * a.c) - l2s) * kLn2;
   a.logprob[row] = lp;
   if (a.entropy_out) a.entropy_out[row] = (l2s - st.a / st.s) * kLn2;
-  if (a.lse_out) a.lse_out[row] = (st.mc + l2s) * kLn2;
+  // m / tau may be a number where m c is none
+  if (a.lse_out) a.lse_out[row] = near ? (mc + l2s) * kLn2 : fmaf(st.m, a.c * kLn2, l2s * kLn2);
 }
 
 __device__ __forceinline__ void store_unscored(const RulesArgs& a, int64_t row) {
@@ -297,7 +368,7 @@ __device__ __forceinline__ void store_unscored(const RulesArgs& a, int64_t row) 
 // 32-bit offset: one instruction a load.  ahead: the lane's first U vectors,
 // loaded by the caller where the slice has that many for every lane (kProcess).
 template <class Tr, int OP, int NT, int U, bool ALIGNED>
-__device__ __forceinline__ void stream_vectors(const RowRules& r, Stat& st, const char* xp, char* op, int nvec, int head,
+__device__ __forceinline__ void stream_vectors(const RowRules& r, LaneStat& st, const char* xp, char* op, int nvec, int head,
                                                int c0, const u32x4* ahead) {
   constexpr int P = Tr::kPerVec;
   constexpr bool kPairs = Tr::kBytes == 2 && OP != kGrad;
@@ -369,7 +440,7 @@ template <class Tr, int OP, int NT, int U>
 __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   __shared__ uint32_t sums[NT / 64];
-  __shared__ Stat sm[NT / 64];
+  __shared__ RowStat sm[NT / 64];
   __shared__ float zy;  // processed logit of the target, if it is a touched column
   constexpr int P = Tr::kPerVec;
   const int tid = threadIdx.x;
@@ -408,7 +479,9 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     r.ga = a.grad_entropy ? fmaf(gh, a.entropy[row], g) : g;
     r.gb = gh * kLn2;
     r.gy = g;
-    if (a.lse[row] == neg_inf()) {  // nothing has weight: no gradient
+    // Nothing has weight, or an lse so far out that its rounding to fp32 is a
+    // factor of e and more of every probability: no gradient.
+    if (fabsf(r.nlse2) >= kFar) {
       r.nlse2 = neg_inf();
       r.ga = r.gb = r.gy = 0.f;
     }
@@ -568,7 +641,7 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
     __syncthreads();
   }
 
-  Stat st = stat_empty();
+  LaneStat st = stat_none();
   auto single = [&](int j) {
     float z = Tr::load1(xp, j);
     stream_cols<OP, 1>(r, &z, r.allowed ? bits_at<1>(r.allowed, c0 + j) : 0u, r.bits ? bits_at<1>(r.bits, j) : 0u, j);
@@ -614,12 +687,12 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   }
 
   if (OP == kScore) {
-    st = stat_wave_merge_nan(st);
-    if ((tid & 63) == 0) sm[tid >> 6] = st;
+    constexpr int W = NT / 64;
+    RowStat whole = stat_merge<64>(st, a.c);
+    if ((tid & 63) == 0) sm[tid >> 6] = whole;
     __syncthreads();
+    if (tid < 64) whole = stat_merge<W>(sm[tid & (W - 1)], a.c);
     if (tid == 0) {
-#pragma unroll
-      for (int k = 1; k < NT / 64; ++k) st = stat_merge_nan(st, sm[k]);
       float z = 0.f;
       if (mine) {
         const int j = static_cast<int>(r.y) - c0;
@@ -631,12 +704,12 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
         }
       }
       if (a.nslices == 1) {
-        store_score(a, row, st, z);
+        store_score(a, row, whole, z);
       } else {
         float* pt = a.part + (row * a.nslices + slice) * 3;
-        pt[0] = st.mc;
-        pt[1] = st.s;
-        pt[2] = st.a;
+        pt[0] = whole.m;
+        pt[1] = whole.s;
+        pt[2] = whole.a;
         if (mine) a.zy[row] = z;
       }
     }
@@ -652,12 +725,12 @@ __global__ void __launch_bounds__(256) k_rules_join(RulesArgs a) {
     if (lane == 0) store_unscored(a, row);
     return;
   }
-  Stat st = stat_empty();
+  RowStat st{neg_inf(), 0.f, 0.f};
   for (int i = lane; i < a.nslices; i += 64) {
     const float* pt = a.part + (row * a.nslices + i) * 3;
-    st = stat_merge_nan(st, Stat{pt[0], pt[1], pt[2]});
+    st = stat_add(st, RowStat{pt[0], pt[1], pt[2]}, a.c);
   }
-  st = stat_wave_merge_nan(st);
+  st = stat_merge<64>(st, a.c);
   // a target outside the vocabulary has no processed logit: not read
   const int64_t y = a.targets[row];
   if (lane == 0) store_score(a, row, st, y >= 0 && y < a.V ? a.zy[row] : 0.f);

@@ -404,9 +404,12 @@ lp_status lp_process_logits(const void* logits, lp_dtype dtype, int64_t T, int64
  * the processed logits (which stay fp32: they are not rounded to `dtype`).
  * logprob fp32 [T] (required); entropy, lse fp32 [T] or NULL; lse is the
  * log-sum-exp of the tempered processed logits, saved for the backward.
- * A target that the grammar does not allow has log-prob -inf.  A processed logit
- * below -2.35e38 temperature weighs nothing, as -inf does (the exponent
- * z log2(e) / temperature is fp32): so does the lowest value of bf16 and fp32.
+ * A target that the grammar does not allow has log-prob -inf.  Finite logits of
+ * any size may stand in a row (masks of -1e10, -1e30 and the like), or fill it:
+ * what counts is how far each lies below the largest.  Only a processed logit
+ * below -2.35e38 temperature weighs nothing, as -inf does (its exponent
+ * z log2(e) / temperature leaves fp32): at temperatures up to 1.43 the lowest value
+ * of bf16 and of fp32 are such.  An lse past fp32 is infinite.
  * A row in which nothing has weight has lse -inf, NaN in logprob and entropy, and gradient 0.
  * workspace >= lp_processed_workspace_bytes(T, V) bytes, 256-byte aligned; scratch only.
  */
@@ -427,6 +430,9 @@ lp_status lp_processed_logprobs_entropy(const void* logits, lp_dtype dtype, int6
  * grad_logits   [T x ld_grad] of `dtype`, rounded once, OVERWRITTEN (unscored
  *               rows get 0; columns past V are left); may not overlap the logits.
  * A target outside [0, V) adds nothing but the row's softmax term.
+ * Probabilities are taken from lse, whose rounding to fp32 makes each off by a
+ * factor of up to exp(|lse| 2^-24).  Where |lse| passes 2^24 / log2(e) = 1.16e7 nothing
+ * of them is left: such rows get gradient 0.
  * Needs no workspace.
  */
 lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dtype, int64_t T, int64_t V,
