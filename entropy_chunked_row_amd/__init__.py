@@ -39,15 +39,17 @@ def _torch():
     return _torch_module
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return LP_BF16
-    if t.dtype == torch.float16:
-        return LP_FP16
-    if t.dtype == torch.float32:
-        return LP_FP32
-    raise TypeError(f"unsupported logits dtype {t.dtype}")
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: LP_BF16, torch.float16: LP_FP16, torch.float32: LP_FP32})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported logits dtype {t.dtype}")
+    return code
 
 
 def _ptr(t) -> Optional[int]:
@@ -72,9 +74,10 @@ def _on(device, **tensors):
 
 def _rows(t, name):
     """2-D tensor with unit stride along columns; returns its leading dimension."""
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride, shape = t.stride(), t.shape
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+    return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
 def _vec(t, name, dtype=None, n=None):
@@ -483,7 +486,7 @@ def _scope(device, stream):
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, expected {device}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return _NO_SCOPE
 
@@ -496,9 +499,9 @@ def _raw_stream(device, stream):
 
 def _same_device(device, named):
     """Every (name, tensor) lives on `device`."""
-    index = device.index
+    index = device.index  # None for the host, which no tensor's device number equals
     for name, t in named:
-        if t is not None and (not t.is_cuda or t.get_device() != index):
+        if t is not None and t.get_device() != index:
             _on(device, **{name: t})
 
 
@@ -513,97 +516,133 @@ class LogitRules:
     [T + 1] into bias_tokens (int32) and bias_values (fp32).  allowed [T, W]
     int32 or uint32 with contiguous rows, W >= ceil(V / 32).
 
-    Types and layouts are checked here, the lengths that depend on T and V and
-    the device by each call that takes the rules.  The tensors are kept, not
-    copied: what they hold when a call runs on the stream is what it reads."""
+    Types and layouts are checked here and again by each call that takes the
+    rules, as are the lengths that depend on T and V and the device.  The
+    tensors are kept, not copied: a call reads them as they are when it is made
+    (resized or pointed elsewhere included), and what they hold when it runs
+    on the stream."""
 
-    __slots__ = ("c", "_per_row", "_whole", "_buffers", "_offsets", "_words")
+    __slots__ = ("_tokens", "_vectors", "_biases", "_allowed")
 
     def __init__(self, tokens=None, hist_len=None, prompt_len=None, row_seq=None, repetition=None, frequency=None,
                  presence=None, bias_offsets=None, bias_tokens=None, bias_values=None, allowed=None):
         torch = _torch()
         i32, f32 = torch.int32, torch.float32
-        self.c = c = _lib.LogitRulesC()
-        self._per_row = per_row = []
-        self._whole = whole = []
-        self._buffers = None
-        if tokens is not None:
-            if tokens.dtype != i32:
-                raise TypeError(f"tokens must be torch.int32, got {tokens.dtype}")
-            ld = _rows(tokens, "tokens")
-            if hist_len is None:
-                raise ValueError("tokens need hist_len")
-            whole.append(("tokens", tokens))
-            # no buffers, or buffers of no tokens: nobody has a history
-            if tokens.numel():
-                c.tokens, c.buffers, c.ld_tokens, c.max_len = tokens.data_ptr(), tokens.size(0), ld, tokens.size(1)
-                if row_seq is None:
-                    self._buffers = tokens.size(0)
-            for name, t, dt in (("hist_len", hist_len, i32), ("prompt_len", prompt_len, i32), ("row_seq", row_seq, i32),
-                                ("repetition", repetition, f32), ("frequency", frequency, f32),
-                                ("presence", presence, f32)):
-                if t is not None:
-                    if t.dtype != dt or not t.is_contiguous():
-                        _vec(t, name, dt)
-                    per_row.append((name, t))
-            if c.tokens:
-                c.hist_len = hist_len.data_ptr()
-                if prompt_len is not None:
-                    c.prompt_len = prompt_len.data_ptr()
-                if row_seq is not None:
-                    c.row_buffer = row_seq.data_ptr()
-                if repetition is not None:
-                    c.repetition = repetition.data_ptr()
-                if frequency is not None:
-                    c.frequency = frequency.data_ptr()
-                if presence is not None:
-                    c.presence = presence.data_ptr()
-        elif any(t is not None for t in (hist_len, prompt_len, row_seq, repetition, frequency, presence)):
+        self._tokens = tokens
+        # (name, field of lp_logit_rules, tensor, dtype) of the per-row arrays
+        self._vectors = vectors = []
+        if hist_len is not None:
+            vectors.append(("hist_len", "hist_len", hist_len, i32))
+        elif tokens is not None:
+            raise ValueError("tokens need hist_len")
+        if prompt_len is not None:
+            vectors.append(("prompt_len", "prompt_len", prompt_len, i32))
+        if row_seq is not None:
+            vectors.append(("row_seq", "row_buffer", row_seq, i32))
+        if repetition is not None:
+            vectors.append(("repetition", "repetition", repetition, f32))
+        if frequency is not None:
+            vectors.append(("frequency", "frequency", frequency, f32))
+        if presence is not None:
+            vectors.append(("presence", "presence", presence, f32))
+        if tokens is None and vectors:
             raise ValueError("penalties need tokens and hist_len")
-        self._offsets = bias_offsets
+        self._biases = None
         if bias_offsets is not None:
             if bias_tokens is None or bias_values is None:
                 raise ValueError("biases need bias_tokens and bias_values")
-            _vec(bias_offsets, "bias_offsets", torch.int64)
-            _vec(bias_tokens, "bias_tokens", i32)
-            n = bias_tokens.numel()
-            _vec(bias_values, "bias_values", f32, n)
-            c.bias_offsets, c.bias_count = bias_offsets.data_ptr(), n
-            c.bias_tokens, c.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
-            whole += (("bias_offsets", bias_offsets), ("bias_tokens", bias_tokens), ("bias_values", bias_values))
+            self._biases = bias_offsets, bias_tokens, bias_values
         elif bias_tokens is not None or bias_values is not None:
             raise ValueError("biases need bias_offsets")
-        self._words = allowed
+        self._allowed = allowed
+        self._layouts()
+
+    @property
+    def _per_row(self):
+        return [(name, t) for name, _, t, _ in self._vectors]
+
+    @property
+    def _whole(self):
+        named = [("tokens", self._tokens), *zip(("bias_offsets", "bias_tokens", "bias_values"), self._biases or ()),
+                 ("allowed", self._allowed)]
+        return [(name, t) for name, t in named if t is not None]
+
+    def _layouts(self):
+        """Types and layouts as they are now; (pitch of tokens, entries of the biases, pitch of allowed)."""
+        torch = _torch()
+        ld_tokens = bias_count = ld_allowed = 0
+        tokens = self._tokens
+        if tokens is not None:
+            if tokens.dtype is not torch.int32:
+                raise TypeError(f"tokens must be torch.int32, got {tokens.dtype}")
+            ld_tokens = _rows(tokens, "tokens")
+            for name, _, t, dt in self._vectors:
+                if t.dtype is not dt or not t.is_contiguous():
+                    _vec(t, name, dt)
+        if self._biases is not None:
+            offsets, ids, values = self._biases
+            bias_count = ids.numel()
+            if offsets.dtype is not torch.int64 or not offsets.is_contiguous():
+                _vec(offsets, "bias_offsets", torch.int64)
+            if ids.dtype is not torch.int32 or not ids.is_contiguous():
+                _vec(ids, "bias_tokens", torch.int32)
+            if values.dtype is not torch.float32 or not values.is_contiguous() or values.numel() != bias_count:
+                _vec(values, "bias_values", torch.float32, bias_count)
+        allowed = self._allowed
         if allowed is not None:
-            if allowed.dtype != i32 and allowed.dtype != torch.uint32:
+            if allowed.dtype is not torch.int32 and allowed.dtype is not torch.uint32:
                 raise TypeError(f"allowed must be int32 or uint32, got {allowed.dtype}")
-            c.ld_allowed = _rows(allowed, "allowed")
-            c.allowed = allowed.data_ptr()
-            whole.append(("allowed", allowed))
+            ld_allowed = _rows(allowed, "allowed")
+        return ld_tokens, bias_count, ld_allowed
 
     def _check(self, T, V, device):
         """The ctypes argument for a call on T rows of V columns on `device`."""
-        for name, t in self._per_row:
-            if t.numel() != T:
-                raise ValueError(f"{name} must have {T} elements, got {t.numel()}")
-        if self._buffers is not None and self._buffers < T:
-            raise ValueError(f"tokens must have a buffer for each of {T} rows, got {self._buffers}")
-        if self._offsets is not None and self._offsets.numel() != T + 1:
-            raise ValueError(f"bias_offsets must have {T + 1} elements, got {self._offsets.numel()}")
-        w = self._words
-        if w is not None and (w.size(0) != T or w.size(1) < (V + 31) // 32):
-            raise ValueError(f"allowed must be [{T}, >= {(V + 31) // 32}], got {list(w.shape)}")
-        _same_device(device, self._per_row)
-        _same_device(device, self._whole)
-        return ctypes.byref(self.c)
+        c = _lib.LogitRulesC()
+        c.ld_tokens, c.bias_count, c.ld_allowed = self._layouts()
+        index = device.index
+        elsewhere = False  # a tensor on another device, reported after every length
+        tokens = self._tokens
+        if tokens is not None:
+            buffers, length = tokens.shape
+            elsewhere = tokens.get_device() != index
+            # no buffers, or buffers of no tokens: nobody has a history
+            some = buffers and length
+            if some:
+                c.tokens, c.buffers, c.max_len = tokens.data_ptr(), buffers, length
+            for name, field, t, _ in self._vectors:
+                if t.numel() != T:
+                    raise ValueError(f"{name} must have {T} elements, got {t.numel()}")
+                if t.get_device() != index:
+                    elsewhere = True
+                if some:
+                    setattr(c, field, t.data_ptr())
+            if some and buffers < T and not c.row_buffer:
+                raise ValueError(f"tokens must have a buffer for each of {T} rows, got {buffers}")
+        if self._biases is not None:
+            offsets, ids, values = self._biases
+            if offsets.numel() != T + 1:
+                raise ValueError(f"bias_offsets must have {T + 1} elements, got {offsets.numel()}")
+            c.bias_offsets, c.bias_tokens, c.bias_values = offsets.data_ptr(), ids.data_ptr(), values.data_ptr()
+            if offsets.get_device() != index or ids.get_device() != index or values.get_device() != index:
+                elsewhere = True
+        allowed = self._allowed
+        if allowed is not None:
+            rows, words = allowed.shape
+            if rows != T or words < (V + 31) // 32:
+                raise ValueError(f"allowed must be [{T}, >= {(V + 31) // 32}], got {list(allowed.shape)}")
+            c.allowed = allowed.data_ptr()
+            if allowed.get_device() != index:
+                elsewhere = True
+        if elsewhere:
+            _same_device(device, self._per_row + self._whole)
+        return ctypes.byref(c)
 
 
 def _processed_operands(logits, rules):
     """(T, V, ld, rules argument) of logits [T, V] under `rules` (None: no rules)."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-D [T, V]")
+    ld = _rows(logits, "logits")
     T, V = logits.shape
-    return T, V, _rows(logits, "logits"), None if rules is None else rules._check(T, V, logits.device)
+    return T, V, ld, None if rules is None else rules._check(T, V, logits.device)
 
 
 def lp_process_logits(logits, rules, mask=None, *, out=None, stream=None):
