@@ -551,10 +551,27 @@ static bool i32_aligned(std::initializer_list<const void*> ps) {
   return true;
 }
 
-// Whether two row-major blocks of T rows share bytes, taken as address ranges.
-static bool ranges_overlap(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t T, int64_t V, size_t e) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + (uintptr_t(T - 1) * ld_b + V) * e && y < x + (uintptr_t(T - 1) * ld_a + V) * e;
+// A row-major block in memory: `width` bytes of each of `rows` rows, `pitch`
+// bytes apart.
+struct Block {
+  uintptr_t at;
+  uint64_t rows, width, pitch;
+  Block(const void* p, int64_t n, int64_t w, int64_t ld, size_t e)
+      : at(reinterpret_cast<uintptr_t>(p)), rows(n), width(uint64_t(w) * e), pitch(uint64_t(ld) * e) {}
+  uintptr_t end() const { return at + (rows - 1) * pitch + width; }
+};
+
+// Whether two blocks share bytes.  Address ranges that do not meet share none,
+// and neither do rows of one pitch that lie beside each other; all else counts
+// as shared.
+static bool share_bytes(const Block& a, const Block& b) {
+  if (a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  // a single row may be taken at the other block's pitch
+  const uint64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if (b.rows > 1 && b.pitch != pitch) return true;
+  const uint64_t apart = a.at < b.at ? (b.at - a.at) % pitch : (pitch - (a.at - b.at) % pitch) % pitch;
+  return apart < a.width || apart + b.width > pitch;
 }
 
 // Checks shared by the calls under rules; fills the fields every one of them
@@ -641,7 +658,8 @@ lp_status lp_process_logits(const void* logits, lp_dtype dtype, int64_t T, int64
   if (ld_out > (int64_t(1) << 40) / T) return fail(LP_ERR_UNSUPPORTED, "%s: T x ld_out past 2^40 elements", fn);
   if (!out || !aligned(out, dtype_bytes(dtype)))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: out is required and must be aligned", fn);
-  if (!(out == logits && ld_out == ld) && ranges_overlap(logits, ld, out, ld_out, T, V, dtype_bytes(dtype)))
+  const size_t e_bytes = dtype_bytes(dtype);
+  if (!(out == logits && ld_out == ld) && share_bytes({logits, T, V, ld, e_bytes}, {out, T, V, ld_out, e_bytes}))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: out overlaps the logits without being them", fn);
   a.out = out;
   a.ld_out = ld_out;
@@ -707,7 +725,8 @@ lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dt
   if (!aligned(targets, 8) || !f32_aligned({lse, entropy, grad_logprob, grad_entropy}) ||
       !aligned(grad_logits, dtype_bytes(dtype)))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
-  if (ranges_overlap(logits, ld, grad_logits, ld_grad, T, V, dtype_bytes(dtype)))
+  const size_t e_bytes = dtype_bytes(dtype);
+  if (share_bytes({logits, T, V, ld, e_bytes}, {grad_logits, T, V, ld_grad, e_bytes}))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: grad_logits overlaps the logits", fn);
   a.targets = targets;
   a.c = exp2_scale(temperature);

@@ -390,7 +390,8 @@ typedef struct lp_logit_rules {
  * out = the logits under the rules, rounded once to `dtype`.  No temperature.
  * logits [T x ld], out [T x ld_out] of `dtype`; out may be the logits
  * themselves (same pointer and ld; the one call that writes an input) but may
- * not overlap them otherwise.  Rows with mask[t] == 0 are left as they were in out, and
+ * not overlap them otherwise (rows of one pitch that lie beside each other do
+ * not, nor do separate address ranges; anything else is refused).  Rows with mask[t] == 0 are left as they were in out, and
  * so are columns past V.  A row whose grammar allows nothing becomes all -inf.
  * Needs no workspace.
  */
@@ -428,10 +429,10 @@ lp_status lp_processed_logprobs_entropy(const void* logits, lp_dtype dtype, int6
  * grammar does not allow j.  The rules themselves get no gradient.
  * lse, entropy  fp32 [T] of the forward (entropy may be NULL without grad_entropy).
  * grad_logits   [T x ld_grad] of `dtype`, rounded once, OVERWRITTEN (unscored
- *               rows get 0; columns past V are left); may not overlap the logits.
+ *               rows get 0; columns past V are left); may not overlap the logits, as above.
  * A target outside [0, V) adds nothing but the row's softmax term.
  * Probabilities are taken from lse, whose rounding to fp32 makes each off by a
- * factor of up to exp(|lse| 2^-24).  Where |lse| passes 2^24 / log2(e) = 1.16e7 nothing
+ * factor of up to exp(|lse| 2^-22) (three roundings to fp32 on the way).  Where |lse| passes 2^24 / log2(e) = 1.16e7 nothing
  * of them is left: such rows get gradient 0.
  * Needs no workspace.
  */
