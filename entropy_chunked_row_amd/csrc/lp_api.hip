@@ -558,6 +558,7 @@ struct Block {
   uint64_t rows, width, pitch;
   Block(const void* p, int64_t n, int64_t w, int64_t ld, size_t e)
       : at(reinterpret_cast<uintptr_t>(p)), rows(n), width(uint64_t(w) * e), pitch(uint64_t(ld) * e) {}
+  Block(const void* p, int64_t n, size_t e) : Block(p, 1, n, n, e) {}
   uintptr_t end() const { return at + (rows - 1) * pitch + width; }
 };
 
@@ -771,6 +772,10 @@ lp_status lp_embedding(const void* weight, lp_dtype dtype, int64_t V, int64_t h,
   if (!weight || !tokens || !out) return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight, tokens and out are required", fn);
   if (!aligned(weight, dtype_bytes(dtype)) || !aligned(out, dtype_bytes(dtype)) || !aligned(tokens, 8))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t e_bytes = dtype_bytes(dtype);
+  const Block written(out, N, h, ld_out, e_bytes);
+  if (share_bytes(written, {weight, V, h, ld_w, e_bytes}) || share_bytes(written, {tokens, N, 8}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: out overlaps an input", fn);
   lp::EmbedArgs a;
   a.weight = weight;
   a.ld_w = ld_w;
@@ -817,6 +822,11 @@ lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N,
     return fail(LP_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %zu bytes, got %zu", fn, w.total,
                 workspace ? workspace_bytes : size_t(0));
   if (!aligned(workspace, 256)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
+  const Block gradient(grad_weight, V * h, 4), scratch(workspace, static_cast<int64_t>(w.total), 1);
+  const Block grads(grad_out, N, h, ld_g, dtype_bytes(dtype)), ids(tokens, N, 8);
+  if (share_bytes(gradient, grads) || share_bytes(gradient, ids) || share_bytes(gradient, scratch) ||
+      share_bytes(scratch, grads) || share_bytes(scratch, ids))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: grad_weight or the workspace overlaps an operand", fn);
   lp::EmbedGradArgs a;
   memset(&a, 0, sizeof(a));
   a.grad = grad_out;
@@ -868,6 +878,10 @@ lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, 
   if (ld_w > (int64_t(1) << 59) / V) return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
   if (!weight || !aligned(weight, dtype_bytes(dtype)))
     return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight is required and must be aligned", fn);
+  const Block dense(weight, V, h, ld_w, dtype_bytes(dtype)), head(packed, V, h / 2, ld_packed, 1);
+  const Block steps(scales, V, (h + group - 1) / group, ld_scales, 2);
+  if (share_bytes(dense, head) || share_bytes(dense, steps) || share_bytes(head, steps))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight, packed and scales overlap", fn);
   lp::W4QuantArgs a;
   a.weight = weight;
   a.ld_w = ld_w;
@@ -905,6 +919,10 @@ lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, in
   if (!hidden || !out) return fail(LP_ERR_INVALID_ARGUMENT, "%s: hidden and out are required", fn);
   if (!aligned(hidden, 16)) return fail(LP_ERR_UNSUPPORTED, "%s: hidden must be 16-byte aligned", fn);
   if (!aligned(out, dtype_bytes(out_dtype))) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned out", fn);
+  const Block written(out, T, V, ld_out, dtype_bytes(out_dtype));
+  if (share_bytes(written, {hidden, T, h, ld_h, 2}) || share_bytes(written, {packed, V, h / 2, ld_packed, 1}) ||
+      share_bytes(written, {scales, V, (h + group - 1) / group, ld_scales, 2}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: out overlaps an input", fn);
   lp::W4Args a;
   a.hidden = static_cast<const uint16_t*>(hidden);
   a.ld_h = ld_h;

@@ -455,7 +455,7 @@ lp_status lp_processed_logprobs_entropy_backward(const void* logits, lp_dtype dt
  *
  * lp_lm_head_w4_quantize lays a head out: per group, scale = amax / 7 rounded to
  * bf16, q = clamp(round-half-even(w / scale), -8, 7) + 8 (8 where the scale
- * is 0).  weight [V x ld_w] of `dtype`.  A group that holds a NaN or an
+ * is 0).  weight [V x ld_w] of `dtype`; weight, packed and scales may not overlap.  A group that holds a NaN or an
  * infinity makes its row's logits NaN.
  */
 lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w,
@@ -465,7 +465,8 @@ lp_status lp_lm_head_w4_quantize(const void* weight, lp_dtype dtype, int64_t V, 
 /*
  * out[t][v] = hidden[t] . weight[v] of such a head; products and sums fp32,
  * rounded once to out_dtype.  hidden bf16 or fp16 [T x ld_h] (further LP_ERR_UNSUPPORTED:
- * fp32, ld_h % 8 != 0, not 16-byte aligned), out [T x ld_out] of out_dtype, columns past V left.
+ * fp32, ld_h % 8 != 0, not 16-byte aligned), out [T x ld_out] of out_dtype, columns past V left;
+ * out may not overlap an input.
  * Up to 64 rows read the head once; more rows read it again for every 64.
  * Needs no workspace.  The result of a row does not depend on the other rows,
  * bit for bit.  Sums run on 24 times the values of hidden: rows that hold an
@@ -480,7 +481,7 @@ lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, in
  * and rounded once to `dtype`.
  * weight [V x ld_w], out [N x ld_out] of `dtype`, h columns used; tokens int64
  * [N].  An id outside [0, V) (padding) gives a row of zeros.  scale must be
- * finite.  Columns of out past h are left.  N == 0 returns LP_OK without launching.
+ * finite.  Columns of out past h are left; out may not overlap an input.  N == 0 returns LP_OK without launching.
  */
 lp_status lp_embedding(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w, const int64_t* tokens,
                        int64_t N, float scale, void* out, int64_t ld_out, void* stream);
@@ -495,7 +496,8 @@ lp_status lp_embedding(const void* weight, lp_dtype dtype, int64_t V, int64_t h,
  * grad_out [N x ld_g] of `dtype`; rows of ids outside [0, V) are ignored.
  * Sums are fp32 in a fixed order (no float atomics): the same bits on every call.
  * workspace >= lp_embedding_workspace_bytes(N, h, V) bytes (0: sizes not
- *   supported; N is at most 2^31 - 1), 256-byte aligned; scratch only.
+ *   supported; N is at most 2^31 - 1), 256-byte aligned; scratch only.  It and
+ *   grad_weight may overlap neither each other nor an input.
  */
 size_t lp_embedding_workspace_bytes(int64_t N, int64_t h, int64_t V);
 lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N, int64_t h, int64_t ld_g,

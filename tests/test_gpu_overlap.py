@@ -33,3 +33,25 @@ def test_rules_beside_their_logits(dtype, gap):
         assert bool((buf[:, V:V + gap] == 5).all())
         with pytest.raises(lp.LPError, match="overlaps"):
             lp.lp_process_logits(buf[:, :V], rules, out=buf[:, V - 1:2 * V - 1])
+
+
+def test_embedding_and_head_beside_their_operands():
+    import torch
+
+    import entropy_chunked_row_amd as lp
+    buf = torch.randn(300, 200, device="cuda").bfloat16()
+    tok = torch.randint(0, 300, (300,), device="cuda")
+    want = lp.lp_embedding(buf[:, :96].contiguous(), tok, 2.0)
+    lp.lp_embedding(buf[:, :96], tok, 2.0, out=buf[:, 97:193])
+    assert torch.equal(buf[:, 97:193], want)
+    with pytest.raises(lp.LPError, match="overlaps"):
+        lp.lp_embedding(buf[:, :96], tok, 2.0, out=buf[:, 95:191])
+    g = torch.randn(50, 64, device="cuda")
+    with pytest.raises(lp.LPError, match="overlaps"):
+        lp.lp_embedding_backward(g, tok[:50] % 10, 10, 1.0, grad_weight=g[5:15])
+    x = torch.randn(4, 64, device="cuda").half()
+    p, s = lp.lp_lm_head_w4_quantize(torch.randn(64, 64, device="cuda"), 32)
+    with pytest.raises(lp.LPError, match="overlaps"):
+        lp.lp_lm_head_w4_logits(x, p, s, 32, out=x)
+    with pytest.raises(lp.LPError, match="overlap"):
+        lp.lp_lm_head_w4_quantize(x, 32, packed=x.view(torch.uint8)[:, :32])
