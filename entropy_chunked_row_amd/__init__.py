@@ -646,8 +646,8 @@ def _processed_operands(logits, rules):
 
 
 def lp_process_logits(logits, rules, mask=None, *, out=None, stream=None):
-    """logits [T, V] under `rules` (LogitRules or None), rounded once to their dtype.  Rows with mask 0 are not
-    written; out may be the logits themselves (in place)."""
+    """logits [T, V] under `rules` (LogitRules or None), rounded once to their dtype.  Rows with mask 0 keep what `out`
+    held, and are 0 where no out is given; out may be the logits themselves (in place)."""
     torch = _torch()
     lib = load()
     dtype = _dtype_code(logits)
@@ -660,7 +660,8 @@ def lp_process_logits(logits, rules, mask=None, *, out=None, stream=None):
     _same_device(dev, (("logits", logits), ("mask", mask), ("out", out)))
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((T, V), dtype=logits.dtype, device=dev)
+            # the kernel leaves unscored rows alone: they are cleared first
+            out = (torch.empty if mask is None else torch.zeros)((T, V), dtype=logits.dtype, device=dev)
         st = lib.lp_process_logits(_ptr(logits), dtype, T, V, ld, c_rules, _ptr(mask), _ptr(out), ld_out,
                                    _raw_stream(dev, stream))
     check("lp_process_logits", st)
