@@ -35,17 +35,18 @@ __device__ __forceinline__ Stat stat_empty() { return Stat{kNegBig, 0.f, 0.f}; }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Merge two partial states of the same row.
+// Merge two partial states of the same row.  A side that has seen nothing
+// (s == 0) adds nothing; a NaN side makes the whole NaN.
 __device__ __forceinline__ Stat stat_merge(Stat x, Stat y) {
   const float mc = fmaxf(x.mc, y.mc);
   float s = 0.f, a = 0.f;
-  if (x.s > 0.f) {
+  if (x.s != 0.f) {
     const float d = x.mc - mc;
     const float r = fast_exp2(d);
     s += x.s * r;
     a += (x.a + x.s * d) * r;
   }
-  if (y.s > 0.f) {
+  if (y.s != 0.f) {
     const float d = y.mc - mc;
     const float r = fast_exp2(d);
     s += y.s * r;
@@ -56,7 +57,7 @@ __device__ __forceinline__ Stat stat_merge(Stat x, Stat y) {
 
 // Move a state to a new, larger reference exponent nmc.
 __device__ __forceinline__ void stat_rebase(Stat& st, float nmc) {
-  if (st.s > 0.f) {
+  if (st.s != 0.f) {
     const float d = st.mc - nmc;
     const float r = fast_exp2(d);
     st.a = (st.a + st.s * d) * r;
@@ -66,8 +67,8 @@ __device__ __forceinline__ void stat_rebase(Stat& st, float nmc) {
 }
 
 // Fold N widened values into the state: one max test, then CH-long partial
-// sums (short chains keep fp32 rounding low).  GUARD clamps t so that a -inf
-// value contributes 0 * finite instead of 0 * -inf to `a`.
+// sums (short chains keep fp32 rounding low).  GUARD clamps t in `a`, so that a
+// -inf value contributes 0 * finite instead of 0 * -inf (a NaN stays in s).
 template <bool GUARD, int N, int CH>
 __device__ __forceinline__ void stat_push(Stat& st, const float* x, float c) {
   float vm = x[0];
@@ -81,11 +82,10 @@ __device__ __forceinline__ void stat_push(Stat& st, const float* x, float c) {
     float ps = 0.f, pa = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      float t = fmaf(x[g + k], c, nmc);
-      if (GUARD) t = fmaxf(t, kNegBig);
+      const float t = fmaf(x[g + k], c, nmc);
       const float e = fast_exp2(t);
       ps += e;
-      pa = fmaf(e, t, pa);
+      pa = fmaf(e, GUARD ? fmaxf(t, kNegBig) : t, pa);
     }
     st.s += ps;
     st.a += pa;
@@ -231,11 +231,11 @@ __device__ __forceinline__ void kl_push(KLState& st, const float* xu, const floa
   }
   const float muc = mu * c, mvc = mv * c;
   if (muc > st.mcu) {
-    if (st.su > 0.f) st.su *= fast_exp2(st.mcu - muc);
+    if (st.su != 0.f) st.su *= fast_exp2(st.mcu - muc);
     st.mcu = muc;
   }
   if (mvc > st.mcv) {
-    if (st.sv > 0.f) {
+    if (st.sv != 0.f) {
       const float r = fast_exp2(st.mcv - mvc);
       st.sv *= r;
       st.C *= r;
@@ -268,17 +268,17 @@ __device__ __forceinline__ KLState kl_merge(KLState x, KLState y) {
   KLState r;
   r.mcu = fmaxf(x.mcu, y.mcu);
   r.su = 0.f;
-  if (x.su > 0.f) r.su += x.su * fast_exp2(x.mcu - r.mcu);
-  if (y.su > 0.f) r.su += y.su * fast_exp2(y.mcu - r.mcu);
+  if (x.su != 0.f) r.su += x.su * fast_exp2(x.mcu - r.mcu);
+  if (y.su != 0.f) r.su += y.su * fast_exp2(y.mcu - r.mcu);
   r.mcv = fmaxf(x.mcv, y.mcv);
   r.sv = 0.f;
   r.C = 0.f;
-  if (x.sv > 0.f) {
+  if (x.sv != 0.f) {
     const float f = fast_exp2(x.mcv - r.mcv);
     r.sv += x.sv * f;
     r.C += x.C * f;
   }
-  if (y.sv > 0.f) {
+  if (y.sv != 0.f) {
     const float f = fast_exp2(y.mcv - r.mcv);
     r.sv += y.sv * f;
     r.C += y.C * f;
