@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace lp {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -120,6 +122,139 @@ __device__ __forceinline__ Stat stat_block_allreduce(Stat st, Stat* sm) {
   for (int k = 1; k < NW; ++k) r = stat_merge(r, sm[k]);
   __syncthreads();
   return r;
+}
+
+// ---------------------------------------------------------------------------
+// states of rows that may hold finite values of any size
+// ---------------------------------------------------------------------------
+
+constexpr float kNoWeight = -1024.f;  // exponents below weigh exactly 0 in fp32
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// Softmax state of some of a row's columns under an exponent scale c: m their
+// largest value that has weight (-inf: none yet), s = sum 2^t and a = sum 2^t t
+// over exponents t relative to m c.  Where |m c| is below kFar ("near") they
+// are t = fma(x, c, -RN(m c)), which rounds once.  The rounding of m c itself,
+// which then stands in every t alike, is an exponent of its own: 1/2 at 2^24, 512
+// at 1e10, 1e22 at 1e30.  Past kFar, where finite masks lie, t = (x - m) c
+// instead, two operations but 0 at m whatever its size (in every column they
+// would cost one instruction more of 13).
+struct RowStat {
+  float m, s, a;
+};
+
+constexpr float kFar = 16777216.f;
+constexpr float kLargest = 3.402823466e38f;
+
+__device__ __forceinline__ bool is_near(float mc) { return fabsf(mc) < kFar; }
+
+// What exponents relative to m0 gain when they are taken relative to m1.  The
+// products are rounded here as they are in the exponents: no contraction.
+__device__ __forceinline__ float reference_gap(float m0, float m1, float c) {
+#pragma clang fp contract(off)
+  const float r0 = m0 * c, r1 = m1 * c;
+  float d = r0 - r1;
+  if (!is_near(r0) || !is_near(r1)) {
+    d = (m0 - m1) * c;
+    // of near ones the rounding of their product is part
+    if (is_near(r0)) d -= fmaf(m0, c, -r0);
+    if (is_near(r1)) d += fmaf(m1, c, -r1);
+  }
+  return d;
+}
+
+// The same for m1 >= m0.  Below kNoWeight nothing is left of a weight; the
+// bound keeps s times the shift finite, and takes an empty side (m0 = -inf) to
+// nothing whatever m1.
+__device__ __forceinline__ float stat_shift(float m0, float m1, float c) {
+  return fmaxf(reference_gap(m0, m1, c), kNoWeight);
+}
+
+// A lane's state while it takes columns: with its reference exponent, which
+// moves only when a larger value comes.
+struct LaneStat : RowStat {
+  float nmc = 0.f;  // -RN(m c); 0 while m is -inf, whose exponents are then -inf or NaN
+};
+
+__device__ __forceinline__ LaneStat stat_none() { return LaneStat{{neg_inf(), 0.f, 0.f}}; }
+
+// Folds N values into the state.  They may be -inf, or so low that their
+// product with c leaves fp32: those weigh 0 and add nothing to `a`.  A NaN
+// stays a NaN in s and a.
+template <int N, int CH>
+__device__ __forceinline__ void stat_push_masked(LaneStat& st, const float* x, float c) {
+  float vm = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) vm = fmaxf(vm, x[k]);
+  if (vm > st.m && vm * c >= -kLargest) {
+    const float d = stat_shift(st.m, vm, c), r = fast_exp2(d);
+    st.a = (st.a + st.s * d) * r;
+    st.s *= r;
+    st.m = vm;
+    st.nmc = -(vm * c);
+  }
+  auto fold = [&](auto exponent) {
+#pragma unroll
+    for (int g = 0; g < N; g += CH) {
+      float ps = 0.f, pa = 0.f;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const float t = exponent(x[g + k]);
+        const float e = fast_exp2(t);
+        ps += e;
+        pa = fmaf(e, fmaxf(t, kNoWeight), pa);
+      }
+      st.s += ps;
+      st.a += pa;
+    }
+  };
+  if (is_near(st.nmc))
+    fold([&](float v) { return fmaf(v, c, st.nmc); });
+  else
+    fold([&](float v) { return (v - st.m) * c; });
+}
+
+// op over N neighbouring lanes (a power of two), in each of them: moves inside
+// the registers (through LDS the twelve steps of a merge cost rows of 2344 to
+// 16609 columns 3 % of their time).  Halves of 8 and 16 lanes may be mirrored,
+// their lanes hold one value by then.
+template <int N, class Op>
+__device__ __forceinline__ float lanes_reduce(float x, Op op) {
+  auto moved = [](float v, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  if constexpr (N >= 2) x = op(x, moved(x, std::integral_constant<int, 0xb1>{}));    // quad: 1 0 3 2
+  if constexpr (N >= 4) x = op(x, moved(x, std::integral_constant<int, 0x4e>{}));    // quad: 2 3 0 1
+  if constexpr (N >= 8) x = op(x, moved(x, std::integral_constant<int, 0x141>{}));   // mirrored in 8
+  if constexpr (N >= 16) x = op(x, moved(x, std::integral_constant<int, 0x140>{}));  // mirrored in 16
+  if constexpr (N >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if constexpr (N >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  return x;
+}
+
+// The whole of N states of N neighbouring lanes, in each: all move to the
+// largest value first, then sums and nothing else.  An empty state adds nothing
+// and a NaN one wins.
+template <int N>
+__device__ __forceinline__ RowStat stat_merge(RowStat st, float c) {
+  const float m = lanes_reduce<N>(st.m, [](float x, float y) { return fmaxf(x, y); });
+  const float d = stat_shift(st.m, m, c), r = fast_exp2(d);
+  auto sum = [](float x, float y) { return x + y; };
+  return RowStat{m, lanes_reduce<N>(st.s * r, sum), lanes_reduce<N>((st.a + st.s * d) * r, sum)};
+}
+
+// As stat_merge, of two states in one lane.
+__device__ __forceinline__ RowStat stat_add(RowStat x, RowStat y, float c) {
+  const float m = fmaxf(x.m, y.m);
+  const float dx = stat_shift(x.m, m, c), rx = fast_exp2(dx), dy = stat_shift(y.m, m, c), ry = fast_exp2(dy);
+  return RowStat{m, x.s * rx + y.s * ry, (x.a + x.s * dx) * rx + (y.a + y.s * dy) * ry};
 }
 
 // ---------------------------------------------------------------------------
@@ -284,6 +419,48 @@ __device__ __forceinline__ KLState kl_merge(KLState x, KLState y) {
     r.C += y.C * f;
   }
   return r;
+}
+
+// The dual state for rows that may hold finite values of any size: the largest
+// values instead of their exponents (RowStat).
+struct KLFar {
+  float mu, su, mv, sv, C;
+};
+
+__device__ __forceinline__ float far_exponent(float x, float m, float c) {
+  const float mc = m * c;
+  if (mc < -kLargest) return x * c;  // none yet: -inf or NaN
+  return is_near(mc) ? fmaf(x, c, -mc) : (x - m) * c;
+}
+
+// To the references of mu and mv, which are no smaller.  C may be infinite
+// (the student gives no weight to what the teacher does); with no weight left
+// of it, it is 0.
+__device__ __forceinline__ void kl_far_move(KLFar& st, float mu, float mv, float c) {
+  st.su *= fast_exp2(stat_shift(st.mu, mu, c));
+  const float r = fast_exp2(stat_shift(st.mv, mv, c));
+  st.sv *= r;
+  st.C = r == 0.f ? 0.f : st.C * r;
+  st.mu = mu;
+  st.mv = mv;
+}
+
+__device__ __forceinline__ void kl_far_push(KLFar& st, float xu, float xv, float c) {
+  const float mu = xu > st.mu && xu * c >= -kLargest ? xu : st.mu, mv = xv > st.mv && xv * c >= -kLargest ? xv : st.mv;
+  if (mu != st.mu || mv != st.mv) kl_far_move(st, mu, mv, c);
+  st.su += fast_exp2(far_exponent(xu, st.mu, c));
+  const float ev = fast_exp2(far_exponent(xv, st.mv, c));
+  st.sv += ev;
+  if (ev > 0.f) st.C += ev * (xv - xu);
+}
+
+// The whole of N states of N neighbouring lanes, in each.
+template <int N>
+__device__ __forceinline__ KLFar kl_far_merge(KLFar st, float c) {
+  auto most = [](float x, float y) { return fmaxf(x, y); };
+  auto sum = [](float x, float y) { return x + y; };
+  kl_far_move(st, lanes_reduce<N>(st.mu, most), lanes_reduce<N>(st.mv, most), c);
+  return KLFar{st.mu, lanes_reduce<N>(st.su, sum), st.mv, lanes_reduce<N>(st.sv, sum), lanes_reduce<N>(st.C, sum)};
 }
 
 // 16 bytes of a row from any element on: one load, also off the 16-byte grid.

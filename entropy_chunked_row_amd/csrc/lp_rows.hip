@@ -53,9 +53,35 @@ __device__ __forceinline__ Stat scan_row(const char* rowp, const RowSplit<Tr>& s
   return st;
 }
 
+// The row again, in states that hold for finite values of any size.
+template <class Tr, int NT>
+__device__ __forceinline__ RowStat scan_row_far(const char* rowp, const RowSplit<Tr>& sp, float c, RowStat* sm) {
+  constexpr int P = Tr::kPerVec, NW = NT / 64;
+  const int tid = threadIdx.x;
+  LaneStat st = stat_none();
+  auto single = [&](int j) {
+    const float x = Tr::load1(rowp, j);
+    stat_push_masked<1, 1>(st, &x, c);
+  };
+  if (tid < sp.head) single(tid);
+  const u32x4* vp = reinterpret_cast<const u32x4*>(rowp + sp.head * Tr::kBytes);
+  for (int i = tid; i < sp.nvec; i += NT) {
+    float x[P];
+    Tr::unpack(__builtin_nontemporal_load(vp + i), x);
+    stat_push_masked<P, P>(st, x, c);
+  }
+  if (tid < sp.tail) single(sp.head + sp.nvec * P + tid);
+  RowStat whole = stat_merge<64>(st, c);
+  if (NW == 1) return whole;
+  if ((tid & 63) == 0) sm[tid >> 6] = whole;
+  __syncthreads();
+  return stat_merge<NW>(sm[tid & (NW - 1)], c);
+}
+
 template <class Tr, int NT, int U>
 __global__ void __launch_bounds__(NT) k_logprobs_entropy(RowArgs args) {
   __shared__ Stat sm[NT / 64];
+  __shared__ RowStat sm_far[NT / 64];
   const int64_t row = args.row0 + blockIdx.x;
   if (args.mask && args.mask[row] == 0) {
     for (int k = threadIdx.x; k < args.K; k += NT) args.logprob[row * args.K + k] = 0.f;
@@ -72,13 +98,24 @@ __global__ void __launch_bounds__(NT) k_logprobs_entropy(RowArgs args) {
   // the branch is uniform.
   if (__builtin_isnan(st.a) && !__builtin_isnan(st.s))
     st = stat_block_allreduce<NT>(scan_row<Tr, NT, U, true>(rowp, sp, c), sm);
+  // Finite masks (-1e10, -1e30, the type's lowest) in all columns of a lane, or
+  // of the row, make the sums 0, infinite or NaN: redo it once more.
+  bool near = true;  // else relative to the value m (far_exponent)
+  float m = 0.f;
+  if (!(st.s > 0.f && st.s <= kLargest) || __builtin_isnan(st.a) || !is_near(st.mc)) {
+    const RowStat far = scan_row_far<Tr, NT>(rowp, sp, c, sm_far);
+    m = far.m;
+    st = Stat{0.f, far.s, far.a};
+    near = false;
+  }
   const float l2s = log2f(st.s);
   for (int k = threadIdx.x; k < args.K; k += NT) {
     const int64_t y = args.targets[row * args.K + k];
     float lp = __builtin_nanf("");
     if (y >= 0 && y < V) {
-      const float ty = fmaf(Tr::load1(rowp, y), c, -st.mc);
-      lp = (ty - l2s) * kLn2;
+      const float x = Tr::load1(rowp, y);
+      const float ty = near ? fmaf(x, c, -st.mc) : far_exponent(x, m, c);
+      if (st.s != 0.f) lp = (ty - l2s) * kLn2;  // 0: nothing in the row has weight
     }
     args.logprob[row * args.K + k] = lp;
   }
@@ -208,9 +245,23 @@ __device__ __forceinline__ KLState scan_kl(const char* up, const char* vp, int V
   return st;
 }
 
+// Both rows again, in states that hold for finite values of any size.
+template <class Tr, int NT>
+__device__ __forceinline__ KLFar scan_kl_far(const char* up, const char* vp, int V, float c, KLFar* sm) {
+  constexpr int NW = NT / 64;
+  KLFar st{neg_inf(), 0.f, neg_inf(), 0.f, 0.f};
+  for (int j = threadIdx.x; j < V; j += NT) kl_far_push(st, Tr::load1(up, j), Tr::load1(vp, j), c);
+  st = kl_far_merge<64>(st, c);
+  if (NW == 1) return st;
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = st;
+  __syncthreads();
+  return kl_far_merge<NW>(sm[threadIdx.x & (NW - 1)], c);
+}
+
 template <class Tr, int NT, int U>
 __global__ void __launch_bounds__(NT) k_kl_full_vocab(KLArgs args) {
   __shared__ KLState sm[NT / 64];
+  __shared__ KLFar sm_far[NT / 64];
   const int64_t row = args.row0 + blockIdx.x;
   const char* up = static_cast<const char*>(args.student) + row * args.ld_s * Tr::kBytes;
   const char* vp = static_cast<const char*>(args.teacher) + row * args.ld_t * Tr::kBytes;
@@ -220,16 +271,30 @@ __global__ void __launch_bounds__(NT) k_kl_full_vocab(KLArgs args) {
   KLState st = kl_block_allreduce<NT>(scan_kl<Tr, NT, U, false>(up, vp, V, aligned_pair, c), sm);
   if (__builtin_isnan(st.C) && !__builtin_isnan(st.su) && !__builtin_isnan(st.sv))
     st = kl_block_allreduce<NT>(scan_kl<Tr, NT, U, true>(up, vp, V, aligned_pair, c), sm);
+  float gap = st.mcv - st.mcu;
+  bool far = false;
+  KLFar wide{};
+  auto counts = [](float s) { return s > 0.f && s <= kLargest; };
+  if (!counts(st.su) || !counts(st.sv) || __builtin_isnan(st.C) || !is_near(st.mcu) || !is_near(st.mcv)) {
+    far = true;
+    wide = scan_kl_far<Tr, NT>(up, vp, V, c, sm_far);
+    st.su = wide.su;
+    st.sv = wide.sv;
+    st.C = wide.C;
+    gap = reference_gap(wide.mv, wide.mu, c);
+  }
   if (threadIdx.x == 0) {
     const float l2u = log2f(st.su), l2v = log2f(st.sv);
-    const float dlse = ((st.mcv - st.mcu) + (l2v - l2u)) * kLn2;
+    const float dlse = (gap + (l2v - l2u)) * kLn2;
     args.kl[row] = st.C / st.sv - dlse;
     if (args.targets) {
       const int64_t y = args.targets[row];
       float lpu = __builtin_nanf(""), lpv = __builtin_nanf("");
       if (y >= 0 && y < V) {
-        lpu = (fmaf(Tr::load1(up, y), c, -st.mcu) - l2u) * kLn2;
-        lpv = (fmaf(Tr::load1(vp, y), c, -st.mcv) - l2v) * kLn2;
+        const float u = Tr::load1(up, y), v = Tr::load1(vp, y);
+        // a row without any weight has none to compare with
+        if (st.su != 0.f) lpu = ((far ? far_exponent(u, wide.mu, c) : fmaf(u, c, -st.mcu)) - l2u) * kLn2;
+        if (st.sv != 0.f) lpv = ((far ? far_exponent(v, wide.mv, c) : fmaf(v, c, -st.mcv)) - l2v) * kLn2;
       }
       if (args.lp_student) args.lp_student[row] = lpu;
       if (args.lp_teacher) args.lp_teacher[row] = lpv;

@@ -37,6 +37,11 @@
  *   (no device-to-host check is made); its entropy is still computed.
  * Special values: -inf logits are zero-probability entries and add nothing to
  *   the entropy; a row containing NaN or +inf, or only -inf, gives NaN.
+ *   Logits that a caller gives may be finite values of any size (masks of -1e10,
+ *   -1e30 and the like): what counts is how far each lies below the row's
+ *   largest.  Those below -2.35e38 temperature weigh nothing, as -inf does
+ *   (z log2(e) / temperature leaves fp32).  Logits that a fused head computes
+ *   must stay within 1e7 temperature.
  */
 #ifndef LP_H_
 #define LP_H_
@@ -216,7 +221,8 @@ lp_status lp_lm_head_logprobs_entropy_backward(const void* hidden, int64_t ld_h,
  *                   "逐Token级别的probs_diff监控", §3.2.  diff_mask NULL = all rows.
  *                   With targets NULL those three outputs must be NULL.
  * Accumulation is fp32 throughout, so fp16 rows whose plain sums overflow
- * stay finite.  Needs no workspace.
+ * stay finite.  The KL is a difference of numbers as large as the models' largest
+ * logits lie apart, and as exact.  Needs no workspace.
  */
 lp_status lp_kl_full_vocab(const void* student, const void* teacher, lp_dtype dtype, int64_t T, int64_t V,
                            int64_t ld_s, int64_t ld_t, float* kl, const int64_t* targets,
