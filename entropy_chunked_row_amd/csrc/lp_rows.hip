@@ -99,10 +99,11 @@ __global__ void __launch_bounds__(NT) k_logprobs_entropy(RowArgs args) {
   if (__builtin_isnan(st.a) && !__builtin_isnan(st.s))
     st = stat_block_allreduce<NT>(scan_row<Tr, NT, U, true>(rowp, sp, c), sm);
   // Finite masks (-1e10, -1e30, the type's lowest) in all columns of a lane, or
-  // of the row, make the sums 0, infinite or NaN: redo it once more.
+  // of the row, make the sums 0, infinite or NaN: redo it once more.  All lanes
+  // or none, though sums next to overflow may differ between lanes by a rounding.
   bool near = true;  // else relative to the value m (far_exponent)
   float m = 0.f;
-  if (!(st.s > 0.f && st.s <= kLargest) || __builtin_isnan(st.a) || !is_near(st.mc)) {
+  if (__any(!(st.s > 0.f && st.s <= kLargest) || __builtin_isnan(st.a) || !is_near(st.mc))) {
     const RowStat far = scan_row_far<Tr, NT>(rowp, sp, c, sm_far);
     m = far.m;
     st = Stat{0.f, far.s, far.a};
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(NT) k_kl_full_vocab(KLArgs args) {
   bool far = false;
   KLFar wide{};
   auto counts = [](float s) { return s > 0.f && s <= kLargest; };
-  if (!counts(st.su) || !counts(st.sv) || __builtin_isnan(st.C) || !is_near(st.mcu) || !is_near(st.mcv)) {
+  if (__any(!counts(st.su) || !counts(st.sv) || __builtin_isnan(st.C) || !is_near(st.mcu) || !is_near(st.mcv))) {
     far = true;
     wide = scan_kl_far<Tr, NT>(up, vp, V, c, sm_far);
     st.su = wide.su;
