@@ -81,13 +81,23 @@ def _strip_comments(text):
     return " ".join("".join(out).split())
 
 
-def _csrc_sha256():
-    """Hash of the kernel sources (comments and layout ignored) that the PMC
-    summary in profiles/ must match."""
+# Sources of operators that no path of this benchmark launches.
+UNCOUNTED_SOURCES = ("lp_embed.hip", "lp_rules.hip", "lp_w4.hip")
+
+
+def _counted_sources():
+    """Sources of the kernels that the PMC summary in profiles/ counts, of their launches, and all headers."""
     import glob
+    files = sorted(glob.glob(os.path.join(ROOT, "entropy_chunked_row_amd", "csrc", "*")))
+    return [f for f in files if os.path.basename(f) not in UNCOUNTED_SOURCES]
+
+
+def _csrc_sha256():
+    """Hash of the counted sources (comments and layout ignored) that the PMC
+    summary in profiles/ must match."""
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "entropy_chunked_row_amd", "csrc", "*"))):
+    for f in _counted_sources():
         h.update(os.path.basename(f).encode())
         with open(f, encoding="utf-8") as fh:
             h.update(_strip_comments(fh.read()).encode())
@@ -103,6 +113,7 @@ def _pmc_doc():
     except (OSError, IndexError, ValueError):
         return None
     if doc.get("source_sha256") != _csrc_sha256():
+        log("profiles/hbm_traffic.md is of other kernel sources: roofline.traffic is left out until it is retaken")
         return None
     return doc
 
