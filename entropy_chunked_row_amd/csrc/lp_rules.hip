@@ -27,8 +27,8 @@
 //      behind the stream cost 100 of 600 us at 4096 x 151936: each is a
 //      partial write of memory that the stream's store has left the cache for).
 // Bound: HBM and, when scoring, the vector unit.  Measured: scoring 8192 x 151936
-// bf16 0.51 ms (5.2 TB/s of what it must read, vector unit 85 % busy; without any
-// rule 0.38 ms), gradient of 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing
+// bf16 0.51 ms (5.2 TB/s of what it must read, 6.6 TB/s with the lines fetched again
+// for touched columns; vector unit 85 % busy; without any rule 0.38 ms), gradient of 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing
 // 256 x 129280 fp16 with histories of up to 4096 tokens 32 us (of which 9 us are
 // the histories' latency: every workgroup of so short a call starts with its
 // history), one row of 151936 7 us.  An LDS word per column in place of bitmap and ranks took 2.5 ms
@@ -271,7 +271,7 @@ __device__ __forceinline__ void stream_vectors(const RowRules& r, LaneStat& st, 
   // Scored rows pass by once: non-temporal loads (8192 x 151936 without rules
   // 0.42 -> 0.38 ms, gradient of 4096 rows 0.52 -> 0.50-0.515).  The logits of a
   // decode step were written just before, and what is left of them in the
-  // caches counts (256 x 129280: 43 us non-temporal, 39 plain).
+  // caches counts (256 x 129280: non-temporal loads take 1.1 times as long).
   auto load = [&](uint32_t i) {
     if (OP == kProcess) return load_vec(xv + i * 16u);
     return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xv + i * 16u)));
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(NT) k_rules(RulesArgs a) {
   // on the grid of what is stored; loads go off it where the input's rows do.
   const RowSplit<Tr> sp(OP == kScore ? xp : op, n);
   // All workgroups of a decode step read their histories at once: the first
-  // logits come in meanwhile (256 x 129280 fp16: 36.3 -> 34.9 us; four vectors a
-  // lane instead of two take registers that cost a workgroup a CU, 39).
+  // logits come in meanwhile (4 % of 256 x 129280 fp16; four vectors a lane
+  // instead of two take registers that cost a workgroup a CU, and 12 %).
   u32x4 ahead[U];
   if (OP == kProcess && sp.nvec >= U * NT) {
 #pragma unroll
@@ -613,8 +613,8 @@ __global__ void __launch_bounds__(256) k_rules_join(RulesArgs a) {
 
 // Slices per row: one where there are rows enough for three workgroups a CU,
 // which is what their registers let be resident, else as many as that takes, of
-// at least kMinSlice columns.  (256 x 129280 fp16: 768 workgroups 36 us, 1024 40,
-// 2048 46, 8192 73; 4096 rows of 151936: one slice 0.61 ms, two 0.59, but scoring
+// at least kMinSlice columns.  (256 x 129280 fp16: 1024 workgroups take 1.1
+// times as long as 768, 2048 1.3, 8192 2 times; 4096 rows of 151936: one slice 0.61 ms, two 0.59, but scoring
 // 0.52 ms with one, 0.525 with two.)
 void set_slices(RulesArgs& a) {
   const int64_t most = (int64_t(a.V) + kMinSlice - 1) / kMinSlice, least = (int64_t(a.V) + kMaxSlice - 1) / kMaxSlice;

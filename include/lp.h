@@ -350,7 +350,8 @@ lp_status lp_prob_diff_stats(const float* lp_a, const float* lp_b, const uint8_t
  *      last entry counts).
  *   3. grammar: bit j % 32 of allowed[t][j / 32] = 0 makes z = -inf, whatever
  *      it was (NaN and +inf too).
- * The temperature, where a call takes one, applies after the rules.
+ * The temperature, where a call takes one, applies after the rules.  (A sampler that
+ * adds biases before the repetition penalty draws from another distribution.)
  *
  * The struct is read on the host during the call; its arrays are device
  * pointers.  A rule is off where its array is NULL; a NULL struct turns every
