@@ -28,10 +28,11 @@
 //      partial write of memory that the stream's store has left the cache for).
 // Bound: HBM and, when scoring, the vector unit.  Measured: scoring 8192 x 151936
 // bf16 0.51 ms (5.2 TB/s of what it must read, 6.6 TB/s with the lines fetched again
-// for touched columns; vector unit 85 % busy; without any rule 0.38 ms), gradient of 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing
-// 256 x 129280 fp16 with histories of up to 4096 tokens 32 us (of which 9 us are
-// the histories' latency: every workgroup of so short a call starts with its
-// history), one row of 151936 7 us.  An LDS word per column in place of bitmap and ranks took 2.5 ms
+// for touched columns; vector unit 85 % busy; without any rule 0.38 ms), gradient
+// of 4096 x 151936 bf16 0.52 ms (5.0 TB/s), processing 256 x 129280 fp16 with
+// histories of up to 4096 tokens 32 us (of which 9 us are the histories' latency:
+// every workgroup of so short a call starts with its history), one row of
+// 151936 7 us.  An LDS word per column in place of bitmap and ranks took 2.5 ms
 // on the first (slices of 4096 columns, each with its own history pass).
 // Counts are integers and the bias entry is a maximum, so the order of the
 // LDS atomics does not change any result.  Nothing of size V is kept between
