@@ -40,3 +40,37 @@ def test_tensors_as_they_are_at_the_call():
     kept["bias_values"].zero_()
     kept["allowed"].fill_(-1)
     assert torch.equal(lp.lp_process_logits(x, rules), x) and np.isfinite(float(x.sum()))
+
+
+def test_one_set_of_rules_in_two_threads():
+    """Calls made at once from two threads, each on a stream of its own, share the rules and nothing else."""
+    import threading
+
+    import torch
+
+    import entropy_chunked_row_amd as lp
+    c = Rules(40, 5003, "bf16", seed=9, L=200, empty_row=False)
+    x, rules = c.device()
+    xs = [x, x.flip(1).contiguous()]
+    y = to_dev(c.targets)
+    want = [lp.lp_process_logits(t, rules) for t in xs], [lp.lp_processed_logprobs_entropy(t, rules, y) for t in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        for _ in range(30):
+            z = lp.lp_process_logits(xs[k], rules, stream=stream)
+            s = lp.lp_processed_logprobs_entropy(xs[k], rules, y, stream=stream)
+            stream.synchronize()
+            if not torch.equal(z, want[0][k]) or not all(torch.equal(a, b) for a, b in zip(s, want[1][k])):
+                wrong.append(k)
+                return
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
