@@ -82,7 +82,7 @@ def _strip_comments(text):
 
 
 # Sources of operators that no path of this benchmark launches.
-UNCOUNTED_SOURCES = ("lp_embed.hip", "lp_rules.hip", "lp_w4.hip")
+UNCOUNTED_SOURCES = ("lp_distill.hip", "lp_embed.hip", "lp_fp8.hip", "lp_rules.hip", "lp_sums.hpp", "lp_top.hip", "lp_w4.hip")
 
 
 def _counted_sources():

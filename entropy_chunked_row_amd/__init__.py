@@ -24,7 +24,10 @@ __all__ = [
     "lp_lm_head_logprobs_entropy_backward_k", "lp_prob_diff_stats", "lp_lm_head_kl_workspace_bytes",
     "lp_lm_head_kl", "lp_lm_head_kl_backward", "LogitRules", "lp_process_logits", "lp_processed_logprobs_entropy",
     "lp_processed_logprobs_entropy_backward", "lp_processed_workspace_bytes", "lp_embedding", "lp_embedding_backward",
-    "lp_embedding_workspace_bytes", "lp_lm_head_w4_quantize", "lp_lm_head_w4_logits", "LPError", "load",
+    "lp_embedding_workspace_bytes", "lp_lm_head_w4_quantize", "lp_lm_head_w4_logits", "lp_top_logits",
+    "lp_top_workspace_bytes", "lp_distill_top", "lp_distill_top_backward", "lp_distill_top_workspace_bytes",
+    "lp_beam_select", "lp_beam_workspace_bytes", "lp_beam_reorder", "lp_lm_head_fp8_quantize", "lp_lm_head_fp8_logits",
+    "lp_lm_head_fp8_workspace_bytes", "LPError", "load",
 ]
 
 
@@ -855,4 +858,281 @@ def lp_lm_head_w4_logits(hidden, packed, scales, group: int = 128, *, out_dtype=
         st = lib.lp_lm_head_w4_logits(_ptr(hidden), dtype, T, h, ld_h, _ptr(packed), ld_p, _ptr(scales), ld_s, V, group,
                                       _ptr(out), _dtype_code(out), _rows(out, "out"), _raw_stream(dev, stream))
     check("lp_lm_head_w4_logits", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the largest logits, distillation from them, beams
+# ---------------------------------------------------------------------------
+
+def lp_top_workspace_bytes(dtype: int, T: int, V: int, K: int) -> int:
+    return int(load().lp_top_workspace_bytes(dtype, T, V, K))
+
+
+def lp_top_logits(logits, K: int, mask=None, temperature: float = 1.0, *, want_rest: bool = True, want_lse: bool = True,
+                  workspace=None, stream=None) -> Tuple:
+    """(ids int64 [T, K], logprob fp32 [T, K], rest [T], lse [T]) of the K largest entries of each row of logits [T, V],
+    K <= min(V, 256): columns from the largest down (equal ones from the lowest column up), their log-probs under softmax(logits /
+    temperature), the log of the mass of all others, and the log-sum-exp.  Unscored rows: ids -1, else 0."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    ld = _rows(logits, "logits")
+    T, V = logits.shape
+    mask = _vec(mask, "mask", torch.uint8, T)
+    dev = logits.device
+    _same_device(dev, (("logits", logits), ("mask", mask)))
+    K = int(K)
+    with _scope(dev, stream):
+        ids = torch.empty((T, max(K, 0)), dtype=torch.int64, device=dev)
+        logprob = torch.empty((T, max(K, 0)), dtype=torch.float32, device=dev)
+        rest = torch.empty(T, dtype=torch.float32, device=dev) if want_rest else None
+        lse = torch.empty(T, dtype=torch.float32, device=dev) if want_lse else None
+        ws, ws_bytes = _workspace(lp_top_workspace_bytes(dtype, T, V, K), dev, workspace)
+        st = lib.lp_top_logits(_ptr(logits), dtype, T, V, ld, K, _ptr(mask), float(temperature), _ptr(ids), _ptr(logprob),
+                               _ptr(rest), _ptr(lse), _ptr(ws), ws_bytes, _raw_stream(dev, stream))
+    check("lp_top_logits", st)
+    return ids, logprob, rest, lse
+
+
+def lp_distill_top_workspace_bytes(dtype: int, T: int, V: int) -> int:
+    return int(load().lp_distill_top_workspace_bytes(dtype, T, V))
+
+
+def _teacher_lists(logits, teacher_ids, teacher_logprob, teacher_rest, mask):
+    """(T, V, ld, K, lists and mask after checks) of logits [T, V] and a teacher's lists [T, K]."""
+    torch = _torch()
+    ld = _rows(logits, "logits")
+    T, V = logits.shape
+    if teacher_ids.dim() != 2 or teacher_ids.size(0) != T:
+        raise ValueError(f"teacher_ids must be [{T}, K], got {list(teacher_ids.shape)}")
+    K = teacher_ids.size(1)
+    teacher_ids = _vec(teacher_ids, "teacher_ids", torch.int64)
+    teacher_logprob = _vec(teacher_logprob, "teacher_logprob", torch.float32, T * K)
+    if teacher_logprob.shape != (T, K):
+        raise ValueError(f"teacher_logprob must be [{T}, {K}], got {list(teacher_logprob.shape)}")
+    teacher_rest = _vec(teacher_rest, "teacher_rest", torch.float32, T)
+    return T, V, ld, K, teacher_ids, teacher_logprob, teacher_rest, _vec(mask, "mask", torch.uint8, T)
+
+
+def lp_distill_top(logits, teacher_ids, teacher_logprob, teacher_rest=None, mask=None, temperature: float = 1.0, *,
+                   want_lse: bool = True, workspace=None, stream=None) -> Tuple:
+    """(loss, lse, lse_rest), fp32 [T]: KL from a teacher's lists (ids int64 [T, K], log-probs fp32 [T, K], and the log of the
+    mass outside them, fp32 [T] or None), as lp_top_logits gives them, to softmax(logits / temperature) of the
+    student's logits [T, V].  Ids outside [0, V) are padding.  lse and lse_rest (the log-sum-exp over columns that no entry names)
+    are for the backward."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    T, V, ld, K, ids, logprob, rest, mask = _teacher_lists(logits, teacher_ids, teacher_logprob, teacher_rest, mask)
+    dev = logits.device
+    _same_device(dev, (("logits", logits), ("teacher_ids", ids), ("teacher_logprob", logprob), ("teacher_rest", rest),
+                       ("mask", mask)))
+    f32 = dict(dtype=torch.float32, device=dev)
+    with _scope(dev, stream):
+        loss = torch.empty(T, **f32)
+        lse = torch.empty(T, **f32) if want_lse else None
+        lse_rest = torch.empty(T, **f32) if want_lse else None
+        ws, ws_bytes = _workspace(lp_distill_top_workspace_bytes(dtype, T, V), dev, workspace)
+        st = lib.lp_distill_top(_ptr(logits), dtype, T, V, ld, K, _ptr(ids), _ptr(logprob), _ptr(rest), _ptr(mask),
+                                float(temperature), _ptr(loss), _ptr(lse), _ptr(lse_rest), _ptr(ws), ws_bytes,
+                                _raw_stream(dev, stream))
+    check("lp_distill_top", st)
+    return loss, lse, lse_rest
+
+
+def lp_distill_top_backward(logits, teacher_ids, teacher_logprob, teacher_rest, mask, temperature: float, lse, lse_rest,
+                            grad_loss, *, grad_logits=None, stream=None):
+    """Gradient [T, V] of sum grad_loss * loss (lp_distill_top) with respect to the student's raw logits, in their dtype."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    T, V, ld, K, ids, logprob, rest, mask = _teacher_lists(logits, teacher_ids, teacher_logprob, teacher_rest, mask)
+    lse = _vec(lse, "lse", torch.float32, T)
+    lse_rest = _vec(lse_rest, "lse_rest", torch.float32, T)
+    grad_loss = _vec(grad_loss, "grad_loss", torch.float32, T)
+    if grad_logits is not None and (grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype):
+        raise ValueError("grad_logits must have the logits' shape and dtype")
+    ld_grad = V if grad_logits is None else _rows(grad_logits, "grad_logits")
+    dev = logits.device
+    _same_device(dev, (("logits", logits), ("teacher_ids", ids), ("teacher_logprob", logprob), ("teacher_rest", rest),
+                       ("mask", mask), ("lse", lse), ("lse_rest", lse_rest), ("grad_loss", grad_loss),
+                       ("grad_logits", grad_logits)))
+    with _scope(dev, stream):
+        if grad_logits is None:
+            grad_logits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+        st = lib.lp_distill_top_backward(_ptr(logits), dtype, T, V, ld, K, _ptr(ids), _ptr(logprob), _ptr(rest), _ptr(mask),
+                                         float(temperature), _ptr(lse), _ptr(lse_rest), _ptr(grad_loss),
+                                         _ptr(grad_logits), ld_grad, _raw_stream(dev, stream))
+    check("lp_distill_top_backward", st)
+    return grad_logits
+
+
+def lp_beam_workspace_bytes(dtype: int, B: int, W: int, V: int, N: int) -> int:
+    return int(load().lp_beam_workspace_bytes(dtype, B, W, V, N))
+
+
+def lp_beam_select(logits, beam_scores, N: Optional[int] = None, finished=None, end_token: int = 0, temperature: float = 1.0,
+                   *, workspace=None, stream=None) -> Tuple:
+    """(scores fp32 [B, N], parents int32 [B, N], tokens int64 [B, N]): the N (default W) best continuations of each
+    request over its W beams, by beam_scores [B, W] + log softmax(logits / temperature), logits [B * W, V].  A beam that
+    is finished (uint8 or bool [B, W]) is one candidate, its score and end_token; one whose score is not finite is none.
+    Places that nothing fills: -inf, -1, -1."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(logits)
+    ld = _rows(logits, "logits")
+    rows, V = logits.shape
+    if beam_scores.dim() != 2 or beam_scores.numel() != rows:
+        raise ValueError(f"beam_scores must be [B, W] for the {rows} rows of logits, got {list(beam_scores.shape)}")
+    B, W = beam_scores.shape
+    N = W if N is None else int(N)
+    beam_scores = _vec(beam_scores, "beam_scores", torch.float32)
+    finished = _vec(finished, "finished", torch.uint8, rows)
+    dev = logits.device
+    _same_device(dev, (("logits", logits), ("beam_scores", beam_scores), ("finished", finished)))
+    with _scope(dev, stream):
+        scores = torch.empty((B, max(N, 0)), dtype=torch.float32, device=dev)
+        parents = torch.empty((B, max(N, 0)), dtype=torch.int32, device=dev)
+        tokens = torch.empty((B, max(N, 0)), dtype=torch.int64, device=dev)
+        ws, ws_bytes = _workspace(lp_beam_workspace_bytes(dtype, B, W, V, N), dev, workspace)
+        st = lib.lp_beam_select(_ptr(logits), dtype, B, W, V, ld, _ptr(beam_scores), _ptr(finished), N, int(end_token),
+                                float(temperature), _ptr(scores), _ptr(parents), _ptr(tokens), _ptr(ws), ws_bytes,
+                                _raw_stream(dev, stream))
+    check("lp_beam_select", st)
+    return scores, parents, tokens
+
+
+def _levels(sizes, strides, name):
+    """(size, stride) of dimensions that one step leads through, sizes of 1 left out."""
+    size, stride = 1, 0
+    for n, st in zip(reversed(sizes), reversed(strides)):
+        if n == 1:
+            continue
+        if size == 1:
+            size, stride = n, st
+        elif st == stride * size:
+            size *= n
+        else:
+            raise ValueError(f"{name}: the dimensions before and behind the beams must each be walked in one step")
+    return size, stride
+
+
+def _state_layout(t, dim, name):
+    """(outer size, its stride, row stride, mid size, its stride, width), strides and width in bytes, of a state whose
+    dimension `dim` is the beams."""
+    e, shape, strides = t.element_size(), list(t.shape), list(t.stride())
+    width, k = 1, len(shape)
+    while k > dim + 1 and (shape[k - 1] == 1 or strides[k - 1] == width):
+        width *= shape[k - 1]
+        k -= 1
+    mid, mid_stride = _levels(shape[dim + 1:k], strides[dim + 1:k], name)
+    outer, outer_stride = _levels(shape[:dim], strides[:dim], name)
+    return outer, outer_stride * e, strides[dim] * e, mid, mid_stride * e, width * e
+
+
+def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
+    """States follow their beams: along dimension `dim`, row b * N + n of the result is row b * W + parents[b, n] of
+    state (W = its size / B), zeros where that parent lies outside [0, W).  state of any dtype, the dimensions before
+    `dim` walked in one step, those behind it in at most two (a prefix of each row of a cache); parents int32 [B, N],
+    as lp_beam_select gives them."""
+    torch = _torch()
+    lib = load()
+    if parents.dim() != 2:
+        raise ValueError(f"parents must be [B, N], got {list(parents.shape)}")
+    parents = _vec(parents, "parents", torch.int32)
+    B, N = parents.shape
+    if not -state.dim() <= dim < state.dim():
+        raise ValueError(f"dim {dim} is outside a state of {state.dim()} dimensions")
+    dim %= state.dim()
+    rows = state.size(dim)
+    if B == 0 or N == 0 or rows == 0 or rows % B:
+        raise ValueError(f"{rows} rows are no beams of {B} requests that {N} slots go on from")
+    shape = list(state.shape)
+    shape[dim] = B * N
+    if out is not None and (list(out.shape) != shape or out.dtype != state.dtype):
+        raise ValueError(f"out must be {shape} of the state's dtype")
+    outer, s_outer, s_row, mid, s_mid, width = _state_layout(state, dim, "state")
+    dev = state.device
+    _same_device(dev, (("state", state), ("parents", parents), ("out", out)))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=state.dtype, device=dev)
+        d_outer, do, dr, d_mid, dm, d_width = _state_layout(out, dim, "out")
+        if d_outer != outer or d_mid * d_width != mid * width:
+            raise ValueError("out cannot be walked as the state is")
+        if d_width != width:
+            if d_mid != 1:
+                raise ValueError("out cannot be walked as the state is")
+            dm = width  # the state's parts lie behind each other in out
+        st = lib.lp_beam_reorder(_ptr(state), s_outer, s_row, s_mid, outer, mid, width, _ptr(parents), B, rows // B, N,
+                                 _ptr(out), do, dr, dm, _raw_stream(dev, stream))
+    check("lp_beam_reorder", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit head
+# ---------------------------------------------------------------------------
+
+def lp_lm_head_fp8_quantize(weight, *, q=None, scales=None, stream=None) -> Tuple:
+    """(q float8_e4m3fn [V, h], scales fp32 [ceil(V / 128), ceil(h / 128)]) of a dense head weight [V, h]
+    (bf16/fp16/fp32)."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(weight)
+    ld_w = _rows(weight, "weight")
+    V, h = weight.shape
+    blocks = ((V + 127) // 128, (h + 127) // 128)
+    for name, t, dt, shape in (("q", q, torch.float8_e4m3fn, (V, h)), ("scales", scales, torch.float32, blocks)):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be {list(shape)} {dt}")
+    dev = weight.device
+    _same_device(dev, (("weight", weight), ("q", q), ("scales", scales)))
+    with _scope(dev, stream):
+        if q is None:
+            q = torch.empty((V, h), dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty(blocks, dtype=torch.float32, device=dev)
+        st = lib.lp_lm_head_fp8_quantize(_ptr(weight), dtype, V, h, ld_w, _ptr(q), _rows(q, "q"), _ptr(scales),
+                                         _rows(scales, "scales"), _raw_stream(dev, stream))
+    check("lp_lm_head_fp8_quantize", st)
+    return q, scales
+
+
+def lp_lm_head_fp8_workspace_bytes(T: int, h: int, V: int) -> int:
+    return int(load().lp_lm_head_fp8_workspace_bytes(T, h, V))
+
+
+def lp_lm_head_fp8_logits(hidden, q, scales, *, out_dtype=None, out=None, workspace=None, stream=None):
+    """Logits [T, V] of hidden [T, h] (bf16/fp16, brought to e4m3 with a scale for each 128 columns of a row) through a head of
+    lp_lm_head_fp8_quantize; out_dtype defaults to hidden's."""
+    torch = _torch()
+    lib = load()
+    dtype = _dtype_code(hidden)
+    ld_h = _rows(hidden, "hidden")
+    T, h = hidden.shape
+    if q.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"q must be float8_e4m3fn, got {q.dtype}")
+    if scales.dtype != torch.float32:
+        raise TypeError(f"scales must be float32, got {scales.dtype}")
+    ld_q, ld_s = _rows(q, "q"), _rows(scales, "scales")
+    V = q.size(0)
+    if q.size(1) != h or scales.shape != ((V + 127) // 128, (h + 127) // 128):
+        raise ValueError(f"hidden [{T}, {h}], q {list(q.shape)} and scales {list(scales.shape)} disagree")
+    if out is not None:
+        if out.dim() != 2 or out.shape != (T, V) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be [{T}, {V}] of out_dtype")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = hidden.dtype
+    dev = hidden.device
+    _same_device(dev, (("hidden", hidden), ("q", q), ("scales", scales), ("out", out)))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((T, V), dtype=out_dtype, device=dev)
+        ws, ws_bytes = _workspace(lp_lm_head_fp8_workspace_bytes(T, h, V), dev, workspace)
+        st = lib.lp_lm_head_fp8_logits(_ptr(hidden), dtype, T, h, ld_h, _ptr(q), ld_q, _ptr(scales), ld_s, V, _ptr(out),
+                                       _dtype_code(out), _rows(out, "out"), _ptr(ws), ws_bytes, _raw_stream(dev, stream))
+    check("lp_lm_head_fp8_logits", st)
     return out

@@ -75,6 +75,23 @@ SIGNATURES = {
     "lp_lm_head_w4_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "lp_lm_head_w4_logits": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp,
                                      c_int, c_i64, c_vp]),
+    "lp_top_workspace_bytes": (ctypes.c_size_t, [c_int, c_i64, c_i64, c_i64]),
+    "lp_top_logits": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_vp, c_f, c_vp, c_vp, c_vp, c_vp, c_vp,
+                              ctypes.c_size_t, c_vp]),
+    "lp_distill_top_workspace_bytes": (ctypes.c_size_t, [c_int, c_i64, c_i64]),
+    "lp_distill_top": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f, c_vp, c_vp, c_vp,
+                               c_vp, ctypes.c_size_t, c_vp]),
+    "lp_distill_top_backward": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f, c_vp, c_vp,
+                                        c_vp, c_vp, c_i64, c_vp]),
+    "lp_beam_workspace_bytes": (ctypes.c_size_t, [c_int, c_i64, c_i64, c_i64, c_i64]),
+    "lp_beam_select": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_i64, c_f, c_vp, c_vp, c_vp,
+                               c_vp, ctypes.c_size_t, c_vp]),
+    "lp_beam_reorder": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_i64,
+                                c_i64, c_i64, c_vp]),
+    "lp_lm_head_fp8_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "lp_lm_head_fp8_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64]),
+    "lp_lm_head_fp8_logits": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp, c_int,
+                                      c_i64, c_vp, ctypes.c_size_t, c_vp]),
     "lp_timing_enable": (None, [c_int]),
     "lp_timing_read": (c_int, [ctypes.c_char_p, ctypes.POINTER(c_i64), ctypes.POINTER(ctypes.c_double)]),
     "lp_timing_clock": (c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i64)]),

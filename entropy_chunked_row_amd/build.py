@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "liblp.so")
 SOURCES = ["lp_api.hip", "lp_rows.hip", "lp_lmhead.hip", "lp_rules.hip", "lp_embed.hip",
-           "lp_w4.hip", "lp_timing.hip"]
+           "lp_w4.hip", "lp_top.hip", "lp_distill.hip", "lp_fp8.hip", "lp_timing.hip"]
 # measurement helper for bench.py (HBM read probe), a library of its own
 PROBE_SRC = os.path.join(PKG, "probe", "lp_probe.hip")
 PROBE_OUT = os.path.join(PKG, "liblp_probe.so")

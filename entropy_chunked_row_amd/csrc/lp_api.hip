@@ -943,4 +943,401 @@ lp_status lp_lm_head_w4_logits(const void* hidden, lp_dtype dtype, int64_t T, in
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// the largest logits, distillation from them, beams
+// ---------------------------------------------------------------------------
+
+// Checks of T rows of V logits and a temperature that the calls below share.
+static lp_status check_rows(const char* fn, const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                            float temperature) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", fn, static_cast<int>(dtype));
+  if (T < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: T < 0", fn);
+  if (V <= 0 || V > kMaxV) return fail(LP_ERR_INVALID_ARGUMENT, "%s: V out of range (1..2^30)", fn);
+  if (ld < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld < V", fn);
+  if (T > (int64_t(1) << 40) || ld > (int64_t(1) << 40) / (T > 0 ? T : 1))
+    return fail(LP_ERR_UNSUPPORTED, "%s: T x ld past 2^40 elements", fn);
+  if (!isfinite(temperature)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: temperature not finite", fn);
+  if (T == 0) return LP_OK;
+  if (!logits || !aligned(logits, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: logits are required and must be aligned", fn);
+  return LP_OK;
+}
+
+static double inverse(float temperature) {
+  return temperature_applies(temperature) ? 1.0 / static_cast<double>(temperature) : 1.0;
+}
+
+static lp_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need)
+    return fail(LP_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %zu bytes, got %zu", fn, need,
+                workspace ? bytes : size_t(0));
+  if (!aligned(workspace, 256)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
+  return LP_OK;
+}
+
+// True if nothing written shares bytes with anything read or written besides
+// (NULL blocks aside).
+static bool apart(std::initializer_list<Block> written, std::initializer_list<Block> read) {
+  for (const Block* w = written.begin(); w != written.end(); ++w) {
+    if (!w->at) continue;
+    for (const Block* o = w + 1; o != written.end(); ++o)
+      if (o->at && share_bytes(*w, *o)) return false;
+    for (const Block& o : read)
+      if (o.at && share_bytes(*w, o)) return false;
+  }
+  return true;
+}
+
+static int64_t bytes_of(size_t n) { return static_cast<int64_t>(n); }
+
+size_t lp_top_workspace_bytes(lp_dtype dtype, int64_t T, int64_t V, int64_t K) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32) return 0;
+  if (T < 0 || T > (int64_t(1) << 40) || V <= 0 || V > kMaxV || K < 1 || K > lp::kMaxTop || K > V) return 0;
+  const size_t n = lp::top_workspace_bytes(static_cast<int>(dtype), T, V, K);
+  return n > 256 ? n : 256;
+}
+
+lp_status lp_top_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                        const uint8_t* mask, float temperature, int64_t* ids, float* logprob, float* rest,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "lp_top_logits";
+  lp_status st = check_rows(fn, logits, dtype, T, V, ld, temperature);
+  if (st != LP_OK) return st;
+  if (K < 1 || K > lp::kMaxTop || K > V)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: K must be in 1..min(V, %d)", fn, lp::kMaxTop);
+  if (T == 0) return ok();
+  if (!ids || !logprob) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ids and logprob are required", fn);
+  if (!aligned(ids, 8) || !f32_aligned({logprob, rest, lse}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t need = lp_top_workspace_bytes(dtype, T, V, K);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != LP_OK) return st;
+  if (!apart({{ids, T * K, 8}, {logprob, T * K, 4}, {rest, T, 4}, {lse, T, 4}, {workspace, bytes_of(need), 1}},
+             {{logits, T, V, ld, dtype_bytes(dtype)}, {mask, T, 1}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps an operand", fn);
+  lp::TopArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = logits;
+  a.ld = ld;
+  a.V = static_cast<int>(V);
+  a.T = T;
+  a.K = static_cast<int>(K);
+  a.mask = mask;
+  a.c = exp2_scale(temperature);
+  a.inv_tau = inverse(temperature);
+  a.ids = ids;
+  a.logprob = logprob;
+  a.rest = rest;
+  a.lse = lse;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_top_logits(static_cast<int>(dtype), a, static_cast<char*>(workspace),
+                                       static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+static lp_status check_distill(const char* fn, const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                               int64_t K, const int64_t* teacher_ids, const float* teacher_logprob,
+                               const float* teacher_rest, const uint8_t* mask, float temperature,
+                               lp::DistillArgs* a) {
+  lp_status st = check_rows(fn, logits, dtype, T, V, ld, temperature);
+  if (st != LP_OK) return st;
+  if (K < 1 || K > lp::kMaxTop) return fail(LP_ERR_INVALID_ARGUMENT, "%s: K must be in 1..%d", fn, lp::kMaxTop);
+  memset(a, 0, sizeof(*a));
+  if (T == 0) return LP_OK;
+  if (!teacher_ids || !teacher_logprob)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: teacher_ids and teacher_logprob are required", fn);
+  if (!aligned(teacher_ids, 8) || !f32_aligned({teacher_logprob, teacher_rest}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  a->x = logits;
+  a->ld = ld;
+  a->V = static_cast<int>(V);
+  a->T = T;
+  a->K = static_cast<int>(K);
+  a->ids = teacher_ids;
+  a->logprob = teacher_logprob;
+  a->rest = teacher_rest;
+  a->mask = mask;
+  a->c = exp2_scale(temperature);
+  a->inv_tau = inverse(temperature);
+  return LP_OK;
+}
+
+size_t lp_distill_top_workspace_bytes(lp_dtype dtype, int64_t T, int64_t V) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32) return 0;
+  if (T < 0 || T > (int64_t(1) << 40) || V <= 0 || V > kMaxV) return 0;
+  const size_t n = lp::distill_workspace_bytes(static_cast<int>(dtype), T, V);
+  return n > 256 ? n : 256;
+}
+
+lp_status lp_distill_top(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                         const int64_t* teacher_ids, const float* teacher_logprob, const float* teacher_rest,
+                         const uint8_t* mask, float temperature, float* loss, float* lse, float* lse_rest,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "lp_distill_top";
+  lp::DistillArgs a;
+  lp_status st = check_distill(fn, logits, dtype, T, V, ld, K, teacher_ids, teacher_logprob, teacher_rest, mask,
+                               temperature, &a);
+  if (st != LP_OK) return st;
+  if (T == 0) return ok();
+  if (!loss) return fail(LP_ERR_INVALID_ARGUMENT, "%s: loss is required", fn);
+  if (!f32_aligned({loss, lse, lse_rest})) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t need = lp_distill_top_workspace_bytes(dtype, T, V);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != LP_OK) return st;
+  if (!apart({{loss, T, 4}, {lse, T, 4}, {lse_rest, T, 4}, {workspace, bytes_of(need), 1}},
+             {{logits, T, V, ld, dtype_bytes(dtype)}, {teacher_ids, T * K, 8}, {teacher_logprob, T * K, 4},
+              {teacher_rest, T, 4}, {mask, T, 1}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps an operand", fn);
+  a.loss = loss;
+  a.lse_out = lse;
+  a.lse_rest_out = lse_rest;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_distill(static_cast<int>(dtype), a, static_cast<char*>(workspace),
+                                    static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+lp_status lp_distill_top_backward(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                                  const int64_t* teacher_ids, const float* teacher_logprob,
+                                  const float* teacher_rest, const uint8_t* mask, float temperature,
+                                  const float* lse, const float* lse_rest, const float* grad_loss,
+                                  void* grad_logits, int64_t ld_grad, void* stream) {
+  const char* fn = "lp_distill_top_backward";
+  lp::DistillArgs a;
+  lp_status st = check_distill(fn, logits, dtype, T, V, ld, K, teacher_ids, teacher_logprob, teacher_rest, mask,
+                               temperature, &a);
+  if (st != LP_OK) return st;
+  if (ld_grad < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_grad < V", fn);
+  if (T == 0) return ok();
+  if (ld_grad > (int64_t(1) << 40) / T) return fail(LP_ERR_UNSUPPORTED, "%s: T x ld_grad past 2^40 elements", fn);
+  if (!lse || !lse_rest || !grad_loss || !grad_logits)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: lse, lse_rest, grad_loss and grad_logits are required", fn);
+  if (!f32_aligned({lse, lse_rest, grad_loss}) || !aligned(grad_logits, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t e_bytes = dtype_bytes(dtype);
+  if (!apart({{grad_logits, T, V, ld_grad, e_bytes}},
+             {{logits, T, V, ld, e_bytes}, {teacher_ids, T * K, 8}, {teacher_logprob, T * K, 4}, {teacher_rest, T, 4},
+              {mask, T, 1}, {lse, T, 4}, {lse_rest, T, 4}, {grad_loss, T, 4}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: grad_logits overlaps an operand", fn);
+  a.lse = lse;
+  a.lse_rest = lse_rest;
+  a.grad_loss = grad_loss;
+  a.out = grad_logits;
+  a.ld_out = ld_grad;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_distill_grad(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+static bool beam_sizes(int64_t B, int64_t W, int64_t N) {
+  return B >= 0 && B <= (int64_t(1) << 34) && W >= 1 && W <= lp::kMaxBeams && N >= 1 && N <= lp::kMaxTop &&
+         W * N <= lp::kMaxBeamLists;
+}
+
+size_t lp_beam_workspace_bytes(lp_dtype dtype, int64_t B, int64_t W, int64_t V, int64_t N) {
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32) return 0;
+  if (!beam_sizes(B, W, N) || V <= 0 || V > kMaxV) return 0;
+  const size_t n = lp::beam_workspace_bytes(static_cast<int>(dtype), B, W, V, N);
+  return n > 256 ? n : 256;
+}
+
+lp_status lp_beam_select(const void* logits, lp_dtype dtype, int64_t B, int64_t W, int64_t V, int64_t ld,
+                         const float* beam_scores, const uint8_t* finished, int64_t N, int64_t end_token,
+                         float temperature, float* scores, int32_t* parents, int64_t* tokens, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const char* fn = "lp_beam_select";
+  if (!beam_sizes(B, W, N))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: B in 0..2^34, W in 1..%d, N in 1..%d, W N up to %d", fn, lp::kMaxBeams,
+                lp::kMaxTop, lp::kMaxBeamLists);
+  lp_status st = check_rows(fn, logits, dtype, B * W, V, ld, temperature);
+  if (st != LP_OK) return st;
+  if (end_token < 0 || end_token >= V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: end_token must be in 0..V-1", fn);
+  if (B == 0) return ok();
+  if (!beam_scores || !scores || !parents || !tokens)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: beam_scores, scores, parents and tokens are required", fn);
+  if (!f32_aligned({beam_scores, scores}) || !aligned(parents, 4) || !aligned(tokens, 8))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned pointer", fn);
+  const size_t need = lp_beam_workspace_bytes(dtype, B, W, V, N);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != LP_OK) return st;
+  if (!apart({{scores, B * N, 4}, {parents, B * N, 4}, {tokens, B * N, 8}, {workspace, bytes_of(need), 1}},
+             {{logits, B * W, V, ld, dtype_bytes(dtype)}, {beam_scores, B * W, 4}, {finished, B * W, 1}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps an operand", fn);
+  lp::TopArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = logits;
+  a.ld = ld;
+  a.V = static_cast<int>(V);
+  a.T = B * W;
+  a.K = static_cast<int>(N);
+  a.W = static_cast<int>(W);
+  a.c = exp2_scale(temperature);
+  a.inv_tau = inverse(temperature);
+  a.beam_scores = beam_scores;
+  a.finished = finished;
+  a.end_token = end_token;
+  a.scores = scores;
+  a.parents = parents;
+  a.ids = tokens;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_beam_select(static_cast<int>(dtype), a, B, static_cast<char*>(workspace),
+                                        static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+lp_status lp_beam_reorder(const void* src, int64_t src_outer, int64_t src_row, int64_t src_mid, int64_t outer,
+                          int64_t mid, int64_t width, const int32_t* parents, int64_t B, int64_t W, int64_t N,
+                          void* dst, int64_t dst_outer, int64_t dst_row, int64_t dst_mid, void* stream) {
+  const char* fn = "lp_beam_reorder";
+  constexpr int64_t kMost = int64_t(1) << 40;  // bytes of a stride or a width; the products below stay in 64 bits
+  if (W < 1 || W > lp::kMaxTop || N < 1 || N > lp::kMaxTop)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: W and N must be in 1..%d", fn, lp::kMaxTop);
+  if (B < 0 || outer < 0 || mid < 0 || width < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: a negative size", fn);
+  for (int64_t x : {src_outer, src_row, src_mid, dst_outer, dst_row, dst_mid, width})
+    if (x < 0 || x > kMost) return fail(LP_ERR_INVALID_ARGUMENT, "%s: strides and width must be in 0..2^40 bytes", fn);
+  if (B == 0 || outer == 0 || mid == 0 || width == 0) return ok();
+  constexpr int64_t kSegs = 0x7fffffff;
+  if (B > kSegs || mid > kSegs || outer > kSegs || B > kSegs / mid || B * mid > kSegs / outer)
+    return fail(LP_ERR_UNSUPPORTED, "%s: more than 2^31-1 of B x mid x outer", fn);
+  if (!src || !dst || !parents) return fail(LP_ERR_INVALID_ARGUMENT, "%s: src, dst and parents are required", fn);
+  if (!aligned(parents, 4)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned parents", fn);
+  // sizes are below 2^40 and 2^31 each: whole extents as doubles, where a
+  // rounding does not matter, before they are formed
+  auto extent = [&](int64_t o, int64_t row, int64_t rows, int64_t m) {
+    return static_cast<double>(outer) * o + static_cast<double>(rows) * row + static_cast<double>(mid) * m + width;
+  };
+  if (extent(src_outer, src_row, B * W, src_mid) > 1e18 || extent(dst_outer, dst_row, B * N, dst_mid) > 1e18)
+    return fail(LP_ERR_UNSUPPORTED, "%s: states past 10^18 bytes", fn);
+  const int64_t part = (mid - 1) * dst_mid + width, rows = (B * N - 1) * dst_row + part;
+  if ((mid > 1 && dst_mid < width) || (B * N > 1 && dst_row < part) || (outer > 1 && dst_outer < rows))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: the strides of dst must be nested: width, mid, row, outer", fn);
+  const Block from(src, (outer - 1) * src_outer + (B * W - 1) * src_row + (mid - 1) * src_mid + width, 1);
+  if (!apart({{dst, (outer - 1) * dst_outer + rows, 1}}, {from, {parents, B * N, 4}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: dst overlaps src or parents", fn);
+  lp::ReorderArgs a;
+  memset(&a, 0, sizeof(a));
+  a.src = src;
+  a.dst = dst;
+  a.outer = outer;
+  a.mid = mid;
+  a.width = width;
+  a.src_outer = outer > 1 ? src_outer : 0;
+  a.src_row = B * W > 1 ? src_row : 0;
+  a.src_mid = mid > 1 ? src_mid : 0;
+  a.dst_outer = outer > 1 ? dst_outer : 0;
+  a.dst_row = B * N > 1 ? dst_row : 0;
+  a.dst_mid = mid > 1 ? dst_mid : 0;
+  a.B = B;
+  a.W = static_cast<int>(W);
+  a.N = static_cast<int>(N);
+  a.parents = parents;
+  if (!lp::beam_reorder_fits(a)) return fail(LP_ERR_UNSUPPORTED, "%s: rows too long for one launch", fn);
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_beam_reorder(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit head
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxFp8H = int64_t(1) << 20, kMaxFp8Pitch = int64_t(1) << 23;
+
+static lp_status check_fp8(const char* fn, int64_t V, int64_t h, const void* q, int64_t ld_q, const float* scales,
+                           int64_t ld_scales) {
+  if (V <= 0 || V > kMaxV || h <= 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: h >= 1 and V in 1..2^30", fn);
+  if (h % 16 || h > kMaxFp8H) return fail(LP_ERR_UNSUPPORTED, "%s: h must be a multiple of 16 up to 2^20", fn);
+  if (ld_q < h || ld_scales < (h + 127) / 128)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_q must be >= h and ld_scales >= ceil(h / 128)", fn);
+  if (ld_q % 16 || ld_q > kMaxFp8Pitch)
+    return fail(LP_ERR_UNSUPPORTED, "%s: ld_q must be a multiple of 16 up to 2^23", fn);
+  if (ld_scales > (int64_t(1) << 58) / V) return fail(LP_ERR_UNSUPPORTED, "%s: scales past 2^60 bytes", fn);
+  if (!q || !scales) return fail(LP_ERR_INVALID_ARGUMENT, "%s: q and scales are required", fn);
+  if (!aligned(q, 16)) return fail(LP_ERR_UNSUPPORTED, "%s: q must be 16-byte aligned", fn);
+  if (!aligned(scales, 4)) return fail(LP_ERR_INVALID_ARGUMENT, "%s: misaligned scales", fn);
+  return LP_OK;
+}
+
+lp_status lp_lm_head_fp8_quantize(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w, void* q,
+                                  int64_t ld_q, float* scales, int64_t ld_scales, void* stream) {
+  const char* fn = "lp_lm_head_fp8_quantize";
+  if (dtype != LP_BF16 && dtype != LP_FP16 && dtype != LP_FP32)
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", fn, static_cast<int>(dtype));
+  lp_status st = check_fp8(fn, V, h, q, ld_q, scales, ld_scales);
+  if (st != LP_OK) return st;
+  if (ld_w < h) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_w < h", fn);
+  if (ld_w > (int64_t(1) << 58) / V) return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
+  if (!weight || !aligned(weight, dtype_bytes(dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight is required and must be aligned", fn);
+  if (!apart({{q, V, h, ld_q, 1}, {scales, (V + 127) / 128, (h + 127) / 128, ld_scales, 4}},
+             {{weight, V, h, ld_w, dtype_bytes(dtype)}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: weight, q and scales overlap", fn);
+  lp::Fp8QuantArgs a;
+  a.weight = weight;
+  a.ld_w = ld_w;
+  a.V = static_cast<int>(V);
+  a.h = static_cast<int>(h);
+  a.q = static_cast<uint8_t*>(q);
+  a.ld_q = ld_q;
+  a.scales = scales;
+  a.ld_s = ld_scales;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_fp8_quantize(static_cast<int>(dtype), a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+size_t lp_lm_head_fp8_workspace_bytes(int64_t T, int64_t h, int64_t V) {
+  if (T < 0 || T > (int64_t(1) << 36) || V <= 0 || V > kMaxV || h <= 0 || h % 16 || h > kMaxFp8H) return 0;
+  const size_t n = lp::fp8_workspace_bytes(T, h, V);
+  return n > 256 ? n : 256;
+}
+
+lp_status lp_lm_head_fp8_logits(const void* hidden, lp_dtype dtype, int64_t T, int64_t h, int64_t ld_h, const void* q,
+                                int64_t ld_q, const float* scales, int64_t ld_scales, int64_t V, void* out,
+                                lp_dtype out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  const char* fn = "lp_lm_head_fp8_logits";
+  if (dtype == LP_FP32) return fail(LP_ERR_UNSUPPORTED, "%s: hidden must be bf16 or fp16", fn);
+  if ((dtype != LP_BF16 && dtype != LP_FP16) ||
+      (out_dtype != LP_BF16 && out_dtype != LP_FP16 && out_dtype != LP_FP32))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d or %d", fn, static_cast<int>(dtype),
+                static_cast<int>(out_dtype));
+  if (T < 0) return fail(LP_ERR_INVALID_ARGUMENT, "%s: T < 0", fn);
+  lp_status st = check_fp8(fn, V, h, q, ld_q, scales, ld_scales);
+  if (st != LP_OK) return st;
+  if (ld_h < h || ld_out < V) return fail(LP_ERR_INVALID_ARGUMENT, "%s: ld_h must be >= h and ld_out >= V", fn);
+  if (T == 0) return ok();
+  if (T > (int64_t(1) << 36) || ld_h > (int64_t(1) << 58) / T || ld_out > (int64_t(1) << 58) / T)
+    return fail(LP_ERR_UNSUPPORTED, "%s: operands past 2^60 bytes", fn);
+  if (!hidden || !out || !aligned(hidden, 2) || !aligned(out, dtype_bytes(out_dtype)))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: hidden and out are required and must be aligned", fn);
+  const size_t need = lp_lm_head_fp8_workspace_bytes(T, h, V);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != LP_OK) return st;
+  if (!apart({{out, T, V, ld_out, dtype_bytes(out_dtype)}, {workspace, bytes_of(need), 1}},
+             {{hidden, T, h, ld_h, 2}, {q, V, h, ld_q, 1}, {scales, (V + 127) / 128, (h + 127) / 128, ld_scales, 4}}))
+    return fail(LP_ERR_INVALID_ARGUMENT, "%s: out or the workspace overlaps an operand", fn);
+  lp::Fp8Args a;
+  a.hidden = static_cast<const uint16_t*>(hidden);
+  a.ld_h = ld_h;
+  a.T = T;
+  a.h = static_cast<int>(h);
+  a.V = static_cast<int>(V);
+  a.weight = static_cast<const uint8_t*>(q);
+  a.ld_w = ld_q;
+  a.scales = scales;
+  a.ld_s = ld_scales;
+  a.out = out;
+  a.out_dtype = static_cast<int>(out_dtype);
+  a.ld_out = ld_out;
+  clear_pending_hip_error();
+  hipError_t e = lp::launch_fp8_logits(static_cast<int>(dtype), a, static_cast<char*>(workspace),
+                                       static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
 }  // extern "C"

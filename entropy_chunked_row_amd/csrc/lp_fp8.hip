@@ -1,0 +1,539 @@
+// An output head in 8-bit floats (e4m3) with a scale for each block of 128 x 128:
+//   out[t][v] = sum over blocks b of 128 columns
+//               sx[t][b] sw[v / 128][b] sum_{k in b} qx[t][k] qw[v][k]
+// The hidden rows are brought to 8 bits first, with a scale for each 128 columns
+// of a row (k_fp8_rows), into the workspace.  Products run on the matrix cores at
+// the rate of 8-bit operands, one block of K at a time from zero; the block's
+// partial sums times the two scales are added to fp32 accumulators.
+#include "lp_gemm.hpp"
+#include "lp_internal.hpp"
+#include "lp_sums.hpp"
+
+namespace lp {
+
+namespace {
+
+constexpr int kBlock = 128;
+constexpr float kLargestE4m3 = 448.f, kPerLargest = 1.f / kLargestE4m3;
+constexpr float kLeastScale = 1.1754943508e-38f;  // 2^-126: a quotient by it is no larger than the value's own scale allows
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// Two e4m3 bytes, rounded to nearest even (NaN stays NaN).
+template <bool HIGH>
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi, uint32_t old) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, static_cast<int>(old), HIGH));
+#else
+  (void)lo, (void)hi;
+  return old;
+#endif
+}
+
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32x2_t quantize8(const float* x, float scale) {
+  uint32_t w0 = 0, w1 = 0;
+  w0 = to_e4m3x2<false>(x[0] / scale, x[1] / scale, w0);
+  w0 = to_e4m3x2<true>(x[2] / scale, x[3] / scale, w0);
+  w1 = to_e4m3x2<false>(x[4] / scale, x[5] / scale, w1);
+  w1 = to_e4m3x2<true>(x[6] / scale, x[7] / scale, w1);
+  return u32x2_t{w0, w1};
+}
+
+__device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax * kPerLargest, kLeastScale); }
+
+// Eight columns from j on of a row of n, zeros behind its end.
+template <class Tr>
+__device__ __forceinline__ void load8(const char* row, int64_t j, int64_t n, float* x) {
+  if (j + 8 <= n) {
+#pragma unroll
+    for (int i = 0; i < 8 / Tr::kPerVec; ++i)
+      Tr::unpack(load_vec(row + (j + i * Tr::kPerVec) * Tr::kBytes), x + i * Tr::kPerVec);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = j + k < n ? Tr::load1(row, j + k) : 0.f;
+  }
+}
+
+// 16 lanes a block of a row, 16 blocks a workgroup.  xq [T x hp], zeros behind
+// column h; sx [blocks x T].
+template <class Tr>
+__global__ void __launch_bounds__(256) k_fp8_rows(Fp8Args a, uint8_t* xq, float* sx, int blocks, int64_t first) {
+  const int64_t i = first + static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (i >= a.T * blocks) return;
+  const int64_t t = i / blocks;
+  const int b = static_cast<int>(i - t * blocks), lane = threadIdx.x & 15;
+  float x[8];
+  load8<Tr>(reinterpret_cast<const char*>(a.hidden) + t * a.ld_h * Tr::kBytes, b * kBlock + lane * 8, a.h, x);
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+  m = lanes_reduce<16>(m, [](float p, float q) { return fmaxf(p, q); });
+  const float scale = scale_of(m);
+  *reinterpret_cast<u32x2_t*>(xq + (t * blocks + b) * kBlock + lane * 8) = quantize8(x, scale);
+  if (lane == 0) sx[static_cast<int64_t>(b) * a.T + t] = scale;
+}
+
+// A workgroup a block of 128 x 128.
+template <class Tr>
+__global__ void __launch_bounds__(256) k_fp8_quantize(Fp8QuantArgs a, int blocks, int64_t first) {
+  __shared__ float sm[4];
+  const int64_t block = first + blockIdx.x;
+  const int vb = static_cast<int>(block / blocks), kb = static_cast<int>(block % blocks);
+  const int lane = threadIdx.x & 15, r0 = threadIdx.x >> 4, j = kb * kBlock + lane * 8;
+  float x[8][8], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t v = static_cast<int64_t>(vb) * kBlock + r0 + i * 16;
+    if (v < a.V) {
+      load8<Tr>(static_cast<const char*>(a.weight) + v * a.ld_w * Tr::kBytes, j, a.h, x[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[i][k]));
+    }
+  }
+  m = lanes_reduce<64>(m, [](float p, float q) { return fmaxf(p, q); });
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+  __syncthreads();
+  const float scale = scale_of(fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])));
+  if (threadIdx.x == 0) a.scales[vb * a.ld_s + kb] = scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t v = static_cast<int64_t>(vb) * kBlock + r0 + i * 16;
+    if (v < a.V && j < a.h) *reinterpret_cast<u32x2_t*>(a.q + v * a.ld_q + j) = quantize8(x[i], scale);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// many rows: tiles of 256 (vocabulary) x BN (rows)
+// ---------------------------------------------------------------------------
+
+struct TileArgs {
+  const uint8_t* weight;
+  int64_t ld_w;
+  const float* sw;
+  int64_t ld_s;
+  const uint8_t* xq;  // [T x hp]
+  const float* sx;    // [blocks x T]
+  int64_t T;
+  int h, V, blocks;
+  int n_vb, n_nb;
+  int64_t t0;  // first row of the launch
+  void* out;
+  int out_dtype;
+  int64_t ld_out;
+};
+
+__device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
+  return i32x8{static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
+               static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+}
+
+__device__ __forceinline__ f32x16_t mfma_32(i32x8 a, i32x8 b, f32x16_t c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+#else
+  (void)a, (void)b;
+  return c;
+#endif
+}
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// Eight e4m3 values as fp16, exactly.
+__device__ __forceinline__ f16x8_t widen8(uint32_t lo, uint32_t hi) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(static_cast<int>(lo), 1.f, false);
+  const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(static_cast<int>(lo), 1.f, true);
+  const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(static_cast<int>(hi), 1.f, false);
+  const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(static_cast<int>(hi), 1.f, true);
+  return f16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+#else
+  (void)lo, (void)hi;
+  return f16x8_t{};
+#endif
+}
+
+// 32 bytes of K a lane of both operands (64 or 128 in all), as fp16.
+__device__ __forceinline__ f32x16_t mfma_32_wide(i32x8 a, i32x8 b, f32x16_t c) {
+#pragma unroll
+  for (int k = 0; k < 8; k += 2)
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(a[k], a[k + 1]), widen8(b[k], b[k + 1]), c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ f32x4_t mfma_16_wide(i32x8 a, i32x8 b, f32x4_t c) {
+#pragma unroll
+  for (int k = 0; k < 8; k += 2)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(a[k], a[k + 1]), widen8(b[k], b[k + 1]), c, 0, 0, 0);
+  return c;
+}
+
+// Neighbouring results of one row to out, rounded once.
+template <int N>
+__device__ __forceinline__ void store_results(void* out, int dtype, int64_t at, const float* x, int valid) {
+  char* p = static_cast<char*>(out);
+  if (N % 4 == 0 && valid >= N) {
+    if (dtype == 2) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) *reinterpret_cast<u32x4_a2*>(p + (at + k) * 4) = Fp32::pack(x + k);
+      return;
+    }
+    if (N == 8) {
+      *reinterpret_cast<u32x4_a2*>(p + at * 2) = dtype == 0 ? Bf16::pack(x) : Fp16::pack(x);
+      return;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k >= valid) continue;
+    if (dtype == 0)
+      Bf16::store1(p, at + k, x[k]);
+    else if (dtype == 1)
+      Fp16::store1(p, at + k, x[k]);
+    else
+      Fp32::store1(p, at + k, x[k]);
+  }
+}
+
+template <int BN, int WGM, int WGN>
+struct Fp8Tile {
+  static constexpr int BM = 256, NW = WGM * WGN, NT = 64 * NW;
+  static constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
+  static constexpr int A_INST = BM / 8 / NW, B_INST = BN / 8 / NW;  // 1 KB loads a wave and stage
+  static constexpr int STAGE = (BM + BN) * kBlock;                  // bytes
+  static constexpr int OUT_PITCH = MI * 32 + 4;                     // floats of a row staged for output
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads a wave");
+  static_assert(NW * 32 * OUT_PITCH * 4 <= 2 * STAGE, "output staging fits the stages");
+};
+
+// One block: K in steps of 128 (one scale block) through two LDS stages, filled
+// direct to LDS.
+template <int BN, int WGM, int WGN, bool WIDE>
+__global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
+  using C = Fp8Tile<BN, WGM, WGN>;
+  constexpr int MI = C::MI, NI = C::NI, NW = C::NW;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * C::STAGE];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WGM, wn = wave / WGM;
+  int vb, nb;
+  {
+    // each XCD (workgroup b runs on XCD b % 8) walks one contiguous range of the
+    // order: groups of 4 vocabulary blocks, in them the row blocks
+    const int all = a.n_vb * a.n_nb, b = blockIdx.x, x = b & 7;
+    const int L = (all >> 3) * x + min(x, all & 7) + (b >> 3);
+    constexpr int G = 4;
+    const int g = L / (G * a.n_nb), size = min(G, a.n_vb - g * G), in = L - g * G * a.n_nb;
+    nb = in / size;
+    vb = g * G + in % size;
+  }
+  const int v0 = vb * C::BM;
+  const int64_t t0 = a.t0 + static_cast<int64_t>(nb) * BN;
+  const int M = a.V - v0, N = static_cast<int>(a.T - t0 < BN ? a.T - t0 : BN);
+  const int hp = a.blocks * kBlock;
+
+  // Loads: slot (j NW + wave) 64 + lane of a stage's 16-byte chunks; its row r and
+  // chunk kc ^ swizzle(r), the same kc for every j.  Rows past the operand are its
+  // last one again; behind the last column the chunk in front of the row's last
+  // block stands in, against zeros of x.
+  const int r = wave * 8 + (lane >> 3), kc = (lane & 7) ^ lds_swz(r);
+  const dtl_rsrc_t wrsrc = dtl_rsrc(a.weight + static_cast<int64_t>(v0) * a.ld_w), xrsrc = dtl_rsrc(a.xq + t0 * hp);
+  const uint32_t tail = static_cast<uint32_t>(kc * 16) >= static_cast<uint32_t>(a.h - (a.blocks - 1) * kBlock) ? kc * 16u : 0u;
+  auto offset = [&](int j, int rows, uint32_t ld) {
+    const int q = j * NW * 8 + r;
+    return static_cast<uint32_t>(q < rows ? q : rows - 1) * ld + kc * 16u;
+  };
+  auto issue = [&](int kt, unsigned char* stage) {
+    const uint32_t back = kt == a.blocks - 1 ? tail : 0u;
+#pragma unroll
+    for (int j = 0; j < C::A_INST; ++j)
+      dtl_load16(wrsrc, reinterpret_cast<uint16_t*>(stage + (j * NW + wave) * 1024), offset(j, M, static_cast<uint32_t>(a.ld_w)) - back,
+                 static_cast<uint32_t>(kt) * kBlock);
+#pragma unroll
+    for (int j = 0; j < C::B_INST; ++j)
+      dtl_load16(xrsrc, reinterpret_cast<uint16_t*>(stage + C::BM * kBlock + (j * NW + wave) * 1024),
+                 offset(j, N, static_cast<uint32_t>(hp)), static_cast<uint32_t>(kt) * kBlock);
+  };
+  // 32 bytes of K of one operand row: chunks g, 2 + g and 4 + g, 6 + g of the two
+  // steps of 64, the same for both operands (the order within K is free).
+  const int r32 = lane & 31, g = lane >> 5;
+  auto fragment = [&](const unsigned char* rows, int row, int s) {
+    const unsigned char* p = rows + (row + r32) * kBlock;
+    const int z = lds_swz(r32);
+    return join(*reinterpret_cast<const u32x4*>(p + (((s * 4 + g) ^ z) << 4)),
+                *reinterpret_cast<const u32x4*>(p + (((s * 4 + 2 + g) ^ z) << 4)));
+  };
+
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[mi][ni][i] = 0.f;
+  f32x16_t zero;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+
+  // this wave's rows of W lie in one block of scales, a lane's column of x is one row
+  const float* sw = a.sw + static_cast<int64_t>(min(v0 + wm * MI * 32, a.V - 1) / kBlock) * a.ld_s;
+  const float* sx[NI];
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) sx[ni] = a.sx + t0 + min(wn * NI * 32 + ni * 32 + r32, N - 1);
+
+  issue(0, lds);
+  for (int kt = 0; kt < a.blocks; ++kt) {
+    unsigned char* X = lds + (kt & 1) * C::STAGE;
+    float f[NI];
+    const float w = sw[kt];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) f[ni] = w * sx[ni][kt * a.T];
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (kt + 1 < a.blocks) issue(kt + 1, lds + ((kt + 1) & 1) * C::STAGE);
+    i32x8 fa[MI][2];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fa[mi][s] = fragment(X, (wm * MI + mi) * 32, s);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const i32x8 b0 = fragment(X + C::BM * kBlock, (wn * NI + ni) * 32, 0);
+      const i32x8 b1 = fragment(X + C::BM * kBlock, (wn * NI + ni) * 32, 1);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        f32x16_t p;
+        if (WIDE)
+          p = mfma_32_wide(fa[mi][1], b1, mfma_32_wide(fa[mi][0], b0, zero));
+        else
+          p = mfma_32(fa[mi][1], b1, mfma_32(fa[mi][0], b0, zero));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[mi][ni][i] = fmaf(p[i], f[ni], acc[mi][ni][i]);
+      }
+    }
+  }
+  __syncthreads();
+
+  // Out: 32 rows at a time through LDS of the wave's own, so that a row's
+  // neighbouring results are stored together.
+  float* own = reinterpret_cast<float*>(lds) + wave * 32 * C::OUT_PITCH;
+  const int vw = v0 + wm * MI * 32;
+  const int per = a.out_dtype == 2 ? 4 : 8, lanes = MI * 32 / per, rows = 64 / lanes;
+  const int col = lane % lanes * per, row0 = lane / lanes;
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(own + r32 * C::OUT_PITCH + mi * 32 + q * 8 + g * 4) =
+            f32x4_t{acc[mi][ni][q * 4], acc[mi][ni][q * 4 + 1], acc[mi][ni][q * 4 + 2], acc[mi][ni][q * 4 + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int q = row0; q < 32; q += rows) {
+      const int t = wn * NI * 32 + ni * 32 + q, v = vw + col;
+      const float* p = own + q * C::OUT_PITCH + col;
+      float x[8];
+      *reinterpret_cast<f32x4_t*>(x) = *reinterpret_cast<const f32x4_t*>(p);
+      if (t >= N || v >= a.V) continue;
+      const int64_t at = (t0 + t) * a.ld_out + v;
+      if (per == 8) {
+        *reinterpret_cast<f32x4_t*>(x + 4) = *reinterpret_cast<const f32x4_t*>(p + 4);
+        store_results<8>(a.out, a.out_dtype, at, x, a.V - v);
+      } else {
+        store_results<4>(a.out, a.out_dtype, at, x, a.V - v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few rows: the head passes by once
+// ---------------------------------------------------------------------------
+
+// Up to 16 rows of x.  K is split over the 8 waves of a workgroup, whose blocks
+// of x stay in registers; the workgroups walk over the head 16 rows at a time,
+// the next 16 rows' bytes in flight.
+template <int NB>
+__global__ void __launch_bounds__(512, 2) k_fp8_few(TileArgs a) {
+  __shared__ float sums[2][8][256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int T = static_cast<int>(a.T), hp = a.blocks * kBlock, tiles = (a.V + 15) / 16;
+  i32x8 x[NB];
+  float sx[NB];
+  int at[NB][2];  // the lane's bytes of a row of the head; those behind its end are its first ones (against zeros)
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int kb = wave + i * 8, t = r < T ? r : T - 1;
+    const bool on = kb < a.blocks;
+    const u32x4 none{0, 0, 0, 0};
+    const u32x4* p = reinterpret_cast<const u32x4*>(a.xq + static_cast<int64_t>(t) * hp + (on ? kb : 0) * kBlock + g * 32);
+    x[i] = join(on ? p[0] : none, on ? p[1] : none);
+    sx[i] = on ? a.sx[static_cast<int64_t>(kb) * a.T + t] : 0.f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int k = kb * kBlock + g * 32 + s * 16;
+      at[i][s] = k < a.h ? k : 0;
+    }
+  }
+  u32x4 w[2][NB][2];
+  auto load = [&](int tile, u32x4 (&dst)[NB][2]) {
+    const int v = tile * 16 + r;
+    const uint8_t* p = a.weight + static_cast<int64_t>(v < a.V ? v : a.V - 1) * a.ld_w;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) dst[i][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + at[i][s]));
+  };
+  auto work = [&](int tile, int buf, u32x4 (&src)[NB][2]) {
+    const float* sw = a.sw + static_cast<int64_t>(tile / 8) * a.ld_s;
+    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int kb = wave + i * 8;
+      const f32x4_t p = mfma_16_wide(join(src[i][0], src[i][1]), x[i], f32x4_t{0.f, 0.f, 0.f, 0.f});
+      const float f = (kb < a.blocks ? sw[kb] : 0.f) * sx[i];
+      // a block that is not there must not count, whatever its stand-in holds
+      if (kb < a.blocks) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
+      }
+    }
+    // lane: rows 4 g .. + 3 of the head, row r of x
+    *reinterpret_cast<f32x4_t*>(&sums[buf][wave][r * 16 + g * 4]) = acc;
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += sums[buf][k][threadIdx.x];
+      const int t = threadIdx.x >> 4, v = tile * 16 + (threadIdx.x & 15);
+      if (t < T && v < a.V) store_results<1>(a.out, a.out_dtype, (a.t0 + t) * a.ld_out + v, &s, 1);
+    }
+  };
+  const int step = gridDim.x;
+  int tile = blockIdx.x;
+  if (tile < tiles) load(tile, w[0]);
+  while (tile < tiles) {
+    if (tile + step < tiles) load(tile + step, w[1]);
+    work(tile, 0, w[0]);
+    tile += step;
+    if (tile >= tiles) break;
+    if (tile + step < tiles) load(tile + step, w[0]);
+    work(tile, 1, w[1]);
+    tile += step;
+  }
+}
+
+template <int BN, int WGM, int WGN, bool WIDE>
+hipError_t launch_tile(TileArgs a, hipStream_t s) {
+  a.n_vb = (a.V + 255) / 256;
+  // blocks of a launch: below 2^32 work-items whatever T
+  const int64_t most = (int64_t(1) << 22) / a.n_vb > 0 ? (int64_t(1) << 22) / a.n_vb : 1;
+  const int64_t T = a.T;
+  for (int64_t t0 = 0; t0 < T; t0 += most * BN) {
+    const int64_t rows = T - t0 < most * BN ? T - t0 : most * BN;
+    a.t0 = t0;
+    a.n_nb = static_cast<int>((rows + BN - 1) / BN);
+    TimedLaunch tl("k_fp8_tile", s);
+    hipLaunchKernelGGL((k_fp8_tile<BN, WGM, WGN, WIDE>), dim3(static_cast<unsigned>(a.n_vb * a.n_nb)), dim3(64 * WGM * WGN), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int NB>
+hipError_t launch_few(const TileArgs& a, hipStream_t s) {
+  const int tiles = (a.V + 15) / 16;
+  TimedLaunch tl("k_fp8_few", s);
+  hipLaunchKernelGGL(k_fp8_few<NB>, dim3(tiles < 256 ? tiles : 256), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+constexpr int64_t kMostGroups = int64_t(1) << 23;  // of 256 threads in a launch: below 2^32 work-items
+
+size_t rows_bytes(int64_t T, int64_t h) { return (size_t(T) * ((h + kBlock - 1) / kBlock) * kBlock + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t fp8_workspace_bytes(int64_t T, int64_t h, int64_t V) {
+  (void)V;
+  return rows_bytes(T, h) + (size_t(T) * ((h + kBlock - 1) / kBlock) * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t s) {
+  TileArgs a{};
+  a.weight = f.weight;
+  a.ld_w = f.ld_w;
+  a.sw = f.scales;
+  a.ld_s = f.ld_s;
+  a.T = f.T;
+  a.h = f.h;
+  a.V = f.V;
+  a.blocks = (f.h + kBlock - 1) / kBlock;
+  a.out = f.out;
+  a.out_dtype = f.out_dtype;
+  a.ld_out = f.ld_out;
+  uint8_t* xq = reinterpret_cast<uint8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(ws + rows_bytes(f.T, f.h));
+  a.xq = xq;
+  a.sx = sx;
+  const int64_t parts = (f.T * a.blocks + 15) / 16;
+  for (int64_t p = 0; p < parts; p += kMostGroups) {
+    const dim3 grid(static_cast<unsigned>(parts - p < kMostGroups ? parts - p : kMostGroups));
+    TimedLaunch tl("k_fp8_rows", s);
+    if (dtype == 0)
+      hipLaunchKernelGGL(k_fp8_rows<Bf16>, grid, dim3(256), 0, s, f, xq, sx, a.blocks, p * 16);
+    else
+      hipLaunchKernelGGL(k_fp8_rows<Fp16>, grid, dim3(256), 0, s, f, xq, sx, a.blocks, p * 16);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.T <= 16 && a.blocks <= 64) {
+    switch ((a.blocks + 7) / 8) {
+      case 1: return launch_few<1>(a, s);
+      case 2: return launch_few<2>(a, s);
+      case 3: return launch_few<3>(a, s);
+      case 4: return launch_few<4>(a, s);
+      case 5: return launch_few<5>(a, s);
+      case 6: return launch_few<6>(a, s);
+      case 7: return launch_few<7>(a, s);
+      default: return launch_few<8>(a, s);
+    }
+  }
+  if (a.out_dtype == 2) {
+    if (a.T <= 64) return launch_tile<64, 4, 2, true>(a, s);
+    if (a.T <= 128) return launch_tile<128, 4, 2, true>(a, s);
+    return launch_tile<256, 4, 2, true>(a, s);
+  }
+  if (a.T <= 64) return launch_tile<64, 4, 2, false>(a, s);
+  if (a.T <= 128) return launch_tile<128, 4, 2, false>(a, s);
+  return launch_tile<256, 4, 2, false>(a, s);
+}
+
+hipError_t launch_fp8_quantize(int dtype, const Fp8QuantArgs& a, hipStream_t s) {
+  const int blocks = (a.h + kBlock - 1) / kBlock;
+  const int64_t all = (int64_t(a.V) + kBlock - 1) / kBlock * blocks;
+  for (int64_t p = 0; p < all; p += kMostGroups) {
+    const dim3 grid(static_cast<unsigned>(all - p < kMostGroups ? all - p : kMostGroups));
+    TimedLaunch tl("k_fp8_quantize", s);
+    if (dtype == 0)
+      hipLaunchKernelGGL(k_fp8_quantize<Bf16>, grid, dim3(256), 0, s, a, blocks, p);
+    else if (dtype == 1)
+      hipLaunchKernelGGL(k_fp8_quantize<Fp16>, grid, dim3(256), 0, s, a, blocks, p);
+    else
+      hipLaunchKernelGGL(k_fp8_quantize<Fp32>, grid, dim3(256), 0, s, a, blocks, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace lp

@@ -211,6 +211,131 @@ hipError_t launch_w4_logits(int dtype, const W4Args& a, hipStream_t s);
 hipError_t launch_w4_quantize(int dtype, const W4QuantArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// the largest logits of rows, and beams
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxTop = 256;        // most entries of a row's list
+constexpr int kMaxBeams = 64;       // most beams of a request
+constexpr int kMaxBeamLists = 4096; // most beams times continuations of one
+
+struct TopArgs {
+  const void* x;
+  int64_t ld;
+  int V;
+  int64_t T;  // rows (beams: B * W)
+  int K;
+  const uint8_t* mask;
+  float c;  // log2(e) / tau_effective
+  double inv_tau;
+  int64_t* ids;    // [T x K]; beams: tokens [B x N]
+  float* logprob;  // [T x K]
+  float* rest;
+  float* lse;
+  // beams
+  int W;  // 0: no beams
+  const float* beam_scores;
+  const uint8_t* finished;
+  int64_t end_token;
+  float* scores;
+  int32_t* parents;
+  // set by the launchers
+  int64_t row0;
+  int slice, nslices;
+  uint64_t* part_keys;  // [T x nslices x K], 0: none
+  float* part_sums;     // [T x nslices x 2]
+};
+
+size_t top_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t K);
+size_t beam_workspace_bytes(int dtype, int64_t B, int64_t W, int64_t V, int64_t N);
+hipError_t launch_top_logits(int dtype, const TopArgs& a, char* ws, hipStream_t s);
+hipError_t launch_beam_select(int dtype, const TopArgs& a, int64_t B, char* ws, hipStream_t s);
+
+// [outer x (B * W or B * N) x mid x width bytes], strides in bytes.
+struct ReorderArgs {
+  const void* src;
+  void* dst;
+  int64_t outer, mid, width;
+  int64_t src_outer, src_row, src_mid, dst_outer, dst_row, dst_mid;
+  int64_t B;
+  int W, N;
+  const int32_t* parents;  // [B x N]
+  // set by the launcher
+  unsigned pieces, seg0;
+};
+
+// False where one row's copy would take more than one launch.
+bool beam_reorder_fits(const ReorderArgs& a);
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// distillation from a teacher's top logits
+// ---------------------------------------------------------------------------
+
+struct DistillArgs {
+  const void* x;
+  int64_t ld;
+  int V;
+  int64_t T;
+  int K;
+  const int64_t* ids;    // [T x K]
+  const float* logprob;  // [T x K]
+  const float* rest;     // [T] or null
+  const uint8_t* mask;
+  float c;
+  double inv_tau;
+  // forward
+  float* loss;
+  float* lse_out;
+  float* lse_rest_out;
+  // gradient
+  const float* lse;
+  const float* lse_rest;
+  const float* grad_loss;
+  void* out;
+  int64_t ld_out;
+  // set by the launchers
+  int64_t row0;
+  int slice, nslices;
+  float* part;  // [T x nslices x 4]: sums of the unlisted, of the listed columns
+};
+
+size_t distill_workspace_bytes(int dtype, int64_t T, int64_t V);
+hipError_t launch_distill(int dtype, const DistillArgs& a, char* ws, hipStream_t s);
+hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// 8-bit head
+// ---------------------------------------------------------------------------
+
+struct Fp8Args {
+  const uint16_t* hidden;  // bf16 or fp16 bits [T x ld_h]
+  int64_t ld_h;
+  int64_t T;
+  int h, V;
+  const uint8_t* weight;  // e4m3 [V x ld_w]
+  int64_t ld_w;
+  const float* scales;  // [ceil(V / 128) x ld_s]
+  int64_t ld_s;
+  void* out;
+  int out_dtype;
+  int64_t ld_out;
+};
+
+struct Fp8QuantArgs {
+  const void* weight;
+  int64_t ld_w;
+  int V, h;
+  uint8_t* q;
+  int64_t ld_q;
+  float* scales;
+  int64_t ld_s;
+};
+
+size_t fp8_workspace_bytes(int64_t T, int64_t h, int64_t V);
+hipError_t launch_fp8_logits(int dtype, const Fp8Args& a, char* ws, hipStream_t s);
+hipError_t launch_fp8_quantize(int dtype, const Fp8QuantArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // fused LM head
 // ---------------------------------------------------------------------------
 

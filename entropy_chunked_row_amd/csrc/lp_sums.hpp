@@ -1,0 +1,126 @@
+// Softmax sums of a row without the entropy's term, and the order of logits:
+// shared by the kernels that choose from a row and that distil from one.
+#pragma once
+
+#include "lp_device.hpp"
+
+namespace lp {
+
+// RowStat without `a`: m the largest value (-inf: none yet), s the sum of 2^t
+// over exponents t relative to m c, near and far as there; values whose m c leaves
+// fp32 are far ones too.
+struct SumStat {
+  float m, s;
+};
+
+struct LaneSum : SumStat {
+  float nmc = 0.f;  // -RN(m c); 0 while m is -inf
+};
+
+__device__ __forceinline__ LaneSum sum_none() { return LaneSum{{neg_inf(), 0.f}}; }
+
+// Folds N values whose largest is vm into the state.  -inf weighs 0; a NaN stays
+// a NaN in s.
+template <int N, int CH>
+__device__ __forceinline__ void sum_push(LaneSum& st, const float* x, float vm, float c) {
+  if (vm > st.m) {
+    st.s *= fast_exp2(stat_shift(st.m, vm, c));
+    st.m = vm;
+    st.nmc = -(vm * c);
+  }
+  auto fold = [&](auto exponent) {
+#pragma unroll
+    for (int g = 0; g < N; g += CH) {
+      float ps = 0.f;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) ps += fast_exp2(exponent(x[g + k]));
+      st.s += ps;
+    }
+  };
+  if (is_near(st.nmc))
+    fold([&](float v) { return fmaf(v, c, st.nmc); });
+  else
+    fold([&](float v) { return (v - st.m) * c; });
+}
+
+__device__ __forceinline__ void sum_push1(LaneSum& st, float x, float c) { sum_push<1, 1>(st, &x, x, c); }
+
+// The whole of N states of N neighbouring lanes, in each of them.
+template <int N>
+__device__ __forceinline__ SumStat sum_merge(SumStat st, float c) {
+  const float m = lanes_reduce<N>(st.m, [](float x, float y) { return fmaxf(x, y); });
+  return SumStat{m, lanes_reduce<N>(st.s * fast_exp2(stat_shift(st.m, m, c)), [](float x, float y) { return x + y; })};
+}
+
+__device__ __forceinline__ SumStat sum_add(SumStat x, SumStat y, float c) {
+  const float m = fmaxf(x.m, y.m);
+  return SumStat{m, x.s * fast_exp2(stat_shift(x.m, m, c)) + y.s * fast_exp2(stat_shift(y.m, m, c))};
+}
+
+// The workgroup's whole state, in every thread; sm holds NT / 64 states.  Ends
+// with no barrier: sm may be written again only after one.
+template <int NT>
+__device__ __forceinline__ SumStat sum_block(SumStat st, float c, SumStat* sm) {
+  constexpr int W = NT / 64;
+  st = sum_merge<64>(st, c);
+  if (W == 1) return st;
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = st;
+  __syncthreads();
+  return sum_merge<W>(sm[threadIdx.x & (W - 1)], c);
+}
+
+__device__ __forceinline__ float sum_exponent(float x, float m, float c) {
+  const float mc = m * c;
+  if (m == neg_inf()) return x * c;  // none yet: -inf or NaN
+  return is_near(mc) ? fmaf(x, c, -mc) : (x - m) * c;
+}
+
+// log-sum-exp of z / tau, natural, in fp64 (scores of different rows are compared
+// and differences of nearly equal ones formed: fp32 would leave a few 2^-24 of
+// their magnitude).  m c carries the rounding of c and of the product; both are
+// taken out again, so that only the exponents' own roundings remain.
+__device__ __forceinline__ double sum_lse(SumStat st, float c, double inv_tau) {
+  if (st.s == 0.f) return -__builtin_inf();
+  const float mc = st.m * c;
+  const double l2s = log2(static_cast<double>(st.s));
+  const double off = is_near(mc) ? static_cast<double>(st.m) * c - static_cast<double>(mc) : 0.0;
+  return static_cast<double>(st.m) * inv_tau + (l2s - off) * 0.69314718055994530942;
+}
+
+// Whole numbers in the order of the values (-0 = 0); NaN of either sign lies outside the infinities.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
+}
+
+// A row's vector v of n columns: whole, or what is left at the end with -inf
+// behind it.  Rows may start at any element.
+template <class Tr>
+__device__ __forceinline__ u32x4 row_vector(const char* xp, int v, int n) {
+  constexpr int P = Tr::kPerVec;
+  if ((v + 1) * P <= n) return load_vec(xp + static_cast<size_t>(v) * 16);
+  float x[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) x[k] = v * P + k < n ? Tr::load1(xp, v * P + k) : neg_inf();
+  return Tr::pack(x);
+}
+
+template <class Tr>
+__device__ __forceinline__ u32x4 no_vector() {
+  const uint32_t w = Tr::kBytes == 2 ? Tr::neg_inf_bits() * 0x10001u : Tr::neg_inf_bits();
+  return u32x4{w, w, w, w};
+}
+
+template <int N>
+__device__ __forceinline__ float largest_of(const float* x) {
+  float m = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  return m;
+}
+
+}  // namespace lp

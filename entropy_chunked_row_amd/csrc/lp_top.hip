@@ -1,0 +1,836 @@
+// The largest logits of rows, and what is chosen from them: the top K of a row
+// with their log-probs and the mass of all others (lp_top_logits), and the best
+// N continuations over the beams of a request (lp_beam_select).
+//
+// A row is read once.  A workgroup owns a row, or a slice of one where rows are
+// few, and
+//   1. reads a first piece of it, spread over its whole length, and takes each
+//      lane's largest value: the K-th largest of these is no larger than the
+//      K-th largest of the row, so nothing below it can be chosen;
+//   2. streams the row.  Vectors of 16 bytes that hold a value at or above that
+//      threshold are kept in LDS, all others are folded into the softmax sums;
+//   3. repeats step 1 on the kept vectors, ranks what reaches the new threshold
+//      by counting, and adds what was not chosen to the sums.
+// So the mass outside the list is a sum of its own, never a difference of two
+// nearly equal ones.  Which lane holds which kept vector depends on the order of
+// LDS atomics; what is left of them is therefore summed exactly (sum_left), and
+// every result is the same bits on every call.  Order is (value descending, column ascending), as one
+// 64-bit key.  More kept vectors than LDS holds (rows that rise steadily, or have
+// most values equal) are counted by digits of the keys instead: right for any
+// row, several more reads of it.
+#include "lp_internal.hpp"
+#include "lp_sums.hpp"
+
+namespace lp {
+
+namespace {
+
+constexpr int kMaxBuffered = 4096;  // keys of a row's or a request's slices that a join takes
+
+// Significant leading bits of order_of for values of a type.
+template <class Tr>
+constexpr int kOrderBits = 32;
+template <>
+constexpr int kOrderBits<Bf16> = 16;
+template <>
+constexpr int kOrderBits<Fp16> = 19;
+
+// By one wave: the largest t with BITS leading bits such that at least `want`
+// of N words are >= t; 0 if even that many are not there (empty places hold 0).
+template <int N, int BITS>
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t* words, int want) {
+  uint32_t w[N / 64];
+#pragma unroll
+  for (int i = 0; i < N / 64; ++i) w[i] = words[(threadIdx.x & 63) + 64 * i];
+  uint32_t t = 0;
+  for (int b = 31; b >= 32 - BITS; --b) {
+    const uint32_t cand = t | 1u << b;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < N / 64; ++i) count += __popcll(__ballot(w[i] >= cand));
+    if (count >= want) t = cand;
+  }
+  return t;
+}
+
+__device__ __forceinline__ uint64_t key_of(float x, int col) {
+  return static_cast<uint64_t>(order_of(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(col));
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return value_of(static_cast<uint32_t>(key >> 32)); }
+__device__ __forceinline__ int key_col(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
+
+// As a threshold: values at or above it.  Never -inf, which is not chosen.
+__device__ __forceinline__ float threshold_of(uint32_t t) {
+  const float x = value_of(t);
+  return x >= -kLargest ? x : -kLargest;  // NaN (t = 0) too
+}
+
+// Keys greater than `key` among n (a 0 behind them where n is odd).
+__device__ __forceinline__ int rank_among(const uint64_t* keys, int n, uint64_t key) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  int r = 0;
+  for (int i = 0; i < n; i += 2) {
+    const u64x2 q = *reinterpret_cast<const u64x2*>(keys + i);
+    r += (q.x > key) + (q.y > key);
+  }
+  return r;
+}
+
+// Adds 1 to a bin; lanes that share the first lane's bin do so as one (rows of
+// equal values would queue up at one address).
+__device__ __forceinline__ void count_bin(uint32_t* hist, bool on, uint32_t bin) {
+  const uint64_t live = __ballot(on);
+  if (!live) return;
+  const int first = __ffsll(static_cast<unsigned long long>(live)) - 1;
+  const uint32_t lead = __shfl(bin, first, 64);
+  const uint64_t same = __ballot(on && bin == lead);
+  if (on && bin != lead) atomicAdd(hist + bin, 1u);
+  if ((threadIdx.x & 63) == first) atomicAdd(hist + lead, static_cast<uint32_t>(__popcll(same)));
+}
+
+// The top `want` finite values of n columns by digits of their keys, whatever
+// the row.  Their keys to `chosen` (unordered), their number returned; all else
+// folded into st.  hist: 256 words and two more of LDS.
+template <class Tr, int NT>
+__device__ int choose_by_digits(const char* xp, int n, int c0, int want, float c, LaneSum& st, uint64_t* chosen,
+                                uint32_t* hist) {
+  constexpr int P = Tr::kPerVec;
+  const int tid = threadIdx.x, vectors = (n + P - 1) / P, rounds = (vectors + NT - 1) / NT;
+  uint32_t* found = hist + 256;  // digit, keys above it
+  uint64_t prefix = 0;
+  int need = want, shift = 64;
+  while (shift > 0) {
+    shift -= 8;
+    __syncthreads();
+    for (int i = tid; i < 256; i += NT) hist[i] = 0;
+    __syncthreads();
+    for (int q = 0; q < rounds; ++q) {
+      const int v = tid + q * NT;
+      float x[P];
+      Tr::unpack(v < vectors ? row_vector<Tr>(xp, v, n) : no_vector<Tr>(), x);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const uint64_t key = key_of(x[k], c0 + v * P + k);
+        const bool on = x[k] >= -kLargest && (shift == 56 || (key >> (shift + 8)) == prefix);
+        count_bin(hist, on, static_cast<uint32_t>(key >> shift) & 255u);
+      }
+    }
+    __syncthreads();
+    if (tid < 64) {
+      // lane l: digits 4 (63 - l) .. + 3, so that lower lanes hold larger ones
+      const int d0 = 4 * (63 - tid);
+      uint32_t h[4], mine = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine += h[k] = hist[d0 + k];
+      uint32_t upto = mine;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t y = __shfl_up(upto, off, 64);
+        if (tid >= off) upto += y;
+      }
+      uint32_t above = upto - mine;
+      if (tid == 63 && upto < static_cast<uint32_t>(need)) found[0] = 0xffffffffu;  // not that many
+      if (above < static_cast<uint32_t>(need) && upto >= static_cast<uint32_t>(need)) {
+        int k = 3;
+        while (above + h[k] < static_cast<uint32_t>(need)) above += h[k--];
+        found[0] = d0 + k;
+        found[1] = above;
+      }
+    }
+    __syncthreads();
+    const uint32_t digit = found[0];
+    if (digit == 0xffffffffu) {  // only in the first round: every finite value is chosen
+      shift = 64;
+      break;
+    }
+    need -= static_cast<int>(found[1]);
+    prefix = prefix << 8 | digit;
+    if (hist[digit] == static_cast<uint32_t>(need)) break;  // the whole bin
+  }
+  const uint64_t least = shift >= 64 ? 0 : prefix << shift;
+  __syncthreads();
+  if (tid == 0) hist[0] = 0;
+  __syncthreads();
+  for (int q = 0; q < rounds; ++q) {
+    const int v = tid + q * NT;
+    float x[P];
+    Tr::unpack(v < vectors ? row_vector<Tr>(xp, v, n) : no_vector<Tr>(), x);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const uint64_t key = key_of(x[k], c0 + v * P + k);
+      if (x[k] >= -kLargest && key >= least) {
+        const uint32_t at = atomicAdd(hist, 1u);
+        if (at < static_cast<uint32_t>(want)) chosen[at] = key;  // never more; a bound all the same
+        x[k] = neg_inf();
+      }
+    }
+    sum_push<P, P>(st, x, largest_of<P>(x), c);
+  }
+  __syncthreads();
+  const int got = static_cast<int>(hist[0]);
+  return got < want ? got : want;
+}
+
+// The outputs of a row from its list in order (LDS) and the states of the list
+// and of all else.
+template <int NT>
+__device__ __forceinline__ void store_top(const TopArgs& a, int64_t row, const uint64_t* top, int got, SumStat rest,
+                                          SumStat listed) {
+  const SumStat whole = sum_add(rest, listed, a.c);
+  const bool bad = !(whole.s > 0.f && whole.s <= kLargest);  // a NaN or +inf in the row, or only -inf
+  const float nan = __builtin_nanf("");
+  if (static_cast<int>(threadIdx.x) >= a.K) return;
+  const double lse = sum_lse(whole, a.c, a.inv_tau);
+  for (int k = threadIdx.x; k < a.K; k += NT) {
+    float lp = bad ? nan : neg_inf();
+    int64_t id = -1;
+    if (k < got && !bad) {
+      lp = static_cast<float>(static_cast<double>(key_value(top[k])) * a.inv_tau - lse);
+      id = key_col(top[k]);
+    }
+    a.ids[row * a.K + k] = id;
+    a.logprob[row * a.K + k] = lp;
+  }
+  if (threadIdx.x == 0) {
+    if (a.rest) a.rest[row] = bad ? nan : static_cast<float>(sum_lse(rest, a.c, a.inv_tau) - lse);
+    if (a.lse) a.lse[row] = static_cast<float>(lse);
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ void store_no_top(const TopArgs& a, int64_t row) {
+  for (int k = threadIdx.x; k < a.K; k += NT) {
+    a.ids[row * a.K + k] = -1;
+    a.logprob[row * a.K + k] = 0.f;
+  }
+  if (threadIdx.x == 0) {
+    if (a.rest) a.rest[row] = 0.f;
+    if (a.lse) a.lse[row] = 0.f;
+  }
+}
+
+// The softmax sum of N values a lane, whichever lane holds which: exponentials
+// relative to the largest are brought to a grid of 2^-38, on which fp64 adds up
+// to 2^14 of them exactly.  spare: 2 NT / 64 doubles of LDS.
+template <int N, int NT>
+__device__ __forceinline__ SumStat sum_left(const float* x, float c, double* spare) {
+  static_assert(N * NT <= 1 << 14, "sums up to 2^14 on a grid of 2^-38 take 52 bits");
+  constexpr int W = NT / 64;
+  auto most = [](float p, float q) { return fmaxf(p, q); };
+  float* tops = reinterpret_cast<float*>(spare);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float m = lanes_reduce<64>(largest_of<N>(x), most);
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
+  m = lanes_reduce<W>(tops[lane & (W - 1)], most);
+  constexpr double kGrid = 16384.0;  // 2^14: what is added to it is rounded to its ulp, 2^-38
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const double e = fast_exp2(sum_exponent(x[i], m, c));
+    sum += (e + kGrid) - kGrid;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane == 0) spare[W + wave] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) sum += spare[W + w];
+  return SumStat{m, static_cast<float>(sum)};
+}
+
+// Whether row `row` takes part: scored, or of a beam that goes on.
+__device__ __forceinline__ bool row_live(const TopArgs& a, int64_t row) {
+  if (a.beam_scores) return a.beam_scores[row] >= -kLargest && a.beam_scores[row] <= kLargest && !(a.finished && a.finished[row]);
+  return !(a.mask && a.mask[row] == 0);
+}
+
+// SHORT: the slice is at most two vectors a lane, all of which are "kept".
+template <class Tr, int NT, int U, bool SHORT>
+__global__ void __launch_bounds__(NT) k_top(TopArgs a) {
+  constexpr int P = Tr::kPerVec, W = NT / 64, kKept = 2 * NT, kKeys = 2 * kKept;
+  __shared__ u32x4 kept[kKept];  // later the keys that are ranked
+  __shared__ uint32_t kept_at[SHORT ? 1 : kKept];
+  constexpr int kWords = SHORT ? 2 * NT : NT;
+  __shared__ uint32_t best[kWords > 258 ? kWords : 258];
+  __shared__ uint64_t top[kMaxTop];
+  __shared__ SumStat sm[2][W];
+  __shared__ uint32_t counts[2], bar;
+  __shared__ double spare[2 * W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const unsigned rel_row = blockIdx.x / static_cast<unsigned>(a.nslices);
+  const int slice = static_cast<int>(blockIdx.x - rel_row * static_cast<unsigned>(a.nslices));
+  const int64_t row = a.row0 + rel_row;
+  if (!row_live(a, row)) {
+    if (!a.part_keys) store_no_top<NT>(a, row);
+    return;
+  }
+  const int c0 = slice * a.slice;
+  const int n = a.V - c0 < a.slice ? a.V - c0 : a.slice;
+  const char* xp = static_cast<const char*>(a.x) + (row * a.ld + c0) * Tr::kBytes;
+  const float c = a.c;
+  LaneSum st = sum_none();
+  u32x4 mine[2];  // kept vectors of this lane, and their numbers
+  int at[2];
+  bool digits = false;
+  if (tid < 2) counts[tid] = 0;
+
+  if (SHORT) {
+    const int vectors = (n + P - 1) / P;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      at[i] = tid + i * NT;
+      mine[i] = at[i] < vectors ? row_vector<Tr>(xp, at[i], n) : no_vector<Tr>();
+    }
+  } else {
+    // Lane's vectors: U pieces of the row a wave, `steps` times 64 vectors each,
+    // so that one step of the workgroup is a sample of the whole row.
+    const int vectors = n / P, steps = (vectors + 64 * U * W - 1) / (64 * U * W);
+    uint32_t v0[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v0[u] = static_cast<uint32_t>((wave * U + u) * steps * 64 + lane);
+    auto load = [&](uint32_t v) {
+      return v < static_cast<uint32_t>(vectors)
+                 ? static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xp + size_t(v) * 16)))
+                 : no_vector<Tr>();
+    };
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = load(v0[u]);
+    {
+      float vm = neg_inf();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[P];
+        Tr::unpack(w[u], x);
+        vm = fmaxf(vm, largest_of<P>(x));
+      }
+      best[tid] = vm > neg_inf() ? order_of(vm) : 0u;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const uint32_t t = kth_largest<NT, kOrderBits<Tr>>(best, a.K);
+      if (lane == 0) bar = t;
+    }
+    __syncthreads();
+    const float floor = threshold_of(bar);
+    auto keep = [&](u32x4 vec, uint32_t v) {
+      const uint32_t k = atomicAdd(counts, 1u);
+      if (k < static_cast<uint32_t>(kKept)) {
+        kept[k] = vec;
+        kept_at[k] = v;
+      }
+    };
+    for (int q = 0;;) {
+      float x[U * P], vm = neg_inf();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Tr::unpack(w[u], x + u * P);
+        const float m = largest_of<P>(x + u * P);
+        if (m >= floor) {
+          keep(w[u], v0[u] + q * 64);
+#pragma unroll
+          for (int k = 0; k < P; ++k) x[u * P + k] = neg_inf();
+        } else {
+          vm = fmaxf(vm, m);
+        }
+      }
+      if (++q == steps) {
+        sum_push<U * P, P>(st, x, vm, c);
+        break;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = load(v0[u] + q * 64);
+      sum_push<U * P, P>(st, x, vm, c);
+    }
+    if (tid == 0 && vectors * P < n) keep(row_vector<Tr>(xp, vectors, n), vectors);
+    __syncthreads();
+    const uint32_t m = counts[0];
+    digits = m > static_cast<uint32_t>(kKept);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t k = tid + i * NT;
+      const bool on = !digits && k < m;
+      mine[i] = on ? kept[k] : no_vector<Tr>();
+      at[i] = on ? static_cast<int>(kept_at[k]) : 0;
+    }
+  }
+
+  int got = 0;
+  SumStat left{neg_inf(), 0.f};  // of the kept vectors, what is not chosen
+  uint64_t* keys = reinterpret_cast<uint64_t*>(kept);
+  if (!digits) {
+    float x[2 * P];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) Tr::unpack(mine[i], x + i * P);
+    if (SHORT) {
+      // of each vector, or of its halves where no lane has a second one: with
+      // fewer words than K nothing could be left out
+      const bool halves = n <= NT * P;
+      const float m0 = largest_of<P>(x), m1 = largest_of<P>(x + P);
+      const float h0 = largest_of<P / 2>(x), h1 = largest_of<P / 2>(x + P / 2);
+      const float lo = halves ? h0 : m0, hi = halves ? h1 : m1;
+      best[tid] = lo > neg_inf() ? order_of(lo) : 0u;
+      best[kWords - NT + tid] = hi > neg_inf() ? order_of(hi) : 0u;
+    } else {
+      const float vm = largest_of<2 * P>(x);
+      best[tid] = vm > neg_inf() ? order_of(vm) : 0u;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const uint32_t t = kth_largest<kWords, kOrderBits<Tr>>(best, a.K);
+      if (lane == 0) bar = t;
+    }
+    __syncthreads();
+    const float floor = threshold_of(bar);
+    auto key_at = [&](int i) { return key_of(x[i], c0 + at[i / P] * P + i % P); };
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i) {
+      if (x[i] >= floor) {
+        const uint32_t k = atomicAdd(counts + 1, 1u);
+        if (k < static_cast<uint32_t>(kKeys)) keys[k] = key_at(i);
+      }
+    }
+    __syncthreads();
+    const int m = static_cast<int>(counts[1]);
+    if (m > kKeys) {
+      digits = true;
+    } else {
+      if (tid == 0 && (m & 1)) keys[m] = 0;
+      __syncthreads();
+      for (int i = tid; i < m; i += NT) {
+        const uint64_t key = keys[i];
+        const int r = rank_among(keys, m, key);
+        if (r < a.K) top[r] = key;
+      }
+      got = m < a.K ? m : a.K;
+      __syncthreads();
+      if (got > 0) {
+        const uint64_t least = top[got - 1];
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i)
+          if (x[i] >= floor && key_at(i) >= least) x[i] = neg_inf();
+      }
+      left = sum_left<2 * P, NT>(x, c, spare);
+    }
+  }
+  if (digits) {  // the same for the whole workgroup
+    __syncthreads();
+    st = sum_none();
+    got = choose_by_digits<Tr, NT>(xp, n, c0, a.K, c, st, keys, best);
+    if (tid == 0 && (got & 1)) keys[got] = 0;
+    __syncthreads();
+    for (int i = tid; i < got; i += NT) top[rank_among(keys, got, keys[i])] = keys[i];
+  }
+  __syncthreads();
+  const SumStat rest = sum_add(sum_block<NT>(st, c, sm[0]), left, c);
+  if (a.part_keys) {
+    const int64_t part = row * a.nslices + slice;
+    for (int k = tid; k < a.K; k += NT) a.part_keys[part * a.K + k] = k < got ? top[k] : 0;
+    if (tid == 0) {
+      a.part_sums[part * 2] = rest.m;
+      a.part_sums[part * 2 + 1] = rest.s;
+    }
+    return;
+  }
+  LaneSum of_list = sum_none();
+  for (int k = tid; k < got; k += NT) sum_push1(of_list, key_value(top[k]), c);
+  store_top<NT>(a, row, top, got, rest, sum_block<NT>(of_list, c, sm[1]));
+}
+
+// A row's slices: their keys are ranked like a slice's own.
+template <int NT>
+__global__ void __launch_bounds__(NT) k_top_join(TopArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint64_t keys[];  // nslices * K and one more
+  __shared__ uint32_t best[NT];
+  __shared__ uint64_t top[kMaxTop];
+  __shared__ SumStat sm[2][NT / 64];
+  __shared__ uint32_t count, bar;
+  const int tid = threadIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
+  if (!row_live(a, row)) {
+    store_no_top<NT>(a, row);
+    return;
+  }
+  const float c = a.c;
+  const int n = a.nslices * a.K;
+  const uint64_t* all = a.part_keys + row * n;
+  if (tid == 0) count = 0;
+  uint32_t most = 0;
+  for (int i = tid; i < n; i += NT) {
+    const uint32_t o = static_cast<uint32_t>(all[i] >> 32);
+    most = o > most ? o : most;
+  }
+  best[tid] = most;
+  __syncthreads();
+  if (tid < 64) {
+    const uint32_t t = kth_largest<NT, 32>(best, a.K);
+    if (tid == 0) bar = t;
+  }
+  __syncthreads();
+  LaneSum st = sum_none();
+  for (int i = tid; i < n; i += NT) {
+    const uint64_t key = all[i];
+    if (key != 0 && static_cast<uint32_t>(key >> 32) >= bar) keys[atomicAdd(&count, 1u)] = key;
+  }
+  for (int i = tid; i < a.nslices; i += NT) {
+    const float* p = a.part_sums + (row * a.nslices + i) * 2;
+    const SumStat both = sum_add(st, SumStat{p[0], p[1]}, c);
+    st.m = both.m;
+    st.s = both.s;
+    st.nmc = both.m > neg_inf() ? -(both.m * c) : 0.f;
+  }
+  __syncthreads();
+  const int m = static_cast<int>(count);
+  if (tid == 0 && (m & 1)) keys[m] = 0;
+  __syncthreads();
+  for (int i = tid; i < m; i += NT) {
+    const uint64_t key = keys[i];
+    const int r = rank_among(keys, m, key);
+    if (r < a.K) top[r] = key;
+  }
+  __syncthreads();
+  const int got = m < a.K ? m : a.K;
+  for (int i = tid; i < n && got > 0; i += NT) {
+    const uint64_t key = all[i];
+    if (key != 0 && key < top[got - 1]) sum_push1(st, key_value(key), c);
+  }
+  LaneSum of_list = sum_none();
+  for (int k = tid; k < got; k += NT) sum_push1(of_list, key_value(top[k]), c);
+  const SumStat rest = sum_block<NT>(st, c, sm[0]);
+  store_top<NT>(a, row, top, got, rest, sum_block<NT>(of_list, c, sm[1]));
+}
+
+// ---------------------------------------------------------------------------
+// beams
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t order_of64(double x) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double value_of64(uint64_t order) {
+  return __longlong_as_double(static_cast<long long>(order & 0x8000000000000000ull ? order ^ 0x8000000000000000ull : ~order));
+}
+
+struct Candidate {
+  uint64_t order;  // of its score
+  uint64_t place;  // beam << 32 | token
+};
+
+// One request: the lists of its beams' slices, scored and ranked.  Scores are
+// fp64 (sum_lse), so that within a beam they keep the order of its logits
+// whatever the size of the sum so far.
+template <int NT>
+__global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
+  extern __shared__ __attribute__((aligned(16))) Candidate cand[];  // W * nslices * K of them
+  __shared__ uint32_t best[NT];
+  __shared__ double gain[kMaxBeams];  // what a beam adds to z / tau; NaN: no continuation
+  __shared__ uint32_t count, bar;
+  const int tid = threadIdx.x;
+  const int64_t b = a.row0 + blockIdx.x;
+  const int W = a.W, N = a.K, per = a.nslices * N, n = W * per;
+  const float c = a.c;
+  if (tid == 0) count = 0;
+  // a wave a beam
+  for (int w = tid >> 6; w < W; w += NT / 64) {
+    const int64_t row = b * W + w;
+    double g = __builtin_nan("");
+    if (row_live(a, row)) {
+      LaneSum st = sum_none();
+      for (int i = tid & 63; i < a.nslices; i += 64) {
+        const float* p = a.part_sums + (row * a.nslices + i) * 2;
+        const SumStat both = sum_add(st, SumStat{p[0], p[1]}, c);
+        st.m = both.m;
+        st.s = both.s;
+      }
+      st.nmc = st.m > neg_inf() ? -(st.m * c) : 0.f;
+      for (int i = tid & 63; i < per; i += 64) {
+        const uint64_t key = a.part_keys[row * per + i];
+        if (key) sum_push1(st, key_value(key), c);
+      }
+      const SumStat whole = sum_merge<64>(st, c);
+      if (whole.s > 0.f && whole.s <= kLargest) g = static_cast<double>(a.beam_scores[row]) - sum_lse(whole, c, a.inv_tau);
+    }
+    if ((tid & 63) == 0) gain[w] = g;
+  }
+  __syncthreads();
+  // candidate i of beam i / per; 0: none
+  auto order_at = [&](int i, uint64_t& place) -> uint64_t {
+    const int w = i / per;
+    const int64_t row = b * W + w;
+    place = static_cast<uint64_t>(w) << 32;
+    if (a.finished && a.finished[row]) {
+      const float s = a.beam_scores[row];
+      place |= static_cast<uint32_t>(a.end_token);
+      return i == w * per && s >= -kLargest && s <= kLargest ? order_of64(s) : 0;
+    }
+    if (__builtin_isnan(gain[w])) return 0;
+    const uint64_t key = a.part_keys[b * n + i];
+    if (!key) return 0;
+    place |= static_cast<uint32_t>(key_col(key));
+    return order_of64(gain[w] + static_cast<double>(key_value(key)) * a.inv_tau);
+  };
+  uint32_t most = 0;
+  uint64_t place;
+  for (int i = tid; i < n; i += NT) {
+    const uint32_t o = static_cast<uint32_t>(order_at(i, place) >> 32);
+    most = o > most ? o : most;
+  }
+  best[tid] = most;
+  __syncthreads();
+  if (tid < 64) {
+    const uint32_t t = kth_largest<NT, 32>(best, N);
+    if (tid == 0) bar = t;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += NT) {
+    const uint64_t o = order_at(i, place);
+    if (o && static_cast<uint32_t>(o >> 32) >= bar) cand[atomicAdd(&count, 1u)] = Candidate{o, place};
+  }
+  __syncthreads();
+  const int m = static_cast<int>(count);
+  for (int i = tid; i < m; i += NT) {
+    const Candidate q = cand[i];
+    int r = 0;
+    for (int j = 0; j < m; ++j) {
+      const Candidate p = cand[j];
+      r += p.order > q.order || (p.order == q.order && p.place < q.place);
+    }
+    if (r < N) {
+      a.scores[b * N + r] = static_cast<float>(value_of64(q.order));
+      a.parents[b * N + r] = static_cast<int32_t>(q.place >> 32);
+      a.ids[b * N + r] = static_cast<int64_t>(q.place & 0xffffffffu);
+    }
+  }
+  for (int r = m + tid; r < N; r += NT) {
+    a.scores[b * N + r] = neg_inf();
+    a.parents[b * N + r] = -1;
+    a.ids[b * N + r] = -1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+constexpr int kShortNT = 256;
+
+int vector_columns(int dtype) { return dtype == 2 ? 4 : 8; }
+
+// Columns of a slice that k_top holds in registers whole.
+int short_slice(int dtype) { return 2 * kShortNT * vector_columns(dtype); }
+
+// Slices per row: one where there are rows for two workgroups a CU and more,
+// else as many as that takes, none shorter than what a workgroup holds in
+// registers, and no more keys than a join takes.
+void set_slices(TopArgs& a, int dtype) {
+  const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
+  const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
+  const int64_t least = short_slice(dtype);
+  int64_t n = (512 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  const int64_t most = (int64_t(a.V) + least - 1) / least;
+  n = n < most ? n : most;
+  n = n < most_keys ? n : most_keys;
+  a.slice = static_cast<int>(((int64_t(a.V) + n - 1) / n + 63) / 64 * 64);
+  a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
+}
+
+template <class Tr, int NT, int U, bool SHORT>
+hipError_t launch_top_nt(TopArgs a, hipStream_t s) {
+  // workgroups of a launch: far below 2^32 work-items whatever T
+  const int64_t rows_per = (int64_t(1) << 21) / a.nslices > 0 ? (int64_t(1) << 21) / a.nslices : 1;
+  for (int64_t r0 = 0; r0 < a.T; r0 += rows_per) {
+    const int64_t rows = a.T - r0 < rows_per ? a.T - r0 : rows_per;
+    a.row0 = r0;
+    TimedLaunch tl("k_top", s);
+    hipLaunchKernelGGL((k_top<Tr, NT, U, SHORT>), dim3(static_cast<unsigned>(rows * a.nslices)), dim3(NT), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// The K-th largest of the lanes' values cuts the better the more lanes there
+// are: with 512 of them and K = 64 a sample of 16384 values leaves 1 in 240 of
+// the row, of 152000 columns about 630 vectors.
+template <class Tr>
+hipError_t launch_top_t(const TopArgs& a, int dtype, hipStream_t s) {
+  constexpr int U = Tr::kBytes == 2 ? 4 : 8;
+  if (a.slice <= short_slice(dtype)) return launch_top_nt<Tr, kShortNT, 1, true>(a, s);
+  if (a.K > 64) return launch_top_nt<Tr, 1024, U, false>(a, s);
+  return launch_top_nt<Tr, 512, U, false>(a, s);
+}
+
+hipError_t launch_top_slices(int dtype, const TopArgs& a, hipStream_t s) {
+  switch (dtype) {
+    case 0: return launch_top_t<Bf16>(a, dtype, s);
+    case 1: return launch_top_t<Fp16>(a, dtype, s);
+    default: return launch_top_t<Fp32>(a, dtype, s);
+  }
+}
+
+}  // namespace
+
+// Keys of every slice, then their sums.
+static size_t part_bytes(const TopArgs& a, size_t* sums_off) {
+  const size_t per_row = size_t(a.nslices) * (size_t(a.K) * 8 + 8);
+  if (size_t(a.T) > (size_t(1) << 60) / per_row) return 0;
+  *sums_off = size_t(a.T) * a.nslices * a.K * 8;
+  return (size_t(a.T) * per_row + 255) / 256 * 256;
+}
+
+size_t top_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t K) {
+  TopArgs a{};
+  a.T = T;
+  a.V = static_cast<int>(V);
+  a.K = static_cast<int>(K);
+  set_slices(a, dtype);
+  size_t off;
+  return a.nslices == 1 ? 256 : part_bytes(a, &off);
+}
+
+size_t beam_workspace_bytes(int dtype, int64_t B, int64_t W, int64_t V, int64_t N) {
+  TopArgs a{};
+  a.T = B * W;
+  a.V = static_cast<int>(V);
+  a.K = static_cast<int>(N);
+  a.W = static_cast<int>(W);
+  set_slices(a, dtype);
+  size_t off;
+  return part_bytes(a, &off);
+}
+
+hipError_t launch_top_logits(int dtype, const TopArgs& args, char* ws, hipStream_t s) {
+  TopArgs a = args;
+  set_slices(a, dtype);
+  if (a.nslices == 1) return launch_top_slices(dtype, a, s);
+  size_t off = 0;
+  part_bytes(a, &off);
+  a.part_keys = reinterpret_cast<uint64_t*>(ws);
+  a.part_sums = reinterpret_cast<float*>(ws + off);
+  hipError_t e = launch_top_slices(dtype, a, s);
+  if (e != hipSuccess) return e;
+  const size_t lds = (size_t(a.nslices) * a.K + 1 + 1) / 2 * 2 * 8;
+  constexpr int64_t kRows = int64_t(1) << 21;
+  for (int64_t r0 = 0; r0 < a.T; r0 += kRows) {
+    const int64_t rows = a.T - r0 < kRows ? a.T - r0 : kRows;
+    a.row0 = r0;
+    TimedLaunch tl("k_top_join", s);
+    hipLaunchKernelGGL(k_top_join<256>, dim3(static_cast<unsigned>(rows)), dim3(256), lds, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_beam_select(int dtype, const TopArgs& args, int64_t B, char* ws, hipStream_t s) {
+  TopArgs a = args;
+  set_slices(a, dtype);
+  size_t off = 0;
+  part_bytes(a, &off);
+  a.part_keys = reinterpret_cast<uint64_t*>(ws);
+  a.part_sums = reinterpret_cast<float*>(ws + off);
+  hipError_t e = launch_top_slices(dtype, a, s);
+  if (e != hipSuccess) return e;
+  const size_t lds = size_t(a.W) * a.nslices * a.K * sizeof(Candidate);
+  constexpr int64_t kRows = int64_t(1) << 21;
+  for (int64_t r0 = 0; r0 < B; r0 += kRows) {
+    const int64_t rows = B - r0 < kRows ? B - r0 : kRows;
+    a.row0 = r0;
+    TimedLaunch tl("k_beam_join", s);
+    hipLaunchKernelGGL(k_beam_join<256>, dim3(static_cast<unsigned>(rows)), dim3(256), lds, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// states that follow their beams
+// ---------------------------------------------------------------------------
+
+// A workgroup takes a piece of one beam's row, reads it once and writes it to
+// every slot that goes on from that beam; beam W stands for slots whose parent
+// is none, which get zeros.  Vec: the widest type that every address and the
+// width are multiples of.
+template <class Vec, int U>
+__global__ void __launch_bounds__(256) k_beam_reorder(ReorderArgs a) {
+  constexpr int kPiece = 256 * U;
+  unsigned i = blockIdx.x;
+  const unsigned piece = i % a.pieces;
+  i /= a.pieces;
+  const int w = static_cast<int>(i % static_cast<unsigned>(a.W + 1));
+  i /= static_cast<unsigned>(a.W + 1);
+  i += a.seg0;  // request, then mid, then outer
+  const unsigned nb = static_cast<unsigned>(a.B), nm = static_cast<unsigned>(a.mid);
+  const int64_t b = i % nb, mid = i / nb % nm, outer = i / nb / nm;
+  const int32_t* parents = a.parents + b * a.N;
+  auto takes = [&](int p) { return w == a.W ? p < 0 || p >= a.W : p == w; };
+  bool any = false;
+  for (int k = threadIdx.x & 63; k < a.N; k += 64) any |= takes(parents[k]);
+  if (!__any(any)) return;
+  const int64_t width = a.width / static_cast<int64_t>(sizeof(Vec)), at = static_cast<int64_t>(piece) * kPiece + threadIdx.x;
+  const Vec* src = reinterpret_cast<const Vec*>(static_cast<const char*>(a.src) + outer * a.src_outer + mid * a.src_mid +
+                                                (b * a.W + (w < a.W ? w : 0)) * a.src_row);
+  Vec v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = w < a.W && at + u * 256 < width ? src[at + u * 256] : Vec{};
+  for (int k = 0; k < a.N; ++k) {
+    if (!takes(parents[k])) continue;
+    Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.dst) + outer * a.dst_outer + mid * a.dst_mid +
+                                      (b * a.N + k) * a.dst_row);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u * 256 < width) dst[at + u * 256] = v[u];
+  }
+}
+
+namespace {
+
+constexpr int kReorderU = 4;  // vectors a lane
+constexpr int64_t kReorderGroups = int64_t(1) << 23;  // workgroups of a launch: 2^31 work-items
+
+// Bytes of the widest type that every address, stride and the width allow.
+int64_t reorder_bytes(const ReorderArgs& a) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) |
+                       static_cast<uint64_t>(a.width | a.src_outer | a.src_mid | a.src_row | a.dst_outer | a.dst_mid | a.dst_row);
+  const int64_t low = static_cast<int64_t>(all & (~all + 1));
+  return low < 16 ? low : 16;
+}
+
+int64_t reorder_pieces(const ReorderArgs& a) {
+  const int64_t piece = reorder_bytes(a) * 256 * kReorderU;
+  return (a.width + piece - 1) / piece;
+}
+
+template <class Vec>
+hipError_t launch_reorder_t(ReorderArgs a, hipStream_t s) {
+  a.pieces = static_cast<unsigned>(reorder_pieces(a));
+  const int64_t per_seg = static_cast<int64_t>(a.pieces) * (a.W + 1), segs = a.B * a.mid * a.outer;
+  const int64_t most = kReorderGroups / per_seg;
+  for (int64_t s0 = 0; s0 < segs; s0 += most) {
+    const int64_t n = segs - s0 < most ? segs - s0 : most;
+    a.seg0 = static_cast<unsigned>(s0);
+    TimedLaunch tl("k_beam_reorder", s);
+    hipLaunchKernelGGL((k_beam_reorder<Vec, kReorderU>), dim3(static_cast<unsigned>(n * per_seg)), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+bool beam_reorder_fits(const ReorderArgs& a) { return reorder_pieces(a) <= kReorderGroups / (a.W + 1); }
+
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
+  switch (reorder_bytes(a)) {
+    case 16: return launch_reorder_t<u32x4>(a, s);
+    case 8: return launch_reorder_t<uint64_t>(a, s);
+    case 4: return launch_reorder_t<uint32_t>(a, s);
+    case 2: return launch_reorder_t<uint16_t>(a, s);
+    default: return launch_reorder_t<uint8_t>(a, s);
+  }
+}
+
+}  // namespace lp

@@ -512,6 +512,147 @@ lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The K largest logits of each scored row, 1 <= K <= min(V, LP_MAX_TOP), and what
+ * they weigh in softmax(z / temperature).
+ * ids      int64 [T x K]: columns from the largest value down, of equal values the
+ *          lowest column first.  Only columns that hold more than -inf are listed:
+ *          where they are fewer than K, what is left holds id -1 and log-prob -inf.
+ * logprob  fp32 [T x K]: their log-probs.
+ * rest     fp32 [T] or NULL: log of the mass of all other columns, summed by
+ *          itself (-inf where nothing is left).
+ * lse      fp32 [T] or NULL: log-sum-exp of the tempered row.
+ * Rows with mask[t] == 0 get ids -1 and 0 elsewhere.  A row that holds NaN or
+ * +inf, or only -inf, gets ids -1 and NaN in logprob and rest.  Finite values of any size count by
+ * how far they lie below the row's largest.
+ * The same bits on every call.
+ * workspace >= lp_top_workspace_bytes(dtype, T, V, K) bytes, 256-byte aligned;
+ * scratch only.  Outputs and workspace may overlap nothing.
+ */
+#define LP_MAX_TOP 256
+#define LP_MAX_BEAMS 64
+
+size_t lp_top_workspace_bytes(lp_dtype dtype, int64_t T, int64_t V, int64_t K);
+lp_status lp_top_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                        const uint8_t* mask, float temperature, int64_t* ids, float* logprob, float* rest,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: KL from a list of K entries a row
+ * (1 <= K <= LP_MAX_TOP), as lp_top_logits writes it, to softmax(z / temperature)
+ * of the student's whole row:
+ *   loss[t] = sum_k p_k (t_k - log q[id_k]) + r (t_rest - log q_rest),
+ *   p_k = exp(t_k), r = exp(t_rest), q_rest = the mass of the columns that no entry names.
+ * teacher_ids      int64 [T x K]; an id outside [0, V) is padding and is not read further.
+ *                  An id listed more than once counts with each of its entries.
+ * teacher_logprob  fp32 [T x K], natural logs at the teacher's temperature; an
+ *                  entry of -inf has no mass (its column still counts as named).
+ * teacher_rest     fp32 [T] or NULL: log of the mass outside the list; NULL: no such term.
+ *                  The masses need not sum to 1.
+ * loss             fp32 [T] (required).  +inf where the teacher has mass and the student none.
+ * lse, lse_rest    fp32 [T] or NULL: log-sum-exp of the tempered row, and over the
+ *                  columns that no entry names (-inf if there are none but -inf);
+ *                  saved for the backward.
+ * Rows with mask[t] == 0 get 0 everywhere.  Rows that hold NaN or +inf, or only -inf, give NaN.
+ * workspace >= lp_distill_top_workspace_bytes(dtype, T, V) bytes, 256-byte aligned; scratch only.
+ * Outputs and workspace may overlap nothing.
+ */
+size_t lp_distill_top_workspace_bytes(lp_dtype dtype, int64_t T, int64_t V);
+lp_status lp_distill_top(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                         const int64_t* teacher_ids, const float* teacher_logprob, const float* teacher_rest,
+                         const uint8_t* mask, float temperature, float* loss, float* lse, float* lse_rest,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of sum over scored rows of grad_loss[t] * loss[t] with respect to the
+ * student's raw logits.  With m = sum_k p_k + r and r_q = exp(lse_rest - lse):
+ *   grad_loss / temperature * (q_j m - masses of the entries that name j)       named columns,
+ *   grad_loss / temperature * exp(z_j / temperature - lse_rest) (m r_q - r)     all others.
+ * lse, lse_rest  fp32 [T] of the forward.
+ * grad_logits    [T x ld_grad] of `dtype`, rounded once, OVERWRITTEN (unscored rows
+ *                get 0; columns past V are left); may overlap no input.
+ * Probabilities are taken from lse and lse_rest, as in the calls under rules: rows with |lse| past
+ * 2^24 / log2(e) get gradient 0, and unnamed columns of rows with such an lse_rest.
+ * Needs no workspace.
+ */
+lp_status lp_distill_top_backward(const void* logits, lp_dtype dtype, int64_t T, int64_t V, int64_t ld, int64_t K,
+                                  const int64_t* teacher_ids, const float* teacher_logprob,
+                                  const float* teacher_rest, const uint8_t* mask, float temperature,
+                                  const float* lse, const float* lse_rest, const float* grad_loss,
+                                  void* grad_logits, int64_t ld_grad, void* stream);
+
+/*
+ * Beam search: the N best continuations of each of B requests over its W beams
+ * (1 <= W <= LP_MAX_BEAMS, 1 <= N <= LP_MAX_TOP, W N <= 4096) and V tokens, by
+ *   score = beam_scores[b][w] + log softmax(logits[b W + w] / temperature)[v].
+ * logits       [B W x ld] of `dtype`, after any rules (-inf: not allowed).
+ * beam_scores  fp32 [B x W].  A beam whose score is not finite goes on with nothing; its row is not read.
+ * finished     uint8 [B x W] or NULL: such a beam is one candidate as it stands, its
+ *              score and end_token (0 <= end_token < V); its row is not read.
+ * scores, parents, tokens   fp32, int32, int64 [B x N], the best first; of equal
+ *              scores the lowest beam and then the lowest token.  A token of logit -inf
+ *              is no candidate, nor is any of a row that holds NaN or +inf.  Places that no
+ *              candidate fills hold -inf, -1 and -1 (which lp_embedding and
+ *              lp_beam_reorder turn into zeros).
+ * Scores are compared in fp64, from log-sums of fp32 exponentials: candidates of
+ * different beams closer than about 1e-6 may come in either order.
+ * workspace >= lp_beam_workspace_bytes(dtype, B, W, V, N) bytes, 256-byte aligned; scratch only.
+ * Outputs and workspace may overlap nothing.
+ */
+size_t lp_beam_workspace_bytes(lp_dtype dtype, int64_t B, int64_t W, int64_t V, int64_t N);
+lp_status lp_beam_select(const void* logits, lp_dtype dtype, int64_t B, int64_t W, int64_t V, int64_t ld,
+                         const float* beam_scores, const uint8_t* finished, int64_t N, int64_t end_token,
+                         float temperature, float* scores, int32_t* parents, int64_t* tokens, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * States follow their beams: row b N + n of dst is row b W + parents[b][n] of src,
+ * zeros where that parent lies outside [0, W).  States of any type, by bytes:
+ * element (o, row, m) is `width` bytes at base + o * *_outer + row * *_row + m * *_mid,
+ * for outer values of o and mid values of m (a prefix of each row of a cache [layers x beams x
+ * heads x positions x width], say).  parents int32 [B x N], 1 <= W, N <= LP_MAX_TOP.
+ * Strides are bytes, not negative, nested in dst (a row's parts within a row, rows
+ * within one o).  src, dst and parents may not meet.
+ * Restrictions (LP_ERR_UNSUPPORTED): more than 2^31 - 1 of B x mid x outer; rows
+ * of which one takes more than 2^23 pieces of 1024 of the widest type that the
+ * strides allow, for all W + 1.
+ */
+lp_status lp_beam_reorder(const void* src, int64_t src_outer, int64_t src_row, int64_t src_mid, int64_t outer,
+                          int64_t mid, int64_t width, const int32_t* parents, int64_t B, int64_t W, int64_t N,
+                          void* dst, int64_t dst_outer, int64_t dst_row, int64_t dst_mid, void* stream);
+
+/*
+ * An output head in 8-bit floats (e4m3: 4 exponent and 3 mantissa bits, no
+ * infinities) with an fp32 scale for each block of 128 x 128:
+ *   weight[v][k] = scales[v / 128][k / 128] * q[v][k].
+ * q       uint8 [V x ld_q].  scales: fp32 [ceil(V / 128) x ld_scales], ld_scales >= ceil(h / 128).
+ * Restrictions (LP_ERR_UNSUPPORTED): h % 16 != 0, h > 2^20, ld_q % 16 != 0, ld_q > 2^23, q not 16-byte
+ *   aligned.
+ *
+ * lp_lm_head_fp8_quantize lays a head out: per block, scale = max(amax x (1 / 448), 2^-126)
+ * in fp32 operations, q = w / scale (fp32) rounded to nearest even.  weight [V x ld_w] of `dtype`;
+ * weight, q and scales may not overlap.  A NaN makes its row's logits NaN, an infinity those of
+ * all rows of its block.
+ */
+lp_status lp_lm_head_fp8_quantize(const void* weight, lp_dtype dtype, int64_t V, int64_t h, int64_t ld_w, void* q,
+                                  int64_t ld_q, float* scales, int64_t ld_scales, void* stream);
+
+/*
+ * out[t][v] = x[t] . weight[v] of such a head, x = the hidden row brought to
+ * e4m3 likewise, with a scale for each 128 of its columns.  Results are rounded once to out_dtype.
+ * Products and sums are fp32 where out_dtype is; where it has 16 bits, products are summed 8 at a
+ * time at 13 bits below the largest of them, which leaves about 2e-5 of a result.  hidden bf16 or fp16 [T x ld_h] (fp32:
+ * LP_ERR_UNSUPPORTED), out [T x ld_out] of out_dtype, columns past V left.
+ * A NaN or an infinity in a hidden row makes its logits NaN.
+ * workspace >= lp_lm_head_fp8_workspace_bytes(T, h, V) bytes (0: sizes not
+ * supported), 256-byte aligned; scratch only.  out and the workspace may overlap nothing.
+ */
+size_t lp_lm_head_fp8_workspace_bytes(int64_t T, int64_t h, int64_t V);
+lp_status lp_lm_head_fp8_logits(const void* hidden, lp_dtype dtype, int64_t T, int64_t h, int64_t ld_h, const void* q,
+                                int64_t ld_q, const float* scales, int64_t ld_scales, int64_t V, void* out,
+                                lp_dtype out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * Per-kernel timing (observability; not part of the method).  While enabled,
  * each library launch is bracketed by two HIP events recorded on its own
  * stream.  lp_timing_enable(1) clears earlier records and starts recording,

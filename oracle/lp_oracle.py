@@ -648,3 +648,168 @@ def w4_logits(hidden, q, scales, group):
     """hidden @ (scales * (q - 8))^T in fp64."""
     s = np.repeat(np.asarray(scales, dtype=np.float64), group, axis=1)[:, :np.asarray(q).shape[1]]
     return np.asarray(hidden, dtype=np.float64) @ ((np.asarray(q) - 8) * s).T
+
+
+# ---------------------------------------------------------------------------
+# the largest logits, distillation from them, beams, the 8-bit head
+# ---------------------------------------------------------------------------
+
+def _top_order(z):
+    """Columns of a row from the largest value down, equal ones from the lowest column up, without those at -inf."""
+    order = np.lexsort((np.arange(z.size), -z))
+    return order[z[order] > -np.inf]
+
+
+def top_logits(logits, K, mask, temperature):
+    """(ids, logprob [T, K], rest, lse [T]) of the K largest logits of each scored row."""
+    z = np.asarray(logits, dtype=np.float64)
+    T, V = z.shape
+    zt = tempered(z, temperature)
+    ids = np.full((T, K), -1, dtype=np.int64)
+    logprob, rest, lse = np.zeros((T, K)), np.zeros(T), np.zeros(T)
+    for t in range(T):
+        if mask is not None and not mask[t]:
+            continue
+        if np.isnan(z[t]).any() or (z[t] == np.inf).any() or not (z[t] > -np.inf).any():
+            logprob[t] = rest[t] = np.nan
+            lse[t] = -np.inf if not np.isnan(z[t]).any() and not (z[t] == np.inf).any() else np.nan
+            continue
+        at = _top_order(z[t])[:K]
+        lse[t] = log_normaliser(zt[t:t + 1])[0]
+        ids[t, :at.size] = at
+        logprob[t] = -np.inf
+        logprob[t, :at.size] = zt[t, at] - lse[t]
+        left = np.delete(zt[t], at)
+        left = left[left > -np.inf]
+        rest[t] = log_normaliser(left[None])[0] - lse[t] if left.size else -np.inf
+    return ids, logprob, rest, lse
+
+
+def _distill_parts(zt, ids, logprob, t):
+    """(entries inside the vocabulary, their masses, columns that no entry names) of row t."""
+    inside = (ids[t] >= 0) & (ids[t] < zt.shape[1])
+    other = np.ones(zt.shape[1], dtype=bool)
+    other[ids[t][inside]] = False
+    return ids[t][inside], np.asarray(logprob[t], dtype=np.float64)[inside], other
+
+
+def _lse1(x):
+    x = x[x > -np.inf]
+    return log_normaliser(x[None])[0] if x.size else -np.inf
+
+
+def distill_top(logits, ids, logprob, rest, mask, temperature):
+    """(loss, lse, lse_rest) of KL from a teacher's lists to the student's rows."""
+    zt = tempered(np.asarray(logits, dtype=np.float64), temperature)
+    T = zt.shape[0]
+    loss, lse, lse_rest = np.zeros(T), np.zeros(T), np.zeros(T)
+    for t in range(T):
+        if mask is not None and not mask[t]:
+            continue
+        at, lp, other = _distill_parts(zt, ids, logprob, t)
+        lse[t], lse_rest[t] = _lse1(zt[t]), _lse1(zt[t][other])
+        with np.errstate(invalid="ignore"):
+            for j, a in zip(at, lp):
+                if a > -np.inf:
+                    loss[t] += np.exp(a) * (a - (zt[t, j] - lse[t]))
+            if rest is not None and rest[t] > -np.inf:
+                loss[t] += np.exp(float(rest[t])) * (float(rest[t]) - (lse_rest[t] - lse[t]))
+    return loss, lse, lse_rest
+
+
+def distill_top_backward(logits, ids, logprob, rest, mask, temperature, grad_loss):
+    """Gradient of sum grad_loss * loss with respect to the raw logits."""
+    z = np.asarray(logits, dtype=np.float64)
+    zt = tempered(z, temperature)
+    tau = temperature if temperature_applies(temperature) else 1.0
+    d = np.zeros_like(z)
+    for t in range(z.shape[0]):
+        if mask is not None and not mask[t]:
+            continue
+        at, lp, other = _distill_parts(zt, ids, logprob, t)
+        p = np.exp(lp)
+        r = np.exp(float(rest[t])) if rest is not None else 0.0
+        lse, lse_rest = _lse1(zt[t]), _lse1(zt[t][other])
+        # d/dz of -sum p log q - r log q_rest: (P + r) q - p - r (the others' share of themselves)
+        row = (p.sum() + r) * np.exp(zt[t] - lse)
+        np.subtract.at(row, at, p)
+        if lse_rest > -np.inf:
+            row[other] -= r * np.exp(zt[t][other] - lse_rest)
+        d[t] = row * float(grad_loss[t]) / tau
+    return d
+
+
+def beam_select(logits, beam_scores, N, finished, end_token, temperature):
+    """(scores, parents, tokens [B, N]) of the best continuations over the beams of each request."""
+    zt = tempered(np.asarray(logits, dtype=np.float64), temperature)
+    B, W = np.asarray(beam_scores).shape
+    scores, parents = np.full((B, N), -np.inf), np.full((B, N), -1, dtype=np.int32)
+    tokens = np.full((B, N), -1, dtype=np.int64)
+    for b in range(B):
+        cand = []
+        for w in range(W):
+            s = float(beam_scores[b, w])
+            if not np.isfinite(s):
+                continue
+            if finished is not None and finished[b, w]:
+                cand.append((-s, w, end_token))
+                continue
+            row = zt[b * W + w]
+            if np.isnan(row).any() or (row == np.inf).any() or not (row > -np.inf).any():
+                continue
+            lse = _lse1(row)
+            cand += [(-(s + row[v] - lse), w, int(v)) for v in _top_order(row)[:N]]
+        for n, (s, w, v) in enumerate(sorted(cand)[:N]):
+            scores[b, n], parents[b, n], tokens[b, n] = -s, w, v
+    return scores, parents, tokens
+
+
+def beam_reorder(state, parents, dim):
+    """Rows of `state` along `dim` gathered by parents [B, N]; zeros where a parent is none."""
+    state = np.moveaxis(np.asarray(state), dim, 0)
+    B, N = parents.shape
+    W = state.shape[0] // B
+    out = np.zeros((B * N, *state.shape[1:]), dtype=state.dtype)
+    for b in range(B):
+        for n in range(N):
+            if 0 <= parents[b, n] < W:
+                out[b * N + n] = state[b * W + parents[b, n]]
+    return np.moveaxis(out, 0, dim)
+
+
+def e4m3(x):
+    """x rounded to the nearest e4m3 value, ties to even (values past 464 and NaN: NaN)."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        step = 2.0 ** (np.maximum(np.floor(np.log2(np.abs(np.where(x == 0, 1, x)))), -6.0) - 3.0)
+        q = np.rint(x / step) * step
+        return np.where(np.abs(q) <= 448.0, q, np.nan)
+
+
+def fp8_scale(amax):
+    """Scale of a block whose largest magnitude is amax, in fp32 operations."""
+    return np.maximum(np.asarray(amax, dtype=np.float32) * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126))
+
+
+def fp8_blocks(x32, rows):
+    """(q, scales fp32) of an fp32 matrix in blocks of `rows` x 128."""
+    x = np.asarray(x32, dtype=np.float32)
+    n, h = x.shape
+    q = np.zeros((n, h))
+    scales = np.zeros((-(-n // rows), -(-h // 128)), dtype=np.float32)
+    for i in range(scales.shape[0]):
+        for j in range(scales.shape[1]):
+            part = x[i * rows:(i + 1) * rows, j * 128:(j + 1) * 128]
+            scales[i, j] = fp8_scale(np.abs(part).max())
+            q[i * rows:(i + 1) * rows, j * 128:(j + 1) * 128] = e4m3(part / scales[i, j])
+    return q, scales
+
+
+def fp8_logits(hidden, q, scales):
+    """(logits, sum of the magnitudes of their terms) of hidden rows through an 8-bit head."""
+    h = np.asarray(hidden).shape[1]
+    x, sx = fp8_blocks(np.asarray(hidden, dtype=np.float32), 1)
+    x = x * np.repeat(sx.astype(np.float64), 128, axis=1)[:, :h]
+    w = np.asarray(q, dtype=np.float64) * np.repeat(np.repeat(np.asarray(scales, dtype=np.float64), 128, axis=0), 128,
+                                                    axis=1)[:np.asarray(q).shape[0], :h]
+    return x @ w.T, np.abs(x) @ np.abs(w).T
