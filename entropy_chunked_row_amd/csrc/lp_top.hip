@@ -5,19 +5,20 @@
 // A row is read once.  A workgroup owns a row, or a slice of one where rows are
 // few, and
 //   1. reads a first piece of it, spread over its whole length, and takes each
-//      lane's largest value: the K-th largest of these is no larger than the
-//      K-th largest of the row, so nothing below it can be chosen;
-//   2. streams the row.  Vectors of 16 bytes that hold a value at or above that
-//      threshold are kept in LDS, all others are folded into the softmax sums;
-//   3. repeats step 1 on the kept vectors, ranks what reaches the new threshold
-//      by counting, and adds what was not chosen to the sums.
-// So the mass outside the list is a sum of its own, never a difference of two
-// nearly equal ones.  Which lane holds which kept vector depends on the order of
-// LDS atomics; what is left of them is therefore summed exactly (sum_left), and
-// every result is the same bits on every call.  Order is (value descending, column ascending), as one
-// 64-bit key.  More kept vectors than LDS holds (rows that rise steadily, or have
-// most values equal) are counted by digits of the keys instead: right for any
-// row, several more reads of it.
+//      lane's largest value: the K-th largest of these, the floor, is no larger
+//      than the K-th largest of the row, so nothing below it can be chosen;
+//   2. streams the row.  Vectors of 16 bytes that hold a value at or above the
+//      floor are kept in LDS, all others are added to a sum of exponentials
+//      relative to the floor, which needs no running maximum.  The floor is taken
+//      anew after 1, 2, 4, 8 ... steps: of 152000 columns about 5 K vectors are kept;
+//   3. repeats step 1 on the kept vectors, ranks what reaches the new floor by
+//      counting, and sums what was not chosen.
+// Short slices are kept whole.  The mass outside the list is a sum of its own,
+// never a difference of two nearly equal ones.  Every result is the same bits on
+// every call: only the order of the keys that are ranked depends on LDS atomics.  Order is (value
+// descending, column ascending), as one 64-bit key.  More kept vectors than LDS
+// holds (rows that rise steadily, or have most values equal) are counted by digits
+// of the keys instead: right for any row, several more reads of it.
 #include "lp_internal.hpp"
 #include "lp_sums.hpp"
 
@@ -209,55 +210,33 @@ __device__ __forceinline__ void store_no_top(const TopArgs& a, int64_t row) {
   }
 }
 
-// The softmax sum of N values a lane, whichever lane holds which: exponentials
-// relative to the largest are brought to a grid of 2^-38, on which fp64 adds up
-// to 2^14 of them exactly.  spare: 2 NT / 64 doubles of LDS.
-template <int N, int NT>
-__device__ __forceinline__ SumStat sum_left(const float* x, float c, double* spare) {
-  static_assert(N * NT <= 1 << 14, "sums up to 2^14 on a grid of 2^-38 take 52 bits");
-  constexpr int W = NT / 64;
-  auto most = [](float p, float q) { return fmaxf(p, q); };
-  float* tops = reinterpret_cast<float*>(spare);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float m = lanes_reduce<64>(largest_of<N>(x), most);
-  if (lane == 0) tops[wave] = m;
-  __syncthreads();
-  m = lanes_reduce<W>(tops[lane & (W - 1)], most);
-  constexpr double kGrid = 16384.0;  // 2^14: what is added to it is rounded to its ulp, 2^-38
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const double e = fast_exp2(sum_exponent(x[i], m, c));
-    sum += (e + kGrid) - kGrid;
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  if (lane == 0) spare[W + wave] = sum;
-  __syncthreads();
-  sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) sum += spare[W + w];
-  return SumStat{m, static_cast<float>(sum)};
-}
-
 // Whether row `row` takes part: scored, or of a beam that goes on.
 __device__ __forceinline__ bool row_live(const TopArgs& a, int64_t row) {
   if (a.beam_scores) return a.beam_scores[row] >= -kLargest && a.beam_scores[row] <= kLargest && !(a.finished && a.finished[row]);
   return !(a.mask && a.mask[row] == 0);
 }
 
-// SHORT: the slice is at most two vectors a lane, all of which are "kept".
-template <class Tr, int NT, int U, bool SHORT>
+// Kept vectors a lane: of a slice kept whole (SHORT) 4.  Of a stream with 256
+// threads (K up to 64) 192 a wave, twice what is expected, so that seven
+// workgroups fit a CU; with 512 (K up to 256) 256, of which 170 are expected.
+template <int NT, bool SHORT>
+constexpr int kHeld = SHORT || NT > 256 ? 4 : 3;
+constexpr int kFewTop = 64;  // most K of the first of these
+
+// SHORT: the slice is at most kHeld vectors a lane, all of which are kept.
+template <class Tr, int NT, bool SHORT>
 __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
-  constexpr int P = Tr::kPerVec, W = NT / 64, kKept = 2 * NT, kKeys = 2 * kKept;
-  __shared__ u32x4 kept[kKept];  // later the keys that are ranked
+  constexpr int P = Tr::kPerVec, U = 4, W = NT / 64, kLane = kHeld<NT, SHORT>, kKept = kLane * NT, kWave = kKept / W, kKeys = 2 * NT, kWords = 2 * NT;
+  __shared__ u32x4 kept[kKept];
   __shared__ uint32_t kept_at[SHORT ? 1 : kKept];
-  constexpr int kWords = SHORT ? 2 * NT : NT;
-  __shared__ uint32_t best[kWords > 258 ? kWords : 258];
-  __shared__ uint64_t top[kMaxTop];
+  __shared__ __attribute__((aligned(16))) uint64_t keys[kKeys];
+  __shared__ uint32_t best[kWords];  // later the digits' counts
+  __shared__ uint64_t top[SHORT || NT > 256 ? kMaxTop : kFewTop];
   __shared__ SumStat sm[2][W];
-  __shared__ uint32_t counts[2], bar;
-  __shared__ double spare[2 * W];
+  __shared__ float far_down[W];
+  __shared__ uint32_t count, bar;
+  __shared__ int held_by[W];
+  static_assert(kWords >= 258, "digits' counts");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const unsigned rel_row = blockIdx.x / static_cast<unsigned>(a.nslices);
   const int slice = static_cast<int>(blockIdx.x - rel_row * static_cast<unsigned>(a.nslices));
@@ -270,133 +249,154 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   const int n = a.V - c0 < a.slice ? a.V - c0 : a.slice;
   const char* xp = static_cast<const char*>(a.x) + (row * a.ld + c0) * Tr::kBytes;
   const float c = a.c;
-  LaneSum st = sum_none();
-  u32x4 mine[2];  // kept vectors of this lane, and their numbers
-  int at[2];
-  bool digits = false;
-  if (tid < 2) counts[tid] = 0;
+  if (tid == 0) count = 0;  // read behind the barriers of take_floor
+  auto word = [](float x) { return x > neg_inf() ? order_of(x) : 0u; };
+  // the floor that `best` gives, in every lane
+  auto take_floor = [&](auto words) {
+    __syncthreads();
+    if (wave == 0) {
+      const uint32_t t = kth_largest<decltype(words)::value, kOrderBits<Tr>>(best, a.K);
+      if (lane == 0) bar = t;
+    }
+    __syncthreads();
+    return threshold_of(bar);
+  };
 
+  SumStat low{neg_inf(), 0.f};  // of what was streamed and not kept: this lane's
+  float lost = neg_inf();       // its largest value
+  bool digits = false;
   if (SHORT) {
     const int vectors = (n + P - 1) / P;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      at[i] = tid + i * NT;
-      mine[i] = at[i] < vectors ? row_vector<Tr>(xp, at[i], n) : no_vector<Tr>();
+    for (int i = 0; i < kLane; ++i) {
+      const int v = tid + i * NT;
+      if (v < vectors) kept[v] = row_vector<Tr>(xp, v, n);
     }
   } else {
-    // Lane's vectors: U pieces of the row a wave, `steps` times 64 vectors each,
-    // so that one step of the workgroup is a sample of the whole row.
+    // The slice in U W pieces of `steps` times 64 vectors, so that one step of the
+    // workgroup is a sample of the whole; a wave goes from piece to piece, so that
+    // each has its share of a piece that holds more of what is kept.
     const int vectors = n / P, steps = (vectors + 64 * U * W - 1) / (64 * U * W);
-    uint32_t v0[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v0[u] = static_cast<uint32_t>((wave * U + u) * steps * 64 + lane);
+    auto number = [&](int u, int q) { return static_cast<uint32_t>(((u * W + ((wave + q) & (W - 1))) * steps + q) * 64 + lane); };
+    // A number past the slice loads its last vector, and is left out of everything.
+    auto there = [&](uint32_t v) { return v < static_cast<uint32_t>(vectors); };
     auto load = [&](uint32_t v) {
-      return v < static_cast<uint32_t>(vectors)
-                 ? static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xp + size_t(v) * 16)))
-                 : no_vector<Tr>();
+      const uint32_t at = v < static_cast<uint32_t>(vectors) ? v : vectors - 1;
+      return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xp + size_t(at) * 16)));
+    };
+    int held = 0;  // vectors that this wave has kept
+    auto keep = [&](bool on, u32x4 vec, uint32_t v) {
+      const uint64_t mask = __ballot(on);
+      if (mask) {
+        const int k = held + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0)));
+        if (on && k < kWave) {
+          kept[wave * kWave + k] = vec;
+          kept_at[wave * kWave + k] = v;
+        }
+        held += __popcll(mask);
+      }
     };
     u32x4 w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = load(v0[u]);
-    {
-      float vm = neg_inf();
+    for (int u = 0; u < U; ++u) w[u] = load(number(u, 0));
+    float high = neg_inf();  // the lane's largest value so far that was kept (`lost`: that was not)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[P];
+      Tr::unpack(w[u], x);
+      if (there(number(u, 0))) high = fmaxf(high, largest_of<P>(x));
+    }
+    best[tid] = word(high);
+    float floor = take_floor(std::integral_constant<int, NT>{});
+    // Exponents are relative to the floor.  With the lowest floor every finite value
+    // is kept and the others' exponents only have to be -inf or NaN.  Floors far
+    // from 0 otherwise (finite masks in all but a few columns) are left to the digits.
+    float fc = floor > -kLargest ? floor * c : 0.f;
+    digits = !is_near(fc);
+    for (int q = 0; !digits;) {
+      float t[U * P];
+      bool low_one[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float x[P];
-        Tr::unpack(w[u], x);
-        vm = fmaxf(vm, largest_of<P>(x));
+        const uint32_t v = number(u, q);
+        Tr::unpack(w[u], t + u * P);
+        const float m = largest_of<P>(t + u * P);
+        const bool hit = m >= floor && there(v);
+        low_one[u] = !hit && there(v);
+        lost = fmaxf(lost, low_one[u] ? m : neg_inf());
+        high = fmaxf(high, hit ? m : neg_inf());
+        keep(hit, w[u], v);
       }
-      best[tid] = vm > neg_inf() ? order_of(vm) : 0u;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const uint32_t t = kth_largest<NT, kOrderBits<Tr>>(best, a.K);
-      if (lane == 0) bar = t;
-    }
-    __syncthreads();
-    const float floor = threshold_of(bar);
-    auto keep = [&](u32x4 vec, uint32_t v) {
-      const uint32_t k = atomicAdd(counts, 1u);
-      if (k < static_cast<uint32_t>(kKept)) {
-        kept[k] = vec;
-        kept_at[k] = v;
+      const bool last = ++q == steps;
+      if (!last) {  // in flight while the exponentials are taken
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = load(number(u, q));
       }
-    };
-    for (int q = 0;;) {
-      float x[U * P], vm = neg_inf();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        Tr::unpack(w[u], x + u * P);
-        const float m = largest_of<P>(x + u * P);
-        if (m >= floor) {
-          keep(w[u], v0[u] + q * 64);
+        float ps = 0.f;
 #pragma unroll
-          for (int k = 0; k < P; ++k) x[u * P + k] = neg_inf();
-        } else {
-          vm = fmaxf(vm, m);
-        }
+        for (int k = 0; k < P; ++k) ps += fast_exp2(fmaf(t[u * P + k], c, -fc));
+        low.s += low_one[u] ? ps : 0.f;
       }
-      if (++q == steps) {
-        sum_push<U * P, P>(st, x, vm, c);
-        break;
+      if (last) break;
+      if ((q & (q - 1)) == 0) {
+        best[tid] = word(fmaxf(high, lost));
+        const float was = floor;
+        floor = take_floor(std::integral_constant<int, NT>{});
+        fc = floor > -kLargest ? floor * c : 0.f;
+        digits = !is_near(fc);
+        low.s *= fast_exp2(stat_shift(was, floor, c));
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = load(v0[u] + q * 64);
-      sum_push<U * P, P>(st, x, vm, c);
     }
-    if (tid == 0 && vectors * P < n) keep(row_vector<Tr>(xp, vectors, n), vectors);
+    low.m = floor;
+    if (wave == 0) keep(lane == 0 && vectors * P < n, row_vector<Tr>(xp, vectors, n), vectors);
+    if (lane == 0) held_by[wave] = held;
     __syncthreads();
-    const uint32_t m = counts[0];
-    digits = m > static_cast<uint32_t>(kKept);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t k = tid + i * NT;
-      const bool on = !digits && k < m;
-      mine[i] = on ? kept[k] : no_vector<Tr>();
-      at[i] = on ? static_cast<int>(kept_at[k]) : 0;
-    }
+    for (int i = 0; i < W; ++i) digits |= held_by[i] > kWave;
   }
 
+  // The kept vectors of this lane, f(values, number of the vector, whether it is
+  // an odd one of the lane's).
+  auto each_kept = [&](auto f) {
+    const int m = SHORT ? (n + P - 1) / P : held_by[wave];
+    for (int k = SHORT ? tid : lane; k < m; k += SHORT ? NT : 64) {
+      const int at = SHORT ? k : wave * kWave + k;
+      float x[P];
+      Tr::unpack(kept[at], x);
+      f(x, SHORT ? k : static_cast<int>(kept_at[at]), (SHORT ? k / NT & 1 : k / 64 & 1) != 0);
+    }
+  };
   int got = 0;
-  SumStat left{neg_inf(), 0.f};  // of the kept vectors, what is not chosen
-  uint64_t* keys = reinterpret_cast<uint64_t*>(kept);
+  LaneSum st = sum_none();
   if (!digits) {
-    float x[2 * P];
+    // Two words a lane, of every other vector; of the halves of its vector where
+    // no lane has two: with fewer words than K nothing could be left out.
+    const bool halves = SHORT ? n <= NT * P : held_by[wave] <= 64;
+    float even = neg_inf(), odd = neg_inf();
+    each_kept([&](const float* x, int, bool second) {
+      const float lo = largest_of<P / 2>(x), hi = largest_of<P / 2>(x + P / 2);
+      even = fmaxf(even, halves ? lo : second ? neg_inf() : fmaxf(lo, hi));
+      odd = fmaxf(odd, halves ? hi : second ? fmaxf(lo, hi) : neg_inf());
+    });
+    best[tid] = word(even);
+    best[NT + tid] = word(odd);
+    const float floor = take_floor(std::integral_constant<int, kWords>{});
+    each_kept([&](const float* x, int v, bool) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) Tr::unpack(mine[i], x + i * P);
-    if (SHORT) {
-      // of each vector, or of its halves where no lane has a second one: with
-      // fewer words than K nothing could be left out
-      const bool halves = n <= NT * P;
-      const float m0 = largest_of<P>(x), m1 = largest_of<P>(x + P);
-      const float h0 = largest_of<P / 2>(x), h1 = largest_of<P / 2>(x + P / 2);
-      const float lo = halves ? h0 : m0, hi = halves ? h1 : m1;
-      best[tid] = lo > neg_inf() ? order_of(lo) : 0u;
-      best[kWords - NT + tid] = hi > neg_inf() ? order_of(hi) : 0u;
-    } else {
-      const float vm = largest_of<2 * P>(x);
-      best[tid] = vm > neg_inf() ? order_of(vm) : 0u;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const uint32_t t = kth_largest<kWords, kOrderBits<Tr>>(best, a.K);
-      if (lane == 0) bar = t;
-    }
-    __syncthreads();
-    const float floor = threshold_of(bar);
-    auto key_at = [&](int i) { return key_of(x[i], c0 + at[i / P] * P + i % P); };
-#pragma unroll
-    for (int i = 0; i < 2 * P; ++i) {
-      if (x[i] >= floor) {
-        const uint32_t k = atomicAdd(counts + 1, 1u);
-        if (k < static_cast<uint32_t>(kKeys)) keys[k] = key_at(i);
+      for (int i = 0; i < P; ++i) {
+        if (x[i] >= floor) {
+          const uint32_t k = atomicAdd(&count, 1u);
+          if (k < static_cast<uint32_t>(kKeys)) keys[k] = key_of(x[i], c0 + v * P + i);
+        }
       }
-    }
+    });
     __syncthreads();
-    const int m = static_cast<int>(counts[1]);
-    if (m > kKeys) {
-      digits = true;
-    } else {
+    const int m = static_cast<int>(count);
+    digits = m > kKeys;
+    if (!digits) {
       if (tid == 0 && (m & 1)) keys[m] = 0;
       __syncthreads();
       for (int i = tid; i < m; i += NT) {
@@ -406,13 +406,14 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
       }
       got = m < a.K ? m : a.K;
       __syncthreads();
-      if (got > 0) {
-        const uint64_t least = top[got - 1];
+      // what is left of the kept vectors
+      const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+      each_kept([&](float* x, int v, bool) {
 #pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          if (x[i] >= floor && key_at(i) >= least) x[i] = neg_inf();
-      }
-      left = sum_left<2 * P, NT>(x, c, spare);
+        for (int i = 0; i < P; ++i)
+          if (x[i] >= floor && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
+        sum_push<P, P>(st, x, largest_of<P>(x), c);
+      });
     }
   }
   if (digits) {  // the same for the whole workgroup
@@ -423,8 +424,30 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
     __syncthreads();
     for (int i = tid; i < got; i += NT) top[rank_among(keys, got, keys[i])] = keys[i];
   }
+  SumStat rest = sum_block<NT>(SHORT || digits ? st : sum_add(low, st, c), c, sm[0]);
+  if (!SHORT && !digits) {
+    auto most = [](float p, float q) { return fmaxf(p, q); };
+    lost = lanes_reduce<64>(lost, most);
+    if (lane == 0) far_down[wave] = lost;
+    __syncthreads();
+    lost = lanes_reduce<W>(far_down[lane & (W - 1)], most);
+    // What lies more than 126 octaves below the floor was added as 0.  Where that
+    // is not small beside what is left, the rest is summed once more.
+    if (lost > neg_inf() && rest.m <= low.m && !(rest.s * fast_exp2(stat_shift(rest.m, low.m, c)) >= 8.5e-22f)) {
+      const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+      st = sum_none();
+      for (int v = tid; v * P < n; v += NT) {
+        float x[P];
+        Tr::unpack(row_vector<Tr>(xp, v, n), x);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (x[i] >= -kLargest && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
+        sum_push<P, P>(st, x, largest_of<P>(x), c);
+      }
+      rest = sum_block<NT>(st, c, sm[0]);
+    }
+  }
   __syncthreads();
-  const SumStat rest = sum_add(sum_block<NT>(st, c, sm[0]), left, c);
   if (a.part_keys) {
     const int64_t part = row * a.nslices + slice;
     for (int k = tid; k < a.K; k += NT) a.part_keys[part * a.K + k] = k < got ? top[k] : 0;
@@ -619,17 +642,17 @@ constexpr int kShortNT = 256;
 
 int vector_columns(int dtype) { return dtype == 2 ? 4 : 8; }
 
-// Columns of a slice that k_top holds in registers whole.
-int short_slice(int dtype) { return 2 * kShortNT * vector_columns(dtype); }
+// Columns of a slice that k_top keeps whole.
+int short_slice(int dtype) { return kHeld<kShortNT, true> * kShortNT * vector_columns(dtype); }
 
-// Slices per row: one where there are rows for two workgroups a CU and more,
-// else as many as that takes, none shorter than what a workgroup holds in
-// registers, and no more keys than a join takes.
+// Slices per row: one where there are rows for four workgroups a CU and more,
+// else as many as that takes, none shorter than what a workgroup keeps
+// whole, and no more keys than a join takes.
 void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
   const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
   const int64_t least = short_slice(dtype);
-  int64_t n = (512 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  int64_t n = (1024 + a.T - 1) / (a.T > 0 ? a.T : 1);
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
   n = n < most_keys ? n : most_keys;
@@ -637,7 +660,7 @@ void set_slices(TopArgs& a, int dtype) {
   a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
 }
 
-template <class Tr, int NT, int U, bool SHORT>
+template <class Tr, int NT, bool SHORT>
 hipError_t launch_top_nt(TopArgs a, hipStream_t s) {
   // workgroups of a launch: far below 2^32 work-items whatever T
   const int64_t rows_per = (int64_t(1) << 21) / a.nslices > 0 ? (int64_t(1) << 21) / a.nslices : 1;
@@ -645,22 +668,19 @@ hipError_t launch_top_nt(TopArgs a, hipStream_t s) {
     const int64_t rows = a.T - r0 < rows_per ? a.T - r0 : rows_per;
     a.row0 = r0;
     TimedLaunch tl("k_top", s);
-    hipLaunchKernelGGL((k_top<Tr, NT, U, SHORT>), dim3(static_cast<unsigned>(rows * a.nslices)), dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((k_top<Tr, NT, SHORT>), dim3(static_cast<unsigned>(rows * a.nslices)), dim3(NT), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-// The K-th largest of the lanes' values cuts the better the more lanes there
-// are: with 512 of them and K = 64 a sample of 16384 values leaves 1 in 240 of
-// the row, of 152000 columns about 630 vectors.
 template <class Tr>
 hipError_t launch_top_t(const TopArgs& a, int dtype, hipStream_t s) {
-  constexpr int U = Tr::kBytes == 2 ? 4 : 8;
-  if (a.slice <= short_slice(dtype)) return launch_top_nt<Tr, kShortNT, 1, true>(a, s);
-  if (a.K > 64) return launch_top_nt<Tr, 1024, U, false>(a, s);
-  return launch_top_nt<Tr, 512, U, false>(a, s);
+  if (a.slice <= short_slice(dtype)) return launch_top_nt<Tr, kShortNT, true>(a, s);
+  // the K-th largest of the lanes' values cuts the better the more lanes there are
+  if (a.K > kFewTop) return launch_top_nt<Tr, 512, false>(a, s);
+  return launch_top_nt<Tr, 256, false>(a, s);
 }
 
 hipError_t launch_top_slices(int dtype, const TopArgs& a, hipStream_t s) {
