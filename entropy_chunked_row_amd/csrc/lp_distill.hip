@@ -11,13 +11,12 @@
 // (q_j m - r w_j, of which neither part can overflow this way).
 //
 // A row is read once.  The listed columns lie in at most K of its 16-byte
-// vectors.  A lane streams vectors tid, tid + NT, ... of its slice, at most 64
-// of them, so which of its own are listed fits one 64-bit word, set in LDS
-// before the stream: a vector costs one bit test.  Listed vectors are left out
-// of the stream; each is taken by the first entry that lies in it, which looks
-// through the list for the others: so an id listed twice counts once in the
-// sums and with both its masses in the gradient, in a fixed order, and the sum over
-// unlisted columns is a sum of its own.
+// vectors.  A lane streams vectors tid, tid + NT, ... of its slice; which of its own are
+// listed is a bit each in LDS, 32 to a word, so a vector costs one bit test.
+// Listed vectors are left out of the stream; each is taken by the first entry that lies
+// in it, which looks through the list for the others: so an id listed twice counts
+// once in the sums and with both its masses in the gradient, in a fixed order, and
+// the sum over unlisted columns is a sum of its own.
 #include "lp_internal.hpp"
 #include "lp_sums.hpp"
 
@@ -26,6 +25,8 @@ namespace lp {
 namespace {
 
 constexpr int kMinDistillSlice = 2048;
+constexpr int kNoCol = 0x7fffffff;
+constexpr int kMaskWords = 8;  // of 32 of a lane's vectors each: the longest slice
 
 // Where a slice's vectors lie: vector v holds columns v P - pad .. + P, those
 // outside [0, n) missing at either end.  The gradient takes pad from its output,
@@ -67,30 +68,43 @@ __device__ __forceinline__ double lanes_sum(double x) {
   return x;
 }
 
-// By one wave: the outputs of a row from the states of its unlisted and its
-// listed columns.  The loss is a difference of nearly equal numbers: fp64.
+// What the listed entries add to a row's loss before its log-sum-exps are known:
+//   loss = terms + mass lse + r (t_rest - (lse_rest - lse)).
+// The loss is a difference of nearly equal numbers: fp64.
+struct Entries {
+  double terms, mass;  // sums of p_k (t_k - z_k / tau) and of p_k
+};
+
+// By one wave, in every lane of it.
 template <class Tr>
-__device__ void store_loss(const DistillArgs& a, int64_t row, SumStat rest, SumStat listed) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ Entries sum_entries(const DistillArgs& a, int64_t row) {
   const char* xp = static_cast<const char*>(a.x) + row * a.ld * Tr::kBytes;
+  Entries e{0.0, 0.0};
+  for (int k = threadIdx.x & 63; k < a.K; k += 64) {
+    const int64_t id = a.ids[row * a.K + k];
+    const float t = a.logprob[row * a.K + k];
+    if (id < 0 || id >= a.V || t == neg_inf()) continue;  // padding, or no mass
+    const double p = exp(static_cast<double>(t));
+    e.terms += p * (static_cast<double>(t) - static_cast<double>(Tr::load1(xp, id)) * a.inv_tau);
+    e.mass += p;
+  }
+  e.terms = lanes_sum(e.terms);
+  e.mass = lanes_sum(e.mass);
+  return e;
+}
+
+// By one thread: the outputs of a row from the states of its unlisted and its
+// listed columns.
+__device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, Entries e, float t_rest, SumStat rest,
+                                           SumStat listed) {
   const double lse = sum_lse(sum_add(rest, listed, a.c), a.c, a.inv_tau);
   const double lse_rest = sum_lse(rest, a.c, a.inv_tau);
-  double sum = 0.0;
-  for (int k = lane; k < a.K; k += 64) {
-    const int64_t id = a.ids[row * a.K + k];
-    if (id < 0 || id >= a.V) continue;
-    const float t = a.logprob[row * a.K + k];
-    if (t == neg_inf()) continue;  // no mass
-    const double logq = static_cast<double>(Tr::load1(xp, id)) * a.inv_tau - lse;
-    sum += exp(static_cast<double>(t)) * (static_cast<double>(t) - logq);
+  double loss = e.terms + e.mass * lse;
+  if (t_rest != neg_inf()) {
+    const double t = t_rest;
+    loss += exp(t) * (t - (lse_rest - lse));
   }
-  sum = lanes_sum(sum);
-  if (lane != 0) return;
-  if (a.rest && a.rest[row] != neg_inf()) {
-    const double t = a.rest[row];
-    sum += exp(t) * (t - (lse_rest - lse));
-  }
-  a.loss[row] = static_cast<float>(sum);
+  a.loss[row] = static_cast<float>(loss);
   if (a.lse_out) a.lse_out[row] = static_cast<float>(lse);
   if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(lse_rest);
 }
@@ -105,7 +119,6 @@ __device__ __forceinline__ void store_no_loss(const DistillArgs& a, int64_t row)
 // others exp2(z c + nr) others.
 struct GradRow {
   float nl, all, gt, nr, others;
-  int zero;  // nothing is left of the probabilities: the row's gradient is 0
 };
 
 // |lse| up to which fp32 says anything of exp(z - lse)
@@ -114,14 +127,15 @@ constexpr float kFarLse = kFar * kLn2;
 template <class Tr, int NT, int U, bool GRAD>
 __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   constexpr int P = Tr::kPerVec, W = NT / 64;
-  __shared__ int cols[kMaxTop];  // column of the slice that an entry names, or -1
+  static_assert(32 % U == 0, "a group's bits lie in one word");
+  __shared__ __attribute__((aligned(16))) int cols[kMaxTop];  // of every entry
   __shared__ float mass[GRAD ? kMaxTop : 1];
-  __shared__ unsigned long long held[NT];
+  __shared__ uint32_t held[kMaskWords][NT];
   __shared__ SumStat sm[2][W];
-  __shared__ GradRow shared_row;
+  __shared__ Entries parts[W];  // of the entries of each wave's threads
   const int tid = threadIdx.x;
-  const unsigned rel_row = blockIdx.x / static_cast<unsigned>(a.nslices);
-  const int slice = static_cast<int>(blockIdx.x - rel_row * static_cast<unsigned>(a.nslices));
+  const unsigned block = spread_block(), rel_row = block / static_cast<unsigned>(a.nslices);
+  const int slice = static_cast<int>(block - rel_row * static_cast<unsigned>(a.nslices));
   const int64_t row = a.row0 + rel_row;
   const int c0 = slice * a.slice;
   const char* xp = static_cast<const char*>(a.x) + (row * a.ld + c0) * Tr::kBytes;
@@ -144,101 +158,134 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     return;
   }
 
-  held[tid] = 0;
+  const int whole_end = vs.whole_end(), first = vs.first();
+  const int steps = (vs.end() + NT - 1) / NT;
+  const char* base = xp - vs.pad * Tr::kBytes;  // 32-bit offsets: a slice is far shorter
+  // U vectors at a time, unconditionally: those outside read one inside
+  auto load = [&](int v) {
+    const int at = min(max(v, first), whole_end - 1);
+    return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(base + static_cast<uint32_t>(at) * 16u)));
+  };
+  // Thread k has entry k (and k + NT).  What follows from its id is under way
+  // before anything waits: the vector it lies in, its logit, the first vectors of
+  // the stream, the row's scalars.
+  constexpr int E = (kMaxTop + NT - 1) / NT;
+  int64_t id[E];
+  float t[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int k = tid + i * NT;
+    id[i] = k < a.K ? a.ids[row * a.K + k] : -1;
+    t[i] = k < a.K ? a.logprob[row * a.K + k] : neg_inf();
+  }
+  const float t_rest = a.rest ? a.rest[row] : neg_inf();
+  const float lse = GRAD ? a.lse[row] : 0.f, lse_rest = GRAD ? a.lse_rest[row] : 0.f, g_loss = GRAD ? a.grad_loss[row] : 0.f;
+  u32x4 w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = whole_end > first ? load(tid + u * NT) : no_vector<Tr>();
+  for (int i = 0; i * 32 < steps; ++i) held[i][tid] = 0;
   __syncthreads();
-  if (tid < 64) {
-    double all = 0.0;
-    for (int k = tid; k < a.K; k += 64) {
-      const int64_t id = a.ids[row * a.K + k], rel = id - c0;
-      const bool inside = id >= 0 && id < a.V, here = rel >= 0 && rel < vs.n;
-      cols[k] = here ? static_cast<int>(rel) : -1;
-      if (GRAD) {
-        const double p = inside ? exp(static_cast<double>(a.logprob[row * a.K + k])) : 0.0;
-        all += p;
-        mass[k] = static_cast<float>(p);
-      }
-      if (here) {
-        const int v = (static_cast<int>(rel) + vs.pad) / P;
-        atomicOr(held + v % NT, 1ull << (v / NT));
-      }
+  u32x4 in[E];  // the vector that the entry lies in
+  float z[E];
+  int col[E];  // on the grid of vectors, or outside
+  Entries e{0.0, 0.0};
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int k = tid + i * NT;
+    const int64_t rel = id[i] - c0;
+    const bool inside = id[i] >= 0 && id[i] < a.V, here = rel >= 0 && rel < vs.n;
+    col[i] = here ? static_cast<int>(rel) + vs.pad : kNoCol;
+    if (here) {
+      const int v = col[i] / P;
+      in[i] = vs.load(xp, v);
+      atomicOr(&held[v / (32 * NT)][v % NT], 1u << (v / NT % 32));
     }
-    if (GRAD) {
-      all = lanes_sum(all);
-      const double r = a.rest ? exp(static_cast<double>(a.rest[row])) : 0.0;
-      const double g = static_cast<double>(a.grad_loss[row]) * a.inv_tau;
-      const float lse = a.lse[row], lse_rest = a.lse_rest[row];
-      all += r;
-      GradRow q;
-      q.zero = fabsf(lse) > kFarLse;
-      q.nl = -lse * kLog2e;
-      q.all = static_cast<float>(all * g);
-      q.gt = static_cast<float>(g);
-      // with no weight outside the list, or none that fp32 tells apart, those columns get 0
-      const bool none = fabsf(lse_rest) > kFarLse;
-      q.nr = none ? neg_inf() : -lse_rest * kLog2e;
-      q.others = none ? 0.f : static_cast<float>((all * exp(static_cast<double>(lse_rest) - static_cast<double>(lse)) - r) * g);
-      if (tid == 0) shared_row = q;
+    z[i] = !GRAD && inside && a.nslices == 1 ? Tr::load1(xp, id[i]) : 0.f;
+    if (k < kMaxTop) cols[k] = col[i];
+    if (GRAD || a.nslices == 1) {
+      const double p = inside ? exp(static_cast<double>(t[i])) : 0.0;
+      e.mass += p;
+      if (GRAD && k < kMaxTop) mass[k] = static_cast<float>(p);
+      if (!GRAD && inside && t[i] != neg_inf())
+        e.terms += p * (static_cast<double>(t[i]) - static_cast<double>(z[i]) * a.inv_tau);
     }
   }
+  if ((tid & ~63) < a.K && (GRAD || a.nslices == 1)) {  // waves with entries
+    e.mass = lanes_sum(e.mass);
+    if (!GRAD) e.terms = lanes_sum(e.terms);
+  }
+  if ((tid & 63) == 0) parts[tid >> 6] = e;
   __syncthreads();
   GradRow gr{};
   if (GRAD) {
-    gr = shared_row;
-    if (gr.zero) {
+    double all = a.rest ? exp(static_cast<double>(t_rest)) : 0.0;
+    const double r = all, g = static_cast<double>(g_loss) * a.inv_tau;
+#pragma unroll
+    for (int i = 0; i < W; ++i) all += parts[i].mass;
+    if (fabsf(lse) > kFarLse) {  // nothing is left of the probabilities
       clear();
       return;
     }
+    gr.nl = -lse * kLog2e;
+    gr.all = static_cast<float>(all * g);
+    gr.gt = static_cast<float>(g);
+    // with no weight outside the list, or none that fp32 tells apart, those columns get 0
+    const bool none = fabsf(lse_rest) > kFarLse;
+    gr.nr = none ? neg_inf() : -lse_rest * kLog2e;
+    gr.others = none ? 0.f : static_cast<float>((all * exp(static_cast<double>(lse_rest) - static_cast<double>(lse)) - r) * g);
   }
-  const unsigned long long own = held[tid];
 
   LaneSum st = sum_none(), listed = sum_none();
-  auto load = [&](int v) {
-    return static_cast<u32x4>(__builtin_nontemporal_load(
-        reinterpret_cast<const u32x4_a2*>(xp + (static_cast<int64_t>(v) * P - vs.pad) * Tr::kBytes)));
-  };
   auto other = [&](float z) { return fast_exp2(fmaf(z, c, gr.nr)) * gr.others; };
-  const int whole_end = vs.whole_end(), first = vs.first();
-  const int steps = (vs.end() + NT - 1) / NT;
-  // U vectors at a time; a bit of `skip` leaves one out
-  auto skips = [&](int q) {
-    uint32_t s = static_cast<uint32_t>(own >> q);
+  auto own = [&](int q) { return held[q >> 5][tid] >> (q & 31) & 1u; };
+
+  // Listed vectors, each by its first entry.
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = tid + (q + u) * NT;
-      if (v < first || v >= whole_end) s |= 1u << u;
+  for (int i = 0; i < E; ++i) {
+    if (col[i] == kNoCol) continue;
+    const int k = tid + i * NT, v = col[i] / P;
+    bool mine = true;
+    uint32_t bits = 0;
+    double ps[P];  // many entries may name one column
+#pragma unroll
+    for (int j = 0; j < P; ++j) ps[j] = 0.0;
+    for (int j = 0; j < a.K; j += 4) {
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 quad = *reinterpret_cast<const i32x4*>(cols + j);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (quad[n] / P != v) continue;
+        mine = mine && j + n >= k;
+        bits |= 1u << (quad[n] % P);
+        if (GRAD) {
+#pragma unroll
+          for (int m = 0; m < P; ++m)
+            if (quad[n] % P == m) ps[m] += mass[j + n];
+        }
+      }
     }
-    return s;
-  };
-  u32x4 w[U];
-  uint32_t skip = skips(0);
-#pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = skip >> u & 1 ? no_vector<Tr>() : load(tid + u * NT);
-  for (int q = 0; q < steps; q += U) {
-    float x[U * P];
-#pragma unroll
-    for (int u = 0; u < U; ++u) Tr::unpack(w[u], x + u * P);
-    const uint32_t now = skip;
-    if (q + U < steps) {
-      skip = skips(q + U);
-#pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = skip >> u & 1 ? no_vector<Tr>() : load(tid + (q + U + u) * NT);
-    }
+    if (!mine) continue;
+    float x[P];
+    Tr::unpack(in[i], x);
     if (GRAD) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (now >> u & 1) continue;
-#pragma unroll
-        for (int k = 0; k < P; ++k) x[u * P + k] = other(x[u * P + k]);
-        __builtin_nontemporal_store(Tr::pack(x + u * P),
-                                    reinterpret_cast<u32x4*>(op + (static_cast<int64_t>(tid + (q + u) * NT) * P - vs.pad) * Tr::kBytes));
-      }
+      for (int m = 0; m < P; ++m)
+        x[m] = bits >> m & 1 ? fmaf(fast_exp2(fmaf(x[m], c, gr.nl)), gr.all, -static_cast<float>(ps[m]) * gr.gt) : other(x[m]);
+      vs.store(op, v, x);
     } else {
-      sum_push<U * P, P>(st, x, largest_of<U * P>(x), c);
+      float y[P];
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        y[m] = bits >> m & 1 ? x[m] : neg_inf();
+        x[m] = bits >> m & 1 ? neg_inf() : x[m];
+      }
+      sum_push<P, P>(listed, y, largest_of<P>(y), c);
+      sum_push<P, P>(st, x, largest_of<P>(x), c);
     }
   }
   // what is not whole, unless an entry lies in it
   auto partial = [&](int v) {
-    if (v % NT != tid || (own >> (v / NT) & 1)) return;
+    if (v % NT != tid || own(v / NT)) return;
     float x[P];
     Tr::unpack(vs.load(xp, v), x);
     if (GRAD) {
@@ -252,49 +299,88 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   if (first) partial(0);
   if (whole_end < vs.end() && (whole_end > 0 || !first)) partial(whole_end);
 
-  for (int k = tid; k < a.K; k += NT) {
-    if (cols[k] < 0) continue;
-    const int v = (cols[k] + vs.pad) / P;
-    bool mine = true;
-    uint32_t bits = 0;
-    double ps[P];  // many entries may name one column
+  // The stream.  Sums are relative to the largest of the wave's first vectors,
+  // without a running maximum.  Where a wave's sum leaves fp32 that way, or is so
+  // small that what was added as 0 (126 octaves below the reference) may count, or
+  // where that reference is far from 0, the slice is summed again with one.
+  SumStat low{neg_inf(), 0.f};
+  if (whole_end > first) {
+    float nmc = 0.f;
+    if (!GRAD) {
+      float m = neg_inf();
 #pragma unroll
-    for (int e = 0; e < P; ++e) ps[e] = 0.0;
-    for (int j = 0; j < a.K; ++j) {
-      if (cols[j] < 0) continue;
-      const int at = cols[j] + vs.pad;
-      if (at / P != v) continue;
-      mine = mine && j >= k;
-      bits |= 1u << (at % P);
-      if (GRAD) {
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          if (at % P == e) ps[e] += mass[j];
+      for (int u = 0; u < U; ++u) {
+        float x[P];
+        Tr::unpack(w[u], x);
+        m = fmaxf(m, largest_of<P>(x));
       }
+      low.m = lanes_reduce<64>(m, [](float p, float q) { return fmaxf(p, q); });
+      nmc = is_near(low.m * c) ? -(low.m * c) : -__builtin_inff();  // far: no sum
     }
-    if (!mine) continue;
-    float x[P];
-    Tr::unpack(vs.load(xp, v), x);
-    if (GRAD) {
+    uint32_t word = 0;
+    for (int q = 0; q < steps; q += U) {
+      if ((q & 31) == 0) word = held[q >> 5][tid];
+      float x[U * P];
 #pragma unroll
-      for (int e = 0; e < P; ++e)
-        x[e] = bits >> e & 1 ? fmaf(fast_exp2(fmaf(x[e], c, gr.nl)), gr.all, -static_cast<float>(ps[e]) * gr.gt) : other(x[e]);
-      vs.store(op, v, x);
-    } else {
+      for (int u = 0; u < U; ++u) Tr::unpack(w[u], x + u * P);
+      if (q + U < steps) {
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        if (bits >> e & 1)
-          sum_push1(listed, x[e], c);
-        else
-          sum_push1(st, x[e], c);
+        for (int u = 0; u < U; ++u) w[u] = load(tid + (q + U + u) * NT);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = tid + (q + u) * NT;
+        const bool on = !(word >> u & 1) && v >= first && v < whole_end;
+        if (GRAD) {
+          if (!on) continue;
+#pragma unroll
+          for (int k = 0; k < P; ++k) x[u * P + k] = other(x[u * P + k]);
+          __builtin_nontemporal_store(Tr::pack(x + u * P),
+                                      reinterpret_cast<u32x4*>(op + (static_cast<int64_t>(v) * P - vs.pad) * Tr::kBytes));
+        } else {
+          float ps = fast_exp2(fmaf(x[u * P], c, nmc));
+#pragma unroll
+          for (int k = 1; k < P; ++k) ps += fast_exp2(fmaf(x[u * P + k], c, nmc));
+          low.s += on ? ps : 0.f;
+        }
+      }
+      word >>= U;
+    }
+    if (!GRAD) {
+      const float whole = lanes_reduce<64>(low.s, [](float p, float q) { return p + q; });
+      if (__syncthreads_or(!(whole >= 8.5e-22f && whole <= kLargest))) {
+        LaneSum over = sum_none();
+        for (int q = 0; q < steps; ++q) {
+          const int v = tid + q * NT;
+          if (v < first || v >= whole_end || own(q)) continue;
+          float x[P];
+          Tr::unpack(load(v), x);
+          sum_push<P, P>(over, x, largest_of<P>(x), c);
+        }
+        low = over;
       }
     }
   }
   if (GRAD) return;
-  const SumStat rest = sum_block<NT>(st, c, sm[0]), top = sum_block<NT>(listed, c, sm[1]);
+  // both states of the workgroup, in every lane of its first wave
+  const SumStat mine[2] = {sum_merge<64>(sum_add(st, low, c), c), sum_merge<64>(listed, c)};
+  if ((tid & 63) == 0) {
+    sm[0][tid >> 6] = mine[0];
+    sm[1][tid >> 6] = mine[1];
+  }
+  __syncthreads();
+  if (tid >= 64) return;
+  const SumStat rest = sum_merge<W>(sm[0][tid & (W - 1)], c), top = sum_merge<W>(sm[1][tid & (W - 1)], c);
+  if (tid != 0) return;
   if (a.nslices == 1) {
-    if (tid < 64) store_loss<Tr>(a, row, rest, top);
-  } else if (tid == 0) {
+    Entries whole = parts[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      whole.terms += parts[i].terms;
+      whole.mass += parts[i].mass;
+    }
+    store_loss(a, row, whole, t_rest, rest, top);
+  } else {
     float* p = a.part + (row * a.nslices + slice) * 4;
     p[0] = rest.m;
     p[1] = rest.s;
@@ -319,15 +405,22 @@ __global__ void __launch_bounds__(256) k_distill_join(DistillArgs a) {
     rest = sum_add(rest, SumStat{p[0], p[1]}, a.c);
     listed = sum_add(listed, SumStat{p[2], p[3]}, a.c);
   }
-  store_loss<Tr>(a, row, sum_merge<64>(rest, a.c), sum_merge<64>(listed, a.c));
+  const Entries e = sum_entries<Tr>(a, row);
+  rest = sum_merge<64>(rest, a.c);
+  listed = sum_merge<64>(listed, a.c);
+  if (lane == 0) store_loss(a, row, e, a.rest ? a.rest[row] : neg_inf(), rest, listed);
 }
 
-// Slices per row: one where there are rows for three workgroups a CU, else as
-// many as that takes; a lane's word takes 64 vectors of a slice.
-void set_slices(DistillArgs& a, int dtype) {
-  const int64_t longest = int64_t(64) * 512 * (dtype == 2 ? 4 : 8) - 128;
+// Slices per row: as many as make three workgroups a CU where rows are few; the
+// bits hold kMaskWords x 32 of a lane's vectors.  For the gradient slices of about
+// kGradSlice columns, whatever the rows.
+constexpr int64_t kRowGroups = 768, kGradSlice = 8192;
+
+void set_slices(DistillArgs& a, int dtype, bool grad) {
+  const int64_t longest = int64_t(32) * kMaskWords * 256 * (dtype == 2 ? 4 : 8) - 128;
   const int64_t most = (int64_t(a.V) + kMinDistillSlice - 1) / kMinDistillSlice, least = (int64_t(a.V) + longest - 1) / longest;
-  int64_t n = (768 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  int64_t n = (kRowGroups + a.T - 1) / (a.T > 0 ? a.T : 1);
+  if (grad && n < a.V / kGradSlice) n = a.V / kGradSlice;
   n = n < most ? n : most;
   n = n > least ? n : least;
   a.slice = static_cast<int>(((int64_t(a.V) + n - 1) / n + 127) / 128 * 128);
@@ -351,7 +444,6 @@ hipError_t launch_distill_nt(DistillArgs a, hipStream_t s) {
 
 template <class Tr, bool GRAD>
 hipError_t launch_distill_t(const DistillArgs& a, hipStream_t s) {
-  if (a.slice >= 16384) return launch_distill_nt<Tr, 512, GRAD>(a, s);
   if (a.slice >= 4096) return launch_distill_nt<Tr, 256, GRAD>(a, s);
   return launch_distill_nt<Tr, 128, GRAD>(a, s);
 }
@@ -371,7 +463,7 @@ size_t distill_workspace_bytes(int dtype, int64_t T, int64_t V) {
   DistillArgs a{};
   a.T = T;
   a.V = static_cast<int>(V);
-  set_slices(a, dtype);
+  set_slices(a, dtype, false);
   if (a.nslices == 1) return 256;
   const size_t per_row = size_t(a.nslices) * 16;
   if (size_t(T) > (size_t(1) << 60) / per_row) return 0;
@@ -380,7 +472,7 @@ size_t distill_workspace_bytes(int dtype, int64_t T, int64_t V) {
 
 hipError_t launch_distill(int dtype, const DistillArgs& args, char* ws, hipStream_t s) {
   DistillArgs a = args;
-  set_slices(a, dtype);
+  set_slices(a, dtype, false);
   a.part = reinterpret_cast<float*>(ws);
   hipError_t e = launch_distill_any<false>(dtype, a, s);
   if (e != hipSuccess || a.nslices == 1) return e;
@@ -403,7 +495,7 @@ hipError_t launch_distill(int dtype, const DistillArgs& args, char* ws, hipStrea
 
 hipError_t launch_distill_grad(int dtype, const DistillArgs& args, hipStream_t s) {
   DistillArgs a = args;
-  set_slices(a, dtype);
+  set_slices(a, dtype, true);
   return launch_distill_any<true>(dtype, a, s);
 }
 

@@ -97,6 +97,15 @@ __device__ __forceinline__ float value_of(uint32_t order) {
   return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
 }
 
+// Which piece of work a workgroup takes: a workgroup runs on XCD blockIdx.x % 8,
+// and rows that a mask leaves out often come in a period of 8 (rows 0 .. 3 of every 16:
+// half the XCDs would have twice the work of the others, 335 us for 290 on 8192 x
+// 151936).  So each eight neighbours go round by another offset.
+__device__ __forceinline__ unsigned spread_block() {
+  const unsigned b = blockIdx.x;
+  return (b | 7u) < gridDim.x ? (b & ~7u) | ((b + (b >> 3) + (b >> 6)) & 7u) : b;
+}
+
 // A row's vector v of n columns: whole, or what is left at the end with -inf
 // behind it.  Rows may start at any element.
 template <class Tr>
@@ -115,11 +124,25 @@ __device__ __forceinline__ u32x4 no_vector() {
   return u32x4{w, w, w, w};
 }
 
+__device__ __forceinline__ float largest3(float a, float b, float c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+#else
+  return fmaxf(fmaxf(a, b), c);
+#endif
+}
+
+// NaN are passed over.  Three at a time by hand: the compiler first brings each
+// value of a pair to canonical form, which widened logits already have.
 template <int N>
 __device__ __forceinline__ float largest_of(const float* x) {
   float m = x[0];
+  int k = 1;
 #pragma unroll
-  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  for (; k + 2 <= N; k += 2) m = largest3(m, x[k], x[k + 1]);
+  if (k < N) m = fmaxf(m, x[k]);
   return m;
 }
 

@@ -233,13 +233,12 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   __shared__ uint32_t best[kWords];  // later the digits' counts
   __shared__ uint64_t top[SHORT || NT > 256 ? kMaxTop : kFewTop];
   __shared__ SumStat sm[2][W];
-  __shared__ float far_down[W];
   __shared__ uint32_t count, bar;
   __shared__ int held_by[W];
   static_assert(kWords >= 258, "digits' counts");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const unsigned rel_row = blockIdx.x / static_cast<unsigned>(a.nslices);
-  const int slice = static_cast<int>(blockIdx.x - rel_row * static_cast<unsigned>(a.nslices));
+  const unsigned block = spread_block(), rel_row = block / static_cast<unsigned>(a.nslices);
+  const int slice = static_cast<int>(block - rel_row * static_cast<unsigned>(a.nslices));
   const int64_t row = a.row0 + rel_row;
   if (!row_live(a, row)) {
     if (!a.part_keys) store_no_top<NT>(a, row);
@@ -263,7 +262,6 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   };
 
   SumStat low{neg_inf(), 0.f};  // of what was streamed and not kept: this lane's
-  float lost = neg_inf();       // its largest value
   bool digits = false;
   if (SHORT) {
     const int vectors = (n + P - 1) / P;
@@ -273,17 +271,16 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
       if (v < vectors) kept[v] = row_vector<Tr>(xp, v, n);
     }
   } else {
-    // The slice in U W pieces of `steps` times 64 vectors, so that one step of the
-    // workgroup is a sample of the whole; a wave goes from piece to piece, so that
-    // each has its share of a piece that holds more of what is kept.
-    const int vectors = n / P, steps = (vectors + 64 * U * W - 1) / (64 * U * W);
-    auto number = [&](int u, int q) { return static_cast<uint32_t>(((u * W + ((wave + q) & (W - 1))) * steps + q) * 64 + lane); };
-    // A number past the slice loads its last vector, and is left out of everything.
-    auto there = [&](uint32_t v) { return v < static_cast<uint32_t>(vectors); };
+    // U W pieces of `steps` times 64 vectors, so that one step of the workgroup is a
+    // sample of the whole; a wave goes from piece to piece, so that each has its
+    // share of a piece that holds more of what is kept.  What is left over behind
+    // the pieces comes last.
+    const int vectors = n / P, steps = vectors / (64 * U * W);
+    const char* base = xp;  // 32-bit offsets: a slice has at most 2^32 bytes
     auto load = [&](uint32_t v) {
-      const uint32_t at = v < static_cast<uint32_t>(vectors) ? v : vectors - 1;
-      return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(xp + size_t(at) * 16)));
+      return static_cast<u32x4>(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(base + v * 16u)));
     };
+    auto number = [&](int u, int q) { return static_cast<uint32_t>(((u * W + ((wave + q) & (W - 1))) * steps + q) * 64) + lane; };
     int held = 0;  // vectors that this wave has kept
     auto keep = [&](bool on, u32x4 vec, uint32_t v) {
       const uint64_t mask = __ballot(on);
@@ -298,35 +295,38 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
       }
     };
     u32x4 w[U];
+    float most = neg_inf();  // the lane's largest value so far
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = load(number(u, 0));
-    float high = neg_inf();  // the lane's largest value so far that was kept (`lost`: that was not)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[P];
       Tr::unpack(w[u], x);
-      if (there(number(u, 0))) high = fmaxf(high, largest_of<P>(x));
+      most = fmaxf(most, largest_of<P>(x));
     }
-    best[tid] = word(high);
+    best[tid] = word(most);
     float floor = take_floor(std::integral_constant<int, NT>{});
     // Exponents are relative to the floor.  With the lowest floor every finite value
     // is kept and the others' exponents only have to be -inf or NaN.  Floors far
     // from 0 otherwise (finite masks in all but a few columns) are left to the digits.
     float fc = floor > -kLargest ? floor * c : 0.f;
     digits = !is_near(fc);
+    auto sum = [&](const float* x, bool on) {
+      float ps = fast_exp2(fmaf(x[0], c, -fc));
+#pragma unroll
+      for (int k = 1; k < P; ++k) ps += fast_exp2(fmaf(x[k], c, -fc));
+      low.s += on ? ps : 0.f;
+    };
     for (int q = 0; !digits;) {
-      float t[U * P];
-      bool low_one[U];
+      float x[U * P];
+      bool hit[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t v = number(u, q);
-        Tr::unpack(w[u], t + u * P);
-        const float m = largest_of<P>(t + u * P);
-        const bool hit = m >= floor && there(v);
-        low_one[u] = !hit && there(v);
-        lost = fmaxf(lost, low_one[u] ? m : neg_inf());
-        high = fmaxf(high, hit ? m : neg_inf());
-        keep(hit, w[u], v);
+        Tr::unpack(w[u], x + u * P);
+        const float m = largest_of<P>(x + u * P);
+        hit[u] = m >= floor;
+        most = fmaxf(most, m);
+        keep(hit[u], w[u], number(u, q));
       }
       const bool last = ++q == steps;
       if (!last) {  // in flight while the exponentials are taken
@@ -334,15 +334,10 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
         for (int u = 0; u < U; ++u) w[u] = load(number(u, q));
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float ps = 0.f;
-#pragma unroll
-        for (int k = 0; k < P; ++k) ps += fast_exp2(fmaf(t[u * P + k], c, -fc));
-        low.s += low_one[u] ? ps : 0.f;
-      }
+      for (int u = 0; u < U; ++u) sum(x + u * P, !hit[u]);
       if (last) break;
       if ((q & (q - 1)) == 0) {
-        best[tid] = word(fmaxf(high, lost));
+        best[tid] = word(most);
         const float was = floor;
         floor = take_floor(std::integral_constant<int, NT>{});
         fc = floor > -kLargest ? floor * c : 0.f;
@@ -350,8 +345,16 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
         low.s *= fast_exp2(stat_shift(was, floor, c));
       }
     }
+    for (int v0 = steps * 64 * U * W; v0 * P < n; v0 += NT) {
+      const int v = v0 + tid;
+      const u32x4 vec = v * P < n ? row_vector<Tr>(xp, v, n) : no_vector<Tr>();
+      float x[P];
+      Tr::unpack(vec, x);
+      const bool on = largest_of<P>(x) >= floor;
+      keep(on, vec, v);
+      sum(x, !on);
+    }
     low.m = floor;
-    if (wave == 0) keep(lane == 0 && vectors * P < n, row_vector<Tr>(xp, vectors, n), vectors);
     if (lane == 0) held_by[wave] = held;
     __syncthreads();
 #pragma unroll
@@ -425,27 +428,23 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
     for (int i = tid; i < got; i += NT) top[rank_among(keys, got, keys[i])] = keys[i];
   }
   SumStat rest = sum_block<NT>(SHORT || digits ? st : sum_add(low, st, c), c, sm[0]);
-  if (!SHORT && !digits) {
-    auto most = [](float p, float q) { return fmaxf(p, q); };
-    lost = lanes_reduce<64>(lost, most);
-    if (lane == 0) far_down[wave] = lost;
-    __syncthreads();
-    lost = lanes_reduce<W>(far_down[lane & (W - 1)], most);
-    // What lies more than 126 octaves below the floor was added as 0.  Where that
-    // is not small beside what is left, the rest is summed once more.
-    if (lost > neg_inf() && rest.m <= low.m && !(rest.s * fast_exp2(stat_shift(rest.m, low.m, c)) >= 8.5e-22f)) {
-      const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
-      st = sum_none();
-      for (int v = tid; v * P < n; v += NT) {
-        float x[P];
-        Tr::unpack(row_vector<Tr>(xp, v, n), x);
+  // What lies more than 126 octaves below the floor was added as 0.  Where that is
+  // not small beside what is left, the rest is summed once more.  (Below the
+  // lowest floor lies nothing.)
+  if (!SHORT && !digits && low.m > -kLargest && rest.m <= low.m &&
+      !(rest.s * fast_exp2(stat_shift(rest.m, low.m, c)) >= 8.5e-22f)) {
+    const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+    st = sum_none();
+    for (int v = tid; v * P < n; v += NT) {
+      float x[P];
+      Tr::unpack(row_vector<Tr>(xp, v, n), x);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (x[i] >= -kLargest && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
-        sum_push<P, P>(st, x, largest_of<P>(x), c);
-      }
-      rest = sum_block<NT>(st, c, sm[0]);
+      for (int i = 0; i < P; ++i)
+        if (x[i] >= -kLargest && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
+      sum_push<P, P>(st, x, largest_of<P>(x), c);
     }
+    __syncthreads();
+    rest = sum_block<NT>(st, c, sm[0]);
   }
   __syncthreads();
   if (a.part_keys) {
@@ -638,12 +637,12 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
 // launches
 // ---------------------------------------------------------------------------
 
-constexpr int kShortNT = 256;
-
-int vector_columns(int dtype) { return dtype == 2 ? 4 : 8; }
+// Threads of k_top: the K-th largest of the lanes' values cuts the better the more
+// lanes there are.
+int threads_of(int K) { return K > kFewTop ? 512 : 256; }
 
 // Columns of a slice that k_top keeps whole.
-int short_slice(int dtype) { return kHeld<kShortNT, true> * kShortNT * vector_columns(dtype); }
+int short_slice(int dtype, int threads) { return 4 * threads * (dtype == 2 ? 4 : 8); }
 
 // Slices per row: one where there are rows for four workgroups a CU and more,
 // else as many as that takes, none shorter than what a workgroup keeps
@@ -651,7 +650,7 @@ int short_slice(int dtype) { return kHeld<kShortNT, true> * kShortNT * vector_co
 void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
   const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
-  const int64_t least = short_slice(dtype);
+  const int64_t least = short_slice(dtype, 256);
   int64_t n = (1024 + a.T - 1) / (a.T > 0 ? a.T : 1);
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
@@ -675,12 +674,15 @@ hipError_t launch_top_nt(TopArgs a, hipStream_t s) {
   return hipSuccess;
 }
 
+template <class Tr, int NT>
+hipError_t launch_top_t(const TopArgs& a, int dtype, hipStream_t s) {
+  if (a.slice <= short_slice(dtype, NT)) return launch_top_nt<Tr, NT, true>(a, s);
+  return launch_top_nt<Tr, NT, false>(a, s);
+}
+
 template <class Tr>
 hipError_t launch_top_t(const TopArgs& a, int dtype, hipStream_t s) {
-  if (a.slice <= short_slice(dtype)) return launch_top_nt<Tr, kShortNT, true>(a, s);
-  // the K-th largest of the lanes' values cuts the better the more lanes there are
-  if (a.K > kFewTop) return launch_top_nt<Tr, 512, false>(a, s);
-  return launch_top_nt<Tr, 256, false>(a, s);
+  return threads_of(a.K) == 512 ? launch_top_t<Tr, 512>(a, dtype, s) : launch_top_t<Tr, 256>(a, dtype, s);
 }
 
 hipError_t launch_top_slices(int dtype, const TopArgs& a, hipStream_t s) {
