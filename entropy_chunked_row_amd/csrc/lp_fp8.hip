@@ -58,9 +58,9 @@ __device__ __forceinline__ void load8(const char* row, int64_t j, int64_t n, flo
 }
 
 // 16 lanes a block of a row, 16 blocks a workgroup.  xq [T x hp], zeros behind
-// column h; sx [blocks x T].
+// column h; sx [blocks x pitch].
 template <class Tr>
-__global__ void __launch_bounds__(256) k_fp8_rows(Fp8Args a, uint8_t* xq, float* sx, int blocks, int64_t first) {
+__global__ void __launch_bounds__(256) k_fp8_rows(Fp8Args a, uint8_t* xq, float* sx, int64_t pitch, int blocks, int64_t first) {
   const int64_t i = first + static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
   if (i >= a.T * blocks) return;
   const int64_t t = i / blocks;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(256) k_fp8_rows(Fp8Args a, uint8_t* xq, float*
   m = lanes_reduce<16>(m, [](float p, float q) { return fmaxf(p, q); });
   const float scale = scale_of(m);
   *reinterpret_cast<u32x2_t*>(xq + (t * blocks + b) * kBlock + lane * 8) = quantize8(x, scale);
-  if (lane == 0) sx[static_cast<int64_t>(b) * a.T + t] = scale;
+  if (lane == 0) sx[b * pitch + t] = scale;
 }
 
 // A workgroup a block of 128 x 128.
@@ -115,8 +115,9 @@ struct TileArgs {
   const float* sw;
   int64_t ld_s;
   const uint8_t* xq;  // [T x hp]
-  const float* sx;    // [blocks x T]
+  const float* sx;    // [blocks x pitch_sx], 256 more behind them
   int64_t T;
+  int64_t pitch_sx;  // T up to a multiple of 4
   int h, V, blocks;
   int n_vb, n_nb;
   int64_t t0;  // first row of the launch
@@ -130,9 +131,9 @@ __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
                static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
 }
 
-__device__ __forceinline__ f32x16_t mfma_32(i32x8 a, i32x8 b, f32x16_t c) {
+__device__ __forceinline__ f32x4_t mfma_16(i32x8 a, i32x8 b, f32x4_t c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 #else
   (void)a, (void)b;
   return c;
@@ -156,18 +157,18 @@ __device__ __forceinline__ f16x8_t widen8(uint32_t lo, uint32_t hi) {
 #endif
 }
 
-// 32 bytes of K a lane of both operands (64 or 128 in all), as fp16.
-__device__ __forceinline__ f32x16_t mfma_32_wide(i32x8 a, i32x8 b, f32x16_t c) {
-#pragma unroll
-  for (int k = 0; k < 8; k += 2)
-    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(a[k], a[k + 1]), widen8(b[k], b[k + 1]), c, 0, 0, 0);
-  return c;
+// 32 bytes of K a lane, as fp16: four operands of 16x16x32 products.
+struct Wide {
+  f16x8_t k[4];
+};
+
+__device__ __forceinline__ Wide widen(i32x8 a) {
+  return Wide{{widen8(a[0], a[1]), widen8(a[2], a[3]), widen8(a[4], a[5]), widen8(a[6], a[7])}};
 }
 
-__device__ __forceinline__ f32x4_t mfma_16_wide(i32x8 a, i32x8 b, f32x4_t c) {
+__device__ __forceinline__ f32x4_t mfma_16(const Wide& a, const Wide& b, f32x4_t c) {
 #pragma unroll
-  for (int k = 0; k < 8; k += 2)
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(a[k], a[k + 1]), widen8(b[k], b[k + 1]), c, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.k[i], b.k[i], c, 0, 0, 0);
   return c;
 }
 
@@ -201,16 +202,21 @@ __device__ __forceinline__ void store_results(void* out, int dtype, int64_t at, 
 template <int BN, int WGM, int WGN>
 struct Fp8Tile {
   static constexpr int BM = 256, NW = WGM * WGN, NT = 64 * NW;
-  static constexpr int MI = BM / WGM / 32, NI = BN / WGN / 32;
+  static constexpr int MI = BM / WGM / 16, NI = BN / WGN / 16;     // 16 x 16 products of a wave
   static constexpr int A_INST = BM / 8 / NW, B_INST = BN / 8 / NW;  // 1 KB loads a wave and stage
-  static constexpr int STAGE = (BM + BN) * kBlock;                  // bytes
-  static constexpr int OUT_PITCH = MI * 32 + 4;                     // floats of a row staged for output
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads a wave");
+  static constexpr int ROWS = (BM + BN) * kBlock;                   // bytes of both operands' rows
+  static constexpr int STAGE = ROWS + 1024;                         // and the scales of up to 256 rows of x
+  static constexpr int OUT_PITCH = MI * 16 + 4;                     // floats of a row staged for output
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BN <= 256, "whole loads a wave");
   static_assert(NW * 32 * OUT_PITCH * 4 <= 2 * STAGE, "output staging fits the stages");
 };
 
-// One block: K in steps of 128 (one scale block) through two LDS stages, filled
-// direct to LDS.
+// One block of 256 x BN: K in steps of 128 (one scale block) through two LDS
+// stages, filled direct to LDS.  A step's products are 16x16x128, a whole scale
+// block each, so a partial sum takes four registers and is scaled while the next
+// products run.  The step's last column of products is held back: behind it the
+// next stage has arrived and this one is free (one barrier a step), and the first
+// operands of the next step are read while it runs.
 template <int BN, int WGM, int WGN, bool WIDE>
 __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   using C = Fp8Tile<BN, WGM, WGN>;
@@ -242,99 +248,143 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   const int r = wave * 8 + (lane >> 3), kc = (lane & 7) ^ lds_swz(r);
   const dtl_rsrc_t wrsrc = dtl_rsrc(a.weight + static_cast<int64_t>(v0) * a.ld_w), xrsrc = dtl_rsrc(a.xq + t0 * hp);
   const uint32_t tail = static_cast<uint32_t>(kc * 16) >= static_cast<uint32_t>(a.h - (a.blocks - 1) * kBlock) ? kc * 16u : 0u;
-  auto offset = [&](int j, int rows, uint32_t ld) {
-    const int q = j * NW * 8 + r;
-    return static_cast<uint32_t>(q < rows ? q : rows - 1) * ld + kc * 16u;
+  // row r of every 8 NW of an operand, no further than its last
+  auto offset = [&](int j, uint32_t last, uint32_t ld) {
+    return min(static_cast<uint32_t>(r) * ld + static_cast<uint32_t>(j * NW * 8) * ld, last) + kc * 16u;
   };
+  const uint32_t ld_w = static_cast<uint32_t>(a.ld_w), ld_x = static_cast<uint32_t>(hp);
+  const uint32_t last_w = static_cast<uint32_t>(min(M, C::BM) - 1) * ld_w, last_x = static_cast<uint32_t>(N - 1) * ld_x;
   auto issue = [&](int kt, unsigned char* stage) {
     const uint32_t back = kt == a.blocks - 1 ? tail : 0u;
 #pragma unroll
     for (int j = 0; j < C::A_INST; ++j)
-      dtl_load16(wrsrc, reinterpret_cast<uint16_t*>(stage + (j * NW + wave) * 1024), offset(j, M, static_cast<uint32_t>(a.ld_w)) - back,
+      dtl_load16(wrsrc, reinterpret_cast<uint16_t*>(stage + (j * NW + wave) * 1024), offset(j, last_w, ld_w) - back,
                  static_cast<uint32_t>(kt) * kBlock);
 #pragma unroll
     for (int j = 0; j < C::B_INST; ++j)
       dtl_load16(xrsrc, reinterpret_cast<uint16_t*>(stage + C::BM * kBlock + (j * NW + wave) * 1024),
-                 offset(j, N, static_cast<uint32_t>(hp)), static_cast<uint32_t>(kt) * kBlock);
+                 offset(j, last_x, ld_x), static_cast<uint32_t>(kt) * kBlock);
+    if (wave == 0)
+      dtl_load16(dtl_rsrc(a.sx + static_cast<int64_t>(kt) * a.pitch_sx + t0), reinterpret_cast<uint16_t*>(stage + C::ROWS), lane * 16u,
+                 0);
   };
-  // 32 bytes of K of one operand row: chunks g, 2 + g and 4 + g, 6 + g of the two
-  // steps of 64, the same for both operands (the order within K is free).
-  const int r32 = lane & 31, g = lane >> 5;
-  auto fragment = [&](const unsigned char* rows, int row, int s) {
-    const unsigned char* p = rows + (row + r32) * kBlock;
-    const int z = lds_swz(r32);
-    return join(*reinterpret_cast<const u32x4*>(p + (((s * 4 + g) ^ z) << 4)),
-                *reinterpret_cast<const u32x4*>(p + (((s * 4 + 2 + g) ^ z) << 4)));
+  // 32 bytes of K of one operand row: chunks g and 4 + g, for both operands alike
+  // (the order within K is free).
+  const int r16 = lane & 15, g = lane >> 4, z16 = lds_swz(r16);
+  auto fragment = [&](const unsigned char* rows, int row) {
+    const unsigned char* p = rows + (row + r16) * kBlock;
+    return join(*reinterpret_cast<const u32x4*>(p + ((g ^ z16) << 4)), *reinterpret_cast<const u32x4*>(p + (((4 + g) ^ z16) << 4)));
+  };
+  auto frag_a = [&](const unsigned char* stage, int mi) { return fragment(stage, (wm * MI + mi) * 16); };
+  auto frag_b = [&](const unsigned char* stage, int ni) { return fragment(stage + C::BM * kBlock, (wn * NI + ni) * 16); };
+  auto scale_b = [&](const unsigned char* stage, int ni) {
+    return reinterpret_cast<const float*>(stage + C::ROWS)[(wn * NI + ni) * 16 + r16];
   };
 
-  f32x16_t acc[MI][NI];
+  f32x4_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mi][ni][i] = 0.f;
-  f32x16_t zero;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // this wave's rows of W lie in one block of scales, a lane's column of x is one row
-  const float* sw = a.sw + static_cast<int64_t>(min(v0 + wm * MI * 32, a.V - 1) / kBlock) * a.ld_s;
-  const float* sx[NI];
-#pragma unroll
-  for (int ni = 0; ni < NI; ++ni) sx[ni] = a.sx + t0 + min(wn * NI * 32 + ni * 32 + r32, N - 1);
+  // this wave's rows of W lie in one block of scales
+  const float* sw = a.sw + static_cast<int64_t>(min(v0 + wm * MI * 16, a.V - 1) / kBlock) * a.ld_s;
+  int none = 0;  // loaded by lanes: a scalar load would be waited for with the reads of LDS
+  asm("" : "+v"(none));
 
+  using Frag = std::conditional_t<WIDE, Wide, i32x8>;
+  auto as_operand = [](i32x8 x) {
+    if constexpr (WIDE)
+      return widen(x);
+    else
+      return x;
+  };
+  Frag fa[MI];
+  i32x8 fb[2];
+  float fx[2], w = sw[0], w_next = 0.f;
   issue(0, lds);
+  if (a.blocks > 1) issue(1, lds + C::STAGE);
+  // the first stage has arrived when only the second's loads are under way
+  if (a.blocks > 1 && wave == 0)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::A_INST + C::B_INST + 1) : "memory");
+  else if (a.blocks > 1)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::A_INST + C::B_INST) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) fa[mi] = as_operand(frag_a(lds, mi));
+  fb[0] = frag_b(lds, 0);
+  fx[0] = scale_b(lds, 0);
+
+  // Products of a column and, between them, the scaling of those of the column
+  // before (of the last step's last column at first).
+  const f32x4_t zero{0.f, 0.f, 0.f, 0.f};
+  f32x4_t part[2][MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) part[1][mi] = zero;
+  float f_before = 0.f;
+  auto add = [&](f32x4_t& to, f32x4_t p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = fmaf(p[i], f_before, to[i]);
+    asm volatile("" : "+v"(to));  // here, or the compiler keeps a whole step's parts for the end
+  };
   for (int kt = 0; kt < a.blocks; ++kt) {
     unsigned char* X = lds + (kt & 1) * C::STAGE;
-    float f[NI];
-    const float w = sw[kt];
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) f[ni] = w * sx[ni][kt * a.T];
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (kt + 1 < a.blocks) issue(kt + 1, lds + ((kt + 1) & 1) * C::STAGE);
-    i32x8 fa[MI][2];
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) fa[mi][s] = fragment(X, (wm * MI + mi) * 32, s);
+    unsigned char* Y = lds + ((kt + 1) & 1) * C::STAGE;
+    const bool next = kt + 1 < a.blocks;
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) {
-      const i32x8 b0 = fragment(X + C::BM * kBlock, (wn * NI + ni) * 32, 0);
-      const i32x8 b1 = fragment(X + C::BM * kBlock, (wn * NI + ni) * 32, 1);
+      const int cur = ni & 1;
+      if (ni + 1 < NI) {
+        fb[cur ^ 1] = frag_b(X, ni + 1);
+        fx[cur ^ 1] = scale_b(X, ni + 1);
+      } else {
+        // every operand of this step is in registers
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (next) {
+          w_next = sw[kt + 1 + none];
+          if (kt + 2 < a.blocks) issue(kt + 2, X);
+          fb[cur ^ 1] = frag_b(Y, 0);
+          fx[cur ^ 1] = scale_b(Y, 0);
+        }
+      }
+      const float f = w * fx[cur];
+      const Frag b = as_operand(fb[cur]);
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
-        f32x16_t p;
-        if (WIDE)
-          p = mfma_32_wide(fa[mi][1], b1, mfma_32_wide(fa[mi][0], b0, zero));
-        else
-          p = mfma_32(fa[mi][1], b1, mfma_32(fa[mi][0], b0, zero));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[mi][ni][i] = fmaf(p[i], f[ni], acc[mi][ni][i]);
+        part[cur][mi] = mfma_16(fa[mi], b, zero);
+        if (ni + 1 == NI && next) fa[mi] = as_operand(frag_a(Y, mi));
+        add(acc[mi][(ni + NI - 1) % NI], part[cur ^ 1][mi]);
       }
+      f_before = f;
+      __builtin_amdgcn_sched_barrier(0);  // no column's operands ahead of their turn
     }
+    static_assert(NI % 2 == 0, "the next step's first column goes to buffer 0");
+    w = w_next;
   }
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) add(acc[mi][NI - 1], part[1][mi]);
   __syncthreads();
 
   // Out: 32 rows at a time through LDS of the wave's own, so that a row's
   // neighbouring results are stored together.
   float* own = reinterpret_cast<float*>(lds) + wave * 32 * C::OUT_PITCH;
-  const int vw = v0 + wm * MI * 32;
-  const int per = a.out_dtype == 2 ? 4 : 8, lanes = MI * 32 / per, rows = 64 / lanes;
+  const int vw = v0 + wm * MI * 16;
+  const int per = a.out_dtype == 2 ? 4 : 8, lanes = MI * 16 / per, rows = 64 / lanes;
   const int col = lane % lanes * per, row0 = lane / lanes;
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni) {
+  for (int ni = 0; ni < NI; ni += 2) {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4_t*>(own + r32 * C::OUT_PITCH + mi * 32 + q * 8 + g * 4) =
-            f32x4_t{acc[mi][ni][q * 4], acc[mi][ni][q * 4 + 1], acc[mi][ni][q * 4 + 2], acc[mi][ni][q * 4 + 3]};
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<f32x4_t*>(own + (q * 16 + r16) * C::OUT_PITCH + mi * 16 + g * 4) = acc[mi][ni + q];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     for (int q = row0; q < 32; q += rows) {
-      const int t = wn * NI * 32 + ni * 32 + q, v = vw + col;
+      const int t = (wn * NI + ni) * 16 + q, v = vw + col;
       const float* p = own + q * C::OUT_PITCH + col;
       float x[8];
       *reinterpret_cast<f32x4_t*>(x) = *reinterpret_cast<const f32x4_t*>(p);
@@ -358,7 +408,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
 
 // Up to 16 rows of x.  K is split over the 8 waves of a workgroup, whose blocks
 // of x stay in registers; the workgroups walk over the head 16 rows at a time,
-// the next 16 rows' bytes in flight.
+// the next 16 rows' bytes and scales in flight.
 template <int NB>
 __global__ void __launch_bounds__(512, 2) k_fp8_few(TileArgs a) {
   __shared__ float sums[2][8][256];
@@ -366,49 +416,54 @@ __global__ void __launch_bounds__(512, 2) k_fp8_few(TileArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int T = static_cast<int>(a.T), hp = a.blocks * kBlock, tiles = (a.V + 15) / 16;
+  // wave's blocks: wave, wave + 8, ...; of them only the last may not be there
+  const bool all = wave + (NB - 1) * 8 < a.blocks;
   i32x8 x[NB];
   float sx[NB];
-  int at[NB][2];  // the lane's bytes of a row of the head; those behind its end are its first ones (against zeros)
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int kb = wave + i * 8, t = r < T ? r : T - 1;
-    const bool on = kb < a.blocks;
-    const u32x4 none{0, 0, 0, 0};
-    const u32x4* p = reinterpret_cast<const u32x4*>(a.xq + static_cast<int64_t>(t) * hp + (on ? kb : 0) * kBlock + g * 32);
-    x[i] = join(on ? p[0] : none, on ? p[1] : none);
-    sx[i] = on ? a.sx[static_cast<int64_t>(kb) * a.T + t] : 0.f;
+    const int kb = i + 1 < NB || all ? wave + i * 8 : 0, t = r < T ? r : T - 1;
+    const u32x4* p = reinterpret_cast<const u32x4*>(a.xq + static_cast<int64_t>(t) * hp + kb * kBlock + g * 32);
+    x[i] = join(p[0], p[1]);
+    sx[i] = a.sx[static_cast<int64_t>(kb) * a.pitch_sx + t];
+  }
+  // the lane's bytes of a row of the head; those behind its end are its first ones (against zeros)
+  const int at = wave * kBlock + g * 32;
+  int end_at[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int k = kb * kBlock + g * 32 + s * 16;
-      at[i][s] = k < a.h ? k : 0;
-    }
+  for (int s = 0; s < 2; ++s) {
+    const int k = at + (NB - 1) * 8 * kBlock + s * 16;
+    end_at[s] = k < a.h ? k : 0;
   }
   u32x4 w[2][NB][2];
-  auto load = [&](int tile, u32x4 (&dst)[NB][2]) {
+  float sw[2];  // lane i: the scale of block i
+  auto load = [&](int tile, u32x4 (&dst)[NB][2], float& scale) {
     const int v = tile * 16 + r;
     const uint8_t* p = a.weight + static_cast<int64_t>(v < a.V ? v : a.V - 1) * a.ld_w;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) dst[i][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + at[i][s]));
+      for (int s = 0; s < 2; ++s)
+        dst[i][s] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(p + (i + 1 < NB ? at + i * 8 * kBlock + s * 16 : end_at[s])));
+    scale = a.sw[static_cast<int64_t>(tile / 8) * a.ld_s + min(wave + (lane & 7) * 8, a.blocks - 1)];
   };
-  auto work = [&](int tile, int buf, u32x4 (&src)[NB][2]) {
-    const float* sw = a.sw + static_cast<int64_t>(tile / 8) * a.ld_s;
+  auto work = [&](int tile, int buf, u32x4 (&src)[NB][2], float scale) {
     f32x4_t acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int kb = wave + i * 8;
-      const f32x4_t p = mfma_16_wide(join(src[i][0], src[i][1]), x[i], f32x4_t{0.f, 0.f, 0.f, 0.f});
-      const float f = (kb < a.blocks ? sw[kb] : 0.f) * sx[i];
-      // a block that is not there must not count, whatever its stand-in holds
-      if (kb < a.blocks) {
+      if (i + 1 == NB && !all) break;
+      if (NB > 6) asm volatile("" : "+v"(x[i]));  // widened anew: the registers hold no more
+      const f32x4_t p = mfma_16(widen(join(src[i][0], src[i][1])), widen(x[i]), f32x4_t{0.f, 0.f, 0.f, 0.f});
+      const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), i)) * sx[i];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
-      }
+      for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
     }
     // lane: rows 4 g .. + 3 of the head, row r of x
     *reinterpret_cast<f32x4_t*>(&sums[buf][wave][r * 16 + g * 4]) = acc;
-    __syncthreads();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // not for the loads under way
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     if (threadIdx.x < 256) {
       float s = 0.f;
 #pragma unroll
@@ -419,14 +474,14 @@ __global__ void __launch_bounds__(512, 2) k_fp8_few(TileArgs a) {
   };
   const int step = gridDim.x;
   int tile = blockIdx.x;
-  if (tile < tiles) load(tile, w[0]);
+  if (tile < tiles) load(tile, w[0], sw[0]);
   while (tile < tiles) {
-    if (tile + step < tiles) load(tile + step, w[1]);
-    work(tile, 0, w[0]);
+    if (tile + step < tiles) load(tile + step, w[1], sw[1]);
+    work(tile, 0, w[0], sw[0]);
     tile += step;
     if (tile >= tiles) break;
-    if (tile + step < tiles) load(tile + step, w[0]);
-    work(tile, 1, w[1]);
+    if (tile + step < tiles) load(tile + step, w[0], sw[0]);
+    work(tile, 1, w[1], sw[1]);
     tile += step;
   }
 }
@@ -459,13 +514,15 @@ hipError_t launch_few(const TileArgs& a, hipStream_t s) {
 
 constexpr int64_t kMostGroups = int64_t(1) << 23;  // of 256 threads in a launch: below 2^32 work-items
 
+int64_t sx_pitch(int64_t T) { return (T + 3) / 4 * 4; }
+
 size_t rows_bytes(int64_t T, int64_t h) { return (size_t(T) * ((h + kBlock - 1) / kBlock) * kBlock + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t fp8_workspace_bytes(int64_t T, int64_t h, int64_t V) {
   (void)V;
-  return rows_bytes(T, h) + (size_t(T) * ((h + kBlock - 1) / kBlock) * 4 + 255) / 256 * 256;
+  return rows_bytes(T, h) + ((size_t(sx_pitch(T)) * ((h + kBlock - 1) / kBlock) + 256) * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t s) {
@@ -485,14 +542,15 @@ hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t 
   float* sx = reinterpret_cast<float*>(ws + rows_bytes(f.T, f.h));
   a.xq = xq;
   a.sx = sx;
+  a.pitch_sx = sx_pitch(f.T);
   const int64_t parts = (f.T * a.blocks + 15) / 16;
   for (int64_t p = 0; p < parts; p += kMostGroups) {
     const dim3 grid(static_cast<unsigned>(parts - p < kMostGroups ? parts - p : kMostGroups));
     TimedLaunch tl("k_fp8_rows", s);
     if (dtype == 0)
-      hipLaunchKernelGGL(k_fp8_rows<Bf16>, grid, dim3(256), 0, s, f, xq, sx, a.blocks, p * 16);
+      hipLaunchKernelGGL(k_fp8_rows<Bf16>, grid, dim3(256), 0, s, f, xq, sx, sx_pitch(f.T), a.blocks, p * 16);
     else
-      hipLaunchKernelGGL(k_fp8_rows<Fp16>, grid, dim3(256), 0, s, f, xq, sx, a.blocks, p * 16);
+      hipLaunchKernelGGL(k_fp8_rows<Fp16>, grid, dim3(256), 0, s, f, xq, sx, sx_pitch(f.T), a.blocks, p * 16);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -510,8 +568,7 @@ hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t 
   }
   if (a.out_dtype == 2) {
     if (a.T <= 64) return launch_tile<64, 4, 2, true>(a, s);
-    if (a.T <= 128) return launch_tile<128, 4, 2, true>(a, s);
-    return launch_tile<256, 4, 2, true>(a, s);
+    return launch_tile<128, 4, 2, true>(a, s);
   }
   if (a.T <= 64) return launch_tile<64, 4, 2, false>(a, s);
   if (a.T <= 128) return launch_tile<128, 4, 2, false>(a, s);
