@@ -199,29 +199,56 @@ __device__ __forceinline__ void store_results(void* out, int dtype, int64_t at, 
   }
 }
 
-template <int BN, int WGM, int WGN>
+// To LDS, with no registers between: 16 bytes a lane (read once, so not kept in
+// the caches), and one float that all lanes take.
+__device__ __forceinline__ void load16_once(const dtl_rsrc_t& rsrc, unsigned char* to, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)(to), 16, at, 0, 0, 2);
+#else
+  (void)rsrc, (void)to, (void)at;
+#endif
+}
+__device__ __forceinline__ void load4_same(const dtl_rsrc_t& rsrc, unsigned char* to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)(to), 4, 0, 0, 0, 0);
+#else
+  (void)rsrc, (void)to;
+#endif
+}
+
+// The 16-byte chunk c of row r of 128 bytes lies at place c ^ chunk_swz(r): reads
+// of 16 bytes take 16 lanes at a time, here the same 8 places of two chunks, which
+// then differ in a bit (0.9 M cycles of conflicts a CU in 4096 rows without).
+__device__ __forceinline__ int chunk_swz(int r) { return r & 7; }
+
+template <int BM_, int BN, int WGM, int WGN, int STAGES_>
 struct Fp8Tile {
-  static constexpr int BM = 256, NW = WGM * WGN, NT = 64 * NW;
+  static constexpr int BM = BM_, STAGES = STAGES_, NW = WGM * WGN, NT = 64 * NW;
   static constexpr int MI = BM / WGM / 16, NI = BN / WGN / 16;     // 16 x 16 products of a wave
   static constexpr int A_INST = BM / 8 / NW, B_INST = BN / 8 / NW;  // 1 KB loads a wave and stage
   static constexpr int ROWS = (BM + BN) * kBlock;                   // bytes of both operands' rows
-  static constexpr int STAGE = ROWS + 1024;                         // and the scales of up to 256 rows of x
+  static constexpr int STAGE = ROWS + 1024 + NW * 256;              // and the scales of up to 256 rows of x and of each wave's rows of the head
   static constexpr int OUT_PITCH = MI * 16 + 4;                     // floats of a row staged for output
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BN <= 256, "whole loads a wave");
-  static_assert(NW * 32 * OUT_PITCH * 4 <= 2 * STAGE, "output staging fits the stages");
+  static_assert(BM / WGM <= kBlock, "a wave's rows of the head lie in one block of scales");
+  static_assert(NW * 32 * OUT_PITCH * 4 <= STAGES * STAGE, "output staging fits the stages");
 };
 
-// One block of 256 x BN: K in steps of 128 (one scale block) through two LDS
-// stages, filled direct to LDS.  A step's products are 16x16x128, a whole scale
-// block each, so a partial sum takes four registers and is scaled while the next
-// products run.  The step's last column of products is held back: behind it the
-// next stage has arrived and this one is free (one barrier a step), and the first
+// One block of BM x BN: K in steps of 128 (one scale block) through LDS stages,
+// filled direct to LDS with the step's scales.  A step's products are 16x16x128, a
+// whole scale block each, so a partial sum takes four registers and is scaled while
+// the next products run.  The step's last column of products is held back: behind it
+// the next stage has arrived and this one is free (one barrier a step), and the first
 // operands of the next step are read while it runs.
-template <int BN, int WGM, int WGN, bool WIDE>
+// 4096 x 7168 x 129280 to bf16: 3.5 ms, 2160 TFLOP/s, the matrix cores busy in 51% of
+// the cycles and the clock near 2.05 GHz; a step of 256 x 256 is 2048 cycles of
+// products, some 1300 of scaling on the same SIMDs and 1500 of LDS, which two waves a
+// SIMD overlap in part.
+template <int BM, int BN, int WGM, int WGN, int STAGES, bool WIDE>
 __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
-  using C = Fp8Tile<BN, WGM, WGN>;
+  using C = Fp8Tile<BM, BN, WGM, WGN, STAGES>;
   constexpr int MI = C::MI, NI = C::NI, NW = C::NW;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * C::STAGE];
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[STAGES * C::STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WGM, wn = wave / WGM;
@@ -245,7 +272,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   // chunk kc ^ swizzle(r), the same kc for every j.  Rows past the operand are its
   // last one again; behind the last column the chunk in front of the row's last
   // block stands in, against zeros of x.
-  const int r = wave * 8 + (lane >> 3), kc = (lane & 7) ^ lds_swz(r);
+  const int r = wave * 8 + (lane >> 3), kc = (lane & 7) ^ chunk_swz(r);
   const dtl_rsrc_t wrsrc = dtl_rsrc(a.weight + static_cast<int64_t>(v0) * a.ld_w), xrsrc = dtl_rsrc(a.xq + t0 * hp);
   const uint32_t tail = static_cast<uint32_t>(kc * 16) >= static_cast<uint32_t>(a.h - (a.blocks - 1) * kBlock) ? kc * 16u : 0u;
   // row r of every 8 NW of an operand, no further than its last
@@ -254,6 +281,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   };
   const uint32_t ld_w = static_cast<uint32_t>(a.ld_w), ld_x = static_cast<uint32_t>(hp);
   const uint32_t last_w = static_cast<uint32_t>(min(M, C::BM) - 1) * ld_w, last_x = static_cast<uint32_t>(N - 1) * ld_x;
+  // this wave's rows of the head lie in one block of scales
+  const float* sw = a.sw + static_cast<int64_t>(min(v0 + wm * C::MI * 16, a.V - 1) / kBlock) * a.ld_s;
   auto issue = [&](int kt, unsigned char* stage) {
     const uint32_t back = kt == a.blocks - 1 ? tail : 0u;
 #pragma unroll
@@ -267,10 +296,11 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
     if (wave == 0)
       dtl_load16(dtl_rsrc(a.sx + static_cast<int64_t>(kt) * a.pitch_sx + t0), reinterpret_cast<uint16_t*>(stage + C::ROWS), lane * 16u,
                  0);
+    load4_same(dtl_rsrc(sw + kt), stage + C::ROWS + 1024 + wave * 256);
   };
   // 32 bytes of K of one operand row: chunks g and 4 + g, for both operands alike
   // (the order within K is free).
-  const int r16 = lane & 15, g = lane >> 4, z16 = lds_swz(r16);
+  const int r16 = lane & 15, g = lane >> 4, z16 = chunk_swz(r16);
   auto fragment = [&](const unsigned char* rows, int row) {
     const unsigned char* p = rows + (row + r16) * kBlock;
     return join(*reinterpret_cast<const u32x4*>(p + ((g ^ z16) << 4)), *reinterpret_cast<const u32x4*>(p + (((4 + g) ^ z16) << 4)));
@@ -281,16 +311,13 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
     return reinterpret_cast<const float*>(stage + C::ROWS)[(wn * NI + ni) * 16 + r16];
   };
 
+  auto scale_a = [&](const unsigned char* stage) { return *reinterpret_cast<const float*>(stage + C::ROWS + 1024 + wave * 256); };
+
   f32x4_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  // this wave's rows of W lie in one block of scales
-  const float* sw = a.sw + static_cast<int64_t>(min(v0 + wm * MI * 16, a.V - 1) / kBlock) * a.ld_s;
-  int none = 0;  // loaded by lanes: a scalar load would be waited for with the reads of LDS
-  asm("" : "+v"(none));
 
   using Frag = std::conditional_t<WIDE, Wide, i32x8>;
   auto as_operand = [](i32x8 x) {
@@ -301,21 +328,29 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   };
   Frag fa[MI];
   i32x8 fb[2];
-  float fx[2], w = sw[0], w_next = 0.f;
-  issue(0, lds);
-  if (a.blocks > 1) issue(1, lds + C::STAGE);
-  // the first stage has arrived when only the second's loads are under way
-  if (a.blocks > 1 && wave == 0)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::A_INST + C::B_INST + 1) : "memory");
-  else if (a.blocks > 1)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::A_INST + C::B_INST) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  float fx[2];
+  // the oldest of the stages under way has arrived when only the others' loads are not back
+  constexpr int LOADS = C::A_INST + C::B_INST + 1;
+#define LP_FP8_ARRIVED(others)                                                                \
+  if (wave == 0)                                                                              \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((others) * (LOADS + 1)) : "memory"); \
+  else                                                                                        \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((others) * LOADS) : "memory")
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+    if (i < a.blocks) issue(i, lds + i * C::STAGE);
+  if (a.blocks >= STAGES) {
+    LP_FP8_ARRIVED(STAGES - 1);
+  } else {
+    LP_FP8_ARRIVED(0);
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) fa[mi] = as_operand(frag_a(lds, mi));
   fb[0] = frag_b(lds, 0);
   fx[0] = scale_b(lds, 0);
+  float w = scale_a(lds), w_next = 0.f;
 
   // Products of a column and, between them, the scaling of those of the column
   // before (of the last step's last column at first).
@@ -329,9 +364,11 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
     for (int i = 0; i < 4; ++i) to[i] = fmaf(p[i], f_before, to[i]);
     asm volatile("" : "+v"(to));  // here, or the compiler keeps a whole step's parts for the end
   };
+  int stage = 0;
   for (int kt = 0; kt < a.blocks; ++kt) {
-    unsigned char* X = lds + (kt & 1) * C::STAGE;
-    unsigned char* Y = lds + ((kt + 1) & 1) * C::STAGE;
+    unsigned char* X = lds + stage * C::STAGE;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    unsigned char* Y = lds + stage * C::STAGE;
     const bool next = kt + 1 < a.blocks;
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) {
@@ -341,13 +378,18 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
         fx[cur ^ 1] = scale_b(X, ni + 1);
       } else {
         // every operand of this step is in registers
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __syncthreads();
+        if (STAGES > 2 && kt + STAGES <= a.blocks) {
+          LP_FP8_ARRIVED(STAGES - 2);
+        } else {
+          LP_FP8_ARRIVED(0);
+        }
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
         if (next) {
-          w_next = sw[kt + 1 + none];
-          if (kt + 2 < a.blocks) issue(kt + 2, X);
+          if (kt + STAGES < a.blocks) issue(kt + STAGES, X);
           fb[cur ^ 1] = frag_b(Y, 0);
           fx[cur ^ 1] = scale_b(Y, 0);
+          w_next = scale_a(Y);
         }
       }
       const float f = w * fx[cur];
@@ -366,6 +408,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
   }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) add(acc[mi][NI - 1], part[1][mi]);
+#undef LP_FP8_ARRIVED
   __syncthreads();
 
   // Out: 32 rows at a time through LDS of the wave's own, so that a row's
@@ -406,89 +449,123 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) k_fp8_tile(TileArgs a) {
 // few rows: the head passes by once
 // ---------------------------------------------------------------------------
 
-// Up to 16 rows of x.  K is split over the 8 waves of a workgroup, whose blocks
-// of x stay in registers; the workgroups walk over the head 16 rows at a time,
-// the next 16 rows' bytes and scales in flight.
-template <int NB>
+// Up to 16 XT rows of x.  K is split over the 8 waves of a workgroup, whose blocks
+// of x stay in registers; the workgroups walk over the head 16 rows at a time.  A
+// wave's pieces of 16 rows x 128 columns, with the piece's scale, come through a
+// ring of its own in LDS, whose other slots are on their way: whole lines of 128
+// bytes a row, and no registers held by what is in flight (8 rows of 5120 x 151936
+// 125 us, 6.3 TB/s, bound by reading the head; with pieces of 16 bytes a row through
+// registers 184, with loads that stay in the caches 148).
+constexpr int few_slots(int XT) { return XT == 1 ? 8 : XT == 2 ? 7 : 5; }
+
+template <int NB, int XT, bool WIDE>
 __global__ void __launch_bounds__(512, 2) k_fp8_few(TileArgs a) {
-  __shared__ float sums[2][8][256];
+  constexpr int R = few_slots(XT), SLOT = 16 * kBlock + 256;
+  __shared__ __attribute__((aligned(256))) unsigned char ring[8 * R * SLOT];
+  __shared__ float sums[2][XT][8][256];
+  static_assert(sizeof(ring) + sizeof(sums) <= 160 * 1024, "LDS of a CU");
+  using Operand = std::conditional_t<WIDE, Wide, i32x8>;
+  auto as_operand = [](i32x8 x) {
+    if constexpr (WIDE)
+      return widen(x);
+    else
+      return x;
+  };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int T = static_cast<int>(a.T), hp = a.blocks * kBlock, tiles = (a.V + 15) / 16;
   // wave's blocks: wave, wave + 8, ...; of them only the last may not be there
   const bool all = wave + (NB - 1) * 8 < a.blocks;
-  i32x8 x[NB];
-  float sx[NB];
+  const int mine = all ? NB : NB - 1;
+  i32x8 x[XT][NB];
+  float sx[XT][NB];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int kb = i + 1 < NB || all ? wave + i * 8 : 0, t = r < T ? r : T - 1;
-    const u32x4* p = reinterpret_cast<const u32x4*>(a.xq + static_cast<int64_t>(t) * hp + kb * kBlock + g * 32);
-    x[i] = join(p[0], p[1]);
-    sx[i] = a.sx[static_cast<int64_t>(kb) * a.pitch_sx + t];
-  }
-  // the lane's bytes of a row of the head; those behind its end are its first ones (against zeros)
-  const int at = wave * kBlock + g * 32;
-  int end_at[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int k = at + (NB - 1) * 8 * kBlock + s * 16;
-    end_at[s] = k < a.h ? k : 0;
-  }
-  u32x4 w[2][NB][2];
-  float sw[2];  // lane i: the scale of block i
-  auto load = [&](int tile, u32x4 (&dst)[NB][2], float& scale) {
-    const int v = tile * 16 + r;
-    const uint8_t* p = a.weight + static_cast<int64_t>(v < a.V ? v : a.V - 1) * a.ld_w;
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        dst[i][s] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(p + (i + 1 < NB ? at + i * 8 * kBlock + s * 16 : end_at[s])));
-    scale = a.sw[static_cast<int64_t>(tile / 8) * a.ld_s + min(wave + (lane & 7) * 8, a.blocks - 1)];
-  };
-  auto work = [&](int tile, int buf, u32x4 (&src)[NB][2], float scale) {
-    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < XT; ++n)
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      if (i + 1 == NB && !all) break;
-      if (NB > 6) asm volatile("" : "+v"(x[i]));  // widened anew: the registers hold no more
-      const f32x4_t p = mfma_16(widen(join(src[i][0], src[i][1])), widen(x[i]), f32x4_t{0.f, 0.f, 0.f, 0.f});
-      const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), i)) * sx[i];
+      const int kb = i < mine ? wave + i * 8 : 0, t = min(n * 16 + r, T - 1);
+      const u32x4* p = reinterpret_cast<const u32x4*>(a.xq + static_cast<int64_t>(t) * hp + kb * kBlock);
+      x[n][i] = join(p[g], p[4 + g]);
+      sx[n][i] = a.sx[static_cast<int64_t>(kb) * a.pitch_sx + t];
+    }
+
+  // A piece: two loads of 8 rows (lane: row lane / 8, chunk kc) and one of the
+  // scale (every lane the same).  Rows behind the head are its last one again;
+  // behind the last column the row's first chunk of that block stands in, against zeros of x.
+  unsigned char* const own = ring + wave * (R * SLOT);
+  const int row = lane >> 3, kc0 = (lane & 7) ^ chunk_swz(row), kc1 = (lane & 7) ^ chunk_swz(row + 8);
+  const int last_bytes = a.h - (a.blocks - 1) * kBlock;
+  const uint32_t ld = static_cast<uint32_t>(a.ld_w);
+  int put_tile = blockIdx.x, put_i = 0, put_slot = 0;
+  auto put = [&]() {
+    const int v = put_tile * 16, kb = wave + put_i * 8, last = min(15, a.V - 1 - v);
+    const int end = kb == a.blocks - 1 ? last_bytes : kBlock;
+    const dtl_rsrc_t w = dtl_rsrc(a.weight + static_cast<int64_t>(v) * a.ld_w + kb * kBlock);
+    unsigned char* to = own + put_slot * SLOT;
+    load16_once(w, to, static_cast<uint32_t>(min(row, last)) * ld + (kc0 * 16 < end ? kc0 * 16 : 0));
+    load16_once(w, to + 1024, static_cast<uint32_t>(min(row + 8, last)) * ld + (kc1 * 16 < end ? kc1 * 16 : 0));
+    load4_same(dtl_rsrc(a.sw + static_cast<int64_t>(put_tile / 8) * a.ld_s + kb), to + 2048);
+    if (++put_i == mine) put_i = 0, put_tile += gridDim.x;
+    put_slot = put_slot + 1 == R ? 0 : put_slot + 1;
+  };
+  if (mine > 0)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], f, acc[q]);
+    for (int i = 0; i < R; ++i)
+      if (put_tile < tiles) put();
+
+  const int z = chunk_swz(r);
+  int slot = 0, buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    f32x4_t acc[XT];
+#pragma unroll
+    for (int n = 0; n < XT; ++n) acc[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (i + 1 == NB && !all) continue;
+      // the oldest piece has arrived when only the others' loads are under way
+      if (put_tile < tiles)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * (R - 1)) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const unsigned char* p = own + slot * SLOT;
+      const i32x8 wq = join(*reinterpret_cast<const u32x4*>(p + r * kBlock + ((g ^ z) << 4)),
+                            *reinterpret_cast<const u32x4*>(p + r * kBlock + (((4 + g) ^ z) << 4)));
+      const float sw = *reinterpret_cast<const float*>(p + 2048);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (put_tile < tiles) put();  // into the slot just read
+      slot = slot + 1 == R ? 0 : slot + 1;
+      const Operand w = as_operand(wq);
+#pragma unroll
+      for (int n = 0; n < XT; ++n) {
+        if (WIDE && NB * XT > 8) asm volatile("" : "+v"(x[n][i]));  // widened anew: the registers hold no more
+        const f32x4_t q = mfma_16(w, as_operand(x[n][i]), f32x4_t{0.f, 0.f, 0.f, 0.f});
+        const float f = sw * sx[n][i];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[n][k] = fmaf(q[k], f, acc[n][k]);
+      }
     }
     // lane: rows 4 g .. + 3 of the head, row r of x
-    *reinterpret_cast<f32x4_t*>(&sums[buf][wave][r * 16 + g * 4]) = acc;
+#pragma unroll
+    for (int n = 0; n < XT; ++n) *reinterpret_cast<f32x4_t*>(&sums[buf][n][wave][r * 16 + g * 4]) = acc[n];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // not for the loads under way
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (threadIdx.x < 256) {
+#pragma unroll
+    for (int e = threadIdx.x; e < XT * 256; e += 512) {
       float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += sums[buf][k][threadIdx.x];
-      const int t = threadIdx.x >> 4, v = tile * 16 + (threadIdx.x & 15);
+      for (int k = 0; k < 8; ++k) s += sums[buf][e >> 8][k][e & 255];
+      const int t = e >> 4, v = tile * 16 + (e & 15);
       if (t < T && v < a.V) store_results<1>(a.out, a.out_dtype, (a.t0 + t) * a.ld_out + v, &s, 1);
     }
-  };
-  const int step = gridDim.x;
-  int tile = blockIdx.x;
-  if (tile < tiles) load(tile, w[0], sw[0]);
-  while (tile < tiles) {
-    if (tile + step < tiles) load(tile + step, w[1], sw[1]);
-    work(tile, 0, w[0], sw[0]);
-    tile += step;
-    if (tile >= tiles) break;
-    if (tile + step < tiles) load(tile + step, w[0], sw[0]);
-    work(tile, 1, w[1], sw[1]);
-    tile += step;
   }
 }
 
-template <int BN, int WGM, int WGN, bool WIDE>
+template <int BM, int BN, int WGM, int WGN, int STAGES, bool WIDE>
 hipError_t launch_tile(TileArgs a, hipStream_t s) {
-  a.n_vb = (a.V + 255) / 256;
+  a.n_vb = (a.V + BM - 1) / BM;
   // blocks of a launch: below 2^32 work-items whatever T
   const int64_t most = (int64_t(1) << 22) / a.n_vb > 0 ? (int64_t(1) << 22) / a.n_vb : 1;
   const int64_t T = a.T;
@@ -497,18 +574,20 @@ hipError_t launch_tile(TileArgs a, hipStream_t s) {
     a.t0 = t0;
     a.n_nb = static_cast<int>((rows + BN - 1) / BN);
     TimedLaunch tl("k_fp8_tile", s);
-    hipLaunchKernelGGL((k_fp8_tile<BN, WGM, WGN, WIDE>), dim3(static_cast<unsigned>(a.n_vb * a.n_nb)), dim3(64 * WGM * WGN), 0, s, a);
+    hipLaunchKernelGGL((k_fp8_tile<BM, BN, WGM, WGN, STAGES, WIDE>), dim3(static_cast<unsigned>(a.n_vb * a.n_nb)), dim3(64 * WGM * WGN), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int NB>
+template <int XT, bool WIDE, int NB = 8>
 hipError_t launch_few(const TileArgs& a, hipStream_t s) {
+  if constexpr (NB > 1)
+    if ((a.blocks + 7) / 8 < NB) return launch_few<XT, WIDE, NB - 1>(a, s);
   const int tiles = (a.V + 15) / 16;
   TimedLaunch tl("k_fp8_few", s);
-  hipLaunchKernelGGL(k_fp8_few<NB>, dim3(tiles < 256 ? tiles : 256), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((k_fp8_few<NB, XT, WIDE>), dim3(tiles < 256 ? tiles : 256), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
@@ -554,25 +633,23 @@ hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.T <= 16 && a.blocks <= 64) {
-    switch ((a.blocks + 7) / 8) {
-      case 1: return launch_few<1>(a, s);
-      case 2: return launch_few<2>(a, s);
-      case 3: return launch_few<3>(a, s);
-      case 4: return launch_few<4>(a, s);
-      case 5: return launch_few<5>(a, s);
-      case 6: return launch_few<6>(a, s);
-      case 7: return launch_few<7>(a, s);
-      default: return launch_few<8>(a, s);
-    }
-  }
+  // The ring reads each line of the head once, the tiles read x again for each block of
+  // it; rows beyond 32 find no registers (17 rows of 5120 x 129280 127 us against 141
+  // in tiles, 32 rows of 8192 x 129280 190 against 210).
+  if (a.T <= 16 && a.blocks <= 64) return launch_few<1, true>(a, s);
+  if (a.T <= 32 && a.blocks <= 64) return a.out_dtype == 2 ? launch_few<2, true>(a, s) : launch_few<2, false>(a, s);
+  // fp32 results: widened operands, whose products keep every bit; rounded to 16 bits
+  // the 8-bit products' own error (2^-15 of a result) is far below the rounding.
+  // Tiles no wider than the rows need, and two workgroups a CU where they fit: 64 rows
+  // of 5120 x 151936 182 us against 219 in tiles of 256 x 64, 128 rows 209 against 234
+  // in 256 x 128, 512 rows to fp32 807 against 875.
   if (a.out_dtype == 2) {
-    if (a.T <= 64) return launch_tile<64, 4, 2, true>(a, s);
-    return launch_tile<128, 4, 2, true>(a, s);
+    if (a.T <= 64) return launch_tile<128, 64, 2, 2, 3, true>(a, s);
+    return launch_tile<128, 128, 2, 2, 2, true>(a, s);
   }
-  if (a.T <= 64) return launch_tile<64, 4, 2, false>(a, s);
-  if (a.T <= 128) return launch_tile<128, 4, 2, false>(a, s);
-  return launch_tile<256, 4, 2, false>(a, s);
+  if (a.T <= 64) return launch_tile<128, 64, 2, 2, 3, false>(a, s);
+  if (a.T <= 128) return launch_tile<128, 128, 2, 2, 2, false>(a, s);
+  return launch_tile<256, 256, 4, 2, 2, false>(a, s);
 }
 
 hipError_t launch_fp8_quantize(int dtype, const Fp8QuantArgs& a, hipStream_t s) {
