@@ -226,13 +226,19 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
       clear();
       return;
     }
-    gr.nl = -lse * kLog2e;
-    gr.all = static_cast<float>(all * g);
+    // What rounding lse log2(e) to fp32 takes off every exponent of the row (1e-6 of the
+    // probabilities at lse = 20) goes into the row's factors; the sum is taken with the
+    // log2(e) / tau that c holds, so that both of an exponent's terms are off alike.
+    const double log2e = static_cast<double>(c) / a.inv_tau;
+    const double el = -lse * log2e, er = -lse_rest * log2e;
+    gr.nl = static_cast<float>(el);
+    gr.all = static_cast<float>(all * g) * fast_exp2(static_cast<float>(el - gr.nl));
     gr.gt = static_cast<float>(g);
     // with no weight outside the list, or none that fp32 tells apart, those columns get 0
     const bool none = fabsf(lse_rest) > kFarLse;
-    gr.nr = none ? neg_inf() : -lse_rest * kLog2e;
-    gr.others = none ? 0.f : static_cast<float>((all * exp(static_cast<double>(lse_rest) - static_cast<double>(lse)) - r) * g);
+    gr.nr = none ? neg_inf() : static_cast<float>(er);
+    gr.others = none ? 0.f : static_cast<float>((all * exp(static_cast<double>(lse_rest) - static_cast<double>(lse)) - r) * g) *
+                            fast_exp2(static_cast<float>(er - gr.nr));
   }
 
   LaneSum st = sum_none(), listed = sum_none();
