@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
     // U W pieces of `steps` times 64 vectors, so that one step of the workgroup is a
     // sample of the whole; a wave goes from piece to piece, so that each has its
     // share of a piece that holds more of what is kept.  What is left over behind
-    // the pieces comes last.
+    // the pieces comes last.  There is at least one step: n >= 4 NT P (set_slices).
     const int vectors = n / P, steps = vectors / (64 * U * W);
     const char* base = xp;  // 32-bit offsets: a slice has at most 2^32 bytes
     auto load = [&](uint32_t v) {
@@ -646,7 +646,9 @@ int short_slice(int dtype, int threads) { return 4 * threads * (dtype == 2 ? 4 :
 
 // Slices per row: one where there are rows for four workgroups a CU and more,
 // else as many as that takes, none shorter than what a workgroup keeps
-// whole, and no more keys than a join takes.
+// whole, and no more keys than a join takes.  Slices are either short ones that are
+// kept whole or each of them, a row's last one too, has the columns of a step of
+// the stream, which has no end without one.
 void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
   const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
@@ -655,8 +657,14 @@ void set_slices(TopArgs& a, int dtype) {
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
   n = n < most_keys ? n : most_keys;
-  a.slice = static_cast<int>(((int64_t(a.V) + n - 1) / n + 63) / 64 * 64);
-  a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
+  const int64_t kept = short_slice(dtype, threads_of(a.K));
+  int64_t last;
+  do {
+    a.slice = static_cast<int>(((int64_t(a.V) + n - 1) / n + 63) / 64 * 64);
+    a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
+    last = a.V - int64_t(a.nslices - 1) * a.slice;
+    n = a.nslices - 1;  // fewer, longer ones; one alone is longer than `kept` if it is not short
+  } while (a.slice > kept && last < kept);
 }
 
 template <class Tr, int NT, bool SHORT>

@@ -246,3 +246,23 @@ def test_workspace_sizes(lib_handle):
     assert L.lp_beam_workspace_bytes(0, 64, 8, 129280, 16) > 0
     for bad in ((7, 1, 1, 10, 1), (0, -1, 1, 10, 1), (0, 1, 65, 10, 1), (0, 1, 64, 10, 65), (0, 1, 1, 0, 1)):
         assert L.lp_beam_workspace_bytes(*bad) == 0
+
+
+def test_no_streamed_slice_is_shorter_than_a_step(lib_handle):
+    """Slices of a row are kept whole (at most 4 vectors a thread: 256 threads up to K = 64, else 512), or all of them
+    hold a step of the stream, as many columns.  Seen through the workspace, which has 8 K + 8 bytes a slice."""
+    rng = np.random.default_rng(0)
+    cases = [(2, 80, 60740, 22), (0, 68, 135830, 43), (2, 35, 159221, 225), (0, 1, 151936, 20), (1, 1, 8193, 5)]
+    for _ in range(3000):
+        V = int(2 ** rng.uniform(10, 18))
+        cases.append((int(rng.integers(0, 3)), int(2 ** rng.uniform(0, 10)), V, int(rng.integers(1, min(256, V) + 1))))
+    for dtype, T, V, K in cases:
+        size = lib_handle.lp_top_workspace_bytes(dtype, T, V, K)
+        per = T * (8 * K + 8)
+        counts = [n for n in range(2, 1025) if -(-n * per // 256) * 256 == size]
+        if len(counts) != 1:
+            continue  # one slice, or sizes that say nothing
+        n = counts[0]
+        kept = 4 * (512 if K > 64 else 256) * (4 if dtype == 2 else 8)
+        slices = [s for s in range(64, V + 64, 64) if -(-V // s) == n] if T < 4 else [-(-(-(-V // n)) // 64) * 64]
+        assert any(s <= kept or V - (n - 1) * s >= kept for s in slices), (dtype, T, V, K, n)

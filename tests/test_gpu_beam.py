@@ -157,3 +157,12 @@ def test_reorder_past_four_gigabytes():
     got = _lp().lp_beam_reorder(x, torch.tensor([[2, 0, 2]], dtype=torch.int32, device="cuda"))
     for k, w in enumerate((2, 0, 2)):
         assert torch.equal(got[k], x[w])
+
+
+@pytest.mark.parametrize("N", [8, 16])
+def test_rows_whose_last_slice_is_shorter(N):
+    rng = np.random.default_rng(N)
+    B, W, V = 10, 8, 53277
+    bits, z = peaked(rng, B * W, V, "fp32")
+    s = clear_scores(rng, z, B, W, N, None, 0, 1.0)
+    check(dev_rows(bits, "fp32"), z, s, N, None, 0, 1.0)

@@ -151,3 +151,40 @@ def test_a_vocabulary_at_the_limit():
     close(host(lse), [np.log(s)], 1e-5)
     close(host(rest), [np.log((V - 4) / s)], 1e-5)
     close(host(p)[0], np.array([30, 30, 20, 0]) - np.log(s), 2e-5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,K", [(600, 20011, 3), (600, 20011, 200), (2, 70001, 3)])
+def test_rests_and_peaks_anywhere(dtype, T, V, K):
+    """The rest far below the list, a rest that lies in a few columns above a far lower floor, values far above the
+    first columns', and columns to keep that all lie in one stretch."""
+    rng = np.random.default_rng(5)
+    z = rng.normal(0, 1, (6, V))
+    z[0] -= 150.0
+    z[0, rng.choice(V, K, replace=False)] += 150.0       # all else 100 to 200 octaves below
+    z[1] -= 300.0
+    z[1, rng.choice(V, K + 2, replace=False)] += np.linspace(300, 330, K + 2)
+    z[2, V - 5:] += 120.0                                 # the end of the row above all before it
+    z[3, V // 2:V // 2 + 700] += np.linspace(3, 9, 700)   # one stretch
+    z[4, :K] += np.linspace(200, 100, K)                  # the first columns
+    z[5, 1::2] = -np.inf
+    bits = to_bits(z, dtype)
+    many = np.tile(bits, (T // 6 + 1, 1))[:T]
+    x = dev_rows(many, dtype)
+    got = [host(g) for g in _lp().lp_top_logits(x, K)]
+    rows = min(T, 6)
+    want = O.top_logits(O.widen(bits[:rows], dtype), K, None, 1.0)
+    assert np.array_equal(got[0][:rows], want[0])
+    for g, w in zip(got[1:], want[1:]):
+        close(g[:rows], w, tol_log(w, 2))
+    for g in got:  # equal rows have equal bits
+        assert all(np.array_equal(g[t], g[t % 6]) for t in range(T))
+
+
+@pytest.mark.parametrize("T,V,K,dtype", [(80, 60740, 22, "fp32"), (68, 135830, 43, "bf16"), (35, 159221, 225, "fp32"),
+                                         (51, 60741, 22, "fp32"), (11, 32970, 250, "fp16")])
+def test_rows_whose_last_slice_is_shorter(T, V, K, dtype):
+    """Slices that are streamed: the last one of a row holds what the others' rounding leaves of it."""
+    rng = np.random.default_rng(V)
+    bits, z = peaked(rng, T, V, dtype)
+    check(dev_rows(bits, dtype), z, K, 1.0)
