@@ -1046,7 +1046,7 @@ def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
         raise ValueError(f"dim {dim} is outside a state of {state.dim()} dimensions")
     dim %= state.dim()
     rows = state.size(dim)
-    if B == 0 or N == 0 or rows == 0 or rows % B:
+    if N == 0 or (rows == 0 or rows % B if B else rows):
         raise ValueError(f"{rows} rows are no beams of {B} requests that {N} slots go on from")
     shape = list(state.shape)
     shape[dim] = B * N
@@ -1065,7 +1065,7 @@ def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
             if d_mid != 1:
                 raise ValueError("out cannot be walked as the state is")
             dm = width  # the state's parts lie behind each other in out
-        st = lib.lp_beam_reorder(_ptr(state), s_outer, s_row, s_mid, outer, mid, width, _ptr(parents), B, rows // B, N,
+        st = lib.lp_beam_reorder(_ptr(state), s_outer, s_row, s_mid, outer, mid, width, _ptr(parents), B, rows // B if B else 1, N,
                                  _ptr(out), do, dr, dm, _raw_stream(dev, stream))
     check("lp_beam_reorder", st)
     return out

@@ -214,3 +214,38 @@ def test_a_vocabulary_at_the_limit():
     other = (1 / s) - 0.2 / (V - 3)
     ref = 1e6 * np.array([q[0] - 0.5, q[1] - 0.2, q[2] - 0.1, other, other, other])
     close(got, ref, 2.0 ** -8 * np.abs(ref) + 1e-4 * np.abs(ref))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V", [(900, 12007), (3, 70001)])
+def test_rests_and_peaks_anywhere(dtype, T, V):
+    """Values far above and far below the first ones that a lane reads, in the list and outside it."""
+    rng = np.random.default_rng(6)
+    K = 9
+    z = rng.normal(0, 1, (6, V))
+    z[0, V // 3:] += 100.0
+    z[1, V - 2] += 250.0
+    z[2, :4000] = -np.inf
+    z[3, 64:] -= 180.0
+    z[4, ::2] -= 240.0
+    z[5, 77] = 400.0
+    bits = to_bits(z, dtype)
+    z = O.widen(bits, dtype)
+    ids, lpk, rest = lists(rng, z, K, 1.0)
+    rows = min(T, 6)
+    want = O.distill_top(z[:rows], ids[:rows], lpk[:rows], rest[:rows], None, 1.0)
+    wide = lambda a: np.tile(a, (T // 6 + 1,) + (1,) * (a.ndim - 1))[:T]  # noqa: E731
+    x, i, p, r = dev_rows(wide(bits), dtype), to_dev(wide(ids)), to_dev(wide(lpk)), to_dev(wide(rest))
+    got = [host(g) for g in _lp().lp_distill_top(x, i, p, r)]
+    mass = np.where((ids >= 0) & (ids < V), np.exp(lpk.astype(np.float64)), 0).sum(1)[:rows] + np.exp(rest.astype(np.float64))[:rows]
+    # logits and log-sums of some hundreds: each is rounded where it is that large
+    size = np.abs(np.where(np.isfinite(want[1]), want[1], 0)) + np.abs(np.where(np.isfinite(want[2]), want[2], 0))
+    close(got[0][:rows], want[0], 2 * SUM * (1 + mass) + 2.0 ** -24 * np.abs(np.where(np.isfinite(want[0]), want[0], 0)) + mass * 2.0 ** -21 * size)
+    for g, w in zip(got[1:], want[1:]):
+        close(g[:rows], w, tol_log(w))
+    for g in got:  # equal rows have equal bits
+        assert all(np.array_equal(g[t], g[t % 6], equal_nan=True) for t in range(T))
+    gl = np.linspace(0.5, 1, T).astype(np.float32)
+    d = _lp().lp_distill_top_backward(x, i, p, r, None, 1.0, to_dev(got[1]), to_dev(got[2]), to_dev(gl))[:rows]
+    ref = O.distill_top_backward(z[:rows], ids[:rows], lpk[:rows], rest[:rows], None, 1.0, gl[:rows])
+    close(host(d.float()), ref, grad_tol(z[:rows], ids[:rows], lpk[:rows], rest[:rows], 1.0, gl[:rows], ref, dtype))

@@ -151,3 +151,22 @@ def test_empty():
     torch = _torch()
     q, s, _, _ = _head(30, 64, 1)
     assert _lp().lp_lm_head_fp8_logits(torch.zeros(0, 64, device="cuda").half(), q, s).shape == (0, 30)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,h,V", [
+    (1, 16, 9001), (4, 1040, 12293), (16, 2064, 8209), (16, 7168, 5000), (16, 8192, 4113), (17, 16, 9001), (32, 1152, 12293),
+    (31, 8192, 4200), (20, 5120, 5003), (33, 128, 40001), (40, 256, 33001), (64, 8208, 300), (65, 144, 33001), (128, 8320, 260),
+    (300, 144, 20001)])
+def test_logits_of_many_tiles(out, T, h, V):
+    """Workgroups that walk over several tiles, K that leaves waves one block fewer or none, one to many blocks."""
+    torch = _torch()
+    q, s, q64, s64 = _head(V, h, T + h + V)
+    rng = np.random.default_rng(V)
+    xb = to_bits(rng.normal(0, 1, (T, h)), "bf16")
+    want, mag = O.fp8_logits(O.widen(xb, "bf16"), q64, s64)
+    hid = to_dev_bits(xb, "bf16")
+    got = _lp().lp_lm_head_fp8_logits(hid, q, s, out_dtype=getattr(torch, OUT[out]))
+    close(host(got.float()), want, _tol(mag, h, want, out))
+    for _ in range(3):  # the same bits on every call
+        assert torch.equal(_lp().lp_lm_head_fp8_logits(hid, q, s, out_dtype=got.dtype), got)
