@@ -15,10 +15,14 @@
 //      counting, and sums what was not chosen.
 // Short slices are kept whole.  The mass outside the list is a sum of its own,
 // never a difference of two nearly equal ones.  Every result is the same bits on
-// every call: only the order of the keys that are ranked depends on LDS atomics.  Order is (value
-// descending, column ascending), as one 64-bit key.  More kept vectors than LDS
-// holds (rows that rise steadily, or have most values equal) are counted by digits
-// of the keys instead: right for any row, several more reads of it.
+// every call: only the order of the keys that are ranked depends on LDS atomics.
+// Order is (value descending, column ascending), as one 64-bit key.  More kept
+// vectors than LDS holds (rows that rise steadily, or have most values equal) are
+// counted by digits of the keys instead: right for any row, several more reads of it.
+// Bound by reading: 6144 scored rows of 151936 bf16, 64 of each, 325 us, 5.8 TB/s
+// (6.8 is what reading alone reaches); what is missing are the waits of a row's end,
+// which the other workgroups of a CU cover in part.  One row of 151936 is 17 us a
+// call, two launches; 512 of 129280 fp16, 16 of each, 38 us, 8 of them the join.
 #include "lp_internal.hpp"
 #include "lp_sums.hpp"
 
@@ -638,14 +642,16 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
 // ---------------------------------------------------------------------------
 
 // Threads of k_top: the K-th largest of the lanes' values cuts the better the more
-// lanes there are.
+// lanes there are, which K = 200 needs; with K = 20 fewer threads wait less for each
+// other (256 rows of 151936: 30 us with 256, 45 with 512).
 int threads_of(int K) { return K > kFewTop ? 512 : 256; }
 
 // Columns of a slice that k_top keeps whole.
 int short_slice(int dtype, int threads) { return 4 * threads * (dtype == 2 ? 4 : 8); }
 
-// Slices per row: one where there are rows for four workgroups a CU and more,
-// else as many as that takes, none shorter than what a workgroup keeps
+// Slices per row: one where there are rows for 1024 threads a CU and more (a batch of
+// 256 rows of 151936: K = 20 30 us, 33 with half as many; K = 200 48, 60 with twice as
+// many), else as many as that takes, none shorter than what a workgroup keeps
 // whole, and no more keys than a join takes.  Slices are either short ones that are
 // kept whole or each of them, a row's last one too, has the columns of a step of
 // the stream, which has no end without one.
@@ -653,7 +659,8 @@ void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
   const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
   const int64_t least = short_slice(dtype, 256);
-  int64_t n = (1024 + a.T - 1) / (a.T > 0 ? a.T : 1);
+  const int64_t groups = 256 * 1024 / threads_of(a.K);
+  int64_t n = (groups + a.T - 1) / (a.T > 0 ? a.T : 1);
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
   n = n < most_keys ? n : most_keys;
