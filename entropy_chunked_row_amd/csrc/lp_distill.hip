@@ -71,6 +71,11 @@ __device__ __forceinline__ double lanes_sum(double x) {
   return x;
 }
 
+// exp(t) to within 2^-23 of it: a teacher's log-probs are no better known, and the
+// fp64 function alone takes longer than all else in a short row.  The same in every
+// place, so that a row's masses agree with their sum.
+__device__ __forceinline__ double mass_of(float t) { return static_cast<double>(expf(t)); }
+
 // What the listed entries add to a row's loss before its log-sum-exps are known:
 //   loss = terms + mass lse + r (t_rest - (lse_rest - lse)).
 // The loss is a difference of nearly equal numbers: fp64.
@@ -87,7 +92,7 @@ __device__ __forceinline__ Entries sum_entries(const DistillArgs& a, int64_t row
     const int64_t id = a.ids[row * a.K + k];
     const float t = a.logprob[row * a.K + k];
     if (id < 0 || id >= a.V || t == neg_inf()) continue;  // padding, or no mass
-    const double p = exp(static_cast<double>(t));
+    const double p = mass_of(t);
     e.terms += p * (static_cast<double>(t) - static_cast<double>(Tr::load1(xp, id)) * a.inv_tau);
     e.mass += p;
   }
@@ -105,7 +110,7 @@ __device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, En
   double loss = e.terms + e.mass * lse;
   if (t_rest != neg_inf()) {
     const double t = t_rest;
-    loss += exp(t) * (t - (lse_rest - lse));
+    loss += mass_of(t_rest) * (t - (lse_rest - lse));
   }
   a.loss[row] = static_cast<float>(loss);
   if (a.lse_out) a.lse_out[row] = static_cast<float>(lse);
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     z[i] = !GRAD && inside && a.nslices == 1 ? Tr::load1(xp, id[i]) : 0.f;
     if (k < kMaxTop) cols[k] = col[i];
     if (GRAD || a.nslices == 1) {
-      const double p = inside ? exp(static_cast<double>(t[i])) : 0.0;
+      const double p = inside ? mass_of(t[i]) : 0.0;
       e.mass += p;
       if (GRAD && k < kMaxTop) mass[k] = static_cast<float>(p);
       if (!GRAD && inside && t[i] != neg_inf())
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   __syncthreads();
   GradRow gr{};
   if (GRAD) {
-    double all = a.rest ? exp(static_cast<double>(t_rest)) : 0.0;
+    double all = a.rest ? mass_of(t_rest) : 0.0;
     const double r = all, g = static_cast<double>(g_loss) * a.inv_tau;
 #pragma unroll
     for (int i = 0; i < W; ++i) all += parts[i].mass;
@@ -244,8 +249,10 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     // log2(e) / tau that c holds, so that both of an exponent's terms are off alike.
     const double er = -lse_rest * (static_cast<double>(c) / a.inv_tau);
     gr.nr = none ? neg_inf() : static_cast<float>(er);
-    gr.others = none ? 0.f : static_cast<float>((all * exp(static_cast<double>(lse_rest) - static_cast<double>(lse)) - r) * g) *
-                            fast_exp2(static_cast<float>(er - gr.nr));
+    const double down = static_cast<double>(lse_rest) - static_cast<double>(lse);
+    const float near = static_cast<float>(down);
+    const double rq = static_cast<double>(expf(near)) * (1.0 + (down - near));
+    gr.others = none ? 0.f : static_cast<float>((all * rq - r) * g) * fast_exp2(static_cast<float>(er - gr.nr));
   }
 
   LaneSum st = sum_none(), listed = sum_none();

@@ -40,8 +40,9 @@ constexpr int kOrderBits<Bf16> = 16;
 template <>
 constexpr int kOrderBits<Fp16> = 19;
 
-// By one wave: the largest t with BITS leading bits such that at least `want`
-// of N words are >= t; 0 if even that many are not there (empty places hold 0).
+// By one wave: a t with at most BITS leading bits such that at least `want` of N
+// words are >= t, and either exactly as many are or t is the largest such; 0 if even
+// that many are not there (empty places hold 0).
 template <int N, int BITS>
 __device__ __forceinline__ uint32_t kth_largest(const uint32_t* words, int want) {
   uint32_t w[N / 64];
@@ -54,6 +55,7 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t* words, int want)
 #pragma unroll
     for (int i = 0; i < N / 64; ++i) count += __popcll(__ballot(w[i] >= cand));
     if (count >= want) t = cand;
+    if (count == want) break;
   }
   return t;
 }
