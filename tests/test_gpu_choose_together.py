@@ -253,3 +253,54 @@ def test_no_requests():
     loss, lse, lse_rest = lp.lp_distill_top(torch.zeros(0, 100, device="cuda"), ids, logp, rest)
     g = lp.lp_distill_top_backward(torch.zeros(0, 100, device="cuda"), ids, logp, rest, None, 1.0, lse, lse_rest, loss)
     assert g.shape == (0, 100)
+
+
+@pytest.mark.parametrize("tau", [1e-4, 0.02, 30.0, 1e6])
+@pytest.mark.parametrize("V", [900, 12007])
+def test_temperatures_far_from_one(tau, V):
+    """Rows as good as one-hot, and as good as flat."""
+    torch, lp = _torch(), _lp()
+    rng = np.random.default_rng(3)
+    bits, z = peaked(rng, 6, V, "fp32")
+    x = to_dev(bits)
+    K = 11
+    got = [host(t) for t in lp.lp_top_logits(x, K, None, tau)]
+    want = O.top_logits(z, K, None, tau)
+    assert np.array_equal(got[0], want[0])
+    # z / tau is taken with 1 / tau in fp64, exponents with log2(e) / tau in fp32: off by 2^-24 of themselves
+    far = 2.0 ** -23 * np.abs(z).max() / tau
+    for g, w in zip(got[1:], want[1:]):
+        close(g, w, tol_log(w, 2) + np.where(np.abs(w) < 80, 0, far))
+    ids, logp, rest = got[0], np.maximum(got[1], -60.0).astype(np.float32), np.maximum(got[2], -60.0).astype(np.float32)
+    y = to_dev((bits + rng.normal(0, 1, bits.shape) * min(tau, 1.0)).astype(np.float32))
+    z = host(y.double())
+    a = [to_dev(t) for t in (ids, logp, rest)]
+    loss, lse, lse_rest = lp.lp_distill_top(y, *a, None, tau)
+    l_o, lse_o, lr_o = O.distill_top(z, ids, logp, rest, None, tau)
+    close(host(lse), lse_o, tol_log(lse_o))
+    close(host(lse_rest), lr_o, tol_log(lr_o))
+    # terms of some (z / tau) each, in fp64, with masses off by 2^-23
+    close(host(loss), l_o, 4 * SUM + 2.0 ** -22 * (np.abs(l_o) + 1))
+    s = torch.zeros(2, 3, device="cuda")
+    sc, pa, to = [host(t) for t in lp.lp_beam_select(x, s, 5, None, 0, tau)]
+    sc_o, pa_o, to_o = O.beam_select(host(x.double()), np.zeros((2, 3), dtype=np.float32), 5, None, 0, tau)
+    close(sc, sc_o, tol_log(sc_o, 2))
+
+
+@pytest.mark.parametrize("T", [8, 20, 50, 100, 300])
+def test_an_8_bit_head_past_four_gigabytes(T):
+    torch, lp = _torch(), _lp()
+    V, h = 600064, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.empty(V, h, dtype=torch.uint8, device="cuda")
+    q[:1000].random_(0, 64, generator=g)
+    for v in range(1000, V, 100000):  # rows that repeat: cheap to fill
+        n = min(100000, V - v)
+        q[v:v + n] = q[:1000].repeat(100, 1)[:n]
+    q[-256:].random_(64, 120, generator=g)
+    q = q.view(torch.float8_e4m3fn)
+    s = torch.rand(V // 128, h // 128, device="cuda", generator=g) + 0.5
+    x = torch.randn(T, h, device="cuda", generator=g).bfloat16()
+    whole = lp.lp_lm_head_fp8_logits(x, q, s)
+    assert torch.equal(whole[:, -256:], lp.lp_lm_head_fp8_logits(x, q[-256:], s[-2:]))
+    assert torch.equal(whole[:, 300032:300288], lp.lp_lm_head_fp8_logits(x, q[300032:300288], s[2344:2346]))
