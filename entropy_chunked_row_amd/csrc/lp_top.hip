@@ -222,7 +222,7 @@ __device__ __forceinline__ bool row_live(const TopArgs& a, int64_t row) {
   return !(a.mask && a.mask[row] == 0);
 }
 
-// Kept vectors a lane: of a slice kept whole (SHORT) 4.  Of a stream with 256
+// Kept vectors a lane: of a slice kept whole (SHORT) 4, in registers.  Of a stream with 256
 // threads (K up to 64) 192 a wave, twice what is expected, so that seven
 // workgroups fit a CU; with 512 (K up to 256) 256, of which 170 are expected.
 template <int NT, bool SHORT>
@@ -233,7 +233,7 @@ constexpr int kFewTop = 64;  // most K of the first of these
 template <class Tr, int NT, bool SHORT>
 __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   constexpr int P = Tr::kPerVec, U = 4, W = NT / 64, kLane = kHeld<NT, SHORT>, kKept = kLane * NT, kWave = kKept / W, kKeys = 2 * NT, kWords = 2 * NT;
-  __shared__ u32x4 kept[kKept];
+  __shared__ u32x4 kept[SHORT ? 1 : kKept];
   __shared__ uint32_t kept_at[SHORT ? 1 : kKept];
   __shared__ __attribute__((aligned(16))) uint64_t keys[kKeys];
   __shared__ uint32_t best[kWords];  // later the digits' counts
@@ -269,12 +269,13 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
 
   SumStat low{neg_inf(), 0.f};  // of what was streamed and not kept: this lane's
   bool digits = false;
+  u32x4 short_kept[SHORT ? kLane : 1];
   if (SHORT) {
     const int vectors = (n + P - 1) / P;
 #pragma unroll
     for (int i = 0; i < kLane; ++i) {
       const int v = tid + i * NT;
-      if (v < vectors) kept[v] = row_vector<Tr>(xp, v, n);
+      short_kept[i] = v < vectors ? row_vector<Tr>(xp, v, n) : no_vector<Tr>();
     }
   } else {
     // U W pieces of `steps` times 64 vectors, so that one step of the workgroup is a
@@ -370,16 +371,34 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   // The kept vectors of this lane, f(values, number of the vector, whether it is
   // an odd one of the lane's).
   auto each_kept = [&](auto f) {
-    const int m = SHORT ? (n + P - 1) / P : held_by[wave];
-    for (int k = SHORT ? tid : lane; k < m; k += SHORT ? NT : 64) {
-      const int at = SHORT ? k : wave * kWave + k;
-      float x[P];
-      Tr::unpack(kept[at], x);
-      f(x, SHORT ? k : static_cast<int>(kept_at[at]), (SHORT ? k / NT & 1 : k / 64 & 1) != 0);
+    if constexpr (SHORT) {
+#pragma unroll
+      for (int i = 0; i < kLane; ++i) {
+        float x[P];
+        Tr::unpack(short_kept[i], x);
+        f(x, tid + i * NT, (i & 1) != 0);
+      }
+    } else {
+      const int m = held_by[wave];
+      for (int k = lane; k < m; k += 64) {
+        float x[P];
+        Tr::unpack(kept[wave * kWave + k], x);
+        f(x, static_cast<int>(kept_at[wave * kWave + k]), (k / 64 & 1) != 0);
+      }
     }
   };
   int got = 0;
+  // the columns of vector v that are in the list weigh nothing in the rest
+  auto leave_out = [&](float* x, int v) {
+    const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+    const float value = got > 0 ? key_value(least) : __builtin_inff();
+    const int col = (got > 0 ? key_col(least) : -1) - c0 - v * P;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (x[i] > value || (x[i] == value && i <= col)) x[i] = neg_inf();
+  };
   LaneSum st = sum_none();
+  bool relative = false;
   if (!digits) {
     // Two words a lane, of every other vector; of the halves of its vector where
     // no lane has two: with fewer words than K nothing could be left out.
@@ -415,13 +434,20 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
       }
       got = m < a.K ? m : a.K;
       __syncthreads();
-      // what is left of the kept vectors
-      const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+      // what is left of the kept vectors, relative to the floor as well
+      if (SHORT) low.m = floor;
+      relative = low.m > -kLargest && is_near(low.m * c);
+      const float mc = low.m * c;
       each_kept([&](float* x, int v, bool) {
+        leave_out(x, v);
+        if (relative) {
+          float ps = fast_exp2(fmaf(x[0], c, -mc));
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (x[i] >= floor && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
-        sum_push<P, P>(st, x, largest_of<P>(x), c);
+          for (int i = 1; i < P; ++i) ps += fast_exp2(fmaf(x[i], c, -mc));
+          low.s += ps;
+        } else {
+          sum_push<P, P>(st, x, largest_of<P>(x), c);
+        }
       });
     }
   }
@@ -433,20 +459,16 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
     __syncthreads();
     for (int i = tid; i < got; i += NT) top[rank_among(keys, got, keys[i])] = keys[i];
   }
-  SumStat rest = sum_block<NT>(SHORT || digits ? st : sum_add(low, st, c), c, sm[0]);
-  // What lies more than 126 octaves below the floor was added as 0.  Where that is
-  // not small beside what is left, the rest is summed once more.  (Below the
-  // lowest floor lies nothing.)
-  if (!SHORT && !digits && low.m > -kLargest && rest.m <= low.m &&
-      !(rest.s * fast_exp2(stat_shift(rest.m, low.m, c)) >= 8.5e-22f)) {
-    const uint64_t least = got > 0 ? top[got - 1] : ~0ull;
+  SumStat rest = sum_block<NT>(digits ? st : sum_add(low, st, c), c, sm[0]);
+  // What lies more than 126 octaves below the floor was added as 0, and what lies 128
+  // above it as infinity.  Where the first is not small beside what is left, or that is
+  // not finite, the rest is summed once more.  (Below the lowest floor lies nothing.)
+  if (relative && !(rest.s >= 8.5e-22f && rest.s <= kLargest)) {
     st = sum_none();
     for (int v = tid; v * P < n; v += NT) {
       float x[P];
       Tr::unpack(row_vector<Tr>(xp, v, n), x);
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (x[i] >= -kLargest && key_of(x[i], c0 + v * P + i) >= least) x[i] = neg_inf();
+      leave_out(x, v);
       sum_push<P, P>(st, x, largest_of<P>(x), c);
     }
     __syncthreads();
@@ -485,11 +507,21 @@ __global__ void __launch_bounds__(NT) k_top_join(TopArgs a) {
   const int n = a.nslices * a.K;
   const uint64_t* all = a.part_keys + row * n;
   if (tid == 0) count = 0;
+  // the first keys stay in registers
+  constexpr int R = 4;
+  uint64_t first[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) first[i] = tid + i * NT < n ? all[tid + i * NT] : 0;
+  auto each_key = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) f(first[i]);
+    for (int i = tid + R * NT; i < n; i += NT) f(all[i]);
+  };
   uint32_t most = 0;
-  for (int i = tid; i < n; i += NT) {
-    const uint32_t o = static_cast<uint32_t>(all[i] >> 32);
+  each_key([&](uint64_t key) {
+    const uint32_t o = static_cast<uint32_t>(key >> 32);
     most = o > most ? o : most;
-  }
+  });
   best[tid] = most;
   __syncthreads();
   if (tid < 64) {
@@ -498,10 +530,9 @@ __global__ void __launch_bounds__(NT) k_top_join(TopArgs a) {
   }
   __syncthreads();
   LaneSum st = sum_none();
-  for (int i = tid; i < n; i += NT) {
-    const uint64_t key = all[i];
+  each_key([&](uint64_t key) {
     if (key != 0 && static_cast<uint32_t>(key >> 32) >= bar) keys[atomicAdd(&count, 1u)] = key;
-  }
+  });
   for (int i = tid; i < a.nslices; i += NT) {
     const float* p = a.part_sums + (row * a.nslices + i) * 2;
     const SumStat both = sum_add(st, SumStat{p[0], p[1]}, c);
@@ -520,10 +551,10 @@ __global__ void __launch_bounds__(NT) k_top_join(TopArgs a) {
   }
   __syncthreads();
   const int got = m < a.K ? m : a.K;
-  for (int i = tid; i < n && got > 0; i += NT) {
-    const uint64_t key = all[i];
-    if (key != 0 && key < top[got - 1]) sum_push1(st, key_value(key), c);
-  }
+  const uint64_t least = got > 0 ? top[got - 1] : 0;
+  each_key([&](uint64_t key) {
+    if (key != 0 && key < least) sum_push1(st, key_value(key), c);
+  });
   LaneSum of_list = sum_none();
   for (int k = tid; k < got; k += NT) sum_push1(of_list, key_value(top[k]), c);
   const SumStat rest = sum_block<NT>(st, c, sm[0]);
