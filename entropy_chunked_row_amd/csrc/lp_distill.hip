@@ -275,18 +275,23 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     double ps[P];  // many entries may name one column
 #pragma unroll
     for (int j = 0; j < P; ++j) ps[j] = 0.0;
-    for (int j = 0; j < a.K; j += 4) {
+    for (int j0 = 0; j0 < a.K; j0 += 32) {  // behind entry K lie none
       typedef int i32x4 __attribute__((ext_vector_type(4)));
-      const i32x4 quad = *reinterpret_cast<const i32x4*>(cols + j);
+      uint32_t match = 0;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (quad[n] / P != v) continue;
-        mine = mine && j + n >= k;
-        bits |= 1u << (quad[n] % P);
+      for (int j = 0; j < 32; j += 4) {
+        const i32x4 quad = *reinterpret_cast<const i32x4*>(cols + j0 + j);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) match |= static_cast<uint32_t>(quad[n]) / P == static_cast<uint32_t>(v) ? 1u << (j + n) : 0u;
+      }
+      for (; match; match &= match - 1) {
+        const int at = j0 + __ffs(static_cast<int>(match)) - 1, in_vec = cols[at] % P;
+        mine = mine && at >= k;
+        bits |= 1u << in_vec;
         if (GRAD) {
+          const double p = mass[at];
 #pragma unroll
-          for (int m = 0; m < P; ++m)
-            if (quad[n] % P == m) ps[m] += mass[j + n];
+          for (int m = 0; m < P; ++m) ps[m] += in_vec == m ? p : 0.0;
         }
       }
     }
@@ -441,7 +446,9 @@ __global__ void __launch_bounds__(256) k_distill_join(DistillArgs a) {
 // bits hold kMaskWords x 32 of a lane's vectors.  For the gradient slices of about
 // kGradSlice columns, whatever the rows: what is read and what is written then lie
 // close together (4096 x 151936 bf16 435 us, 461 with 16384 columns, 508 with whole rows).
-constexpr int64_t kRowGroups = 768, kGradSlice = 8192;
+// Short rows are not cut for the loss: a join would cost more than it saves (1 to 256
+// rows of 32000 15 us, 18 with slices).
+constexpr int64_t kRowGroups = 768, kGradSlice = 8192, kWholeRow = 32768;
 
 void set_slices(DistillArgs& a, int dtype, bool grad) {
   const int64_t longest = int64_t(32) * kMaskWords * 256 * (dtype == 2 ? 4 : 8) - 128;
@@ -449,6 +456,7 @@ void set_slices(DistillArgs& a, int dtype, bool grad) {
   int64_t n = (kRowGroups + a.T - 1) / (a.T > 0 ? a.T : 1);
   if (grad && n < a.V / kGradSlice) n = a.V / kGradSlice;
   n = n < most ? n : most;
+  if (!grad && a.V <= kWholeRow) n = 1;
   n = n > least ? n : least;
   a.slice = static_cast<int>(((int64_t(a.V) + n - 1) / n + 127) / 128 * 128);
   a.nslices = static_cast<int>((int64_t(a.V) + a.slice - 1) / a.slice);
@@ -471,7 +479,7 @@ hipError_t launch_distill_nt(DistillArgs a, hipStream_t s) {
 
 template <class Tr, bool GRAD>
 hipError_t launch_distill_t(const DistillArgs& a, hipStream_t s) {
-  // 128 threads where that leaves a few vectors each (2000 rows of 4099: 19 us, 23 with
+  // 128 threads where that leaves a few vectors each (2000 rows of 4099: 15 us, 18 with
   // 256; of 7300 columns the same), 256 for long slices (8192 x 151936 292 us, 305 with
   // 128; gradient 435 and 451)
   if (a.slice >= 6144) return launch_distill_nt<Tr, 256, GRAD>(a, s);

@@ -631,12 +631,28 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
     place |= static_cast<uint32_t>(key_col(key));
     return order_of64(gain[w] + static_cast<double>(key_value(key)) * a.inv_tau);
   };
-  uint32_t most = 0;
-  uint64_t place;
-  for (int i = tid; i < n; i += NT) {
-    const uint32_t o = static_cast<uint32_t>(order_at(i, place) >> 32);
-    most = o > most ? o : most;
+  // the first candidates stay in registers
+  constexpr int R = 2;
+  Candidate first[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    first[i].order = 0;
+    if (tid + i * NT < n) first[i].order = order_at(tid + i * NT, first[i].place);
   }
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) f(first[i]);
+    for (int i = tid + R * NT; i < n; i += NT) {
+      Candidate q;
+      q.order = order_at(i, q.place);
+      f(q);
+    }
+  };
+  uint32_t most = 0;
+  each([&](const Candidate& q) {
+    const uint32_t o = static_cast<uint32_t>(q.order >> 32);
+    most = o > most ? o : most;
+  });
   best[tid] = most;
   __syncthreads();
   if (tid < 64) {
@@ -644,10 +660,9 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
     if (tid == 0) bar = t;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += NT) {
-    const uint64_t o = order_at(i, place);
-    if (o && static_cast<uint32_t>(o >> 32) >= bar) cand[atomicAdd(&count, 1u)] = Candidate{o, place};
-  }
+  each([&](const Candidate& q) {
+    if (q.order && static_cast<uint32_t>(q.order >> 32) >= bar) cand[atomicAdd(&count, 1u)] = q;
+  });
   __syncthreads();
   const int m = static_cast<int>(count);
   for (int i = tid; i < m; i += NT) {
@@ -682,21 +697,29 @@ int threads_of(int K) { return K > kFewTop ? 512 : 256; }
 // Columns of a slice that k_top keeps whole.
 int short_slice(int dtype, int threads) { return 4 * threads * (dtype == 2 ? 4 : 8); }
 
-// Slices per row: one where there are rows for 1024 threads a CU and more (a batch of
-// 256 rows of 151936: K = 20 30 us, 33 with half as many; K = 200 48, 60 with twice as
-// many), else as many as that takes, none shorter than what a workgroup keeps
-// whole, and no more keys than a join takes.  Slices are either short ones that are
+// Slices per row: one where there are rows for four workgroups a CU and more, else as
+// many as that takes (256 rows of 151936, K = 20: 30 us, 33 with half as many).  With K
+// past 64 joins take longer: one workgroup a CU, and 1024 keys a join (K = 200, 256 rows
+// 40 us, 49 with twice as many; 37 rows 29 us, 38 with 4096 keys).  None is
+// shorter than what a workgroup keeps whole.  Slices are either short ones that are
 // kept whole or each of them, a row's last one too, has the columns of a step of
-// the stream, which has no end without one.
+// the stream, which has no end without one.  Short rows are not cut, but for beams,
+// which are joined anyway: a join would cost more than it saves (1 to 256 rows of 32000:
+// K = 20 17 us, 19 with slices; K = 200 20 and 26 to 34; 256 rows of 65000 21 and 24,
+// 27 and 38).
+constexpr int64_t kWholeRow = 65536;
+
 void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
-  const int64_t most_keys = kMaxBuffered / lists > 1 ? kMaxBuffered / lists : 1;
+  const bool many = a.K > kFewTop;
+  const int64_t keys = many ? 1024 : kMaxBuffered, most_keys = keys / lists > 1 ? keys / lists : 1;
   const int64_t least = short_slice(dtype, 256);
-  const int64_t groups = 256 * 1024 / threads_of(a.K);
+  const int64_t groups = many ? 256 : 1024;
   int64_t n = (groups + a.T - 1) / (a.T > 0 ? a.T : 1);
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
   n = n < most_keys ? n : most_keys;
+  if (a.W == 0 && a.V <= kWholeRow) n = 1;
   const int64_t kept = short_slice(dtype, threads_of(a.K));
   int64_t last;
   do {
