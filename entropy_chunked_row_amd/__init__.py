@@ -1021,13 +1021,13 @@ def _levels(sizes, strides, name):
 def _state_layout(t, dim, name):
     """(outer size, its stride, row stride, mid size, its stride, width), strides and width in bytes, of a state whose
     dimension `dim` is the beams."""
-    e, shape, strides = t.element_size(), list(t.shape), list(t.stride())
+    e, shape, strides = t.element_size(), t.shape, t.stride()
     width, k = 1, len(shape)
     while k > dim + 1 and (shape[k - 1] == 1 or strides[k - 1] == width):
         width *= shape[k - 1]
         k -= 1
-    mid, mid_stride = _levels(shape[dim + 1:k], strides[dim + 1:k], name)
-    outer, outer_stride = _levels(shape[:dim], strides[:dim], name)
+    mid, mid_stride = _levels(shape[dim + 1:k], strides[dim + 1:k], name) if k > dim + 1 else (1, 0)
+    outer, outer_stride = _levels(shape[:dim], strides[:dim], name) if dim else (1, 0)
     return outer, outer_stride * e, strides[dim] * e, mid, mid_stride * e, width * e
 
 
@@ -1058,13 +1058,17 @@ def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
     with _scope(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=state.dtype, device=dev)
-        d_outer, do, dr, d_mid, dm, d_width = _state_layout(out, dim, "out")
-        if d_outer != outer or d_mid * d_width != mid * width:
-            raise ValueError("out cannot be walked as the state is")
-        if d_width != width:
-            if d_mid != 1:
+            dm = width
+            dr = mid * width
+            do = B * N * dr
+        else:
+            d_outer, do, dr, d_mid, dm, d_width = _state_layout(out, dim, "out")
+            if d_outer != outer or d_mid * d_width != mid * width:
                 raise ValueError("out cannot be walked as the state is")
-            dm = width  # the state's parts lie behind each other in out
+            if d_width != width:
+                if d_mid != 1:
+                    raise ValueError("out cannot be walked as the state is")
+                dm = width  # the state's parts lie behind each other in out
         st = lib.lp_beam_reorder(_ptr(state), s_outer, s_row, s_mid, outer, mid, width, _ptr(parents), B, rows // B if B else 1, N,
                                  _ptr(out), do, dr, dm, _raw_stream(dev, stream))
     check("lp_beam_reorder", st)

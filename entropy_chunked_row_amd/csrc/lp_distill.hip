@@ -18,8 +18,8 @@
 // once in the sums and with both its masses in the gradient, in a fixed order, and
 // the sum over unlisted columns is a sum of its own.
 // Bound by HBM: lists of 64 on 6144 scored rows of 151936 bf16 289 us, 6.5 TB/s of
-// reading (6.8 is what reading alone reaches); the gradient of 4096 such rows 425 us,
-// 5.9 TB/s read and written (6.1 is an elementwise kernel's).
+// reading (6.8 is what reading alone reaches); the gradient of 4096 such rows 412 us,
+// 6.0 TB/s read and written (6.1 is an elementwise kernel's).
 #include "lp_internal.hpp"
 #include "lp_sums.hpp"
 
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(256) k_distill_join(DistillArgs a) {
 // Slices per row: as many as make three workgroups a CU where rows are few; the
 // bits hold kMaskWords x 32 of a lane's vectors.  For the gradient slices of about
 // kGradSlice columns, whatever the rows: what is read and what is written then lie
-// close together (4096 x 151936 bf16 435 us, 461 with 16384 columns, 508 with whole rows).
+// close together (4096 x 151936 bf16 422 us back to back, 446 with 16384 columns, 472 with 32768).
 // Short rows are not cut for the loss: a join would cost more than it saves (1 to 256
 // rows of 32000 15 us, 18 with slices).
 constexpr int64_t kRowGroups = 768, kGradSlice = 8192, kWholeRow = 32768;
@@ -481,7 +481,7 @@ template <class Tr, bool GRAD>
 hipError_t launch_distill_t(const DistillArgs& a, hipStream_t s) {
   // 128 threads where that leaves a few vectors each (2000 rows of 4099: 15 us, 18 with
   // 256; of 7300 columns the same), 256 for long slices (8192 x 151936 292 us, 305 with
-  // 128; gradient 435 and 451)
+  // 128; gradient 435 and 451, before listed vectors took less)
   if (a.slice >= 6144) return launch_distill_nt<Tr, 256, GRAD>(a, s);
   return launch_distill_nt<Tr, 128, GRAD>(a, s);
 }

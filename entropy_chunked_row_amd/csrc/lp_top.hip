@@ -19,10 +19,10 @@
 // Order is (value descending, column ascending), as one 64-bit key.  More kept
 // vectors than LDS holds (rows that rise steadily, or have most values equal) are
 // counted by digits of the keys instead: right for any row, several more reads of it.
-// Bound by reading: 6144 scored rows of 151936 bf16, 64 of each, 325 us, 5.8 TB/s
+// Bound by reading: 6144 scored rows of 151936 bf16, 64 of each, 322 us, 5.8 TB/s
 // (6.8 is what reading alone reaches); what is missing are the waits of a row's end,
-// which the other workgroups of a CU cover in part.  One row of 151936 is 17 us a
-// call, two launches; 512 of 129280 fp16, 16 of each, 38 us, 8 of them the join.
+// which the other workgroups of a CU cover in part.  One row of 151936 is 16 us a
+// call, two launches; 512 of 129280 fp16, 16 of each, 38 us, 9 of them the join.
 #include "lp_internal.hpp"
 #include "lp_sums.hpp"
 
