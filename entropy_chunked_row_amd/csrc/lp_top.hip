@@ -580,8 +580,7 @@ struct Candidate {
 
 // One request: the lists of its beams' slices, scored and ranked.  Scores are
 // fp64 (sum_lse), so that within a beam they keep the order of its logits
-// whatever the size of the sum so far.  512 threads: 4 beams of 19 slices 4 us, 6 with
-// 256; 8 beams of 2 slices 9 us with either.
+// whatever the size of the sum so far.
 template <int NT>
 __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
   extern __shared__ __attribute__((aligned(16))) Candidate cand[];  // W * nslices * K of them
@@ -833,7 +832,7 @@ hipError_t launch_beam_select(int dtype, const TopArgs& args, int64_t B, char* w
     const int64_t rows = B - r0 < kRows ? B - r0 : kRows;
     a.row0 = r0;
     TimedLaunch tl("k_beam_join", s);
-    hipLaunchKernelGGL(k_beam_join<512>, dim3(static_cast<unsigned>(rows)), dim3(512), lds, s, a);
+    hipLaunchKernelGGL(k_beam_join<256>, dim3(static_cast<unsigned>(rows)), dim3(256), lds, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
