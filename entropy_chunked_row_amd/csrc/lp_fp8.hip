@@ -223,7 +223,7 @@ __device__ __forceinline__ int chunk_swz(int r) { return r & 7; }
 
 template <int BM_, int BN, int WGM, int WGN, int STAGES_>
 struct Fp8Tile {
-  static constexpr int BM = BM_, STAGES = STAGES_, NW = WGM * WGN, NT = 64 * NW;
+  static constexpr int BM = BM_, STAGES = STAGES_, NW = WGM * WGN;
   static constexpr int MI = BM / WGM / 16, NI = BN / WGN / 16;     // 16 x 16 products of a wave
   static constexpr int A_INST = BM / 8 / NW, B_INST = BN / 8 / NW;  // 1 KB loads a wave and stage
   static constexpr int ROWS = (BM + BN) * kBlock;                   // bytes of both operands' rows

@@ -69,12 +69,6 @@ __device__ __forceinline__ SumStat sum_block(SumStat st, float c, SumStat* sm) {
   return sum_merge<W>(sm[threadIdx.x & (W - 1)], c);
 }
 
-__device__ __forceinline__ float sum_exponent(float x, float m, float c) {
-  const float mc = m * c;
-  if (m == neg_inf()) return x * c;  // none yet: -inf or NaN
-  return is_near(mc) ? fmaf(x, c, -mc) : (x - m) * c;
-}
-
 // log-sum-exp of z / tau, natural, in fp64 (scores of different rows are compared
 // and differences of nearly equal ones formed: fp32 would leave a few 2^-24 of
 // their magnitude).  m c carries the rounding of c and of the product; both are
