@@ -479,9 +479,9 @@ hipError_t launch_distill_nt(DistillArgs a, hipStream_t s) {
 
 template <class Tr, bool GRAD>
 hipError_t launch_distill_t(const DistillArgs& a, hipStream_t s) {
-  // 128 threads where that leaves a few vectors each (2000 rows of 4099: 15 us, 18 with
+  // 128 threads where that leaves a few vectors each (2000 rows of 4099: 19 us, 23 with
   // 256; of 7300 columns the same), 256 for long slices (8192 x 151936 292 us, 305 with
-  // 128; gradient 435 and 451, before listed vectors took less)
+  // 128; gradient 435 and 451; all of these before listed vectors took less)
   if (a.slice >= 6144) return launch_distill_nt<Tr, 256, GRAD>(a, s);
   return launch_distill_nt<Tr, 128, GRAD>(a, s);
 }
