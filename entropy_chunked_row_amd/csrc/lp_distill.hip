@@ -73,7 +73,9 @@ __device__ __forceinline__ double lanes_sum(double x) {
 
 // exp(t) to within 2^-23 of it: a teacher's log-probs are no better known, and the
 // fp64 function alone takes longer than all else in a short row.  The same in every
-// place, so that a row's masses agree with their sum.
+// place, so that a row's masses agree with their sum.  0 from about -104 down: an entry
+// without mass adds nothing to the loss, also where the student's log is -inf and the
+// term would be 0 times infinity (finite masks in the teacher's logits, -inf in the student's).
 __device__ __forceinline__ double mass_of(float t) { return static_cast<double>(expf(t)); }
 
 // What the listed entries add to a row's loss before its log-sum-exps are known:
@@ -91,8 +93,8 @@ __device__ __forceinline__ Entries sum_entries(const DistillArgs& a, int64_t row
   for (int k = threadIdx.x & 63; k < a.K; k += 64) {
     const int64_t id = a.ids[row * a.K + k];
     const float t = a.logprob[row * a.K + k];
-    if (id < 0 || id >= a.V || t == neg_inf()) continue;  // padding, or no mass
     const double p = mass_of(t);
+    if (id < 0 || id >= a.V || p == 0.0) continue;  // padding, or no mass
     e.terms += p * (static_cast<double>(t) - static_cast<double>(Tr::load1(xp, id)) * a.inv_tau);
     e.mass += p;
   }
@@ -108,10 +110,8 @@ __device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, En
   const double lse = sum_lse(sum_add(rest, listed, a.c), a.c, a.inv_tau);
   const double lse_rest = sum_lse(rest, a.c, a.inv_tau);
   double loss = e.terms + e.mass * lse;
-  if (t_rest != neg_inf()) {
-    const double t = t_rest;
-    loss += mass_of(t_rest) * (t - (lse_rest - lse));
-  }
+  const double r = mass_of(t_rest);
+  if (r != 0.0) loss += r * (static_cast<double>(t_rest) - (lse_rest - lse));
   a.loss[row] = static_cast<float>(loss);
   if (a.lse_out) a.lse_out[row] = static_cast<float>(lse);
   if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(lse_rest);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
       const double p = inside ? mass_of(t[i]) : 0.0;
       e.mass += p;
       if (GRAD && k < kMaxTop) mass[k] = static_cast<float>(p);
-      if (!GRAD && inside && t[i] != neg_inf())
+      if (!GRAD && p != 0.0)
         e.terms += p * (static_cast<double>(t[i]) - static_cast<double>(z[i]) * a.inv_tau);
     }
   }

@@ -545,8 +545,11 @@ lp_status lp_top_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V
  * teacher_ids      int64 [T x K]; an id outside [0, V) is padding and is not read further.
  *                  An id listed more than once counts with each of its entries.
  * teacher_logprob  fp32 [T x K], natural logs at the teacher's temperature; an
- *                  entry of -inf has no mass (its column still counts as named).
- * teacher_rest     fp32 [T] or NULL: log of the mass outside the list; NULL: no such term.
+ *                  entry whose exp is 0 in fp32 (-inf, and finite ones below about -104,
+ *                  as finite masks give them) has no mass and adds nothing, whatever the
+ *                  student gives its column, which still counts as named.
+ * teacher_rest     fp32 [T] or NULL: log of the mass outside the list; NULL, or no mass as
+ *                  above: no such term.
  *                  The masses need not sum to 1.
  * loss             fp32 [T] (required).  +inf where the teacher has mass and the student none.
  * lse, lse_rest    fp32 [T] or NULL: log-sum-exp of the tempered row, and over the

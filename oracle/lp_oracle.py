@@ -698,6 +698,12 @@ def _lse1(x):
     return log_normaliser(x[None])[0] if x.size else -np.inf
 
 
+def list_mass(t):
+    """exp(t), 0 where fp32 holds nothing of it: such an entry of a list has no mass, whatever the student gives its column."""
+    p = np.exp(np.asarray(t, dtype=np.float64))
+    return np.where(p.astype(np.float32) == 0, 0.0, p)
+
+
 def distill_top(logits, ids, logprob, rest, mask, temperature):
     """(loss, lse, lse_rest) of KL from a teacher's lists to the student's rows."""
     zt = tempered(np.asarray(logits, dtype=np.float64), temperature)
@@ -709,11 +715,11 @@ def distill_top(logits, ids, logprob, rest, mask, temperature):
         at, lp, other = _distill_parts(zt, ids, logprob, t)
         lse[t], lse_rest[t] = _lse1(zt[t]), _lse1(zt[t][other])
         with np.errstate(invalid="ignore"):
-            for j, a in zip(at, lp):
-                if a > -np.inf:
-                    loss[t] += np.exp(a) * (a - (zt[t, j] - lse[t]))
-            if rest is not None and rest[t] > -np.inf:
-                loss[t] += np.exp(float(rest[t])) * (float(rest[t]) - (lse_rest[t] - lse[t]))
+            for j, a, p in zip(at, lp, list_mass(lp)):
+                if p != 0:
+                    loss[t] += p * (a - (zt[t, j] - lse[t]))
+            if rest is not None and list_mass(rest[t]) != 0:
+                loss[t] += list_mass(rest[t]) * (float(rest[t]) - (lse_rest[t] - lse[t]))
     return loss, lse, lse_rest
 
 
@@ -727,8 +733,8 @@ def distill_top_backward(logits, ids, logprob, rest, mask, temperature, grad_los
         if mask is not None and not mask[t]:
             continue
         at, lp, other = _distill_parts(zt, ids, logprob, t)
-        p = np.exp(lp)
-        r = np.exp(float(rest[t])) if rest is not None else 0.0
+        p = list_mass(lp)
+        r = float(list_mass(rest[t])) if rest is not None else 0.0
         lse, lse_rest = _lse1(zt[t]), _lse1(zt[t][other])
         # d/dz of -sum p log q - r log q_rest: (P + r) q - p - r (the others' share of themselves)
         row = (p.sum() + r) * np.exp(zt[t] - lse)
