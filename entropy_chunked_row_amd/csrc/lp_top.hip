@@ -434,8 +434,10 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
       }
       got = m < a.K ? m : a.K;
       __syncthreads();
-      // what is left of the kept vectors, relative to the floor as well
-      if (SHORT) low.m = floor;
+      // what is left of the kept vectors, relative to the floor as well where it is
+      // near 0 (a streamed slice's is, or the lowest: others went to the digits); elsewhere
+      // the state stays empty, since one of no weight at the floor would hide lower ones
+      if (SHORT && is_near(floor * c)) low.m = floor;
       relative = low.m > -kLargest && is_near(low.m * c);
       const float mc = low.m * c;
       each_kept([&](float* x, int v, bool) {
