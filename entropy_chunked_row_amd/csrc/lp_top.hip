@@ -575,14 +575,18 @@ __device__ __forceinline__ double value_of64(uint64_t order) {
   return __longlong_as_double(static_cast<long long>(order & 0x8000000000000000ull ? order ^ 0x8000000000000000ull : ~order));
 }
 
+// place orders candidates of equal scores: the lowest beam, its largest logit, the
+// lowest column (a beam's lists are in the order of its columns' slices).
 struct Candidate {
   uint64_t order;  // of its score
-  uint64_t place;  // beam << 32 | token
+  uint64_t place;  // beam << 48 | ~order of its logit << 16 | number of its key among the request's
 };
+static_assert(kMaxBuffered <= 1 << 16 && kMaxBeamLists <= kMaxBuffered, "a key's number in 16 bits");
 
-// One request: the lists of its beams' slices, scored and ranked.  Scores are
-// fp64 (sum_lse), so that within a beam they keep the order of its logits
-// whatever the size of the sum so far.
+// One request: the lists of its beams' slices, scored and ranked.  Scores are fp64
+// (sum_lse).  Where the sum so far takes up the differences of a beam's logits (1e20, or
+// the largest finite number, for beams that are not there; temperatures as large), place
+// keeps their order.
 template <int NT>
 __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
   extern __shared__ __attribute__((aligned(16))) Candidate cand[];  // W * nslices * K of them
@@ -621,16 +625,15 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
   auto order_at = [&](int i, uint64_t& place) -> uint64_t {
     const int w = i / per;
     const int64_t row = b * W + w;
-    place = static_cast<uint64_t>(w) << 32;
+    place = static_cast<uint64_t>(w) << 48 | static_cast<uint64_t>(i);
     if (a.finished && a.finished[row]) {
       const float s = a.beam_scores[row];
-      place |= static_cast<uint32_t>(a.end_token);
       return i == w * per && s >= -kLargest && s <= kLargest ? order_of64(s) : 0;
     }
     if (__builtin_isnan(gain[w])) return 0;
     const uint64_t key = a.part_keys[b * n + i];
     if (!key) return 0;
-    place |= static_cast<uint32_t>(key_col(key));
+    place |= static_cast<uint64_t>(~static_cast<uint32_t>(key >> 32)) << 16;
     return order_of64(gain[w] + static_cast<double>(key_value(key)) * a.inv_tau);
   };
   // the first candidates stay in registers
@@ -675,9 +678,11 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
       r += p.order > q.order || (p.order == q.order && p.place < q.place);
     }
     if (r < N) {
+      const int w = static_cast<int>(q.place >> 48);
+      const bool ended = a.finished && a.finished[b * W + w];
       a.scores[b * N + r] = static_cast<float>(value_of64(q.order));
-      a.parents[b * N + r] = static_cast<int32_t>(q.place >> 32);
-      a.ids[b * N + r] = static_cast<int64_t>(q.place & 0xffffffffu);
+      a.parents[b * N + r] = w;
+      a.ids[b * N + r] = ended ? a.end_token : key_col(a.part_keys[b * n + static_cast<int>(q.place & 0xffffu)]);
     }
   }
   for (int r = m + tid; r < N; r += NT) {

@@ -592,7 +592,8 @@ lp_status lp_distill_top_backward(const void* logits, lp_dtype dtype, int64_t T,
  * finished     uint8 [B x W] or NULL: such a beam is one candidate as it stands, its
  *              score and end_token (0 <= end_token < V); its row is not read.
  * scores, parents, tokens   fp32, int32, int64 [B x N], the best first; of equal
- *              scores the lowest beam and then the lowest token.  A token of logit -inf
+ *              scores the lowest beam, then its largest logit (a score so far of 1e20 takes
+ *              up their differences), then the lowest token.  A token of logit -inf
  *              is no candidate, nor is any of a row that holds NaN or +inf.  Places that no
  *              candidate fills hold -inf, -1 and -1 (which lp_embedding and
  *              lp_beam_reorder turn into zeros).

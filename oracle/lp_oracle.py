@@ -758,14 +758,15 @@ def beam_select(logits, beam_scores, N, finished, end_token, temperature):
             if not np.isfinite(s):
                 continue
             if finished is not None and finished[b, w]:
-                cand.append((-s, w, end_token))
+                cand.append((-s, w, 0, end_token))
                 continue
             row = zt[b * W + w]
             if np.isnan(row).any() or (row == np.inf).any() or not (row > -np.inf).any():
                 continue
             lse = _lse1(row)
-            cand += [(-(s + row[v] - lse), w, int(v)) for v in _top_order(row)[:N]]
-        for n, (s, w, v) in enumerate(sorted(cand)[:N]):
+            # of one beam by its logits, whatever its score leaves of their differences
+            cand += [(-(s + row[v] - lse), w, n, int(v)) for n, v in enumerate(_top_order(row)[:N])]
+        for n, (s, w, _, v) in enumerate(sorted(cand)[:N]):
             scores[b, n], parents[b, n], tokens[b, n] = -s, w, v
     return scores, parents, tokens
 
