@@ -1034,8 +1034,8 @@ def _state_layout(t, dim, name):
 def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
     """States follow their beams: along dimension `dim`, row b * N + n of the result is row b * W + parents[b, n] of
     state (W = its size / B), zeros where that parent lies outside [0, W).  state of any dtype, the dimensions before
-    `dim` walked in one step, those behind it in at most two (a prefix of each row of a cache); parents int32 [B, N],
-    as lp_beam_select gives them."""
+    `dim` walked in one step, those behind it in at most two (a prefix of each row of a cache); out likewise, in the
+    state's parts where neither is dense behind `dim`; parents int32 [B, N], as lp_beam_select gives them."""
     torch = _torch()
     lib = load()
     if parents.dim() != 2:
@@ -1066,9 +1066,12 @@ def lp_beam_reorder(state, parents, *, dim: int = 0, out=None, stream=None):
             if d_outer != outer or d_mid * d_width != mid * width:
                 raise ValueError("out cannot be walked as the state is")
             if d_width != width:
-                if d_mid != 1:
+                if mid == 1:  # out's parts lie behind each other in the state
+                    mid, width, s_mid = d_mid, d_width, d_width
+                elif d_mid == 1:
+                    dm = width  # the state's parts lie behind each other in out
+                else:
                     raise ValueError("out cannot be walked as the state is")
-                dm = width  # the state's parts lie behind each other in out
         st = lib.lp_beam_reorder(_ptr(state), s_outer, s_row, s_mid, outer, mid, width, _ptr(parents), B, rows // B if B else 1, N,
                                  _ptr(out), do, dr, dm, _raw_stream(dev, stream))
     check("lp_beam_reorder", st)
