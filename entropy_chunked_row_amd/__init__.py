@@ -1022,6 +1022,8 @@ def _state_layout(t, dim, name):
     """(outer size, its stride, row stride, mid size, its stride, width), strides and width in bytes, of a state whose
     dimension `dim` is the beams."""
     e, shape, strides = t.element_size(), t.shape, t.stride()
+    if 0 in shape:  # strides say nothing
+        return 0, 0, 0, 0, 0, 0
     width, k = 1, len(shape)
     while k > dim + 1 and (shape[k - 1] == 1 or strides[k - 1] == width):
         width *= shape[k - 1]

@@ -1,4 +1,5 @@
-"""States and results of different layouts: dense into a prefix of each row of a larger cache, and the other way round."""
+"""States and results of different layouts: dense into a prefix of each row of a larger cache, the other way round, and
+states without an element."""
 import numpy as np
 import pytest
 
@@ -43,3 +44,16 @@ def test_layouts_that_share_no_walk_are_refused():
     out = torch.zeros(6, 4, 2, 9, device="cuda")[..., :8]                # 8 parts of 8
     with pytest.raises(ValueError, match="walked"):
         _lp().lp_beam_reorder(state, p, out=out)
+
+
+@pytest.mark.parametrize("shape,dim", [((2, 0, 6, 3), 2), ((0, 2, 6, 3), 2), ((2, 6, 0), 1), ((6, 4, 0, 5), 0), ((6, 0, 4, 5), 0),
+                                       ((3, 0, 6), 2)])
+def test_states_without_an_element(shape, dim):
+    import torch
+    p = to_dev(np.array(PARENTS[1], dtype=np.int32))
+    want = list(shape)
+    want[dim] = 10
+    state = torch.zeros(shape, device="cuda")
+    assert list(_lp().lp_beam_reorder(state, p, dim=dim).shape) == want
+    out = torch.zeros(want, device="cuda")
+    assert _lp().lp_beam_reorder(state, p, dim=dim, out=out) is out
