@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
     // U W pieces of `steps` times 64 vectors, so that one step of the workgroup is a
     // sample of the whole; a wave goes from piece to piece, so that each has its
     // share of a piece that holds more of what is kept.  What is left over behind
-    // the pieces comes last.  There is at least one step: n >= 4 NT P (set_slices).
+    // the pieces comes last.  There is at least one step: n >= 4 NT P (set_slices; the
+    // loop below ends all the same without one).
     const int vectors = n / P, steps = vectors / (64 * U * W);
     const char* base = xp;  // 32-bit offsets: a slice has at most 2^32 bytes
     auto load = [&](uint32_t v) {
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
         most = fmaxf(most, m);
         keep(hit[u], w[u], number(u, q));
       }
-      const bool last = ++q == steps;
+      const bool last = ++q >= steps;
       if (!last) {  // in flight while the exponentials are taken
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = load(number(u, q));
