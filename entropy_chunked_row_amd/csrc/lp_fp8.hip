@@ -76,7 +76,9 @@ __global__ void __launch_bounds__(256) k_fp8_rows(Fp8Args a, uint8_t* xq, float*
   if (lane == 0) sx[b * pitch + t] = scale;
 }
 
-// A workgroup a block of 128 x 128.
+// A workgroup a block of 128 x 128, which stays in registers between the search for its
+// largest magnitude and the rounding.  Bound by HBM: 5120 x 151936 bf16 445 us, 5.2 TB/s read
+// and written (6.1 is an elementwise kernel's), fp32 713 us, 5.5.
 template <class Tr>
 __global__ void __launch_bounds__(256) k_fp8_quantize(Fp8QuantArgs a, int blocks, int64_t first) {
   __shared__ float sm[4];
@@ -638,8 +640,9 @@ hipError_t launch_fp8_logits(int dtype, const Fp8Args& f, char* ws, hipStream_t 
   // in tiles, 32 rows of 8192 x 129280 190 against 210).
   if (a.T <= 16 && a.blocks <= 64) return launch_few<1, true>(a, s);
   if (a.T <= 32 && a.blocks <= 64) return a.out_dtype == 2 ? launch_few<2, true>(a, s) : launch_few<2, false>(a, s);
-  // fp32 results: widened operands, whose products keep every bit; rounded to 16 bits
-  // the 8-bit products' own error (2^-15 of a result) is far below the rounding.
+  // fp32 results: widened operands, whose products keep every bit.  Before a rounding to 16
+  // bits (2e-4 or 2e-3 of a value) the 8-bit products' own error, 1e-5 to 5e-5 of the logits'
+  // rms, is small, and widening would take twice the time (512 rows 773 us against 430).
   // Tiles no wider than the rows need, and two workgroups a CU where they fit: 64 rows
   // of 5120 x 151936 182 us against 219 in tiles of 256 x 64, 128 rows 209 against 234
   // in 256 x 128, 512 rows to fp32 807 against 875.

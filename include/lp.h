@@ -643,9 +643,15 @@ lp_status lp_lm_head_fp8_quantize(const void* weight, lp_dtype dtype, int64_t V,
 /*
  * out[t][v] = x[t] . weight[v] of such a head, x = the hidden row brought to
  * e4m3 likewise, with a scale for each 128 of its columns.  Results are rounded once to out_dtype.
- * Products and sums are fp32 where out_dtype is; where it has 16 bits, products are summed 8 at a
- * time at 13 bits below the largest of them, which leaves about 2e-5 of a result.  hidden bf16 or fp16 [T x ld_h] (fp32:
- * LP_ERR_UNSUPPORTED), out [T x ld_out] of out_dtype, columns past V left.
+ * Products are exact and sums fp32 where out_dtype is, and for up to 16 rows of h up to 8192
+ * whatever it is.  For other 16-bit results products are summed 8 at a time, and of each what lies
+ * 2^-13 below the largest of them is dropped: less than 2^-10 of the sum of the terms'
+ * magnitudes, and 1e-5 to 5e-5 of the logits' rms as measured over terms of both signs (normal
+ * to heavy-tailed; sums that cancel are off by as much), where a rounding to fp16 takes 2e-4
+ * and one to bf16 2e-3 of a value.  So a row's 16-bit logits may differ by that
+ * between a batch of up to 16 rows and a larger one.
+ * hidden bf16 or fp16 [T x ld_h] (fp32: LP_ERR_UNSUPPORTED), out [T x ld_out] of out_dtype, columns
+ * past V left.
  * A NaN or an infinity in a hidden row makes its logits NaN.
  * workspace >= lp_lm_head_fp8_workspace_bytes(T, h, V) bytes (0: sizes not
  * supported), 256-byte aligned; scratch only.  out and the workspace may overlap nothing.
