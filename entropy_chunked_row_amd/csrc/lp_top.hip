@@ -712,10 +712,12 @@ int short_slice(int dtype, int threads) { return 4 * threads * (dtype == 2 ? 4 :
 // shorter than what a workgroup keeps whole.  Slices are either short ones that are
 // kept whole or each of them, a row's last one too, has the columns of a step of
 // the stream, which has no end without one.  Short rows are not cut, but for beams,
-// which are joined anyway: a join would cost more than it saves (1 to 256 rows of 32000:
-// K = 20 17 us, 19 with slices; K = 200 20 and 26 to 34; 256 rows of 65000 21 and 24,
-// 27 and 38).
-constexpr int64_t kWholeRow = 65536;
+// which are joined anyway: up to 128 KB a row a join costs about what it saves.  us a call,
+// whole and in slices, K = 20, 1 / 64 / 256 rows: 20000 bf16 13 / 13 / 14 and 17 / 18 / 19, 65000 bf16
+// 18 / 20 / 21 and 17 / 18 / 24, 32000 fp32 18 / 19 / 21 and 16 / 17 / 21 (500 rows 23 and 26), 65000
+// fp32 25 / 25 / 29 and 16 / 18 / 27; K = 200: 65000 bf16 25 / 26 / 27 either way, 65000 fp32
+// 32 / 32 / 36 and 25 / 28 / 35.
+constexpr int64_t kWholeRow = 131072;  // bytes
 
 void set_slices(TopArgs& a, int dtype) {
   const int64_t lists = (a.W > 0 ? a.W : 1) * static_cast<int64_t>(a.K);
@@ -727,7 +729,7 @@ void set_slices(TopArgs& a, int dtype) {
   const int64_t most = (int64_t(a.V) + least - 1) / least;
   n = n < most ? n : most;
   n = n < most_keys ? n : most_keys;
-  if (a.W == 0 && a.V <= kWholeRow) n = 1;
+  if (a.W == 0 && int64_t(a.V) * (dtype == 2 ? 4 : 2) <= kWholeRow) n = 1;
   const int64_t kept = short_slice(dtype, threads_of(a.K));
   int64_t last;
   do {
