@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   if (whole_end < vs.end() && (whole_end > 0 || !first)) partial(whole_end);
 
   // The stream.  Sums are relative to the largest of the wave's first vectors,
-  // without a running maximum.  Where a wave's sum leaves fp32 that way, or is so
+  // without a running maximum.  Where a wave's sum passes 2^100 that way, or is so
   // small that what was added as 0 (126 octaves below the reference) may count, or
   // where that reference is far from 0, the slice is summed again with one.
   SumStat low{neg_inf(), 0.f};
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     }
     if (!GRAD) {
       const float whole = lanes_reduce<64>(low.s, [](float p, float q) { return p + q; });
-      if (__syncthreads_or(!(whole >= 8.5e-22f && whole <= kLargest))) {
+      if (__syncthreads_or(!(whole >= 8.5e-22f && whole <= kMostSum))) {
         LaneSum over = sum_none();
         for (int q = 0; q < steps; ++q) {
           const int v = tid + q * NT;

@@ -19,12 +19,23 @@ struct LaneSum : SumStat {
 
 __device__ __forceinline__ LaneSum sum_none() { return LaneSum{{neg_inf(), 0.f}}; }
 
+// s 2^d, d <= 0.  A sum relative to a value that a kernel took early may be as large as
+// kMostSum, so that something is left of it where 2^d alone is below fp32: two halves.
+__device__ __forceinline__ float sum_scaled(float s, float d) {
+  const float r = fast_exp2(0.5f * d);
+  return s * r * r;
+}
+
+// The largest sum of a workgroup or wave relative to such a value that is kept: 2^27 of
+// them still add up.
+constexpr float kMostSum = 1.2676506e30f;  // 2^100
+
 // Folds N values whose largest is vm into the state.  -inf weighs 0; a NaN stays
 // a NaN in s.
 template <int N, int CH>
 __device__ __forceinline__ void sum_push(LaneSum& st, const float* x, float vm, float c) {
   if (vm > st.m) {
-    st.s *= fast_exp2(stat_shift(st.m, vm, c));
+    st.s = sum_scaled(st.s, stat_shift(st.m, vm, c));
     st.m = vm;
     st.nmc = -(vm * c);
   }
@@ -49,12 +60,12 @@ __device__ __forceinline__ void sum_push1(LaneSum& st, float x, float c) { sum_p
 template <int N>
 __device__ __forceinline__ SumStat sum_merge(SumStat st, float c) {
   const float m = lanes_reduce<N>(st.m, [](float x, float y) { return fmaxf(x, y); });
-  return SumStat{m, lanes_reduce<N>(st.s * fast_exp2(stat_shift(st.m, m, c)), [](float x, float y) { return x + y; })};
+  return SumStat{m, lanes_reduce<N>(sum_scaled(st.s, stat_shift(st.m, m, c)), [](float x, float y) { return x + y; })};
 }
 
 __device__ __forceinline__ SumStat sum_add(SumStat x, SumStat y, float c) {
   const float m = fmaxf(x.m, y.m);
-  return SumStat{m, x.s * fast_exp2(stat_shift(x.m, m, c)) + y.s * fast_exp2(stat_shift(y.m, m, c))};
+  return SumStat{m, sum_scaled(x.s, stat_shift(x.m, m, c)) + sum_scaled(y.s, stat_shift(y.m, m, c))};
 }
 
 // The workgroup's whole state, in every thread; sm holds NT / 64 states.  Ends

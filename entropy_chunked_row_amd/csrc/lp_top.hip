@@ -465,8 +465,9 @@ __global__ void __launch_bounds__(NT) k_top(TopArgs a) {
   SumStat rest = sum_block<NT>(digits ? st : sum_add(low, st, c), c, sm[0]);
   // What lies more than 126 octaves below the floor was added as 0, and what lies 128
   // above it as infinity.  Where the first is not small beside what is left, or that is
-  // not finite, the rest is summed once more.  (Below the lowest floor lies nothing.)
-  if (relative && !(rest.s >= 8.5e-22f && rest.s <= kLargest)) {
+  // too large to be added up with others, the rest is summed once more.  (Below the
+  // lowest floor lies nothing.)
+  if (relative && !(rest.s >= 8.5e-22f && rest.s <= kMostSum)) {
     st = sum_none();
     for (int v = tid; v * P < n; v += NT) {
       float x[P];
