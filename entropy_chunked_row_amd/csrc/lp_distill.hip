@@ -78,43 +78,66 @@ __device__ __forceinline__ double lanes_sum(double x) {
 // term would be 0 times infinity (finite masks in the teacher's logits, -inf in the student's).
 __device__ __forceinline__ double mass_of(float t) { return static_cast<double>(expf(t)); }
 
-// What the listed entries add to a row's loss before its log-sum-exps are known:
-//   loss = terms + mass lse + r (t_rest - (lse_rest - lse)).
-// The loss is a difference of nearly equal numbers: fp64.
+// What listed entries add to a row's loss before its log-sum-exps are known: with m the
+// largest value of the row's state and l = lse - m / tau,
+//   loss = sum over waves (terms + mass ((m - ref) / tau + l)) + r (t_rest - (lse_rest - lse)).
+// The loss is a difference of nearly equal numbers: fp64; and relative to the largest
+// value that a wave's entries name, since beside values of finite masks fp64 holds nothing else.
 struct Entries {
-  double terms, mass;  // sums of p_k (t_k - z_k / tau) and of p_k
+  double terms, mass;  // sums of p_k (t_k - (z_k - ref) / tau) and of p_k
+  float ref;           // the largest finite z_k of an entry with mass, 0 if there is none
 };
+
+// z, or nothing where an entry has no mass
+__device__ __forceinline__ float candidate_ref(float z, double p) { return p != 0.0 ? z : neg_inf(); }
+__device__ __forceinline__ float reduce_ref(float z) {
+  const float m = lanes_reduce<64>(z, [](float x, float y) { return fmaxf(x, y); });
+  return m > neg_inf() ? m : 0.f;
+}
 
 // By one wave, in every lane of it.
 template <class Tr>
 __device__ __forceinline__ Entries sum_entries(const DistillArgs& a, int64_t row) {
   const char* xp = static_cast<const char*>(a.x) + row * a.ld * Tr::kBytes;
-  Entries e{0.0, 0.0};
-  for (int k = threadIdx.x & 63; k < a.K; k += 64) {
-    const int64_t id = a.ids[row * a.K + k];
-    const float t = a.logprob[row * a.K + k];
-    const double p = mass_of(t);
-    if (id < 0 || id >= a.V || p == 0.0) continue;  // padding, or no mass
-    e.terms += p * (static_cast<double>(t) - static_cast<double>(Tr::load1(xp, id)) * a.inv_tau);
-    e.mass += p;
+  Entries e{0.0, 0.0, neg_inf()};
+  constexpr int E = kMaxTop / 64;
+  float t[E], z[E];
+  double p[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int k = static_cast<int>(threadIdx.x & 63) + i * 64;
+    const int64_t id = k < a.K ? a.ids[row * a.K + k] : -1;
+    const bool inside = id >= 0 && id < a.V;  // else padding
+    t[i] = inside ? a.logprob[row * a.K + k] : neg_inf();
+    z[i] = inside ? Tr::load1(xp, id) : 0.f;
+    p[i] = mass_of(t[i]);
+    e.mass += p[i];
+    e.ref = fmaxf(e.ref, candidate_ref(z[i], p[i]));
   }
+  e.ref = reduce_ref(e.ref);
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (p[i] != 0.0) e.terms += p[i] * (static_cast<double>(t[i]) - below(z[i], e.ref, a.inv_tau));
   e.terms = lanes_sum(e.terms);
   e.mass = lanes_sum(e.mass);
   return e;
 }
 
-// By one thread: the outputs of a row from the states of its unlisted and its
-// listed columns.
-__device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, Entries e, float t_rest, SumStat rest,
+// By one thread: the outputs of a row from the entries of N waves and the states of
+// its unlisted and its listed columns.
+template <int N>
+__device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, const Entries* e, float t_rest, SumStat rest,
                                            SumStat listed) {
-  const double lse = sum_lse(sum_add(rest, listed, a.c), a.c, a.inv_tau);
-  const double lse_rest = sum_lse(rest, a.c, a.inv_tau);
-  double loss = e.terms + e.mass * lse;
+  const SumStat whole = sum_add(rest, listed, a.c);
+  const double log_sum = sum_log(whole, a.c);
+  double loss = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) loss += e[i].terms + e[i].mass * (below(whole.m, e[i].ref, a.inv_tau) + log_sum);
   const double r = mass_of(t_rest);
-  if (r != 0.0) loss += r * (static_cast<double>(t_rest) - (lse_rest - lse));
+  if (r != 0.0) loss += r * (static_cast<double>(t_rest) - sum_gap(rest, whole, log_sum, a.c, a.inv_tau));
   a.loss[row] = static_cast<float>(loss);
-  if (a.lse_out) a.lse_out[row] = static_cast<float>(lse);
-  if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(lse_rest);
+  if (a.lse_out) a.lse_out[row] = static_cast<float>(sum_lse(whole, a.c, a.inv_tau));
+  if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(sum_lse(rest, a.c, a.inv_tau));
 }
 
 __device__ __forceinline__ void store_no_loss(const DistillArgs& a, int64_t row) {
@@ -200,7 +223,8 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   u32x4 in[E];  // the vector that the entry lies in
   float z[E];
   int col[E];  // on the grid of vectors, or outside
-  Entries e{0.0, 0.0};
+  Entries e{0.0, 0.0, neg_inf()};
+  double p[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int k = tid + i * NT;
@@ -215,16 +239,23 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     z[i] = !GRAD && inside && a.nslices == 1 ? Tr::load1(xp, id[i]) : 0.f;
     if (k < kMaxTop) cols[k] = col[i];
     if (GRAD || a.nslices == 1) {
-      const double p = inside ? mass_of(t[i]) : 0.0;
-      e.mass += p;
-      if (GRAD && k < kMaxTop) mass[k] = static_cast<float>(p);
-      if (!GRAD && p != 0.0)
-        e.terms += p * (static_cast<double>(t[i]) - static_cast<double>(z[i]) * a.inv_tau);
+      p[i] = inside ? mass_of(t[i]) : 0.0;
+      e.mass += p[i];
+      if (GRAD && k < kMaxTop) mass[k] = static_cast<float>(p[i]);
+      if (!GRAD) e.ref = fmaxf(e.ref, candidate_ref(z[i], p[i]));
     }
   }
   if ((tid & ~63) < a.K && (GRAD || a.nslices == 1)) {  // waves with entries
+    if (!GRAD) {
+      e.ref = reduce_ref(e.ref);
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (p[i] != 0.0) e.terms += p[i] * (static_cast<double>(t[i]) - below(z[i], e.ref, a.inv_tau));
+      e.terms = lanes_sum(e.terms);
+    }
     e.mass = lanes_sum(e.mass);
-    if (!GRAD) e.terms = lanes_sum(e.terms);
+  } else {
+    e.ref = 0.f;
   }
   if ((tid & 63) == 0) parts[tid >> 6] = e;
   __syncthreads();
@@ -404,13 +435,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   const SumStat rest = sum_merge<W>(sm[0][tid & (W - 1)], c), top = sum_merge<W>(sm[1][tid & (W - 1)], c);
   if (tid != 0) return;
   if (a.nslices == 1) {
-    Entries whole = parts[0];
-#pragma unroll
-    for (int i = 1; i < W; ++i) {
-      whole.terms += parts[i].terms;
-      whole.mass += parts[i].mass;
-    }
-    store_loss(a, row, whole, t_rest, rest, top);
+    store_loss<W>(a, row, parts, t_rest, rest, top);
   } else {
     float* p = a.part + (row * a.nslices + slice) * 4;
     p[0] = rest.m;
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(256) k_distill_join(DistillArgs a) {
   const Entries e = sum_entries<Tr>(a, row);
   rest = sum_merge<64>(rest, a.c);
   listed = sum_merge<64>(listed, a.c);
-  if (lane == 0) store_loss(a, row, e, a.rest ? a.rest[row] : neg_inf(), rest, listed);
+  if (lane == 0) store_loss<1>(a, row, &e, a.rest ? a.rest[row] : neg_inf(), rest, listed);
 }
 
 // Slices per row: as many as make three workgroups a CU where rows are few; the

@@ -80,16 +80,32 @@ __device__ __forceinline__ SumStat sum_block(SumStat st, float c, SumStat* sm) {
   return sum_merge<W>(sm[threadIdx.x & (W - 1)], c);
 }
 
-// log-sum-exp of z / tau, natural, in fp64 (scores of different rows are compared
-// and differences of nearly equal ones formed: fp32 would leave a few 2^-24 of
+// log-sum-exp of z / tau less m / tau, natural, in fp64 (scores of different rows are
+// compared and differences of nearly equal ones formed: fp32 would leave a few 2^-24 of
 // their magnitude).  m c carries the rounding of c and of the product; both are
-// taken out again, so that only the exponents' own roundings remain.
-__device__ __forceinline__ double sum_lse(SumStat st, float c, double inv_tau) {
+// taken out again, so that only the exponents' own roundings remain.  Whatever is taken
+// from a log-sum or added to one is taken relative to m first: in rows of finite masks (m of
+// 1e38) fp64 holds nothing of the logs beside m itself.
+__device__ __forceinline__ double sum_log(SumStat st, float c) {
   if (st.s == 0.f) return -__builtin_inf();
   const float mc = st.m * c;
   const double l2s = log2(static_cast<double>(st.s));
   const double off = is_near(mc) ? static_cast<double>(st.m) * c - static_cast<double>(mc) : 0.0;
-  return static_cast<double>(st.m) * inv_tau + (l2s - off) * 0.69314718055994530942;
+  return (l2s - off) * 0.69314718055994530942;
+}
+
+// (x - m) / tau
+__device__ __forceinline__ double below(float x, float m, double inv_tau) {
+  return (static_cast<double>(x) - static_cast<double>(m)) * inv_tau;
+}
+
+__device__ __forceinline__ double sum_lse(SumStat st, float c, double inv_tau) {
+  return st.s == 0.f ? -__builtin_inf() : static_cast<double>(st.m) * inv_tau + sum_log(st, c);
+}
+
+// Log-sum-exp of a part of a row less the whole's, whose sum_log is given.
+__device__ __forceinline__ double sum_gap(SumStat part, SumStat whole, double whole_log, float c, double inv_tau) {
+  return part.s == 0.f ? -__builtin_inf() : below(part.m, whole.m, inv_tau) + (sum_log(part, c) - whole_log);
 }
 
 // Whole numbers in the order of the values (-0 = 0); NaN of either sign lies outside the infinities.

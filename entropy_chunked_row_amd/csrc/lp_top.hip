@@ -187,20 +187,20 @@ __device__ __forceinline__ void store_top(const TopArgs& a, int64_t row, const u
   const bool bad = !(whole.s > 0.f && whole.s <= kLargest);  // a NaN or +inf in the row, or only -inf
   const float nan = __builtin_nanf("");
   if (static_cast<int>(threadIdx.x) >= a.K) return;
-  const double lse = sum_lse(whole, a.c, a.inv_tau);
+  const double log_sum = sum_log(whole, a.c);
   for (int k = threadIdx.x; k < a.K; k += NT) {
     float lp = bad ? nan : neg_inf();
     int64_t id = -1;
     if (k < got && !bad) {
-      lp = static_cast<float>(static_cast<double>(key_value(top[k])) * a.inv_tau - lse);
+      lp = static_cast<float>(below(key_value(top[k]), whole.m, a.inv_tau) - log_sum);
       id = key_col(top[k]);
     }
     a.ids[row * a.K + k] = id;
     a.logprob[row * a.K + k] = lp;
   }
   if (threadIdx.x == 0) {
-    if (a.rest) a.rest[row] = bad ? nan : static_cast<float>(sum_lse(rest, a.c, a.inv_tau) - lse);
-    if (a.lse) a.lse[row] = static_cast<float>(lse);
+    if (a.rest) a.rest[row] = bad ? nan : static_cast<float>(sum_gap(rest, whole, log_sum, a.c, a.inv_tau));
+    if (a.lse) a.lse[row] = static_cast<float>(sum_lse(whole, a.c, a.inv_tau));
   }
 }
 
@@ -586,14 +586,15 @@ struct Candidate {
 static_assert(kMaxBuffered <= 1 << 16 && kMaxBeamLists <= kMaxBuffered, "a key's number in 16 bits");
 
 // One request: the lists of its beams' slices, scored and ranked.  Scores are fp64
-// (sum_lse).  Where the sum so far takes up the differences of a beam's logits (1e20, or
+// (sum_log).  Where the sum so far takes up the differences of a beam's logits (1e20, or
 // the largest finite number, for beams that are not there; temperatures as large), place
 // keeps their order.
 template <int NT>
 __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
   extern __shared__ __attribute__((aligned(16))) Candidate cand[];  // W * nslices * K of them
   __shared__ uint32_t best[NT];
-  __shared__ double gain[kMaxBeams];  // what a beam adds to z / tau; NaN: no continuation
+  __shared__ double gain[kMaxBeams];  // what a beam adds to (z - m) / tau; NaN: no continuation
+  __shared__ float most[kMaxBeams];   // m
   __shared__ uint32_t count, bar;
   const int tid = threadIdx.x;
   const int64_t b = a.row0 + blockIdx.x;
@@ -618,7 +619,8 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
         if (key) sum_push1(st, key_value(key), c);
       }
       const SumStat whole = sum_merge<64>(st, c);
-      if (whole.s > 0.f && whole.s <= kLargest) g = static_cast<double>(a.beam_scores[row]) - sum_lse(whole, c, a.inv_tau);
+      if (whole.s > 0.f && whole.s <= kLargest) g = static_cast<double>(a.beam_scores[row]) - sum_log(whole, c);
+      if ((tid & 63) == 0) most[w] = whole.m;
     }
     if ((tid & 63) == 0) gain[w] = g;
   }
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
     const uint64_t key = a.part_keys[b * n + i];
     if (!key) return 0;
     place |= static_cast<uint64_t>(~static_cast<uint32_t>(key >> 32)) << 16;
-    return order_of64(gain[w] + static_cast<double>(key_value(key)) * a.inv_tau);
+    return order_of64(gain[w] + below(key_value(key), most[w], a.inv_tau));
   };
   // the first candidates stay in registers
   constexpr int R = 2;
@@ -655,12 +657,12 @@ __global__ void __launch_bounds__(NT) k_beam_join(TopArgs a) {
       f(q);
     }
   };
-  uint32_t most = 0;
+  uint32_t first_word = 0;
   each([&](const Candidate& q) {
     const uint32_t o = static_cast<uint32_t>(q.order >> 32);
-    most = o > most ? o : most;
+    first_word = o > first_word ? o : first_word;
   });
-  best[tid] = most;
+  best[tid] = first_word;
   __syncthreads();
   if (tid < 64) {
     const uint32_t t = kth_largest<NT, 32>(best, N);

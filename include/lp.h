@@ -523,7 +523,8 @@ lp_status lp_embedding_backward(const void* grad_out, lp_dtype dtype, int64_t N,
  * lse      fp32 [T] or NULL: log-sum-exp of the tempered row.
  * Rows with mask[t] == 0 get ids -1 and 0 elsewhere.  A row that holds NaN or
  * +inf, or only -inf, gets ids -1 and NaN in logprob and rest.  Finite values of any size count by
- * how far they lie below the row's largest.
+ * how far they lie below the row's largest (a row of one value is uniform, whatever the value);
+ * results below what fp32 holds are -inf.
  * The same bits on every call.
  * workspace >= lp_top_workspace_bytes(dtype, T, V, K) bytes, 256-byte aligned;
  * scratch only.  Outputs and workspace may overlap nothing.
@@ -556,6 +557,7 @@ lp_status lp_top_logits(const void* logits, lp_dtype dtype, int64_t T, int64_t V
  *                  columns that no entry names (-inf if there are none but -inf);
  *                  saved for the backward.
  * Rows with mask[t] == 0 get 0 everywhere.  Rows that hold NaN or +inf, or only -inf, give NaN.
+ * Finite values of any size count as in lp_top_logits.
  * workspace >= lp_distill_top_workspace_bytes(dtype, T, V) bytes, 256-byte aligned; scratch only.
  * Outputs and workspace may overlap nothing.
  */

@@ -660,11 +660,19 @@ def _top_order(z):
     return order[z[order] > -np.inf]
 
 
+def _below_largest(z, temperature):
+    """(rows tempered, relative to their largest entry; that entry tempered): entries of any size count by how far they
+    lie below the largest, of which fp64 would leave nothing at 1e38."""
+    m = z.max(axis=1)
+    m = np.where(np.isfinite(m), m, 0.0)
+    return tempered(z - m[:, None], temperature), tempered(m, temperature)
+
+
 def top_logits(logits, K, mask, temperature):
     """(ids, logprob [T, K], rest, lse [T]) of the K largest logits of each scored row."""
     z = np.asarray(logits, dtype=np.float64)
     T, V = z.shape
-    zt = tempered(z, temperature)
+    zt, most = _below_largest(z, temperature)
     ids = np.full((T, K), -1, dtype=np.int64)
     logprob, rest, lse = np.zeros((T, K)), np.zeros(T), np.zeros(T)
     for t in range(T):
@@ -675,13 +683,14 @@ def top_logits(logits, K, mask, temperature):
             lse[t] = -np.inf if not np.isnan(z[t]).any() and not (z[t] == np.inf).any() else np.nan
             continue
         at = _top_order(z[t])[:K]
-        lse[t] = log_normaliser(zt[t:t + 1])[0]
+        log_sum = log_normaliser(zt[t:t + 1])[0]
+        lse[t] = most[t] + log_sum
         ids[t, :at.size] = at
         logprob[t] = -np.inf
-        logprob[t, :at.size] = zt[t, at] - lse[t]
+        logprob[t, :at.size] = zt[t, at] - log_sum
         left = np.delete(zt[t], at)
         left = left[left > -np.inf]
-        rest[t] = log_normaliser(left[None])[0] - lse[t] if left.size else -np.inf
+        rest[t] = log_normaliser(left[None])[0] - log_sum if left.size else -np.inf
     return ids, logprob, rest, lse
 
 
@@ -706,7 +715,7 @@ def list_mass(t):
 
 def distill_top(logits, ids, logprob, rest, mask, temperature):
     """(loss, lse, lse_rest) of KL from a teacher's lists to the student's rows."""
-    zt = tempered(np.asarray(logits, dtype=np.float64), temperature)
+    zt, most = _below_largest(np.asarray(logits, dtype=np.float64), temperature)
     T = zt.shape[0]
     loss, lse, lse_rest = np.zeros(T), np.zeros(T), np.zeros(T)
     for t in range(T):
@@ -720,13 +729,14 @@ def distill_top(logits, ids, logprob, rest, mask, temperature):
                     loss[t] += p * (a - (zt[t, j] - lse[t]))
             if rest is not None and list_mass(rest[t]) != 0:
                 loss[t] += list_mass(rest[t]) * (float(rest[t]) - (lse_rest[t] - lse[t]))
+            lse[t], lse_rest[t] = lse[t] + most[t], lse_rest[t] + most[t]
     return loss, lse, lse_rest
 
 
 def distill_top_backward(logits, ids, logprob, rest, mask, temperature, grad_loss):
     """Gradient of sum grad_loss * loss with respect to the raw logits."""
     z = np.asarray(logits, dtype=np.float64)
-    zt = tempered(z, temperature)
+    zt, _ = _below_largest(z, temperature)
     tau = temperature if temperature_applies(temperature) else 1.0
     d = np.zeros_like(z)
     for t in range(z.shape[0]):
@@ -747,7 +757,7 @@ def distill_top_backward(logits, ids, logprob, rest, mask, temperature, grad_los
 
 def beam_select(logits, beam_scores, N, finished, end_token, temperature):
     """(scores, parents, tokens [B, N]) of the best continuations over the beams of each request."""
-    zt = tempered(np.asarray(logits, dtype=np.float64), temperature)
+    zt, _ = _below_largest(np.asarray(logits, dtype=np.float64), temperature)
     B, W = np.asarray(beam_scores).shape
     scores, parents = np.full((B, N), -np.inf), np.full((B, N), -1, dtype=np.int32)
     tokens = np.full((B, N), -1, dtype=np.int64)
@@ -765,7 +775,7 @@ def beam_select(logits, beam_scores, N, finished, end_token, temperature):
                 continue
             lse = _lse1(row)
             # of one beam by its logits, whatever its score leaves of their differences
-            cand += [(-(s + row[v] - lse), w, n, int(v)) for n, v in enumerate(_top_order(row)[:N])]
+            cand += [(-(s + (row[v] - lse)), w, n, int(v)) for n, v in enumerate(_top_order(row)[:N])]
         for n, (s, w, _, v) in enumerate(sorted(cand)[:N]):
             scores[b, n], parents[b, n], tokens[b, n] = -s, w, v
     return scores, parents, tokens
