@@ -106,18 +106,20 @@ __device__ __forceinline__ Entries sum_entries(const DistillArgs& a, int64_t row
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int k = static_cast<int>(threadIdx.x & 63) + i * 64;
+    p[i] = 0.0;
+    if (i * 64 >= a.K) continue;  // for the whole wave
     const int64_t id = k < a.K ? a.ids[row * a.K + k] : -1;
+    t[i] = k < a.K ? a.logprob[row * a.K + k] : neg_inf();
     const bool inside = id >= 0 && id < a.V;  // else padding
-    t[i] = inside ? a.logprob[row * a.K + k] : neg_inf();
     z[i] = inside ? Tr::load1(xp, id) : 0.f;
-    p[i] = mass_of(t[i]);
+    p[i] = inside ? mass_of(t[i]) : 0.0;
     e.mass += p[i];
     e.ref = fmaxf(e.ref, candidate_ref(z[i], p[i]));
   }
   e.ref = reduce_ref(e.ref);
 #pragma unroll
   for (int i = 0; i < E; ++i)
-    if (p[i] != 0.0) e.terms += p[i] * (static_cast<double>(t[i]) - below(z[i], e.ref, a.inv_tau));
+    if (i * 64 < a.K && p[i] != 0.0) e.terms += p[i] * (static_cast<double>(t[i]) - below(z[i], e.ref, a.inv_tau));
   e.terms = lanes_sum(e.terms);
   e.mass = lanes_sum(e.mass);
   return e;
@@ -129,15 +131,15 @@ template <int N>
 __device__ __forceinline__ void store_loss(const DistillArgs& a, int64_t row, const Entries* e, float t_rest, SumStat rest,
                                            SumStat listed) {
   const SumStat whole = sum_add(rest, listed, a.c);
-  const double log_sum = sum_log(whole, a.c);
+  const double log_sum = sum_log(whole, a.c), log_rest = sum_log(rest, a.c);
   double loss = 0.0;
 #pragma unroll
   for (int i = 0; i < N; ++i) loss += e[i].terms + e[i].mass * (below(whole.m, e[i].ref, a.inv_tau) + log_sum);
   const double r = mass_of(t_rest);
-  if (r != 0.0) loss += r * (static_cast<double>(t_rest) - sum_gap(rest, whole, log_sum, a.c, a.inv_tau));
+  if (r != 0.0) loss += r * (static_cast<double>(t_rest) - sum_gap(rest, log_rest, whole, log_sum, a.inv_tau));
   a.loss[row] = static_cast<float>(loss);
-  if (a.lse_out) a.lse_out[row] = static_cast<float>(sum_lse(whole, a.c, a.inv_tau));
-  if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(sum_lse(rest, a.c, a.inv_tau));
+  if (a.lse_out) a.lse_out[row] = static_cast<float>(sum_lse(whole, log_sum, a.inv_tau));
+  if (a.lse_rest_out) a.lse_rest_out[row] = static_cast<float>(sum_lse(rest, log_rest, a.inv_tau));
 }
 
 __device__ __forceinline__ void store_no_loss(const DistillArgs& a, int64_t row) {

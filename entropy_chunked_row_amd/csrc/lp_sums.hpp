@@ -99,13 +99,12 @@ __device__ __forceinline__ double below(float x, float m, double inv_tau) {
   return (static_cast<double>(x) - static_cast<double>(m)) * inv_tau;
 }
 
-__device__ __forceinline__ double sum_lse(SumStat st, float c, double inv_tau) {
-  return st.s == 0.f ? -__builtin_inf() : static_cast<double>(st.m) * inv_tau + sum_log(st, c);
+// The log-sum-exp itself, and a part's less the whole row's, from states and their sum_log.
+__device__ __forceinline__ double sum_lse(SumStat st, double log_sum, double inv_tau) {
+  return st.s == 0.f ? -__builtin_inf() : static_cast<double>(st.m) * inv_tau + log_sum;
 }
-
-// Log-sum-exp of a part of a row less the whole's, whose sum_log is given.
-__device__ __forceinline__ double sum_gap(SumStat part, SumStat whole, double whole_log, float c, double inv_tau) {
-  return part.s == 0.f ? -__builtin_inf() : below(part.m, whole.m, inv_tau) + (sum_log(part, c) - whole_log);
+__device__ __forceinline__ double sum_gap(SumStat part, double part_log, SumStat whole, double whole_log, double inv_tau) {
+  return part.s == 0.f ? -__builtin_inf() : below(part.m, whole.m, inv_tau) + (part_log - whole_log);
 }
 
 // Whole numbers in the order of the values (-0 = 0); NaN of either sign lies outside the infinities.

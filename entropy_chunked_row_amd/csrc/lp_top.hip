@@ -199,8 +199,8 @@ __device__ __forceinline__ void store_top(const TopArgs& a, int64_t row, const u
     a.logprob[row * a.K + k] = lp;
   }
   if (threadIdx.x == 0) {
-    if (a.rest) a.rest[row] = bad ? nan : static_cast<float>(sum_gap(rest, whole, log_sum, a.c, a.inv_tau));
-    if (a.lse) a.lse[row] = static_cast<float>(sum_lse(whole, a.c, a.inv_tau));
+    if (a.rest) a.rest[row] = bad ? nan : static_cast<float>(sum_gap(rest, sum_log(rest, a.c), whole, log_sum, a.inv_tau));
+    if (a.lse) a.lse[row] = static_cast<float>(sum_lse(whole, log_sum, a.inv_tau));
   }
 }
 
